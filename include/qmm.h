@@ -67,7 +67,9 @@ enum {
     QMM_EINVAL_PTR = -3,   /* null or misaligned pointer for a non-empty call  */
     QMM_ENOMEM = -4,       /* workspace allocation failed                      */
     QMM_ECUDA = -5,        /* CUDA runtime error (detail in qmm_last_error)    */
-    QMM_ETIMEOUT = -6      /* a bounded device wait expired (qmm_device_status)*/
+    QMM_ETIMEOUT = -6,     /* a bounded device wait expired (qmm_device_status)*/
+    QMM_EINDEX = -7        /* a kernel met a row index or an offset out of range
+                              and skipped it (qmm_device_status)              */
 };
 
 /*
@@ -239,6 +241,119 @@ QMM_API int qmm_t(int type, const void *W_blocks, int64_t H, int64_t N, int64_t 
 QMM_API int qmm_gate_up(int type_gate, const void *W_gate, int type_up, const void *W_up, int64_t N, int64_t K,
                         const float *x, int64_t M, float *h, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Block-scaled 8-bit floats, and expert layers built on them
+ * ---------------------------------------------------------------------------
+ * Weights W[N,K] as e4m3 codes (one byte each: sign, 4 exponent and 3
+ * mantissa bits, largest value 448, no infinity), row-major, with one fp32
+ * scale per block of 128 x 128, S[ceil(N/128)][ceil(K/128)]:
+ *   w[n,k] = S[n/128][k/128] * code(n,k).
+ * The last blocks may be short.  Activations and results are fp32, fp16 or
+ * bf16 (qmm_ftype); activations are rounded inside the call to e4m3 codes
+ * with one fp32 scale per 128 values of a row, as qmm_f8_quantize does it.
+ * K must be a multiple of 16 (rows of codes are then 16-byte multiples, as the
+ * bulk copies need) and at most 2^24.  W is 16-byte aligned and contiguous; S
+ * 4-byte aligned; x and y are row-major with a row pitch of ldx / ldy elements
+ * (>= the row length) and only need their type's alignment.
+ */
+typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2 } qmm_ftype;
+
+/* Most experts of a grouped call, and most choices per token of qmm_route. */
+#define QMM_F8_MAX_EXPERTS 1024
+#define QMM_ROUTE_MAX_K 32
+
+/*
+ * qmm_f8_quantize -- the activation quantiser on its own: for each row of
+ * x[M,K] and each block b of 128 values (any K; the last may be short)
+ *   s[m,b] = max(max|x| / 448, 2^-126),  q = e4m3(x * (1 / s)),
+ * divisions and product rounded to fp32, codes to nearest with ties to even.
+ *   x : device [M] rows of type x_type, ldx elements apart.
+ *   q : device [M][K] codes;  s : device [M][ceil(K/128)] fp32.
+ * Bit-for-bit reproducible.  A block that holds a NaN or an infinity gets a
+ * NaN or infinite scale and NaN codes where x is not finite.
+ */
+QMM_API int qmm_f8_quantize(int x_type, const void *x, int64_t M, int64_t K, int64_t ldx, void *q, float *s,
+                            void *stream);
+
+/*
+ * qmm_f8 -- y[M,N] = W[N,K] . x[M,K]^T:
+ *   y[m,n] = sum_b sx[m,b] * S[n/128,b] * sum_{k in b} qx[m,k] * code(n,k),
+ * the inner sums on the fp8 tensor cores (exact products, fp32 accumulation
+ * over the 128 terms), the outer one in fp32, rounded once to y's type.
+ * Accuracy against the f64 value of that formula, before the rounding to
+ * y's type: |dy| <= 2^-17 * sum_b |sx S| * sum_k |qx code|.
+ * Results do not depend on timing: repeated calls agree bit for bit.
+ * Two launches (quantiser, product); uses the per-(device, stream) workspace
+ * of qmm (make one call of the largest size before graph capture).
+ * K == 0 writes y = 0.  M*N below 2^31 tiles of 16 x 128.
+ */
+QMM_API int qmm_f8(const void *W, const float *S, int64_t N, int64_t K, int x_type, const void *x, int64_t M,
+                   int64_t ldx, int y_type, void *y, int64_t ldy, void *stream);
+
+/*
+ * qmm_f8_experts -- the same product grouped by expert, the group sizes on
+ * the device: for every expert e < E and row r, offsets[e] <= r < offsets[e+1],
+ *   y[r] = W[e] . x[rows ? rows[r] : r].
+ *   W, S    : [E][N][K] codes, [E][ceil(N/128)][ceil(K/128)] scales.
+ *   E       : 1 <= E <= QMM_F8_MAX_EXPERTS.
+ *   x       : device [M] rows, ldx elements apart.
+ *   offsets : device [E+1] int32, not decreasing, from 0 up to at most R.
+ *             Groups may be empty.  Rows from offsets[E] on are not written.
+ *   rows    : device [R] int32, the row of x of each row of y, or null (row r
+ *             of y is row r of x; then M = R).
+ *   R       : rows of y (at least offsets[E]).
+ * The sizes are never read on the host: the call can be captured in a graph
+ * and replayed with other offsets.  An offset or a row index out of range is
+ * skipped, its rows of y are undefined, and qmm_device_status() reports
+ * QMM_EINDEX.
+ */
+QMM_API int qmm_f8_experts(const void *W, const float *S, int64_t E, int64_t N, int64_t K, int x_type, const void *x,
+                           int64_t M, int64_t ldx, const int32_t *offsets, const int32_t *rows, int64_t R, int y_type,
+                           void *y, int64_t ldy, void *stream);
+
+/*
+ * qmm_route -- the router of an expert layer.  For each token the k experts
+ * with the largest logits in falling order (ties: the lowest index; NaN counts
+ * as -inf; a token may choose experts at -inf when fewer than k others are
+ * left, their weight is 0), their weights, and the pairs (t, j) sorted by
+ * expert, pairs of one expert in order of t.
+ *   score     : QMM_ROUTE_SOFTMAX over all E logits, or QMM_ROUTE_SIGMOID.
+ *   normalize : divide the k weights by their sum (a sum of 0 leaves them 0).
+ *   factor    : multiplies the weights.
+ *   logits    : device [T] rows of E values of type x_type, ldx apart.
+ *   weights, experts : device [T][k] fp32 / int32.
+ *   offsets   : device [E+1] int32, the groups for qmm_f8_experts.
+ *   rows      : device [T*k] int32, the token of each sorted row.
+ *   slots     : device [T][k] int32, the sorted row of each pair.
+ * 1 <= E <= QMM_F8_MAX_EXPERTS, 1 <= k <= min(E, QMM_ROUTE_MAX_K), T*k < 2^31.
+ * T == 0 writes offsets = 0.
+ */
+#define QMM_ROUTE_SOFTMAX 0
+#define QMM_ROUTE_SIGMOID 1
+QMM_API int qmm_route(int x_type, const void *logits, int64_t T, int64_t E, int64_t ldx, int k, int score,
+                      int normalize, float factor, float *weights, int32_t *experts, int32_t *offsets, int32_t *rows,
+                      int32_t *slots, void *stream);
+
+/*
+ * qmm_f8_moe -- the gated MLP of every token's experts and their weighted sum:
+ *   h[r] = silu(W_gate[e] . x[t]) * (W_up[e] . x[t]),  r = slots[t,j], e its expert,
+ *   y[t] = sum_j weights[t,j] * (W_down[e] . h[slots[t,j]]),
+ * x and h rounded as in qmm_f8_quantize, the sum over j in fp32 in order of j.
+ *   x, y                      : device [T] rows of H values, ldx / ldy apart.
+ *   weights, offsets, slots   : as qmm_route writes them (k choices per token;
+ *                               every row below offsets[E] in exactly one slot).
+ *   W_gate, W_up              : [E][I][H] codes, scales [E][ceil(I/128)][ceil(H/128)].
+ *   W_down                    : [E][H][I] codes, scales [E][ceil(H/128)][ceil(I/128)].
+ * H and I multiples of 16.  Four launches: quantiser (one row of codes per
+ * slot), gate and up with the SiLU and h's rounding, down, weighted sum.
+ * Errors as qmm_f8_experts.
+ */
+QMM_API int qmm_f8_moe(int x_type, const void *x, int64_t T, int64_t H, int64_t ldx, int k, const float *weights,
+                       const int32_t *offsets, const int32_t *slots, int64_t E, int64_t I, const void *W_gate,
+                       const float *S_gate, const void *W_up, const float *S_up, const void *W_down,
+                       const float *S_down, int y_type, void *y, int64_t ldy, void *stream);
+
 /* Name of a status code. */
 QMM_API const char *qmm_strerror(int status);
 
@@ -248,8 +363,8 @@ QMM_API const char *qmm_last_error(void);
 /*
  * qmm_device_status -- synchronise `stream` and report whether any kernel of
  * this library on the current device gave up on a bounded wait since the
- * last call (QMM_ETIMEOUT; the flag is then cleared), or QMM_ECUDA if the
- * synchronisation itself failed.
+ * last call (QMM_ETIMEOUT), or met an index out of range (QMM_EINDEX); the
+ * flags are then cleared.  QMM_ECUDA if the synchronisation itself failed.
  */
 QMM_API int qmm_device_status(void *stream);
 

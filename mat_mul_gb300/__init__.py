@@ -10,9 +10,19 @@ library is missing or no GPU is present the calls raise.
     h = q.qmm_gate_up(q.Q4_K, Wg, q.Q4_K, Wu, N, K, x)           # silu(Wg x) * (Wu x)
     o = q.qmm_t(q.Q8_0, V_cache, H, T, D, p)      # p: [H, M, T] -> [H, M, D]
     w = q.qmm_dequant(q.Q6_K, blocks, n_elems)    # cuda f32 [n_elems]
+
+Weights in 8-bit floats (e4m3 codes, one fp32 scale per 128 x 128 block), x and
+y in float32, float16 or bfloat16:
+
+    y = q.qmm_f8(W, S, x)                         # W [N, K] codes, S its scales, x [M, K] -> [M, N]
+    r = q.qmm_route(logits, k)                    # a token's k experts, their weights, the pairs by expert
+    y = q.qmm_f8_experts(W, S, x, r.offsets, rows=r.rows)   # W [E, N, K]: one row per (token, expert)
+    y = q.qmm_f8_moe(x, r, Wg, Sg, Wu, Su, Wd, Sd)          # the whole gated expert MLP, [T, H]
+    c, s = q.qmm_f8_quantize(x)                   # codes and scales of activations
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -27,6 +37,7 @@ QMM_EINVAL_PTR = -3
 QMM_ENOMEM = -4
 QMM_ECUDA = -5
 QMM_ETIMEOUT = -6
+QMM_EINDEX = -7
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libqmm.so")
@@ -72,6 +83,13 @@ def load():
     L.qmm_set_prefill_path.restype = I
     L.qmm_inject_stall.argtypes = [I]
     L.qmm_inject_stall.restype = I
+    L.qmm_f8_quantize.argtypes = [I, P, I64, I64, I64, P, P, P]
+    L.qmm_f8.argtypes = [P, P, I64, I64, I, P, I64, I64, I, P, I64, P]
+    L.qmm_f8_experts.argtypes = [P, P, I64, I64, I64, I, P, I64, I64, P, P, I64, I, P, I64, P]
+    L.qmm_route.argtypes = [I, P, I64, I64, I64, I, I, I, ctypes.c_float, P, P, P, P, P, P]
+    L.qmm_f8_moe.argtypes = [I, P, I64, I64, I64, I, P, P, P, I64, I64, P, P, P, P, P, P, I, P, I64, P]
+    for f in ("qmm_f8_quantize", "qmm_f8", "qmm_f8_experts", "qmm_route", "qmm_f8_moe"):
+        getattr(L, f).restype = I
     for f in ("qmm_dequant", "qmm", "qmm_noalloc", "qmm_quantize_act", "qmm_device_status",
               "qmm_release", "qmm_group", "qmm_t", "qmm_gate_up"):
         getattr(L, f).restype = I
@@ -228,6 +246,179 @@ def qmm_quantize_act(x, stream=None):
     _check(load().qmm_quantize_act(_ptr(x2), int(M), int(K), _ptr(q), _ptr(d), _ptr(s),
                                    _stream_handle(stream)))
     return q, d, s
+
+
+# ---------------------------------------------------------------------------
+# Block-scaled 8-bit floats and expert layers
+# ---------------------------------------------------------------------------
+F8_BLOCK = 128          # values per scale along K, weight rows per scale along N
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
+_SCORES = {"softmax": ROUTE_SOFTMAX, "sigmoid": ROUTE_SIGMOID}
+_ftypes = {}            # torch dtype -> qmm_ftype, filled on first use
+
+
+def _ftype(dtype, what):
+    if not _ftypes:
+        import torch
+        _ftypes.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    t = _ftypes.get(dtype)
+    if t is None:
+        raise ValueError(f"{what} must be float32, float16 or bfloat16, not {dtype}")
+    return t
+
+
+def _rows2d(t, what):
+    """t as [rows, columns] with adjacent columns: (rows, columns, row pitch)."""
+    if t.dim() == 1:
+        t = t.unsqueeze(0)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a matrix whose row elements are adjacent, got shape {tuple(t.shape)} "
+                         f"strides {t.stride()}")
+    rows, cols = t.shape
+    # (a pitch below the row length, as of an expanded tensor, is refused by the library)
+    return rows, cols, t.stride(0) if rows > 1 else cols
+
+
+def _f8_weights(W, S, dims, what):
+    """Shape of the codes W, after the checks of W and of its scales S."""
+    import torch
+    if W.dtype not in (torch.float8_e4m3fn, torch.uint8) or W.dim() != dims or not W.is_contiguous():
+        raise ValueError(f"{what}: codes must be a contiguous {dims}-d float8_e4m3fn (or uint8) tensor")
+    shape = tuple(W.shape)
+    want = shape[:-2] + (-(-shape[-2] // F8_BLOCK), -(-shape[-1] // F8_BLOCK))
+    if S.dtype != torch.float32 or tuple(S.shape) != want or not S.is_contiguous():
+        raise ValueError(f"{what}: scales must be a contiguous float32 tensor of shape {want}, got {tuple(S.shape)}")
+    return shape
+
+
+def _same_device(*ts):
+    _require_cuda(*ts)
+    dev = ts[0].device
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and on {t.device}")
+
+
+def _f8_out(y, rows, cols, dtype, device):
+    """The result tensor and its row pitch: y checked, or a new one."""
+    import torch
+    if y is None:
+        return torch.empty((rows, cols), dtype=dtype, device=device), cols
+    r, c, ldy = _rows2d(y, "y")
+    if (r, c) != (rows, cols):
+        raise ValueError(f"y has shape {tuple(y.shape)}, expected {(rows, cols)}")
+    return y, ldy
+
+
+def _int32(t, n, what):
+    import torch
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of {n} elements, got {t.dtype} {tuple(t.shape)}")
+
+
+def qmm_f8_quantize(x, stream=None):
+    """(codes float8_e4m3fn [M, K], scales float32 [M, ceil(K/128)]) of a device
+    tensor x [M, K] (or [K]) of float32, float16 or bfloat16 rows."""
+    import torch
+    _require_cuda(x)
+    M, K, ldx = _rows2d(x, "x")
+    ft = _ftype(x.dtype, "x")
+    c = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+    s = torch.empty((M, -(-K // F8_BLOCK)), dtype=torch.float32, device=x.device)
+    _check(load().qmm_f8_quantize(ft, _ptr(x), M, K, ldx, _ptr(c), _ptr(s), _stream_handle(stream)))
+    return c, s
+
+
+def qmm_f8(W, S, x, y=None, dtype=None, stream=None):
+    """y[M, N] = W . x^T for codes W [N, K] (float8_e4m3fn or uint8), scales S
+    [ceil(N/128), ceil(K/128)] and x [M, K] (or [K]) of float32, float16 or
+    bfloat16; y has x's type unless dtype (or y) says otherwise.  K a multiple
+    of 16.  Rows of x and y may be further apart than their length."""
+    _same_device(x, W, S, y)
+    N, K = _f8_weights(W, S, 2, "W")
+    M, cols, ldx = _rows2d(x, "x")
+    if cols != K:
+        raise ValueError(f"x has {cols} columns, W {K}")
+    y, ldy = _f8_out(y, M, N, dtype or x.dtype, x.device)
+    _check(load().qmm_f8(_ptr(W), _ptr(S), N, K, _ftype(x.dtype, "x"), _ptr(x), M, ldx, _ftype(y.dtype, "y"), _ptr(y),
+                         ldy, _stream_handle(stream)))
+    return y
+
+
+def qmm_f8_experts(W, S, x, offsets, rows=None, y=None, dtype=None, stream=None):
+    """The product grouped by expert: y[r] = W[e] . x[rows[r]] (or x[r] without
+    rows) for offsets[e] <= r < offsets[e+1]; W [E, N, K] codes, S their scales,
+    offsets int32 [E+1] and rows int32 on the device.  Returns y [R, N], R the
+    length of rows (or of x); rows of y from offsets[E] on are not written."""
+    _same_device(x, W, S, offsets, rows, y)
+    E, N, K = _f8_weights(W, S, 3, "W")
+    M, cols, ldx = _rows2d(x, "x")
+    if cols != K:
+        raise ValueError(f"x has {cols} columns, W {K}")
+    _int32(offsets, E + 1, "offsets")
+    R = M
+    if rows is not None:
+        R = rows.numel()
+        _int32(rows, R, "rows")
+    y, ldy = _f8_out(y, R, N, dtype or x.dtype, x.device)
+    _check(load().qmm_f8_experts(_ptr(W), _ptr(S), E, N, K, _ftype(x.dtype, "x"), _ptr(x), M, ldx, _ptr(offsets),
+                                 _ptr(rows), R, _ftype(y.dtype, "y"), _ptr(y), ldy, _stream_handle(stream)))
+    return y
+
+
+#: What qmm_route returns: weights [T, k] float32 and experts [T, k] int32 of each token's
+#: choices, the groups offsets [E+1], the token of each sorted row rows [T*k], and the sorted
+#: row of each pair slots [T, k] (all int32).
+Route = collections.namedtuple("Route", "weights experts offsets rows slots")
+
+
+def qmm_route(logits, k, score="softmax", normalize=True, factor=1.0, stream=None):
+    """The k experts of each token with the largest logits [T, E], their weights
+    (softmax or sigmoid scores, divided by their sum when normalize), and the
+    (token, choice) pairs sorted by expert; see Route."""
+    import torch
+    _require_cuda(logits)
+    T, E, ld = _rows2d(logits, "logits")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, not {score!r}")
+    k = int(k)
+    dev, i32 = logits.device, torch.int32
+    n = max(k, 0)
+    weights = torch.empty((T, n), dtype=torch.float32, device=dev)
+    ints = torch.empty(3 * T * n + E + 1, dtype=i32, device=dev)
+    experts, slots, rows, offsets = ints.split([T * n, T * n, T * n, E + 1])
+    experts, slots = experts.view(T, n), slots.view(T, n)
+    _check(load().qmm_route(_ftype(logits.dtype, "logits"), _ptr(logits), T, E, ld, k, _SCORES[score],
+                            int(bool(normalize)), float(factor), _ptr(weights), _ptr(experts), _ptr(offsets),
+                            _ptr(rows), _ptr(slots), _stream_handle(stream)))
+    return Route(weights, experts, offsets, rows, slots)
+
+
+def qmm_f8_moe(x, route, W_gate, S_gate, W_up, S_up, W_down, S_down, y=None, dtype=None, stream=None):
+    """y[t] = sum_j weights[t, j] * W_down[e] . h, h = silu(W_gate[e] . x[t]) *
+    (W_up[e] . x[t]), over the choices of route (a Route, as qmm_route returns
+    it): x [T, H], W_gate and W_up [E, I, H], W_down [E, H, I] codes with their
+    scales.  H and I multiples of 16."""
+    import torch
+    weights, _, offsets, _, slots = route
+    _same_device(x, W_gate, S_gate, W_up, S_up, W_down, S_down, weights, offsets, slots, y)
+    E, I, H = _f8_weights(W_gate, S_gate, 3, "W_gate")
+    if _f8_weights(W_up, S_up, 3, "W_up") != (E, I, H) or _f8_weights(W_down, S_down, 3, "W_down") != (E, H, I):
+        raise ValueError(f"W_up must be {(E, I, H)} and W_down {(E, H, I)} for W_gate {(E, I, H)}, got "
+                         f"{tuple(W_up.shape)} and {tuple(W_down.shape)}")
+    T, cols, ldx = _rows2d(x, "x")
+    if cols != H:
+        raise ValueError(f"x has {cols} columns, the experts {H}")
+    if weights.dim() != 2 or weights.shape[0] != T or weights.dtype != torch.float32 or not weights.is_contiguous():
+        raise ValueError(f"route.weights must be a contiguous float32 tensor of {T} rows, got {tuple(weights.shape)}")
+    k = weights.shape[1]
+    _int32(offsets, E + 1, "route.offsets")
+    _int32(slots, T * k, "route.slots")
+    y, ldy = _f8_out(y, T, H, dtype or x.dtype, x.device)
+    _check(load().qmm_f8_moe(_ftype(x.dtype, "x"), _ptr(x), T, H, ldx, k, _ptr(weights), _ptr(offsets), _ptr(slots), E,
+                             I, _ptr(W_gate), _ptr(S_gate), _ptr(W_up), _ptr(S_up), _ptr(W_down), _ptr(S_down),
+                             _ftype(y.dtype, "y"), _ptr(y), ldy, _stream_handle(stream)))
+    return y
 
 
 def qmm_device_status(stream=None) -> int:

@@ -1,0 +1,660 @@
+// f8_gemm.cu -- y = W.x with W and x in e4m3 codes, an fp32 scale per
+// 128 x 128 block of W and per 128 values of a row of x, over one matrix or
+// over groups of rows with a matrix each (experts); optionally the gated pair
+// h = silu(Wg.x) * (Wu.x) written back as codes and scales.
+//
+//   y[r, n] = sum_b  xs[b, r] * Ws[n/128, b] * sum_{k in block b} xq[r, k] W[n, k]
+//
+// The inner sums run on the fifth-generation tensor cores (tcgen05
+// kind::f8f6f4, fp32 accumulation: products of two e4m3 values are exact in
+// fp32), one 128-wide block of K at a time into a fresh TMEM buffer; the
+// epilogue warps take each finished block out of TMEM and add it, times its
+// two scales, to fp32 accumulators in registers.  The scales change from
+// block to block and are arbitrary fp32, so they cannot ride inside the MMA.
+//
+// The weights are the M operand: TMEM lane = weight row n, TMEM column =
+// token.  One scale of W covers all 128 lanes of a tile, the number of token
+// columns follows the rows there are (16 .. 256 in steps of 16, so a group
+// of three rows costs a 16-column MMA), a warp's 32 lanes are 32 consecutive
+// n of one row of y, and for the gated pair the 128 lanes of a token are
+// exactly one scale block of h.
+//
+// A tile is 128 weight rows x up to BT tokens.  The grid is one CTA per SM.
+// Whole rounds of tiles go round the CTAs; the tiles that would leave the last
+// round partly empty (all of them when they are fewer than the CTAs) are cut
+// along K so that every CTA has the same number of K blocks.  The CTAs that
+// share a tile put their fp32 partial tiles into the workspace, and the last
+// one to arrive adds them in K order and stores: no CTA waits for another,
+// and the order of the sum does not depend on which one is last.
+//
+// Warp roles: 0 = copies (TMA, 128-byte swizzle), 1 = MMA issue, 2 = scales,
+// 3 = tensor memory; 4..11 = epilogue (warp w: TMEM lanes 32*(w%4), token
+// columns of half (w-4)/4).  All waits are bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "f8_internal.h"
+#include "qmm_device.cuh"
+#include "qmm_internal.h"
+
+namespace qk {
+
+namespace {
+
+constexpr int BW = 128, BK = 128;
+constexpr int THREADS = 384;
+constexpr int SC_STAGES = 4;
+constexpr int MIN_SHARE = 2;  // least K blocks of cut tiles per CTA
+constexpr int SMEM_MAX = 232448;
+
+template <int BT, bool DUAL>
+struct Cfg {
+    static constexpr int NA = DUAL ? 2 : 1;            // weight matrices per tile
+    static constexpr int XBOX = BT < 64 ? BT : 64;     // rows per token copy
+    static constexpr int W_BYTES = BW * BK, X_BYTES = BT * BK;
+    static constexpr int STAGE = NA * W_BYTES + X_BYTES;
+    static constexpr int SC_BYTES = NA * BT * 4;
+    static constexpr int HALF = BT / 2;                // token columns per epilogue warp
+    static constexpr int CH = HALF < 16 ? HALF : 16;   // columns per TMEM load
+    static constexpr int AMAX_BYTES = DUAL ? 4 * BT * 4 : 0;
+    static constexpr int CUM_BYTES = (QMM_F8_MAX_EXPERTS + 4) * 4;
+    static constexpr int FIXED = SC_STAGES * SC_BYTES + AMAX_BYTES + CUM_BYTES + 512 + 1024;
+    static constexpr int FIT = (SMEM_MAX - FIXED) / STAGE;
+    static constexpr int STAGES = FIT > 12 ? 12 : FIT;
+    static constexpr int OFF_SC = STAGES * STAGE;
+    static constexpr int OFF_AMAX = OFF_SC + SC_STAGES * SC_BYTES;
+    static constexpr int OFF_CUM = OFF_AMAX + AMAX_BYTES;
+    static constexpr int OFF_BAR = OFF_CUM + CUM_BYTES;
+    static constexpr int SMEM = OFF_BAR + 512 + 1024;
+    static constexpr int D_COLS = NA * BT;             // one TMEM buffer
+    static constexpr int TMEM_COLS = 2 * D_COLS < 32 ? 32 : 2 * D_COLS;
+    static constexpr int PART = NA * BT * BW;          // floats of a partial tile
+    static_assert(STAGES >= 3 && SMEM <= SMEM_MAX, "shared memory");
+    static_assert(TMEM_COLS <= 512, "tensor memory");
+    static_assert(8 * (2 * STAGES + 2 * SC_STAGES + 5) + 32 <= 512, "barrier area");
+};
+
+struct Params {
+    const float *Ws, *W2s, *xs;
+    int64_t ld_s;
+    const int32_t *offsets;
+    int E, R, N, nb, kb;
+    int y_type;
+    void *y;
+    int64_t ldy;
+    uint8_t *hq;
+    int64_t ld_h;
+    float *hs;
+    int64_t ld_hs;
+    float *part;
+    unsigned *count;
+    int *status;
+    int stop;  // the first CTA issues no copy from this K block on (failure test hook)
+};
+
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+// K-major operand in 128-byte swizzled rows, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr) {
+    uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(1) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// D[tmem] (+)= A[smem] . B[smem]^T, e4m3 x e4m3 -> fp32
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// N consecutive fp32 columns of this warp's 32 TMEM lanes: issue, then wait.
+// The wait takes the registers as operands so that no use of them moves
+// before it.
+__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(a));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+// A piece of a tile: tokens [row0, row0 + ntok) of expert e against weight
+// rows 128 * nblk .., K blocks [k0, k1).
+struct Piece {
+    int e, nblk, row0, ntok, k0, k1;
+    int64_t tile;
+};
+
+// The pieces of this CTA in order: first its share of the tiles that are cut
+// along K, then its whole tiles.
+struct Schedule {
+    const int *cum;  // shared memory: tiles before expert e, [E + 1]
+    const int32_t *offsets;
+    int E, R, kb, nb, G, c;
+    int64_t tiles, whole;  // tiles [0, whole) go round the CTAs uncut
+    int64_t units, sharing;  // K blocks of the cut tiles, and the CTAs that share them
+    int64_t u, u1;         // K blocks of the cut tiles, counted from tile `whole`
+    int64_t next_whole;
+
+    __device__ __forceinline__ void init() {
+        tiles = cum[E];
+        // A whole round is kept uncut; the last full round joins the rest, so
+        // that a cut tile has two or three parts.
+        whole = tiles % G == 0 ? tiles : tiles > G ? (tiles / G - 1) * G : 0;
+        units = (tiles - whole) * kb;
+        sharing = min(static_cast<int64_t>(G), (units + MIN_SHARE - 1) / MIN_SHARE);
+        u = c < sharing ? units * c / sharing : 0;
+        u1 = c < sharing ? units * (c + 1) / sharing : 0;
+        next_whole = c;
+    }
+    __device__ __forceinline__ bool next(Piece &p) {
+        if (u < u1) {
+            p.tile = whole + u / kb;
+            p.k0 = static_cast<int>(u % kb);
+            p.k1 = static_cast<int>(min(static_cast<int64_t>(kb), p.k0 + (u1 - u)));
+            u += p.k1 - p.k0;
+        } else if (next_whole < whole) {
+            p.tile = next_whole;
+            next_whole += G;
+            p.k0 = 0;
+            p.k1 = kb;
+        } else {
+            return false;
+        }
+        int lo = 0, hi = E - 1;  // the expert whose tiles hold p.tile
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (cum[mid] <= p.tile) lo = mid;
+            else hi = mid - 1;
+        }
+        p.e = lo;
+        const int local = static_cast<int>(p.tile - cum[lo]);
+        const int nt = (cum[lo + 1] - cum[lo]) / nb;
+        const int r0 = offsets ? __ldg(offsets + lo) : 0;
+        const int n = offsets ? __ldg(offsets + lo + 1) - r0 : R;
+        const int per = ((n + nt - 1) / nt + 15) & ~15;  // <= bt, so the last tile is not empty
+        const int tt = local % nt;
+        p.nblk = local / nt;
+        p.row0 = r0 + tt * per;
+        p.ntok = min(per, n - tt * per);
+        return true;
+    }
+    // The CTAs [c0, c1] that hold a part of cut tile `tile`.
+    __device__ __forceinline__ void sharers(int64_t tile, int &c0, int &c1) const {
+        const int64_t a = (tile - whole) * kb;
+        c0 = static_cast<int>(((a + 1) * sharing - 1) / units);
+        c1 = static_cast<int>(((a + kb) * sharing - 1) / units);
+    }
+};
+
+__device__ __forceinline__ void store_y(void *y, int type, int64_t i, float v) {
+    if (type == QMM_F32) static_cast<float *>(y)[i] = v;
+    else if (type == QMM_F16) static_cast<__half *>(y)[i] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
+}
+
+template <int BT, bool DUAL>
+__global__ void __launch_bounds__(THREADS, 1)
+    f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2,
+                   const __grid_constant__ CUtensorMap tmX, const Params P) {
+    using C = Cfg<BT, DUAL>;
+    constexpr int NA = C::NA;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const uint32_t stage0 = smem_u32(smem);
+    const uint32_t bar = smem_u32(smem + C::OFF_BAR);
+    const uint32_t full = bar, empty = full + 8 * C::STAGES;
+    const uint32_t sc_full = empty + 8 * C::STAGES, sc_empty = sc_full + 8 * SC_STAGES;
+    const uint32_t d_full = sc_empty + 8 * SC_STAGES, d_empty = d_full + 16;
+    const uint32_t done = d_empty + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 480);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_BAR + 484);
+    volatile unsigned *arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 488);
+    int *cum = reinterpret_cast<int *>(smem + C::OFF_CUM);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (int s = 0; s < SC_STAGES; ++s) {
+            mbar_init(sc_full + 8 * s, 1);
+            mbar_init(sc_empty + 8 * s, 8);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(d_full + 8 * s, 1);
+            mbar_init(d_empty + 8 * s, 8);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 3) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(C::TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (warp == 0) {
+        // tiles before each expert.  Only the codes and scales of x come from
+        // the launch before this one; offsets were complete before it started.
+        int base = 0;
+        for (int e0 = 0; e0 < P.E; e0 += 32) {
+            const int e = e0 + lane;
+            int t = 0;
+            if (e < P.E) {
+                const int lo = P.offsets ? __ldg(P.offsets + e) : 0;
+                const int hi = P.offsets ? __ldg(P.offsets + e + 1) : P.R;
+                if (lo < 0 || hi < lo || hi > P.R) atomicOr(P.status, STATUS_INDEX);
+                else t = (hi - lo + BT - 1) / BT * P.nb;
+            }
+            int incl = t;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (e < P.E) cum[e] = base + incl - t;
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) cum[P.E] = base;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    Schedule sch;
+    sch.cum = cum;
+    sch.offsets = P.offsets;
+    sch.E = P.E;
+    sch.R = P.R;
+    sch.kb = P.kb;
+    sch.nb = P.nb;
+    sch.G = static_cast<int>(gridDim.x);
+    sch.c = static_cast<int>(blockIdx.x);
+    sch.init();
+    Piece p;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // Copies.  Weights may be fetched before the quantiser is done.
+            const int stop = blockIdx.x == 0 ? P.stop : NO_STOP;
+            int it = 0;
+            bool ok = true;
+            pdl_wait();
+            pdl_trigger();
+            while (ok && sch.next(p)) {
+                const int boxes = (p.ntok + C::XBOX - 1) / C::XBOX;
+                const uint32_t bytes = NA * C::W_BYTES + boxes * C::XBOX * BK;
+                const int wrow = p.e * P.N + p.nblk * BW;
+                for (int k = p.k0; k < p.k1; ++k, ++it) {
+                    const int s = it % C::STAGES;
+                    if (it >= stop || *abort_flag ||
+                        (it >= C::STAGES && !mbar_wait(empty + 8 * s, ((it / C::STAGES) - 1) & 1, P.status))) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = stage0 + s * C::STAGE, b = full + 8 * s;
+                    mbar_arrive_expect_tx(b, bytes);
+                    tma_2d(st, &tmW, k * BK, wrow, b);
+                    if constexpr (DUAL) tma_2d(st + C::W_BYTES, &tmW2, k * BK, wrow, b);
+                    for (int x = 0; x < boxes; ++x)
+                        tma_2d(st + NA * C::W_BYTES + x * C::XBOX * BK, &tmX, k * BK, p.row0 + x * C::XBOX, b);
+                }
+            }
+            if (!ok && it < stop) *abort_flag = 1;
+            // no CTA ends with copies in flight
+            for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
+                mbar_wait(full + 8 * (i % C::STAGES), (i / C::STAGES) & 1, P.status);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            while (ok && sch.next(p)) {
+                const uint32_t cols = (p.ntok + 15) & ~15;
+                const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((BW >> 4) << 24);
+                for (int k = p.k0; k < p.k1; ++k, ++it) {
+                    const int s = it % C::STAGES, d = it & 1;
+                    if (*abort_flag || !mbar_wait(full + 8 * s, (it / C::STAGES) & 1, P.status) ||
+                        (it >= 2 && !mbar_wait(d_empty + 8 * d, ((it >> 1) - 1) & 1, P.status))) {
+                        ok = false;
+                        *abort_flag = 1;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = stage0 + s * C::STAGE;
+                    const uint64_t b = smem_desc(st + NA * C::W_BYTES);
+#pragma unroll
+                    for (int m = 0; m < NA; ++m) {
+                        const uint64_t a = smem_desc(st + m * C::W_BYTES);
+#pragma unroll
+                        for (int q = 0; q < BK / 32; ++q)
+                            mma_f8(tmem + d * C::D_COLS + m * BT, a + 2 * q, b + 2 * q, idesc, q ? 1u : 0u);
+                    }
+                    mma_commit(empty + 8 * s);
+                    mma_commit(d_full + 8 * d);
+                }
+            }
+            mma_commit(done);
+        }
+    } else if (warp == 2) {
+        // Scales: the products xs[b, token] * Ws[.., b] of a K block, BT (two
+        // times BT) floats per stage.  The loads run PRE blocks ahead.
+        constexpr int PER = BT < 32 ? 1 : BT / 32, PRE = 4;
+        pdl_wait();
+        Schedule ahead = sch;
+        Piece a;
+        float v[PRE][PER], w[PRE][NA];
+        bool more = ahead.next(a);
+        int ka = more ? a.k0 : 0;
+        auto fetch = [&](int slot) {
+            if (!more) return;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int t = lane + 32 * i;
+                v[slot][i] = t < a.ntok ? __ldg(P.xs + ka * P.ld_s + a.row0 + t) : 0.0f;
+            }
+            const int64_t ws = (static_cast<int64_t>(a.e) * P.nb + a.nblk) * P.kb + ka;
+            w[slot][0] = __ldg(P.Ws + ws);
+            if constexpr (DUAL) w[slot][1] = __ldg(P.W2s + ws);
+            if (++ka == a.k1) {
+                more = ahead.next(a);
+                ka = more ? a.k0 : 0;
+            }
+        };
+        int total = 0;
+        while (sch.next(p)) total += p.k1 - p.k0;
+#pragma unroll
+        for (int i = 0; i < PRE; ++i) fetch(i);
+        bool ok = true;
+        for (int it0 = 0; ok && it0 < total; it0 += PRE) {
+#pragma unroll
+            for (int i = 0; i < PRE; ++i) {
+                const int it = it0 + i;
+                if (!ok || it >= total) break;
+                const int s = it % SC_STAGES;
+                ok = !*abort_flag;
+                if (ok && it >= SC_STAGES) ok = mbar_wait(sc_empty + 8 * s, ((it / SC_STAGES) - 1) & 1, P.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                float *sc = reinterpret_cast<float *>(smem + C::OFF_SC + s * C::SC_BYTES);
+#pragma unroll
+                for (int q = 0; q < PER; ++q)
+                    if (lane + 32 * q < BT) {
+#pragma unroll
+                        for (int m = 0; m < NA; ++m) sc[m * BT + lane + 32 * q] = v[i][q] * w[i][m];
+                    }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sc_full + 8 * s);
+                fetch(i);
+            }
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + half * C::HALF;
+        pdl_wait();
+        int it = 0;
+        bool ok = true;
+        while (ok && sch.next(p)) {
+            float acc[NA][C::HALF];
+#pragma unroll
+            for (int m = 0; m < NA; ++m)
+#pragma unroll
+                for (int i = 0; i < C::HALF; ++i) acc[m][i] = 0.0f;
+            const int mine = min(C::HALF, p.ntok - half * C::HALF);  // this warp's token columns (may be <= 0)
+            for (int k = p.k0; k < p.k1; ++k, ++it) {
+                const int d = it & 1, s = it % SC_STAGES;
+                ok = !*abort_flag && mbar_wait(d_full + 8 * d, (it >> 1) & 1, P.status) &&
+                     mbar_wait(sc_full + 8 * s, (it / SC_STAGES) & 1, P.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                tc_fence_after();
+                const float *sc = reinterpret_cast<const float *>(smem + C::OFF_SC + s * C::SC_BYTES) + half * C::HALF;
+#pragma unroll
+                for (int m = 0; m < NA; ++m)
+#pragma unroll
+                    for (int c = 0; c < C::HALF; c += C::CH)
+                        if (c < mine) {
+                            uint32_t r[C::CH];
+                            tmem_ld(lane_base + d * C::D_COLS + m * BT + c, r);
+                            tmem_wait(r);
+#pragma unroll
+                            for (int i = 0; i < C::CH; i += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(sc + m * BT + c + i);
+                                acc[m][c + i] = fmaf(__uint_as_float(r[i]), f.x, acc[m][c + i]);
+                                acc[m][c + i + 1] = fmaf(__uint_as_float(r[i + 1]), f.y, acc[m][c + i + 1]);
+                                acc[m][c + i + 2] = fmaf(__uint_as_float(r[i + 2]), f.z, acc[m][c + i + 2]);
+                                acc[m][c + i + 3] = fmaf(__uint_as_float(r[i + 3]), f.w, acc[m][c + i + 3]);
+                            }
+                        }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(d_empty + 8 * d);
+                    mbar_arrive(sc_empty + 8 * s);
+                }
+            }
+            // every epilogue warp passes here once per piece, also after a wait
+            // that gave up, so that none is left at a barrier alone
+            if (named_barrier_or(1, 256, !ok)) break;
+            bool store = true;
+            if (p.k1 - p.k0 < P.kb) {
+                // a part of a cut tile: into the workspace; the last of its
+                // CTAs adds the parts in K order
+                int c0, c1;
+                sch.sharers(p.tile, c0, c1);
+                float *mypart = P.part + (static_cast<int64_t>(blockIdx.x) * 2 + (p.k0 == 0)) * C::PART;
+#pragma unroll
+                for (int m = 0; m < NA; ++m)
+#pragma unroll
+                    for (int i = 0; i < C::HALF; ++i)
+                        if (i < mine)
+                            mypart[(m * BT + half * C::HALF + i) * BW + 32 * quarter + lane] = acc[m][i];
+                __threadfence();
+                named_barrier(1, 256);
+                if (threadIdx.x == 128) *arrived = atomicAdd(P.count + c0, 1u);
+                named_barrier(1, 256);
+                store = *arrived == static_cast<unsigned>(c1 - c0);
+                named_barrier(1, 256);
+                if (store) {
+                    __threadfence();
+#pragma unroll
+                    for (int m = 0; m < NA; ++m)
+#pragma unroll
+                        for (int i = 0; i < C::HALF; ++i) acc[m][i] = 0.0f;
+                    for (int c = c0; c <= c1; ++c) {
+                        const float *q = P.part + (static_cast<int64_t>(c) * 2 + (c == c0)) * C::PART;
+#pragma unroll
+                        for (int m = 0; m < NA; ++m)
+#pragma unroll
+                            for (int i = 0; i < C::HALF; ++i)
+                                if (i < mine)
+                                    acc[m][i] += __ldcg(q + (m * BT + half * C::HALF + i) * BW + 32 * quarter + lane);
+                    }
+                }
+            }
+            if (!store) continue;
+            const int n = p.nblk * BW + 32 * quarter + lane;
+            const int64_t row = p.row0 + half * C::HALF;
+            if constexpr (!DUAL) {
+                if (n < P.N) {
+#pragma unroll
+                    for (int i = 0; i < C::HALF; ++i)
+                        if (i < mine) store_y(P.y, P.y_type, (row + i) * P.ldy + n, acc[0][i]);
+                }
+            } else {
+                // h = silu(g) * u, its largest |h| over the tile's 128 rows n
+                // (one scale block of h), then its codes
+                uint32_t *amax = reinterpret_cast<uint32_t *>(smem + C::OFF_AMAX) + half * C::HALF;
+#pragma unroll
+                for (int i = 0; i < C::HALF; ++i)
+                    if (i < mine) {
+                        const float g = acc[0][i];
+                        const float h = n < P.N ? __fdiv_rn(g, 1.0f + expf(-g)) * acc[1][i] : 0.0f;
+                        acc[0][i] = h;
+                        const uint32_t a = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
+                        if (lane == 0) amax[quarter * BT + i] = a;
+                    }
+                named_barrier(2 + half, 128);
+#pragma unroll
+                for (int i = 0; i < C::HALF; ++i)
+                    if (i < mine) {
+                        const uint32_t a = max(max(amax[i], amax[BT + i]), max(amax[2 * BT + i], amax[3 * BT + i]));
+                        float s = __fdiv_rn(__uint_as_float(a), 448.0f);
+                        s = s < 1.17549435e-38f ? 1.17549435e-38f : s;
+                        if (n < P.N)
+                            P.hq[(row + i) * P.ld_h + n] =
+                                __nv_cvt_float_to_fp8(acc[0][i] * __fdiv_rn(1.0f, s), __NV_SATFINITE, __NV_E4M3);
+                        if (quarter == 0 && lane == 0) P.hs[p.nblk * P.ld_hs + row + i] = s;
+                    }
+                named_barrier(2 + half, 128);  // amax may be overwritten
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 3) {
+        mbar_wait(done, 0, P.status);  // every MMA has completed
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS)
+                     : "memory");
+    }
+}
+
+bool encode_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int64_t ld, int box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+    const cuuint32_t box[2] = {BK, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t es[2] = {1, 1};
+    return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BT, bool DUAL>
+cudaError_t launch_bt(const F8Gemm &g, cudaStream_t st, int num_sms) {
+    using C = Cfg<BT, DUAL>;
+    CUtensorMap tw = {}, tw2 = {}, tx = {};
+    if (!encode_rows(&tw, g.W, g.E * g.N, g.K, g.K, BW) || (DUAL && !encode_rows(&tw2, g.W2, g.E * g.N, g.K, g.K, BW)) ||
+        !encode_rows(&tx, g.xq, g.R, g.K, g.ld_q, C::XBOX))
+        return cudaErrorInvalidValue;
+    Params p = {};
+    p.Ws = g.Ws;
+    p.W2s = g.W2s;
+    p.xs = g.xs;
+    p.ld_s = g.ld_s;
+    p.offsets = g.offsets;
+    p.E = g.E;
+    p.R = static_cast<int>(g.R);
+    p.N = static_cast<int>(g.N);
+    p.nb = static_cast<int>(f8_blocks(g.N));
+    p.kb = static_cast<int>(f8_blocks(g.K));
+    p.y_type = g.y_type;
+    p.y = g.y;
+    p.ldy = g.ldy;
+    p.hq = g.hq;
+    p.ld_h = g.ld_h;
+    p.hs = g.hs;
+    p.ld_hs = g.ld_hs;
+    p.part = g.part;
+    p.count = g.count;
+    p.status = g.status;
+    p.stop = inject_stop_stage();
+    cudaError_t e = set_smem_attrs(f8_gemm_kernel<BT, DUAL>, C::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, f8_gemm_kernel<BT, DUAL>, tw, tw2, tx, p);
+}
+
+// Tokens per tile: the mean rows of a group, rounded up to a tile width.
+int tile_tokens(int64_t R, int E, bool dual) {
+    const int64_t mean = (R + E - 1) / E;
+    int bt = 16;
+    while (bt < mean && bt < (dual ? 128 : 256)) bt *= 2;
+    return bt;
+}
+
+template <bool DUAL>
+cudaError_t launch_any(const F8Gemm &g, cudaStream_t st, int num_sms) {
+    switch (tile_tokens(g.R, g.E, DUAL)) {
+    case 16: return launch_bt<16, DUAL>(g, st, num_sms);
+    case 32: return launch_bt<32, DUAL>(g, st, num_sms);
+    case 64: return launch_bt<64, DUAL>(g, st, num_sms);
+    case 128: return launch_bt<128, DUAL>(g, st, num_sms);
+    default:
+        if constexpr (DUAL) return launch_bt<128, DUAL>(g, st, num_sms);
+        else return launch_bt<256, DUAL>(g, st, num_sms);
+    }
+}
+
+}  // namespace
+
+size_t f8_part_bytes(int64_t R, int E, bool dual, int num_sms) {
+    return static_cast<size_t>(num_sms) * 2 * (dual ? 2 : 1) * tile_tokens(R, E, dual) * BW * sizeof(float);
+}
+
+bool f8_available() { return tensor_map_encoder() != nullptr; }
+
+cudaError_t launch_f8_gemm(const F8Gemm &g, cudaStream_t st, int num_sms) {
+    return g.W2 ? launch_any<true>(g, st, num_sms) : launch_any<false>(g, st, num_sms);
+}
+
+}  // namespace qk

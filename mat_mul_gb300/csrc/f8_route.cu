@@ -1,0 +1,259 @@
+// f8_route.cu -- the router of an expert layer: the k largest logits of each
+// token, their weights, and the (token, choice) pairs sorted by expert.
+//
+// One warp per token holds the token's logits in registers as order-preserving
+// integers (index in expert order on a tie, NaN as -inf, -0 as +0) and takes
+// the largest k times with two warp reductions each.  The pairs are sorted by
+// counting: stable, so the rows of an expert are in token order and the
+// result does not depend on the launch.  Up to TOKENS tokens are one launch of
+// one CTA.  More take two: the first leaves a histogram per CTA, and in the
+// second each CTA adds up the histograms before its own.  Bound by latency
+// below a few thousand tokens and by the reading of the logits above.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "f8_internal.h"
+#include "qmm_device.cuh"
+#include "qmm_internal.h"
+
+namespace qk {
+
+namespace {
+
+constexpr int TOKENS = 128;  // tokens per CTA
+constexpr int WARPS = 16;
+constexpr int THREADS = 32 * WARPS;
+
+struct RouteParams {
+    const void *x;
+    int64_t T, ldx;
+    int x_type, E, k, score, normalize, fused;
+    float factor;
+    float *weights;
+    int32_t *experts, *offsets, *rows, *slots, *hist;
+};
+
+__device__ __forceinline__ float load_logit(const RouteParams &P, int64_t i) {
+    if (P.x_type == QMM_F32) return __ldg(static_cast<const float *>(P.x) + i);
+    if (P.x_type == QMM_F16) return __half2float(static_cast<const __half *>(P.x)[i]);
+    return __bfloat162float(static_cast<const __nv_bfloat16 *>(P.x)[i]);
+}
+
+// Integers in the order of the floats; 0 is below every one of them.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);  // -0 + 0 = +0
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The choices of one token; lane j < k returns its expert.
+template <int VPL>
+__device__ __forceinline__ int choose(const RouteParams &P, int64_t t, int lane) {
+    uint32_t key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = lane + 32 * i;
+        float v = e < P.E ? load_logit(P, t * P.ldx + e) : 0.0f;
+        if (v != v) v = -INFINITY;
+        key[i] = e < P.E ? order_key(v) : 0u;
+    }
+    float top = 0.0f, rest = 0.0f;
+    if (P.score == QMM_ROUTE_SOFTMAX) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) m = max(m, key[i]);
+        top = key_value(__reduce_max_sync(0xffffffffu, m));
+        if (top == -INFINITY) top = 0.0f;  // nothing to choose from: every weight 0
+        if (!P.normalize) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (key[i]) rest += expf(key_value(key[i]) - top);
+            rest = warp_sum(rest);
+        }
+    }
+    int mine = 0;
+    uint32_t mine_key = 0;
+    for (int j = 0; j < P.k; ++j) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) m = max(m, key[i]);
+        m = __reduce_max_sync(0xffffffffu, m);
+        unsigned at = 0xffffffffu;
+#pragma unroll
+        for (int i = VPL - 1; i >= 0; --i)
+            if (key[i] == m) at = lane + 32 * i;
+        at = __reduce_min_sync(0xffffffffu, at);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (at == static_cast<unsigned>(lane + 32 * i)) key[i] = 0u;
+        if (lane == j) mine = static_cast<int>(at), mine_key = m;
+    }
+    const float v = key_value(mine_key);
+    float w = 0.0f;
+    if (lane < P.k) w = P.score == QMM_ROUTE_SOFTMAX ? expf(v - top) : __fdiv_rn(1.0f, 1.0f + expf(-v));
+    float total = P.normalize ? warp_sum(w) : P.score == QMM_ROUTE_SOFTMAX ? rest : 1.0f;
+    if (total != 0.0f) w = __fdiv_rn(w, total);
+    if (lane < P.k) {
+        P.weights[t * P.k + lane] = w * P.factor;
+        P.experts[t * P.k + lane] = mine;
+    }
+    return mine;
+}
+
+// Stable positions of the pairs [p0, p1) of this CTA: cnt[e] is the next row
+// of expert e.  One warp, 32 pairs at a time, in order.
+__device__ __forceinline__ void place(const RouteParams &P, int *cnt, const int *chosen, int64_t p0, int n, int lane) {
+    for (int i = 0; i < n; i += 32) {
+        const bool on = i + lane < n;
+        const int e = on ? chosen[i + lane] : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        if (on) {
+            const int row = cnt[e] + __popc(same & ((1u << lane) - 1u));
+            const int64_t pair = p0 + i + lane;
+            P.rows[row] = static_cast<int32_t>(pair / P.k);
+            P.slots[pair] = row;
+        }
+        __syncwarp();
+        if (on && (same >> lane) == 1u) cnt[e] += __popc(same);  // the last lane of each expert
+        __syncwarp();
+    }
+}
+
+// First CTA-sized scan: cnt[e] (counts) -> exclusive sums, in place; the
+// total is returned.  One warp.
+__device__ __forceinline__ int scan_experts(int *cnt, int E, int lane) {
+    int base = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + lane;
+        const int v = e < E ? cnt[e] : 0;
+        int incl = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        if (e < E) cnt[e] = base + incl - v;
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return base;
+}
+
+template <int VPL>
+__global__ void __launch_bounds__(THREADS) route_choose_kernel(const RouteParams P) {
+    __shared__ int cnt[QMM_F8_MAX_EXPERTS];
+    __shared__ int chosen[TOKENS * QMM_ROUTE_MAX_K];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int e = threadIdx.x; e < P.E; e += THREADS) cnt[e] = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * TOKENS;
+    const int nt = static_cast<int>(min(static_cast<int64_t>(TOKENS), P.T - t0));
+    for (int i = warp; i < nt; i += WARPS) {
+        const int e = choose<VPL>(P, t0 + i, lane);
+        if (lane < P.k) {
+            chosen[i * P.k + lane] = e;
+            atomicAdd(cnt + e, 1);
+        }
+    }
+    __syncthreads();
+    if (P.fused) {
+        if (warp == 0) {
+            const int total = scan_experts(cnt, P.E, lane);
+            __syncwarp();
+            for (int e = lane; e < P.E; e += 32) P.offsets[e] = cnt[e];
+            if (lane == 0) P.offsets[P.E] = total;
+            __syncwarp();
+            place(P, cnt, chosen, t0 * P.k, nt * P.k, lane);
+        }
+    } else {
+        for (int e = threadIdx.x; e < P.E; e += THREADS) P.hist[static_cast<int64_t>(blockIdx.x) * P.E + e] = cnt[e];
+    }
+}
+
+// Second launch: cnt[e] = all pairs of experts before e + the pairs of e in
+// CTAs before this one, then the positions.
+__global__ void __launch_bounds__(THREADS) route_place_kernel(const RouteParams P) {
+    __shared__ int cnt[QMM_F8_MAX_EXPERTS], before[QMM_F8_MAX_EXPERTS];
+    __shared__ int chosen[TOKENS * QMM_ROUTE_MAX_K];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int e = threadIdx.x; e < P.E; e += THREADS) cnt[e] = before[e] = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * TOKENS;
+    const int n = static_cast<int>(min(static_cast<int64_t>(TOKENS), P.T - t0)) * P.k;
+    for (int i = threadIdx.x; i < n; i += THREADS) chosen[i] = P.experts[t0 * P.k + i];
+    const int64_t all = static_cast<int64_t>(gridDim.x) * P.E, mine = static_cast<int64_t>(blockIdx.x) * P.E;
+    for (int64_t i = threadIdx.x; i < all; i += THREADS) {
+        const int h = P.hist[i];
+        if (h) {
+            const int e = static_cast<int>(i % P.E);
+            atomicAdd(cnt + e, h);
+            if (i < mine) atomicAdd(before + e, h);
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int total = scan_experts(cnt, P.E, lane);
+        __syncwarp();
+        if (blockIdx.x == 0) {
+            for (int e = lane; e < P.E; e += 32) P.offsets[e] = cnt[e];
+            if (lane == 0) P.offsets[P.E] = total;
+        }
+        for (int e = lane; e < P.E; e += 32) cnt[e] += before[e];
+        __syncwarp();
+        place(P, cnt, chosen, t0 * P.k, n, lane);
+    }
+}
+
+using Kernel = void (*)(const RouteParams);
+Kernel choose_kernel(int E) {
+    if (E <= 32) return route_choose_kernel<1>;
+    if (E <= 64) return route_choose_kernel<2>;
+    if (E <= 128) return route_choose_kernel<4>;
+    if (E <= 256) return route_choose_kernel<8>;
+    if (E <= 512) return route_choose_kernel<16>;
+    return route_choose_kernel<32>;
+}
+
+cudaError_t launch(Kernel kern, int64_t blocks, RouteParams &p, cudaStream_t st) {
+    cudaError_t e = prefer_max_shared(kern);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<const RouteParams>(p));
+}
+
+}  // namespace
+
+size_t f8_route_hist_bytes(int64_t T, int E) {
+    return T <= TOKENS ? 0 : static_cast<size_t>((T + TOKENS - 1) / TOKENS) * E * sizeof(int32_t);
+}
+int f8_route_launches(int64_t T) { return T <= TOKENS ? 1 : 2; }
+
+cudaError_t launch_f8_route(const F8Route &r, cudaStream_t st) {
+    RouteParams p = {r.x,      r.T,       r.ldx,     r.x_type,  r.E,    r.k,     r.score, r.normalize,
+                     r.T <= TOKENS, r.factor, r.weights, r.experts, r.offsets, r.rows, r.slots, r.hist};
+    const int64_t blocks = (r.T + TOKENS - 1) / TOKENS;
+    cudaError_t e = launch(choose_kernel(r.E), blocks, p, st);
+    if (e != cudaSuccess || p.fused) return e;
+    return launch(route_place_kernel, blocks, p, st);
+}
+
+}  // namespace qk

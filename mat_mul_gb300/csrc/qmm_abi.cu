@@ -15,6 +15,7 @@
 #include "../../include/qmm.h"
 #include "qmm_device.cuh"
 
+#include "f8_internal.h"
 #include "qmm_internal.h"
 
 namespace {
@@ -209,6 +210,19 @@ int inject_stop_stage() {
         if (g_inject.compare_exchange_weak(v, v - 1)) return 1;
     return NO_STOP;
 }
+void clear_error() { g_err[0] = 0; }
+int f8_context(F8Context &c) {
+    const cudaError_t e = cudaGetDevice(&c.dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    DeviceInfo di;
+    if (int rc = device_info(c.dev, di)) return rc;
+    c.num_sms = di.num_sms;
+    c.status = di.status;
+    return QMM_OK;
+}
+int f8_workspace(const F8Context &c, cudaStream_t st, size_t bytes, void **ptr) {
+    return workspace(c.dev, st, bytes, ptr);
+}
 }  // namespace qk
 
 namespace {
@@ -304,6 +318,7 @@ const char *qmm_strerror(int status) {
     case QMM_ENOMEM: return "QMM_ENOMEM";
     case QMM_ECUDA: return "QMM_ECUDA";
     case QMM_ETIMEOUT: return "QMM_ETIMEOUT";
+    case QMM_EINDEX: return "QMM_EINDEX";
     default: return "QMM_UNKNOWN";
     }
 }
@@ -715,6 +730,8 @@ int qmm_device_status(void *stream) {
     if (word) {
         e = cudaMemset(di.status, 0, sizeof word);
         if (e != cudaSuccess) return cuda_fail(e, "status clear");
+        if (!(word & qk::STATUS_TIMEOUT))
+            return fail(QMM_EINDEX, "a row index or an offset was out of range (status word 0x%x)", word);
         return fail(QMM_ETIMEOUT, "a bounded device wait expired (status word 0x%x)", word);
     }
     return QMM_OK;

@@ -55,7 +55,7 @@ inline int block_bytes(int t) {
 inline int block_weights(int t) { return t == QMM_Q8_0 ? 32 : 256; }
 
 // Status bits a kernel may raise in the per-device status word.
-enum : int { STATUS_TIMEOUT = 1 };
+enum : int { STATUS_TIMEOUT = 1, STATUS_INDEX = 2 };
 
 // Limit of every bounded wait, in SM clock cycles (2^31: about one second at
 // the 2 GHz class clocks of this part, longer at lower clocks).  The cycle
