@@ -30,23 +30,17 @@
 // Warp roles: 0 = copies (TMA, 128-byte swizzle), 1 = MMA issue, 2 = scales,
 // 3 = tensor memory; 4..11 = epilogue (warp w: TMEM lanes 32*(w%4), token
 // columns of half (w-4)/4).  All waits are bounded.
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
-#include "f8_internal.h"
-#include "qmm_device.cuh"
-#include "qmm_internal.h"
+#include "f8_gemm.cuh"
 
 namespace qk {
 
 namespace {
 
-constexpr int BW = 128, BK = 128;
+using namespace f8;
+
+constexpr int BW = 128;
 constexpr int THREADS = 384;
 constexpr int SC_STAGES = 4;
-constexpr int MIN_SHARE = 2;  // least K blocks of cut tiles per CTA
 constexpr int SMEM_MAX = 232448;
 
 template <int BT, bool DUAL>
@@ -94,24 +88,6 @@ struct Params {
     int stop;  // the first CTA issues no copy from this K block on (failure test hook)
 };
 
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-}
-
-// K-major operand in 128-byte swizzled rows, 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr) {
-    uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>(1) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
-}
-
 // D[tmem] (+)= A[smem] . B[smem]^T, e4m3 x e4m3 -> fp32
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -125,9 +101,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
 // N consecutive fp32 columns of this warp's 32 TMEM lanes: issue, then wait.
 // The wait takes the registers as operands so that no use of them moves
 // before it.
@@ -156,75 +129,6 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
                  :
                  : "memory");
 }
-
-// A piece of a tile: tokens [row0, row0 + ntok) of expert e against weight
-// rows 128 * nblk .., K blocks [k0, k1).
-struct Piece {
-    int e, nblk, row0, ntok, k0, k1;
-    int64_t tile;
-};
-
-// The pieces of this CTA in order: first its share of the tiles that are cut
-// along K, then its whole tiles.
-struct Schedule {
-    const int *cum;  // shared memory: tiles before expert e, [E + 1]
-    const int32_t *offsets;
-    int E, R, kb, nb, G, c;
-    int64_t tiles, whole;  // tiles [0, whole) go round the CTAs uncut
-    int64_t units, sharing;  // K blocks of the cut tiles, and the CTAs that share them
-    int64_t u, u1;         // K blocks of the cut tiles, counted from tile `whole`
-    int64_t next_whole;
-
-    __device__ __forceinline__ void init() {
-        tiles = cum[E];
-        // A whole round is kept uncut; the last full round joins the rest, so
-        // that a cut tile has two or three parts.
-        whole = tiles % G == 0 ? tiles : tiles > G ? (tiles / G - 1) * G : 0;
-        units = (tiles - whole) * kb;
-        sharing = min(static_cast<int64_t>(G), (units + MIN_SHARE - 1) / MIN_SHARE);
-        u = c < sharing ? units * c / sharing : 0;
-        u1 = c < sharing ? units * (c + 1) / sharing : 0;
-        next_whole = c;
-    }
-    __device__ __forceinline__ bool next(Piece &p) {
-        if (u < u1) {
-            p.tile = whole + u / kb;
-            p.k0 = static_cast<int>(u % kb);
-            p.k1 = static_cast<int>(min(static_cast<int64_t>(kb), p.k0 + (u1 - u)));
-            u += p.k1 - p.k0;
-        } else if (next_whole < whole) {
-            p.tile = next_whole;
-            next_whole += G;
-            p.k0 = 0;
-            p.k1 = kb;
-        } else {
-            return false;
-        }
-        int lo = 0, hi = E - 1;  // the expert whose tiles hold p.tile
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (cum[mid] <= p.tile) lo = mid;
-            else hi = mid - 1;
-        }
-        p.e = lo;
-        const int local = static_cast<int>(p.tile - cum[lo]);
-        const int nt = (cum[lo + 1] - cum[lo]) / nb;
-        const int r0 = offsets ? __ldg(offsets + lo) : 0;
-        const int n = offsets ? __ldg(offsets + lo + 1) - r0 : R;
-        const int per = ((n + nt - 1) / nt + 15) & ~15;  // <= bt, so the last tile is not empty
-        const int tt = local % nt;
-        p.nblk = local / nt;
-        p.row0 = r0 + tt * per;
-        p.ntok = min(per, n - tt * per);
-        return true;
-    }
-    // The CTAs [c0, c1] that hold a part of cut tile `tile`.
-    __device__ __forceinline__ void sharers(int64_t tile, int &c0, int &c1) const {
-        const int64_t a = (tile - whole) * kb;
-        c0 = static_cast<int>(((a + 1) * sharing - 1) / units);
-        c1 = static_cast<int>(((a + kb) * sharing - 1) / units);
-    }
-};
 
 __device__ __forceinline__ void store_y(void *y, int type, int64_t i, float v) {
     if (type == QMM_F32) static_cast<float *>(y)[i] = v;
@@ -277,28 +181,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (warp == 0) {
-        // tiles before each expert.  Only the codes and scales of x come from
-        // the launch before this one; offsets were complete before it started.
-        int base = 0;
-        for (int e0 = 0; e0 < P.E; e0 += 32) {
-            const int e = e0 + lane;
-            int t = 0;
-            if (e < P.E) {
-                const int lo = P.offsets ? __ldg(P.offsets + e) : 0;
-                const int hi = P.offsets ? __ldg(P.offsets + e + 1) : P.R;
-                if (lo < 0 || hi < lo || hi > P.R) atomicOr(P.status, STATUS_INDEX);
-                else t = (hi - lo + BT - 1) / BT * P.nb;
-            }
-            int incl = t;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            if (e < P.E) cum[e] = base + incl - t;
-            base += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        if (lane == 0) cum[P.E] = base;
+        // only the codes and scales of x come from the launch before this one;
+        // the offsets were complete before it started
+        f8::count_tiles(cum, P.offsets, P.E, P.R, BT, P.nb, lane, P.status);
     }
     tc_fence_before();
     __syncthreads();
@@ -314,11 +199,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     sch.nb = P.nb;
     sch.G = static_cast<int>(gridDim.x);
     sch.c = static_cast<int>(blockIdx.x);
+    sch.step = 0;
     sch.init();
     Piece p;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             // Copies.  Weights may be fetched before the quantiser is done.
             const int stop = blockIdx.x == 0 ? P.stop : NO_STOP;
             int it = 0;
@@ -332,7 +218,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int k = p.k0; k < p.k1; ++k, ++it) {
                     const int s = it % C::STAGES;
                     if (it >= stop || *abort_flag ||
-                        (it >= C::STAGES && !mbar_wait(empty + 8 * s, ((it / C::STAGES) - 1) & 1, P.status))) {
+                        (it >= C::STAGES && !mbar_spin(empty + 8 * s, ((it / C::STAGES) - 1) & 1, P.status))) {
                         ok = false;
                         break;
                     }
@@ -347,10 +233,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok && it < stop) *abort_flag = 1;
             // no CTA ends with copies in flight
             for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
-                mbar_wait(full + 8 * (i % C::STAGES), (i / C::STAGES) & 1, P.status);
+                mbar_spin(full + 8 * (i % C::STAGES), (i / C::STAGES) & 1, P.status);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             int it = 0;
             bool ok = true;
             while (ok && sch.next(p)) {
@@ -358,8 +244,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((BW >> 4) << 24);
                 for (int k = p.k0; k < p.k1; ++k, ++it) {
                     const int s = it % C::STAGES, d = it & 1;
-                    if (*abort_flag || !mbar_wait(full + 8 * s, (it / C::STAGES) & 1, P.status) ||
-                        (it >= 2 && !mbar_wait(d_empty + 8 * d, ((it >> 1) - 1) & 1, P.status))) {
+                    if (*abort_flag || !mbar_spin(full + 8 * s, (it / C::STAGES) & 1, P.status) ||
+                        (it >= 2 && !mbar_spin(d_empty + 8 * d, ((it >> 1) - 1) & 1, P.status))) {
                         ok = false;
                         *abort_flag = 1;
                         break;
@@ -417,7 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!ok || it >= total) break;
                 const int s = it % SC_STAGES;
                 ok = !*abort_flag;
-                if (ok && it >= SC_STAGES) ok = mbar_wait(sc_empty + 8 * s, ((it / SC_STAGES) - 1) & 1, P.status);
+                if (ok && it >= SC_STAGES) ok = mbar_spin(sc_empty + 8 * s, ((it / SC_STAGES) - 1) & 1, P.status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) {
                     *abort_flag = 1;
@@ -450,8 +336,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int mine = min(C::HALF, p.ntok - half * C::HALF);  // this warp's token columns (may be <= 0)
             for (int k = p.k0; k < p.k1; ++k, ++it) {
                 const int d = it & 1, s = it % SC_STAGES;
-                ok = !*abort_flag && mbar_wait(d_full + 8 * d, (it >> 1) & 1, P.status) &&
-                     mbar_wait(sc_full + 8 * s, (it / SC_STAGES) & 1, P.status);
+                ok = !*abort_flag && mbar_spin(d_full + 8 * d, (it >> 1) & 1, P.status) &&
+                     mbar_spin(sc_full + 8 * s, (it / SC_STAGES) & 1, P.status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) {
                     *abort_flag = 1;
@@ -563,21 +449,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == 3) {
-        mbar_wait(done, 0, P.status);  // every MMA has completed
+        mbar_spin(done, 0, P.status);  // every MMA has completed
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS)
                      : "memory");
     }
-}
-
-bool encode_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int64_t ld, int box_rows) {
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
-    const cuuint32_t box[2] = {BK, static_cast<cuuint32_t>(box_rows)};
-    const cuuint32_t es[2] = {1, 1};
-    return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int BT, bool DUAL>
@@ -632,8 +508,16 @@ int tile_tokens(int64_t R, int E, bool dual) {
     return bt;
 }
 
+// Which kernel: 0 this one, 1 f8_wide.cu on single CTAs, 2 on pairs.
+int path_of(int64_t R, int E) {
+    const int64_t mean = (R + E - 1) / E;
+    if (mean <= 128) return 0;
+    return E == 1 || mean > 1024 ? 2 : 1;
+}
+
 template <bool DUAL>
 cudaError_t launch_any(const F8Gemm &g, cudaStream_t st, int num_sms) {
+    if (const int w = path_of(g.R, g.E)) return launch_f8_wide(g, w == 2, st, num_sms);
     switch (tile_tokens(g.R, g.E, DUAL)) {
     case 16: return launch_bt<16, DUAL>(g, st, num_sms);
     case 32: return launch_bt<32, DUAL>(g, st, num_sms);
@@ -648,6 +532,7 @@ cudaError_t launch_any(const F8Gemm &g, cudaStream_t st, int num_sms) {
 }  // namespace
 
 size_t f8_part_bytes(int64_t R, int E, bool dual, int num_sms) {
+    if (path_of(R, E)) return f8_wide_part_bytes(num_sms);
     return static_cast<size_t>(num_sms) * 2 * (dual ? 2 : 1) * tile_tokens(R, E, dual) * BW * sizeof(float);
 }
 

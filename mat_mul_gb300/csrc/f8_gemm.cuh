@@ -1,0 +1,181 @@
+// f8_gemm.cuh -- what the two block-scaled 8-bit-float product kernels share:
+// TMA and tcgen05 wrappers, and the schedule that cuts the work into pieces.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "f8_internal.h"
+#include "qmm_device.cuh"
+#include "qmm_internal.h"
+
+namespace qk {
+namespace f8 {
+
+constexpr int BK = 128;        // values of K per stage: one scale block
+constexpr int MIN_SHARE = 2;   // least K blocks of cut tiles per CTA
+
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+// One lane of a converged warp, the same one each time.  The compiler knows
+// that a branch on it holds one thread, and feeds the tensor-core and copy
+// instructions their uniform registers directly: behind "lane == 0" four MMAs
+// and two commits took 745 cycles to issue, behind this 410 (a K block of
+// 128 x 256 takes the tensor cores 512).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// mbar_wait without the long sleep: the stages of these kernels change hands
+// every few hundred cycles.
+__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, int *status) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (clock64() - t0 > WAIT_LIMIT_CYCLES) {
+            atomicOr(status, STATUS_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// K-major operand in 128-byte swizzled rows, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr) {
+    uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(1) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// A piece of a tile: tokens [row0, row0 + ntok) of expert e against block nblk
+// of weight rows, K blocks [k0, k1).
+struct Piece {
+    int e, nblk, row0, ntok, k0, k1, tile;
+};
+
+// The pieces of this CTA (or pair) in order: first its share of the tiles that
+// are cut along K, then its whole tiles.  (Tiles and K blocks of cut tiles are
+// below 2^31: the caller checks the sizes.)
+struct Schedule {
+    const int *cum;  // shared memory: tiles before expert e, [E + 1]
+    const int32_t *offsets;
+    int E, R, kb, nb, G, c;
+    int step;            // tokens per tile; 0: the rows of an expert split evenly over its tiles
+    int tiles, whole;    // tiles [0, whole) go round the CTAs uncut
+    int units, sharing;  // K blocks of the cut tiles, and the CTAs that share them
+    int u, u1;           // this CTA's of them, counted from tile `whole`
+    int next_whole;
+
+    __device__ __forceinline__ void init() {
+        tiles = cum[E];
+        // A whole round is kept uncut; the last full round joins the rest, so
+        // that a cut tile has two or three parts.
+        whole = tiles % G == 0 ? tiles : tiles > G ? (tiles / G - 1) * G : 0;
+        units = (tiles - whole) * kb;
+        sharing = min(G, (units + MIN_SHARE - 1) / MIN_SHARE);
+        u = c < sharing ? static_cast<int>(static_cast<int64_t>(units) * c / sharing) : 0;
+        u1 = c < sharing ? static_cast<int>(static_cast<int64_t>(units) * (c + 1) / sharing) : 0;
+        next_whole = c;
+    }
+    __device__ __forceinline__ bool next(Piece &p) {
+        if (u < u1) {
+            const int t = u / kb;
+            p.tile = whole + t;
+            p.k0 = u - t * kb;
+            p.k1 = min(kb, p.k0 + (u1 - u));
+            u += p.k1 - p.k0;
+        } else if (next_whole < whole) {
+            p.tile = next_whole;
+            next_whole += G;
+            p.k0 = 0;
+            p.k1 = kb;
+        } else {
+            return false;
+        }
+        int lo = 0, hi = E - 1;  // the expert whose tiles hold p.tile
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (cum[mid] <= p.tile) lo = mid;
+            else hi = mid - 1;
+        }
+        p.e = lo;
+        const int local = p.tile - cum[lo];
+        const int nt = (cum[lo + 1] - cum[lo]) / nb;
+        const int r0 = offsets ? __ldg(offsets + lo) : 0;
+        const int n = offsets ? __ldg(offsets + lo + 1) - r0 : R;
+        // (an even share rounded up to 16 is at most a whole tile, so the last tile is not empty)
+        const int per = step ? step : ((n + nt - 1) / nt + 15) & ~15;
+        p.nblk = local / nt;
+        const int tt = local - p.nblk * nt;
+        p.row0 = r0 + tt * per;
+        p.ntok = min(per, n - tt * per);
+        return true;
+    }
+    // The CTAs [c0, c1] that hold a part of cut tile `tile`.
+    __device__ __forceinline__ void sharers(int tile, int &c0, int &c1) const {
+        const int64_t a = static_cast<int64_t>(tile - whole) * kb;
+        c0 = static_cast<int>(((a + 1) * sharing - 1) / units);
+        c1 = static_cast<int>(((a + kb) * sharing - 1) / units);
+    }
+};
+
+// Tiles before each expert, cum[0 .. E], for tiles of `tokens` rows times nb
+// row blocks of W; one warp.  Offsets out of order or out of [0, R] raise
+// STATUS_INDEX and leave their expert without tiles.
+__device__ __forceinline__ void count_tiles(int *cum, const int32_t *offsets, int E, int R, int tokens, int nb, int lane,
+                                            int *status) {
+    int base = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + lane;
+        int t = 0;
+        if (e < E) {
+            const int lo = offsets ? __ldg(offsets + e) : 0;
+            const int hi = offsets ? __ldg(offsets + e + 1) : R;
+            if (lo < 0 || hi < lo || hi > R) atomicOr(status, STATUS_INDEX);
+            else t = (hi - lo + tokens - 1) / tokens * nb;
+        }
+        int incl = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (e < E) cum[e] = base + incl - t;
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) cum[E] = base;
+}
+
+// Rows of codes [rows][K], ld bytes apart, in boxes of 128 bytes x box_rows.
+inline bool encode_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int64_t ld, int box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+    const cuuint32_t box[2] = {BK, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t es[2] = {1, 1};
+    return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace f8
+}  // namespace qk
