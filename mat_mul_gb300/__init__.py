@@ -250,82 +250,110 @@ def qmm_quantize_act(x, stream=None):
 
 # ---------------------------------------------------------------------------
 # Block-scaled 8-bit floats and expert layers
+#
+# A decode step makes these calls once per projection, with a few microseconds
+# of GPU work each: the checks below read each tensor's attributes once, pass
+# plain integers to the library and take the current stream's handle without
+# making a stream object.
 # ---------------------------------------------------------------------------
 F8_BLOCK = 128          # values per scale along K, weight rows per scale along N
 ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
 _SCORES = {"softmax": ROUTE_SOFTMAX, "sigmoid": ROUTE_SIGMOID}
-_ftypes = {}            # torch dtype -> qmm_ftype, filled on first use
+_f8 = None              # what the calls below need of torch and the library, made on first use
 
 
-def _ftype(dtype, what):
-    if not _ftypes:
+class _F8:
+    def __init__(self):
         import torch
-        _ftypes.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
-    t = _ftypes.get(dtype)
-    if t is None:
-        raise ValueError(f"{what} must be float32, float16 or bfloat16, not {dtype}")
-    return t
+        self.lib = load()
+        self.empty = torch.empty
+        self.float32, self.int32, self.e4m3 = torch.float32, torch.int32, torch.float8_e4m3fn
+        self.codes = (torch.float8_e4m3fn, torch.uint8)
+        self.ftypes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # qmm_ftype
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+    def ftype(self, dtype, what):
+        t = self.ftypes.get(dtype)
+        if t is None:
+            raise ValueError(f"{what} must be float32, float16 or bfloat16, not {dtype}")
+        return t
+
+
+def _f8_state():
+    global _f8
+    if _f8 is None:
+        _f8 = _F8()
+    return _f8
+
+
+def _device_index(first, *others):
+    """The CUDA device of every tensor given (None: left out)."""
+    if not first.is_cuda:
+        _require_cuda(first)
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            _require_cuda(t)
+            raise ValueError(f"tensors on {first.device} and on {t.device}")
+    return dev
 
 
 def _rows2d(t, what):
-    """t as [rows, columns] with adjacent columns: (rows, columns, row pitch)."""
-    if t.dim() == 1:
-        t = t.unsqueeze(0)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be a matrix whose row elements are adjacent, got shape {tuple(t.shape)} "
-                         f"strides {t.stride()}")
-    rows, cols = t.shape
-    # (a pitch below the row length, as of an expanded tensor, is refused by the library)
-    return rows, cols, t.stride(0) if rows > 1 else cols
+    """t as rows of adjacent elements: (rows, columns, row pitch)."""
+    shape = t.shape
+    if len(shape) == 2:
+        rows, cols = shape
+        ld, one = t.stride()
+        if one == 1 or cols <= 1:
+            # (a pitch below the row length, as of an expanded tensor, is refused by the library)
+            return rows, cols, ld if rows > 1 else cols
+    elif len(shape) == 1 and (shape[0] <= 1 or t.stride(0) == 1):
+        return 1, shape[0], shape[0]
+    raise ValueError(f"{what} must be a matrix whose row elements are adjacent, got shape {tuple(shape)} "
+                     f"strides {t.stride()}")
 
 
-def _f8_weights(W, S, dims, what):
+def _f8_weights(f, W, S, dims, what):
     """Shape of the codes W, after the checks of W and of its scales S."""
-    import torch
-    if W.dtype not in (torch.float8_e4m3fn, torch.uint8) or W.dim() != dims or not W.is_contiguous():
+    shape = W.shape
+    if W.dtype not in f.codes or len(shape) != dims or not W.is_contiguous():
         raise ValueError(f"{what}: codes must be a contiguous {dims}-d float8_e4m3fn (or uint8) tensor")
-    shape = tuple(W.shape)
-    want = shape[:-2] + (-(-shape[-2] // F8_BLOCK), -(-shape[-1] // F8_BLOCK))
-    if S.dtype != torch.float32 or tuple(S.shape) != want or not S.is_contiguous():
+    want = (*shape[:-2], -(-shape[-2] // F8_BLOCK), -(-shape[-1] // F8_BLOCK))
+    if S.dtype != f.float32 or S.shape != want or not S.is_contiguous():
         raise ValueError(f"{what}: scales must be a contiguous float32 tensor of shape {want}, got {tuple(S.shape)}")
     return shape
 
 
-def _same_device(*ts):
-    _require_cuda(*ts)
-    dev = ts[0].device
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and on {t.device}")
-
-
-def _f8_out(y, rows, cols, dtype, device):
+def _f8_out(f, y, rows, cols, dtype, device):
     """The result tensor and its row pitch: y checked, or a new one."""
-    import torch
     if y is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device), cols
+        return f.empty((rows, cols), dtype=dtype, device=device), cols
     r, c, ldy = _rows2d(y, "y")
-    if (r, c) != (rows, cols):
+    if r != rows or c != cols:
         raise ValueError(f"y has shape {tuple(y.shape)}, expected {(rows, cols)}")
     return y, ldy
 
 
-def _int32(t, n, what):
-    import torch
-    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+def _int32(f, t, n, what):
+    if t.dtype != f.int32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of {n} elements, got {t.dtype} {tuple(t.shape)}")
 
 
 def qmm_f8_quantize(x, stream=None):
     """(codes float8_e4m3fn [M, K], scales float32 [M, ceil(K/128)]) of a device
     tensor x [M, K] (or [K]) of float32, float16 or bfloat16 rows."""
-    import torch
-    _require_cuda(x)
+    f = _f8_state()
+    dev = _device_index(x)
     M, K, ldx = _rows2d(x, "x")
-    ft = _ftype(x.dtype, "x")
-    c = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
-    s = torch.empty((M, -(-K // F8_BLOCK)), dtype=torch.float32, device=x.device)
-    _check(load().qmm_f8_quantize(ft, _ptr(x), M, K, ldx, _ptr(c), _ptr(s), _stream_handle(stream)))
+    ft = f.ftype(x.dtype, "x")
+    device = x.device
+    c = f.empty((M, K), dtype=f.e4m3, device=device)
+    s = f.empty((M, -(-K // F8_BLOCK)), dtype=f.float32, device=device)
+    rc = f.lib.qmm_f8_quantize(ft, x.data_ptr(), M, K, ldx, c.data_ptr(), s.data_ptr(),
+                               f.stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc)
     return c, s
 
 
@@ -334,14 +362,19 @@ def qmm_f8(W, S, x, y=None, dtype=None, stream=None):
     [ceil(N/128), ceil(K/128)] and x [M, K] (or [K]) of float32, float16 or
     bfloat16; y has x's type unless dtype (or y) says otherwise.  K a multiple
     of 16.  Rows of x and y may be further apart than their length."""
-    _same_device(x, W, S, y)
-    N, K = _f8_weights(W, S, 2, "W")
+    f = _f8_state()
+    dev = _device_index(x, W, S, y)
+    N, K = _f8_weights(f, W, S, 2, "W")
     M, cols, ldx = _rows2d(x, "x")
     if cols != K:
         raise ValueError(f"x has {cols} columns, W {K}")
-    y, ldy = _f8_out(y, M, N, dtype or x.dtype, x.device)
-    _check(load().qmm_f8(_ptr(W), _ptr(S), N, K, _ftype(x.dtype, "x"), _ptr(x), M, ldx, _ftype(y.dtype, "y"), _ptr(y),
-                         ldy, _stream_handle(stream)))
+    xt = x.dtype
+    ft = f.ftype(xt, "x")
+    y, ldy = _f8_out(f, y, M, N, dtype or xt, x.device)
+    rc = f.lib.qmm_f8(W.data_ptr(), S.data_ptr(), N, K, ft, x.data_ptr(), M, ldx, f.ftype(y.dtype, "y"), y.data_ptr(),
+                      ldy, f.stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc)
     return y
 
 
@@ -350,19 +383,26 @@ def qmm_f8_experts(W, S, x, offsets, rows=None, y=None, dtype=None, stream=None)
     rows) for offsets[e] <= r < offsets[e+1]; W [E, N, K] codes, S their scales,
     offsets int32 [E+1] and rows int32 on the device.  Returns y [R, N], R the
     length of rows (or of x); rows of y from offsets[E] on are not written."""
-    _same_device(x, W, S, offsets, rows, y)
-    E, N, K = _f8_weights(W, S, 3, "W")
+    f = _f8_state()
+    dev = _device_index(x, W, S, offsets, rows, y)
+    E, N, K = _f8_weights(f, W, S, 3, "W")
     M, cols, ldx = _rows2d(x, "x")
     if cols != K:
         raise ValueError(f"x has {cols} columns, W {K}")
-    _int32(offsets, E + 1, "offsets")
-    R = M
+    _int32(f, offsets, E + 1, "offsets")
+    R, index = M, None
     if rows is not None:
         R = rows.numel()
-        _int32(rows, R, "rows")
-    y, ldy = _f8_out(y, R, N, dtype or x.dtype, x.device)
-    _check(load().qmm_f8_experts(_ptr(W), _ptr(S), E, N, K, _ftype(x.dtype, "x"), _ptr(x), M, ldx, _ptr(offsets),
-                                 _ptr(rows), R, _ftype(y.dtype, "y"), _ptr(y), ldy, _stream_handle(stream)))
+        _int32(f, rows, R, "rows")
+        index = rows.data_ptr()
+    xt = x.dtype
+    ft = f.ftype(xt, "x")
+    y, ldy = _f8_out(f, y, R, N, dtype or xt, x.device)
+    rc = f.lib.qmm_f8_experts(W.data_ptr(), S.data_ptr(), E, N, K, ft, x.data_ptr(), M, ldx, offsets.data_ptr(), index, R,
+                              f.ftype(y.dtype, "y"), y.data_ptr(), ldy,
+                              f.stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc)
     return y
 
 
@@ -376,21 +416,23 @@ def qmm_route(logits, k, score="softmax", normalize=True, factor=1.0, stream=Non
     """The k experts of each token with the largest logits [T, E], their weights
     (softmax or sigmoid scores, divided by their sum when normalize), and the
     (token, choice) pairs sorted by expert; see Route."""
-    import torch
-    _require_cuda(logits)
+    f = _f8_state()
+    dev = _device_index(logits)
     T, E, ld = _rows2d(logits, "logits")
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, not {score!r}")
     k = int(k)
-    dev, i32 = logits.device, torch.int32
-    n = max(k, 0)
-    weights = torch.empty((T, n), dtype=torch.float32, device=dev)
-    ints = torch.empty(3 * T * n + E + 1, dtype=i32, device=dev)
-    experts, slots, rows, offsets = ints.split([T * n, T * n, T * n, E + 1])
-    experts, slots = experts.view(T, n), slots.view(T, n)
-    _check(load().qmm_route(_ftype(logits.dtype, "logits"), _ptr(logits), T, E, ld, k, _SCORES[score],
-                            int(bool(normalize)), float(factor), _ptr(weights), _ptr(experts), _ptr(offsets),
-                            _ptr(rows), _ptr(slots), _stream_handle(stream)))
+    n = k if k > 0 else 0
+    ft, device, empty, i32 = f.ftype(logits.dtype, "logits"), logits.device, f.empty, f.int32
+    weights = empty((T, n), dtype=f.float32, device=device)
+    experts, slots = empty((2, T, n), dtype=i32, device=device).unbind(0)
+    rows = empty(T * n, dtype=i32, device=device)
+    offsets = empty(E + 1, dtype=i32, device=device)
+    rc = f.lib.qmm_route(ft, logits.data_ptr(), T, E, ld, k, _SCORES[score], 1 if normalize else 0, factor,
+                         weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
+                         f.stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc)
     return Route(weights, experts, offsets, rows, slots)
 
 
@@ -399,25 +441,31 @@ def qmm_f8_moe(x, route, W_gate, S_gate, W_up, S_up, W_down, S_down, y=None, dty
     (W_up[e] . x[t]), over the choices of route (a Route, as qmm_route returns
     it): x [T, H], W_gate and W_up [E, I, H], W_down [E, H, I] codes with their
     scales.  H and I multiples of 16."""
-    import torch
+    f = _f8_state()
     weights, _, offsets, _, slots = route
-    _same_device(x, W_gate, S_gate, W_up, S_up, W_down, S_down, weights, offsets, slots, y)
-    E, I, H = _f8_weights(W_gate, S_gate, 3, "W_gate")
-    if _f8_weights(W_up, S_up, 3, "W_up") != (E, I, H) or _f8_weights(W_down, S_down, 3, "W_down") != (E, H, I):
+    dev = _device_index(x, W_gate, S_gate, W_up, S_up, W_down, S_down, weights, offsets, slots, y)
+    E, I, H = shape = _f8_weights(f, W_gate, S_gate, 3, "W_gate")
+    if _f8_weights(f, W_up, S_up, 3, "W_up") != shape or _f8_weights(f, W_down, S_down, 3, "W_down") != (E, H, I):
         raise ValueError(f"W_up must be {(E, I, H)} and W_down {(E, H, I)} for W_gate {(E, I, H)}, got "
                          f"{tuple(W_up.shape)} and {tuple(W_down.shape)}")
     T, cols, ldx = _rows2d(x, "x")
     if cols != H:
         raise ValueError(f"x has {cols} columns, the experts {H}")
-    if weights.dim() != 2 or weights.shape[0] != T or weights.dtype != torch.float32 or not weights.is_contiguous():
-        raise ValueError(f"route.weights must be a contiguous float32 tensor of {T} rows, got {tuple(weights.shape)}")
-    k = weights.shape[1]
-    _int32(offsets, E + 1, "route.offsets")
-    _int32(slots, T * k, "route.slots")
-    y, ldy = _f8_out(y, T, H, dtype or x.dtype, x.device)
-    _check(load().qmm_f8_moe(_ftype(x.dtype, "x"), _ptr(x), T, H, ldx, k, _ptr(weights), _ptr(offsets), _ptr(slots), E,
-                             I, _ptr(W_gate), _ptr(S_gate), _ptr(W_up), _ptr(S_up), _ptr(W_down), _ptr(S_down),
-                             _ftype(y.dtype, "y"), _ptr(y), ldy, _stream_handle(stream)))
+    wshape = weights.shape
+    if len(wshape) != 2 or wshape[0] != T or weights.dtype != f.float32 or not weights.is_contiguous():
+        raise ValueError(f"route.weights must be a contiguous float32 tensor of {T} rows, got {tuple(wshape)}")
+    k = wshape[1]
+    _int32(f, offsets, E + 1, "route.offsets")
+    _int32(f, slots, T * k, "route.slots")
+    xt = x.dtype
+    ft = f.ftype(xt, "x")
+    y, ldy = _f8_out(f, y, T, H, dtype or xt, x.device)
+    rc = f.lib.qmm_f8_moe(ft, x.data_ptr(), T, H, ldx, k, weights.data_ptr(), offsets.data_ptr(), slots.data_ptr(), E, I,
+                          W_gate.data_ptr(), S_gate.data_ptr(), W_up.data_ptr(), S_up.data_ptr(), W_down.data_ptr(),
+                          S_down.data_ptr(), f.ftype(y.dtype, "y"), y.data_ptr(), ldy,
+                          f.stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc)
     return y
 
 

@@ -116,6 +116,7 @@ int product(const void *W, const float *S, int64_t E, int64_t N, int64_t K, int 
     f.zero = reinterpret_cast<unsigned *>(ws);
     f.n_zero = c.num_sms;
     f.status = c.status;
+    f.dev = c.dev;
     cudaError_t e = qk::launch_f8_quantize(f, st, c.num_sms);
     if (e != cudaSuccess) return cuda_error(e, "quantize launch");
     qk::count_launches(1);
@@ -137,6 +138,7 @@ int product(const void *W, const float *S, int64_t E, int64_t N, int64_t K, int 
     g.part = reinterpret_cast<float *>(ws + COUNT_BYTES + q.q_bytes + q.s_bytes);
     g.count = f.zero;
     g.status = c.status;
+    g.dev = c.dev;
     e = qk::launch_f8_gemm(g, st, c.num_sms);
     if (e != cudaSuccess) return cuda_error(e, "product launch");
     qk::count_launches(1);
@@ -170,6 +172,7 @@ int qmm_f8_quantize(int x_type, const void *x, int64_t M, int64_t K, int64_t ldx
     f.s_row = qk::f8_blocks(K);
     f.s_blk = 1;
     f.status = c.status;
+    f.dev = c.dev;
     const cudaError_t e = qk::launch_f8_quantize(f, static_cast<cudaStream_t>(stream), c.num_sms);
     if (e != cudaSuccess) return cuda_error(e, "quantize launch");
     qk::count_launches(1);
@@ -243,7 +246,7 @@ int qmm_route(int x_type, const void *logits, int64_t T, int64_t E, int64_t ldx,
         if (int rc = qk::f8_workspace(c, st, bytes, &hist)) return rc;
     const qk::F8Route r = {x_type,  logits,  T,       T > 1 ? ldx : E, static_cast<int>(E), k,
                            score,   normalize, factor, weights, experts, offsets, rows, slots,
-                           static_cast<int32_t *>(hist)};
+                           static_cast<int32_t *>(hist), c.dev};
     const cudaError_t e = qk::launch_f8_route(r, st);
     if (e != cudaSuccess) return cuda_error(e, "route launch");
     qk::count_launches(qk::f8_route_launches(T));
@@ -317,6 +320,7 @@ int qmm_f8_moe(int x_type, const void *x, int64_t T, int64_t H, int64_t ldx, int
     f.zero = count;
     f.n_zero = static_cast<int>(2 * COUNT_BYTES / 4);
     f.status = c.status;
+    f.dev = c.dev;
     cudaError_t e = qk::launch_f8_quantize(f, st, c.num_sms);
     if (e != cudaSuccess) return cuda_error(e, "quantize launch");
     qk::count_launches(1);
@@ -342,6 +346,7 @@ int qmm_f8_moe(int x_type, const void *x, int64_t T, int64_t H, int64_t ldx, int
     g.part = partial;
     g.count = count;
     g.status = c.status;
+    g.dev = c.dev;
     e = qk::launch_f8_gemm(g, st, c.num_sms);
     if (e != cudaSuccess) return cuda_error(e, "gate and up launch");
     qk::count_launches(1);
@@ -363,7 +368,8 @@ int qmm_f8_moe(int x_type, const void *x, int64_t T, int64_t H, int64_t ldx, int
     if (e != cudaSuccess) return cuda_error(e, "down launch");
     qk::count_launches(1);
 
-    e = qk::launch_f8_combine(d, ldd, R, weights, slots, T, k, H, y_type, y, T > 1 ? ldy : H, c.status, st, c.num_sms);
+    e = qk::launch_f8_combine(d, ldd, R, weights, slots, T, k, H, y_type, y, T > 1 ? ldy : H, c.status, st, c.num_sms,
+                              c.dev);
     if (e != cudaSuccess) return cuda_error(e, "weighted sum launch");
     qk::count_launches(1);
     return QMM_OK;

@@ -485,7 +485,8 @@ cudaError_t launch_bt(const F8Gemm &g, cudaStream_t st, int num_sms) {
     p.count = g.count;
     p.status = g.status;
     p.stop = inject_stop_stage();
-    cudaError_t e = set_smem_attrs(f8_gemm_kernel<BT, DUAL>, C::SMEM);
+    static OncePerDevice ready;
+    const cudaError_t e = ready(g.dev, [] { return set_smem_attrs(f8_gemm_kernel<BT, DUAL>, C::SMEM); });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms));

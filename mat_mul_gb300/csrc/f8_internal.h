@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/qmm.h"
 
 namespace qk {
@@ -42,6 +44,7 @@ struct F8Quant {
     unsigned *zero;
     int n_zero;
     int *status;
+    int dev;
 };
 cudaError_t launch_f8_quantize(const F8Quant &q, cudaStream_t st, int num_sms);
 
@@ -71,6 +74,7 @@ struct F8Gemm {
     float *part;      // f8_part_bytes()
     unsigned *count;  // one per CTA, zero before the launch
     int *status;
+    int dev;
 };
 size_t f8_part_bytes(int64_t R, int E, bool dual, int num_sms);
 bool f8_available();
@@ -90,6 +94,7 @@ struct F8Route {
     float *weights;
     int32_t *experts, *offsets, *rows, *slots;
     int32_t *hist;
+    int dev;
 };
 size_t f8_route_hist_bytes(int64_t T, int E);
 int f8_route_launches(int64_t T);
@@ -99,7 +104,21 @@ cudaError_t launch_f8_route(const F8Route &r, cudaStream_t st);
 // outside [0, R) raise STATUS_INDEX and count as zero rows.
 cudaError_t launch_f8_combine(const float *d, int64_t ldd, int64_t R, const float *w, const int32_t *slots, int64_t T,
                               int k, int64_t H, int y_type, void *y, int64_t ldy, int *status, cudaStream_t st,
-                              int num_sms);
+                              int num_sms, int dev);
+
+// Launch attributes and what else a kernel needs once per device: `make` runs
+// until it has succeeded on device `dev`.
+struct OncePerDevice {
+    std::atomic<uint64_t> done{0};
+    template <class F>
+    cudaError_t operator()(int dev, F make) {
+        const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+        if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        const cudaError_t e = make();
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 // Library context for the entry points outside qmm_abi.cu.
 struct F8Context {

@@ -243,7 +243,10 @@ cudaError_t quantize_t(const F8Quant &q, cudaStream_t st, int num_sms) {
                      reinterpret_cast<uintptr_t>(q.x) % (4 * es) == 0 && reinterpret_cast<uintptr_t>(q.q) % 4 == 0;
     const void *kern = vec ? reinterpret_cast<const void *>(f8_quantize_kernel<T, true>)
                            : reinterpret_cast<const void *>(f8_quantize_kernel<T, false>);
-    cudaError_t e = vec ? prefer_max_shared(f8_quantize_kernel<T, true>) : prefer_max_shared(f8_quantize_kernel<T, false>);
+    static OncePerDevice ready[2];
+    const cudaError_t e = ready[vec](q.dev, [&] {
+        return vec ? prefer_max_shared(f8_quantize_kernel<T, true>) : prefer_max_shared(f8_quantize_kernel<T, false>);
+    });
     if (e != cudaSuccess) return e;
     const int64_t blocks = (p.items + QUANT_THREADS / 32 - 1) / (QUANT_THREADS / 32);
     const int64_t cap = static_cast<int64_t>(num_sms) * 8;
@@ -253,8 +256,9 @@ cudaError_t quantize_t(const F8Quant &q, cudaStream_t st, int num_sms) {
 }
 
 template <int T>
-cudaError_t combine_t(CombineParams &p, cudaStream_t st, int num_sms) {
-    cudaError_t e = prefer_max_shared(f8_combine_kernel<T>);
+cudaError_t combine_t(CombineParams &p, cudaStream_t st, int num_sms, int dev) {
+    static OncePerDevice ready;
+    const cudaError_t e = ready(dev, [] { return prefer_max_shared(f8_combine_kernel<T>); });
     if (e != cudaSuccess) return e;
     const int64_t blocks = (p.T * ((p.H + 3) / 4) + 255) / 256, cap = static_cast<int64_t>(num_sms) * 8;
     void *args[] = {&p};
@@ -272,11 +276,11 @@ cudaError_t launch_f8_quantize(const F8Quant &q, cudaStream_t st, int num_sms) {
 
 cudaError_t launch_f8_combine(const float *d, int64_t ldd, int64_t R, const float *w, const int32_t *slots, int64_t T,
                               int k, int64_t H, int y_type, void *y, int64_t ldy, int *status, cudaStream_t st,
-                              int num_sms) {
+                              int num_sms, int dev) {
     CombineParams p = {d, ldd, R, T, H, ldy, w, slots, k, y, status};
-    if (y_type == QMM_F32) return combine_t<QMM_F32>(p, st, num_sms);
-    if (y_type == QMM_F16) return combine_t<QMM_F16>(p, st, num_sms);
-    return combine_t<QMM_BF16>(p, st, num_sms);
+    if (y_type == QMM_F32) return combine_t<QMM_F32>(p, st, num_sms, dev);
+    if (y_type == QMM_F16) return combine_t<QMM_F16>(p, st, num_sms, dev);
+    return combine_t<QMM_BF16>(p, st, num_sms, dev);
 }
 
 }  // namespace qk

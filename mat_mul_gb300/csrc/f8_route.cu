@@ -226,8 +226,6 @@ Kernel choose_kernel(int E) {
 }
 
 cudaError_t launch(Kernel kern, int64_t blocks, RouteParams &p, cudaStream_t st) {
-    cudaError_t e = prefer_max_shared(kern);
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(THREADS);
@@ -251,7 +249,14 @@ cudaError_t launch_f8_route(const F8Route &r, cudaStream_t st) {
     RouteParams p = {r.x,      r.T,       r.ldx,     r.x_type,  r.E,    r.k,     r.score, r.normalize,
                      r.T <= TOKENS, r.factor, r.weights, r.experts, r.offsets, r.rows, r.slots, r.hist};
     const int64_t blocks = (r.T + TOKENS - 1) / TOKENS;
-    cudaError_t e = launch(choose_kernel(r.E), blocks, p, st);
+    static OncePerDevice ready;
+    cudaError_t e = ready(r.dev, [] {
+        cudaError_t q = prefer_max_shared(route_place_kernel);
+        for (int n = 32; n <= 1024 && q == cudaSuccess; n *= 2) q = prefer_max_shared(choose_kernel(n));
+        return q;
+    });
+    if (e != cudaSuccess) return e;
+    e = launch(choose_kernel(r.E), blocks, p, st);
     if (e != cudaSuccess || p.fused) return e;
     return launch(route_place_kernel, blocks, p, st);
 }

@@ -608,13 +608,6 @@ cudaError_t launch_wide(const F8Gemm &g, cudaStream_t st, int num_sms) {
     p.count = g.count;
     p.status = g.status;
     p.stop = inject_stop_stage();
-    cudaError_t e = set_smem_attrs(kern, C::SMEM);
-    if (e != cudaSuccess) return e;
-    // the register split needs what the launch brings: a build with fewer
-    // registers per thread would wait for them forever
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-    if (fa.numRegs != C::REGS) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
@@ -628,14 +621,28 @@ cudaError_t launch_wide(const F8Gemm &g, cudaStream_t st, int num_sms) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int groups = num_sms / CG;
-    cfg.gridDim = dim3(static_cast<unsigned>(groups * CG));
-    if (CG == 2) {
-        int fit = 0;
-        if ((e = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg)) != cudaSuccess) return e;
-        if (fit >= 1 && fit < groups) groups = fit;
-        cfg.gridDim = dim3(static_cast<unsigned>(groups * CG));
-    }
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms / CG * CG));
+    static OncePerDevice ready;
+    static std::atomic<int> resident[64];  // CTAs that run at once, per device
+    const cudaError_t e = ready(g.dev, [&] {
+        cudaError_t r = set_smem_attrs(kern, C::SMEM);
+        if (r != cudaSuccess) return r;
+        // the register split needs what the launch brings: a build with fewer
+        // registers per thread would wait for them forever
+        cudaFuncAttributes fa;
+        if ((r = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return r;
+        if (fa.numRegs != C::REGS) return cudaErrorInvalidConfiguration;
+        int groups = num_sms / CG;
+        if (CG == 2) {
+            int fit = 0;
+            if ((r = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg)) != cudaSuccess) return r;
+            if (fit >= 1 && fit < groups) groups = fit;
+        }
+        resident[g.dev & 63].store(groups * CG);
+        return cudaSuccess;
+    });
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(resident[g.dev & 63].load()));
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, tw, tw2, tx, p);
 }
