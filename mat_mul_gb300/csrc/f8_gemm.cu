@@ -46,28 +46,32 @@ constexpr int SMEM_MAX = 232448;
 template <int BT, bool DUAL>
 struct Cfg {
     static constexpr int NA = DUAL ? 2 : 1;            // weight matrices per tile
+    // K blocks per step: every wait and hand-over of a step costs the roles a
+    // few hundred cycles, about what a 16 KB weight block takes to arrive
+    static constexpr int KS = BT <= (DUAL ? 32 : 64) ? 2 : 1;
     static constexpr int XBOX = BT < 64 ? BT : 64;     // rows per token copy
     static constexpr int W_BYTES = BW * BK, X_BYTES = BT * BK;
-    static constexpr int STAGE = NA * W_BYTES + X_BYTES;
-    static constexpr int SC_BYTES = NA * BT * 4;
+    static constexpr int BLOCK = NA * W_BYTES + X_BYTES, STAGE = KS * BLOCK;
+    static constexpr int SC_FLOATS = BT + 4;           // a K block's scales: of the tokens, of the weights
+    static constexpr int SC_BYTES = KS * SC_FLOATS * 4;
     static constexpr int HALF = BT / 2;                // token columns per epilogue warp
     static constexpr int CH = HALF < 16 ? HALF : 16;   // columns per TMEM load
     static constexpr int AMAX_BYTES = DUAL ? 4 * BT * 4 : 0;
     static constexpr int CUM_BYTES = (QMM_F8_MAX_EXPERTS + 4) * 4;
     static constexpr int FIXED = SC_STAGES * SC_BYTES + AMAX_BYTES + CUM_BYTES + 512 + 1024;
     static constexpr int FIT = (SMEM_MAX - FIXED) / STAGE;
-    static constexpr int STAGES = FIT > 12 ? 12 : FIT;
+    static constexpr int STAGES = FIT > 8 ? 8 : FIT;
     static constexpr int OFF_SC = STAGES * STAGE;
     static constexpr int OFF_AMAX = OFF_SC + SC_STAGES * SC_BYTES;
     static constexpr int OFF_CUM = OFF_AMAX + AMAX_BYTES;
     static constexpr int OFF_BAR = OFF_CUM + CUM_BYTES;
     static constexpr int SMEM = OFF_BAR + 512 + 1024;
-    static constexpr int D_COLS = NA * BT;             // one TMEM buffer
+    static constexpr int D_COLS = KS * NA * BT;        // one TMEM buffer: a step's sums
     static constexpr int TMEM_COLS = 2 * D_COLS < 32 ? 32 : 2 * D_COLS;
     static constexpr int PART = NA * BT * BW;          // floats of a partial tile
     static_assert(STAGES >= 3 && SMEM <= SMEM_MAX, "shared memory");
     static_assert(TMEM_COLS <= 512, "tensor memory");
-    static_assert(8 * (2 * STAGES + 2 * SC_STAGES + 5) + 32 <= 512, "barrier area");
+    static_assert(8 * (2 * STAGES + 2 * SC_STAGES + 5) + 32 <= 480, "barrier area");
 };
 
 struct Params {
@@ -85,7 +89,7 @@ struct Params {
     float *part;
     unsigned *count;
     int *status;
-    int stop;  // the first CTA issues no copy from this K block on (failure test hook)
+    int stop;  // the first CTA issues no copy from this step on (failure test hook)
 };
 
 // D[tmem] (+)= A[smem] . B[smem]^T, e4m3 x e4m3 -> fp32
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2,
                    const __grid_constant__ CUtensorMap tmX, const Params P) {
     using C = Cfg<BT, DUAL>;
-    constexpr int NA = C::NA;
+    constexpr int NA = C::NA, KS = C::KS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -153,7 +157,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t d_full = sc_empty + 8 * SC_STAGES, d_empty = d_full + 16;
     const uint32_t done = d_empty + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 480);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_BAR + 484);
     volatile unsigned *arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 488);
     int *cum = reinterpret_cast<int *>(smem + C::OFF_CUM);
 
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(empty + 8 * s, 1);
         }
         for (int s = 0; s < SC_STAGES; ++s) {
-            mbar_init(sc_full + 8 * s, 1);
+            mbar_init(sc_full + 8 * s, 32);
             mbar_init(sc_empty + 8 * s, 8);
         }
         for (int s = 0; s < 2; ++s) {
@@ -171,7 +174,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(d_empty + 8 * s, 8);
         }
         mbar_init(done, 1);
-        *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 3) {
@@ -205,32 +207,51 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp == 0) {
         if (elect_one()) {
-            // Copies.  Weights may be fetched before the quantiser is done.
-            const int stop = blockIdx.x == 0 ? P.stop : NO_STOP;
-            int it = 0;
+            // Copies.  The weights of the first steps are asked for before the
+            // launch in front is done (it writes only the codes and scales of x),
+            // so that they stream in while x is quantised.
+            int stop = NO_STOP;
+            if (blockIdx.x == 0 && P.stop != NO_STOP) {  // the failure test hook: at the latest the last step is left out
+                Schedule all = sch;
+                for (stop = -1; all.next(p);) stop += (p.k1 - p.k0 + KS - 1) / KS;
+                stop = min(stop, P.stop);
+            }
+            int it = 0, early = 0;
             bool ok = true;
+            auto weights = [&](const Piece &q, int k, int s) {
+                const int kc = min(KS, q.k1 - k), wrow = q.e * P.N + q.nblk * BW;
+                const int boxes = (q.ntok + C::XBOX - 1) / C::XBOX;
+                const uint32_t st = stage0 + s * C::STAGE, b = full + 8 * s;
+                mbar_arrive_expect_tx(b, kc * (NA * C::W_BYTES + boxes * C::XBOX * BK));
+                for (int j = 0; j < kc; ++j) {
+                    tma_2d(st + j * C::BLOCK, &tmW, (k + j) * BK, wrow, b);
+                    if constexpr (DUAL) tma_2d(st + j * C::BLOCK + C::W_BYTES, &tmW2, (k + j) * BK, wrow, b);
+                }
+            };
+            {
+                Schedule first = sch;
+                while (early < C::STAGES && early < stop && first.next(p))
+                    for (int k = p.k0; k < p.k1 && early < C::STAGES && early < stop; k += KS, ++early) weights(p, k, early);
+            }
             pdl_wait();
             pdl_trigger();
             while (ok && sch.next(p)) {
                 const int boxes = (p.ntok + C::XBOX - 1) / C::XBOX;
-                const uint32_t bytes = NA * C::W_BYTES + boxes * C::XBOX * BK;
-                const int wrow = p.e * P.N + p.nblk * BW;
-                for (int k = p.k0; k < p.k1; ++k, ++it) {
+                for (int k = p.k0; k < p.k1; k += KS, ++it) {
                     const int s = it % C::STAGES;
-                    if (it >= stop || *abort_flag ||
+                    if (it >= stop ||
                         (it >= C::STAGES && !mbar_spin(empty + 8 * s, ((it / C::STAGES) - 1) & 1, P.status))) {
                         ok = false;
                         break;
                     }
-                    const uint32_t st = stage0 + s * C::STAGE, b = full + 8 * s;
-                    mbar_arrive_expect_tx(b, bytes);
-                    tma_2d(st, &tmW, k * BK, wrow, b);
-                    if constexpr (DUAL) tma_2d(st + C::W_BYTES, &tmW2, k * BK, wrow, b);
-                    for (int x = 0; x < boxes; ++x)
-                        tma_2d(st + NA * C::W_BYTES + x * C::XBOX * BK, &tmX, k * BK, p.row0 + x * C::XBOX, b);
+                    if (it >= early) weights(p, k, s);
+                    const uint32_t st = stage0 + s * C::STAGE + NA * C::W_BYTES, b = full + 8 * s;
+                    const int kc = min(KS, p.k1 - k);
+                    for (int j = 0; j < kc; ++j)
+                        for (int x = 0; x < boxes; ++x)
+                            tma_2d(st + j * C::BLOCK + x * C::XBOX * BK, &tmX, (k + j) * BK, p.row0 + x * C::XBOX, b);
                 }
             }
-            if (!ok && it < stop) *abort_flag = 1;
             // no CTA ends with copies in flight
             for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
                 mbar_spin(full + 8 * (i % C::STAGES), (i / C::STAGES) & 1, P.status);
@@ -242,23 +263,26 @@ __global__ void __launch_bounds__(THREADS, 1)
             while (ok && sch.next(p)) {
                 const uint32_t cols = (p.ntok + 15) & ~15;
                 const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((BW >> 4) << 24);
-                for (int k = p.k0; k < p.k1; ++k, ++it) {
+                for (int k = p.k0; k < p.k1; k += KS, ++it) {
                     const int s = it % C::STAGES, d = it & 1;
-                    if (*abort_flag || !mbar_spin(full + 8 * s, (it / C::STAGES) & 1, P.status) ||
+                    if (!mbar_spin(full + 8 * s, (it / C::STAGES) & 1, P.status) ||
                         (it >= 2 && !mbar_spin(d_empty + 8 * d, ((it >> 1) - 1) & 1, P.status))) {
                         ok = false;
-                        *abort_flag = 1;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = stage0 + s * C::STAGE;
-                    const uint64_t b = smem_desc(st + NA * C::W_BYTES);
 #pragma unroll
-                    for (int m = 0; m < NA; ++m) {
-                        const uint64_t a = smem_desc(st + m * C::W_BYTES);
+                    for (int j = 0; j < KS; ++j) {
+                        if (k + j >= p.k1) break;
+                        const uint32_t st = stage0 + s * C::STAGE + j * C::BLOCK;
+                        const uint64_t b = smem_desc(st + NA * C::W_BYTES);
 #pragma unroll
-                        for (int q = 0; q < BK / 32; ++q)
-                            mma_f8(tmem + d * C::D_COLS + m * BT, a + 2 * q, b + 2 * q, idesc, q ? 1u : 0u);
+                        for (int m = 0; m < NA; ++m) {
+                            const uint64_t a = smem_desc(st + m * C::W_BYTES);
+#pragma unroll
+                            for (int q = 0; q < BK / 32; ++q)
+                                mma_f8(tmem + d * C::D_COLS + (j * NA + m) * BT, a + 2 * q, b + 2 * q, idesc, q ? 1u : 0u);
+                        }
                     }
                     mma_commit(empty + 8 * s);
                     mma_commit(d_full + 8 * d);
@@ -267,60 +291,30 @@ __global__ void __launch_bounds__(THREADS, 1)
             mma_commit(done);
         }
     } else if (warp == 2) {
-        // Scales: the products xs[b, token] * Ws[.., b] of a K block, BT (two
-        // times BT) floats per stage.  The loads run PRE blocks ahead.
-        constexpr int PER = BT < 32 ? 1 : BT / 32, PRE = 4;
+        // Scales of a step, by asynchronous copies straight into shared memory.
         pdl_wait();
-        Schedule ahead = sch;
-        Piece a;
-        float v[PRE][PER], w[PRE][NA];
-        bool more = ahead.next(a);
-        int ka = more ? a.k0 : 0;
-        auto fetch = [&](int slot) {
-            if (!more) return;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int t = lane + 32 * i;
-                v[slot][i] = t < a.ntok ? __ldg(P.xs + ka * P.ld_s + a.row0 + t) : 0.0f;
-            }
-            const int64_t ws = (static_cast<int64_t>(a.e) * P.nb + a.nblk) * P.kb + ka;
-            w[slot][0] = __ldg(P.Ws + ws);
-            if constexpr (DUAL) w[slot][1] = __ldg(P.W2s + ws);
-            if (++ka == a.k1) {
-                more = ahead.next(a);
-                ka = more ? a.k0 : 0;
-            }
-        };
-        int total = 0;
-        while (sch.next(p)) total += p.k1 - p.k0;
-#pragma unroll
-        for (int i = 0; i < PRE; ++i) fetch(i);
+        int it = 0;
         bool ok = true;
-        for (int it0 = 0; ok && it0 < total; it0 += PRE) {
-#pragma unroll
-            for (int i = 0; i < PRE; ++i) {
-                const int it = it0 + i;
-                if (!ok || it >= total) break;
+        while (ok && sch.next(p)) {
+            const int64_t ws = (static_cast<int64_t>(p.e) * P.nb + p.nblk) * P.kb;
+            const float *w = (DUAL && lane == 1 ? P.W2s : P.Ws) + ws;
+            const float *x = P.xs + p.row0;
+            for (int k = p.k0; k < p.k1; k += KS, ++it) {
                 const int s = it % SC_STAGES;
-                ok = !*abort_flag;
-                if (ok && it >= SC_STAGES) ok = mbar_spin(sc_empty + 8 * s, ((it / SC_STAGES) - 1) & 1, P.status);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) {
-                    *abort_flag = 1;
-                    break;
+                if (it >= SC_STAGES)
+                    ok = __all_sync(0xffffffffu, mbar_spin(sc_empty + 8 * s, ((it / SC_STAGES) - 1) & 1, P.status));
+                if (!ok) break;
+                const uint32_t dst = smem_u32(smem + C::OFF_SC) + s * C::SC_BYTES;
+                const int kc = min(KS, p.k1 - k);
+                for (int j = 0; j < kc; ++j) {
+                    for (int t = lane; t < BT; t += 32)
+                        copy4(dst + 4 * (j * C::SC_FLOATS + t), x + (k + j) * P.ld_s + min(t, p.ntok - 1));
+                    if (lane < NA) copy4(dst + 4 * (j * C::SC_FLOATS + BT + lane), w + k + j);
                 }
-                float *sc = reinterpret_cast<float *>(smem + C::OFF_SC + s * C::SC_BYTES);
-#pragma unroll
-                for (int q = 0; q < PER; ++q)
-                    if (lane + 32 * q < BT) {
-#pragma unroll
-                        for (int m = 0; m < NA; ++m) sc[m * BT + lane + 32 * q] = v[i][q] * w[i][m];
-                    }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sc_full + 8 * s);
-                fetch(i);
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sc_full + 8 * s) : "memory");
             }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp >= 4) {
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + half * C::HALF;
@@ -334,34 +328,40 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < C::HALF; ++i) acc[m][i] = 0.0f;
             const int mine = min(C::HALF, p.ntok - half * C::HALF);  // this warp's token columns (may be <= 0)
-            for (int k = p.k0; k < p.k1; ++k, ++it) {
+            for (int k = p.k0; k < p.k1; k += KS, ++it) {
                 const int d = it & 1, s = it % SC_STAGES;
-                ok = !*abort_flag && mbar_spin(d_full + 8 * d, (it >> 1) & 1, P.status) &&
-                     mbar_spin(sc_full + 8 * s, (it / SC_STAGES) & 1, P.status);
+                ok = mbar_spin(sc_full + 8 * s, (it / SC_STAGES) & 1, P.status) &&
+                     mbar_spin(d_full + 8 * d, (it >> 1) & 1, P.status);
                 ok = __all_sync(0xffffffffu, ok);
-                if (!ok) {
-                    *abort_flag = 1;
-                    break;
-                }
+                if (!ok) break;
                 tc_fence_after();
-                const float *sc = reinterpret_cast<const float *>(smem + C::OFF_SC + s * C::SC_BYTES) + half * C::HALF;
+                const float *sc = reinterpret_cast<const float *>(smem + C::OFF_SC + s * C::SC_BYTES);
+                if (mine > 0) {
 #pragma unroll
-                for (int m = 0; m < NA; ++m)
+                    for (int j = 0; j < KS; ++j) {
+                        if (k + j >= p.k1) break;
 #pragma unroll
-                    for (int c = 0; c < C::HALF; c += C::CH)
-                        if (c < mine) {
-                            uint32_t r[C::CH];
-                            tmem_ld(lane_base + d * C::D_COLS + m * BT + c, r);
-                            tmem_wait(r);
+                        for (int m = 0; m < NA; ++m) {
+                            const float w = sc[j * C::SC_FLOATS + BT + m];
 #pragma unroll
-                            for (int i = 0; i < C::CH; i += 4) {
-                                const float4 f = *reinterpret_cast<const float4 *>(sc + m * BT + c + i);
-                                acc[m][c + i] = fmaf(__uint_as_float(r[i]), f.x, acc[m][c + i]);
-                                acc[m][c + i + 1] = fmaf(__uint_as_float(r[i + 1]), f.y, acc[m][c + i + 1]);
-                                acc[m][c + i + 2] = fmaf(__uint_as_float(r[i + 2]), f.z, acc[m][c + i + 2]);
-                                acc[m][c + i + 3] = fmaf(__uint_as_float(r[i + 3]), f.w, acc[m][c + i + 3]);
-                            }
+                            for (int c = 0; c < C::HALF; c += C::CH)
+                                if (c < mine) {
+                                    uint32_t r[C::CH];
+                                    tmem_ld(lane_base + d * C::D_COLS + (j * NA + m) * BT + c, r);
+                                    tmem_wait(r);
+#pragma unroll
+                                    for (int i = 0; i < C::CH; i += 4) {
+                                        const float4 f =
+                                            *reinterpret_cast<const float4 *>(sc + j * C::SC_FLOATS + half * C::HALF + c + i);
+                                        acc[m][c + i] = fmaf(__uint_as_float(r[i]), f.x * w, acc[m][c + i]);
+                                        acc[m][c + i + 1] = fmaf(__uint_as_float(r[i + 1]), f.y * w, acc[m][c + i + 1]);
+                                        acc[m][c + i + 2] = fmaf(__uint_as_float(r[i + 2]), f.z * w, acc[m][c + i + 2]);
+                                        acc[m][c + i + 3] = fmaf(__uint_as_float(r[i + 3]), f.w * w, acc[m][c + i + 3]);
+                                    }
+                                }
                         }
+                    }
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -390,7 +390,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (threadIdx.x == 128) *arrived = atomicAdd(P.count + c0, 1u);
                 named_barrier(1, 256);
                 store = *arrived == static_cast<unsigned>(c1 - c0);
-                named_barrier(1, 256);
                 if (store) {
                     __threadfence();
 #pragma unroll
@@ -502,10 +501,10 @@ cudaError_t launch_bt(const F8Gemm &g, cudaStream_t st, int num_sms) {
 }
 
 // Tokens per tile: the mean rows of a group, rounded up to a tile width.
-int tile_tokens(int64_t R, int E, bool dual) {
+int tile_tokens(int64_t R, int E) {
     const int64_t mean = (R + E - 1) / E;
     int bt = 16;
-    while (bt < mean && bt < (dual ? 128 : 256)) bt *= 2;
+    while (bt < mean && bt < 128) bt *= 2;
     return bt;
 }
 
@@ -519,14 +518,11 @@ int path_of(int64_t R, int E) {
 template <bool DUAL>
 cudaError_t launch_any(const F8Gemm &g, cudaStream_t st, int num_sms) {
     if (const int w = path_of(g.R, g.E)) return launch_f8_wide(g, w == 2, st, num_sms);
-    switch (tile_tokens(g.R, g.E, DUAL)) {
+    switch (tile_tokens(g.R, g.E)) {
     case 16: return launch_bt<16, DUAL>(g, st, num_sms);
     case 32: return launch_bt<32, DUAL>(g, st, num_sms);
     case 64: return launch_bt<64, DUAL>(g, st, num_sms);
-    case 128: return launch_bt<128, DUAL>(g, st, num_sms);
-    default:
-        if constexpr (DUAL) return launch_bt<128, DUAL>(g, st, num_sms);
-        else return launch_bt<256, DUAL>(g, st, num_sms);
+    default: return launch_bt<128, DUAL>(g, st, num_sms);
     }
 }
 
@@ -534,7 +530,7 @@ cudaError_t launch_any(const F8Gemm &g, cudaStream_t st, int num_sms) {
 
 size_t f8_part_bytes(int64_t R, int E, bool dual, int num_sms) {
     if (path_of(R, E)) return f8_wide_part_bytes(num_sms);
-    return static_cast<size_t>(num_sms) * 2 * (dual ? 2 : 1) * tile_tokens(R, E, dual) * BW * sizeof(float);
+    return static_cast<size_t>(num_sms) * 2 * (dual ? 2 : 1) * tile_tokens(R, E) * BW * sizeof(float);
 }
 
 bool f8_available() { return tensor_map_encoder() != nullptr; }

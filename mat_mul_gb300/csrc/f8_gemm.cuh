@@ -54,6 +54,10 @@ __device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, int *st
     }
 }
 
+__device__ __forceinline__ void copy4(uint32_t dst, const float *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // K-major operand in 128-byte swizzled rows, 8-row groups 1024 bytes apart.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr) {
     uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);

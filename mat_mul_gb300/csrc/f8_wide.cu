@@ -159,10 +159,6 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
                  : "memory");
 }
 
-__device__ __forceinline__ void copy4(uint32_t dst, const float *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-
 // acc[0..1] += (a, b) * (s, s)
 __device__ __forceinline__ void fma2(float &x, float &y, uint32_t a, uint32_t b, float s) {
     asm("{\n\t.reg .b64 p, q, r;\n\t"
@@ -479,7 +475,6 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
                 if (threadIdx.x == 128) *arrived = atomicAdd(P.count + c0 * CG + rank, 1u);
                 named_barrier(1, EPI_THREADS);
                 store = *arrived == static_cast<unsigned>(c1 - c0);
-                named_barrier(1, EPI_THREADS);
                 if (store) {
                     __threadfence();
 #pragma unroll
