@@ -85,8 +85,6 @@ struct Codes {
           s_bytes(static_cast<size_t>(up(qk::f8_blocks(K) * ld_s * 4, 1024))) {}
 };
 
-constexpr size_t COUNT_BYTES = 4096;  // counters: one word per CTA
-
 // The product of one matrix (offsets null) or of E matrices over row groups.
 int product(const void *W, const float *S, int64_t E, int64_t N, int64_t K, int x_type, const void *x, int64_t M,
             int64_t ldx, const int32_t *offsets, const int32_t *rows, int64_t R, int y_type, void *y, int64_t ldy,
@@ -97,24 +95,23 @@ int product(const void *W, const float *S, int64_t E, int64_t N, int64_t K, int 
     const Codes q(R, K);
     char *ws = nullptr;
     const size_t part = qk::f8_part_bytes(R, static_cast<int>(E), false, c.num_sms);
-    if (int rc = qk::f8_workspace(c, st, COUNT_BYTES + q.q_bytes + q.s_bytes + part, reinterpret_cast<void **>(&ws)))
-        return rc;
+    if (int rc = qk::f8_workspace(c, st, q.q_bytes + q.s_bytes + part, reinterpret_cast<void **>(&ws))) return rc;
+    unsigned *count = nullptr;
+    if (int rc = qk::f8_counters(c, st, &count)) return rc;
     qk::F8Quant f = {};
     f.x_type = x_type;
     f.x = x;
     f.M = M;
     f.K = K;
     f.ldx = ldx;
-    f.q = reinterpret_cast<uint8_t *>(ws + COUNT_BYTES);
+    f.q = reinterpret_cast<uint8_t *>(ws);
     f.ld_q = q.ld;
-    f.s = reinterpret_cast<float *>(ws + COUNT_BYTES + q.q_bytes);
+    f.s = reinterpret_cast<float *>(ws + q.q_bytes);
     f.s_row = 1;
     f.s_blk = q.ld_s;
     f.map = rows;
     f.rows_max = R;
     f.count = rows ? offsets + E : nullptr;
-    f.zero = reinterpret_cast<unsigned *>(ws);
-    f.n_zero = c.num_sms;
     f.status = c.status;
     f.dev = c.dev;
     cudaError_t e = qk::launch_f8_quantize(f, st, c.num_sms);
@@ -135,8 +132,8 @@ int product(const void *W, const float *S, int64_t E, int64_t N, int64_t K, int 
     g.y_type = y_type;
     g.y = y;
     g.ldy = ldy;
-    g.part = reinterpret_cast<float *>(ws + COUNT_BYTES + q.q_bytes + q.s_bytes);
-    g.count = f.zero;
+    g.part = reinterpret_cast<float *>(ws + q.q_bytes + q.s_bytes);
+    g.count = count;
     g.status = c.status;
     g.dev = c.dev;
     e = qk::launch_f8_gemm(g, st, c.num_sms);
@@ -282,7 +279,7 @@ int qmm_f8_moe(int x_type, const void *x, int64_t T, int64_t H, int64_t ldx, int
     qk::F8Context c;
     if (int rc = qk::f8_context(c)) return rc;
     if (!qk::f8_available()) return refuse(QMM_ECUDA, "the driver has no tensor map encoder");
-    // workspace: counters | codes and scales of x per row | of h | the rows of
+    // workspace: codes and scales of x per row | of h | the rows of
     // the down product in fp32 | partial tiles
     const Codes qx(R, H), qh(R, I);
     const int64_t ldd = up(H, 4);
@@ -290,12 +287,12 @@ int qmm_f8_moe(int x_type, const void *x, int64_t T, int64_t H, int64_t ldx, int
     const size_t part1 = qk::f8_part_bytes(R, static_cast<int>(E), true, c.num_sms);
     const size_t part2 = qk::f8_part_bytes(R, static_cast<int>(E), false, c.num_sms);
     const size_t part = part1 > part2 ? part1 : part2;
-    char *ws = nullptr;
-    if (int rc = qk::f8_workspace(c, st, 2 * COUNT_BYTES + qx.q_bytes + qx.s_bytes + qh.q_bytes + qh.s_bytes + d_bytes + part,
-                                  reinterpret_cast<void **>(&ws)))
+    char *at = nullptr;
+    if (int rc = qk::f8_workspace(c, st, qx.q_bytes + qx.s_bytes + qh.q_bytes + qh.s_bytes + d_bytes + part,
+                                  reinterpret_cast<void **>(&at)))
         return rc;
-    unsigned *count = reinterpret_cast<unsigned *>(ws);
-    char *at = ws + 2 * COUNT_BYTES;
+    unsigned *count = nullptr;
+    if (int rc = qk::f8_counters(c, st, &count)) return rc;
     uint8_t *xq = reinterpret_cast<uint8_t *>(at);
     float *xs = reinterpret_cast<float *>(at += qx.q_bytes);
     uint8_t *hq = reinterpret_cast<uint8_t *>(at += qx.s_bytes);
@@ -317,8 +314,6 @@ int qmm_f8_moe(int x_type, const void *x, int64_t T, int64_t H, int64_t ldx, int
     f.map = slots;
     f.k = k;
     f.rows_max = R;
-    f.zero = count;
-    f.n_zero = static_cast<int>(2 * COUNT_BYTES / 4);
     f.status = c.status;
     f.dev = c.dev;
     cudaError_t e = qk::launch_f8_quantize(f, st, c.num_sms);
@@ -363,7 +358,6 @@ int qmm_f8_moe(int x_type, const void *x, int64_t T, int64_t H, int64_t ldx, int
     g.y_type = QMM_F32;
     g.y = d;
     g.ldy = ldd;
-    g.count = count + COUNT_BYTES / 4;
     e = qk::launch_f8_gemm(g, st, c.num_sms);
     if (e != cudaSuccess) return cuda_error(e, "down launch");
     qk::count_launches(1);

@@ -391,12 +391,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 named_barrier(1, 256);
                 store = *arrived == static_cast<unsigned>(c1 - c0);
                 if (store) {
+                    if (threadIdx.x == 128) P.count[c0] = 0u;  // zero again for the next launch
                     __threadfence();
 #pragma unroll
                     for (int m = 0; m < NA; ++m)
 #pragma unroll
                         for (int i = 0; i < C::HALF; ++i) acc[m][i] = 0.0f;
-                    for (int c = c0; c <= c1; ++c) {
+                    // (the parts of a few CTAs at a time, so that their loads overlap)
+                    constexpr int U = NA * C::HALF <= 32 ? 32 / (NA * C::HALF) : 1;
+                    for (int c = c0; U == 1 && c <= c1; ++c) {
                         const float *q = P.part + (static_cast<int64_t>(c) * 2 + (c == c0)) * C::PART;
 #pragma unroll
                         for (int m = 0; m < NA; ++m)
@@ -404,6 +407,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                             for (int i = 0; i < C::HALF; ++i)
                                 if (i < mine)
                                     acc[m][i] += __ldcg(q + (m * BT + half * C::HALF + i) * BW + 32 * quarter + lane);
+                    }
+                    for (int c = c0; U > 1 && c <= c1; c += U) {
+                        float v[U][NA][C::HALF];
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const float *q = P.part + (static_cast<int64_t>(c + u) * 2 + (c + u == c0)) * C::PART;
+#pragma unroll
+                            for (int m = 0; m < NA; ++m)
+#pragma unroll
+                                for (int i = 0; i < C::HALF; ++i)
+                                    v[u][m][i] = c + u <= c1 && i < mine
+                                                     ? __ldcg(q + (m * BT + half * C::HALF + i) * BW + 32 * quarter + lane)
+                                                     : 0.0f;
+                        }
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+#pragma unroll
+                            for (int m = 0; m < NA; ++m)
+#pragma unroll
+                                for (int i = 0; i < C::HALF; ++i) acc[m][i] += v[u][m][i];
                     }
                 }
             }

@@ -15,7 +15,7 @@ namespace qk {
 namespace f8 {
 
 constexpr int BK = 128;        // values of K per stage: one scale block
-constexpr int MIN_SHARE = 2;   // least K blocks of cut tiles per CTA
+constexpr int MIN_SHARE = 4;   // least K blocks of cut tiles per CTA
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
     asm volatile(

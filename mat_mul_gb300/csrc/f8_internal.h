@@ -28,7 +28,6 @@ inline int64_t f8_blocks(int64_t n) { return (n + F8_BLOCK - 1) / F8_BLOCK; }
 //   map, k > 0  (scatter)  : x[t] goes to the rows map[t*k .. t*k+k), each in
 //                            [0, rows_max), t < M.
 // An index out of range raises STATUS_INDEX and its row is skipped.
-// zero, n_zero: words the kernel sets to 0 (the product's counters).
 struct F8Quant {
     int x_type;
     const void *x;
@@ -41,8 +40,6 @@ struct F8Quant {
     int k;
     int64_t rows_max;
     const int32_t *count;
-    unsigned *zero;
-    int n_zero;
     int *status;
     int dev;
 };
@@ -72,7 +69,7 @@ struct F8Gemm {
     float *hs;
     int64_t ld_hs;
     float *part;      // f8_part_bytes()
-    unsigned *count;  // one per CTA, zero before the launch
+    unsigned *count;  // one per CTA, zero before the launch and after it (unless a wait ran out)
     int *status;
     int dev;
 };
@@ -127,6 +124,7 @@ struct F8Context {
 };
 int f8_context(F8Context &c);
 int f8_workspace(const F8Context &c, cudaStream_t st, size_t bytes, void **ptr);
+int f8_counters(const F8Context &c, cudaStream_t st, unsigned **ptr);  // num_sms zeroed words
 void clear_error();
 
 }  // namespace qk

@@ -28,22 +28,45 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// Four consecutive values at p (16 / 8-byte aligned).
-template <int T>
-__device__ __forceinline__ void load4(const void *p, float (&v)[4]) {
+// V consecutive values (aligned to their size, at most 16 bytes) as fp32, and
+// the largest |v| as the bits of an fp32.
+template <int T, int V>
+__device__ __forceinline__ uint32_t load_values(const void *p, float (&v)[V]) {
+    uint32_t a = 0;
     if constexpr (T == QMM_F32) {
-        const float4 a = __ldg(static_cast<const float4 *>(p));
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    } else {
-        using E = typename Elem<T>::type;
-        const uint2 a = __ldg(static_cast<const uint2 *>(p));
-        const E *e = reinterpret_cast<const E *>(&a);
+        const float4 q = __ldg(static_cast<const float4 *>(p));
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = to_f32(e[i]);
+        for (int i = 0; i < V; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
+    } else {
+        uint32_t w[V / 2];
+        if constexpr (V == 8) {
+            const uint4 q = __ldg(static_cast<const uint4 *>(p));
+            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        } else {
+            const uint2 q = __ldg(static_cast<const uint2 *>(p));
+            w[0] = q.x, w[1] = q.y;
+        }
+        uint32_t m = 0;  // two 16-bit maxima: |v| in either 16-bit type is in the order of its bits
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+            if constexpr (T == QMM_BF16) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                v[2 * i] = f.x, v[2 * i + 1] = f.y;
+            }
+        }
+        m = max(m & 0xffffu, m >> 16);
+        if constexpr (T == QMM_BF16) a = m << 16;
+        else a = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
     }
+    return a;
 }
 
-__device__ __forceinline__ uint32_t codes4(const float (&v)[4], float inv) {
+__device__ __forceinline__ uint32_t codes4(const float *v, float inv) {
     const float2 a = make_float2(v[0] * inv, v[1] * inv), b = make_float2(v[2] * inv, v[3] * inv);
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
@@ -53,8 +76,7 @@ __device__ __forceinline__ uint32_t codes4(const float (&v)[4], float inv) {
 struct QuantParams {
     const uint8_t *x;
     int64_t M, ldx;
-    int K, kb, groups;  // groups of UNROLL blocks per row
-    int64_t items;      // source rows (or output rows with a gather map) * groups
+    int K, kb, groups;  // blocks of a row, and warp steps that cover them
     uint8_t *q;
     int64_t ld_q;
     float *s;
@@ -63,25 +85,28 @@ struct QuantParams {
     int k;
     int64_t rows_max;
     const int32_t *count;
-    unsigned *zero;
-    int n_zero;
     int *status;
 };
 
 constexpr int QUANT_THREADS = 256;
-constexpr int UNROLL = 4;  // blocks a warp has in flight
+constexpr int UNROLL = 4;  // loads a warp has in flight
 
-// One warp per group of UNROLL blocks of a row, lane i holding values
-// 4i .. 4i+3 of each block.  VEC: rows, K and the base allow 4-value loads
-// and 4-code stores (whole groups of four lie inside or outside the row).
-template <int T, bool VEC>
+// V values per lane and load: 8 (16 lanes per block, two blocks per load; the
+// 16-bit types) or 4 (the whole warp on a block).  One warp takes the
+// UNROLL * 32 * V / 128 blocks of a row that UNROLL loads hold.  The two
+// divisions of a block's scale are done once for all of them, by the lanes
+// that each take one of the warp's blocks, instead of once per block by every
+// lane: at 4 values per lane and a division per block the kernel was bound by
+// instruction issue (8191 x 5120 bf16: 39 us; see the figures at the launch).
+// VEC: rows, K and the bases allow whole groups of V values (inside or outside
+// the row) and of V codes.
+template <int T, int V, bool VEC>
 __global__ void __launch_bounds__(QUANT_THREADS) f8_quantize_kernel(const QuantParams P) {
     using E = typename Elem<T>::type;
+    constexpr int LPB = F8_BLOCK / V, BPL = 32 / LPB;  // lanes per block, blocks per load
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < P.n_zero; i += QUANT_THREADS) P.zero[i] = 0u;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, in_block = lane % LPB;
     const bool gather = P.map && P.k == 0;
     int64_t rows = P.M;
     if (gather) {
@@ -91,7 +116,7 @@ __global__ void __launch_bounds__(QUANT_THREADS) f8_quantize_kernel(const QuantP
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * (QUANT_THREADS / 32) + (threadIdx.x >> 5);
          it < rows * P.groups; it += static_cast<int64_t>(gridDim.x) * (QUANT_THREADS / 32)) {
         const int64_t r = it / P.groups;
-        const int b0 = static_cast<int>(it - r * P.groups) * UNROLL;
+        const int b0 = static_cast<int>(it - r * P.groups) * (UNROLL * BPL) + lane / LPB;  // this lane's first block
         int64_t src = r;
         if (gather) {
             src = __ldg(P.map + r);
@@ -101,33 +126,44 @@ __global__ void __launch_bounds__(QUANT_THREADS) f8_quantize_kernel(const QuantP
             }
         }
         const E *row = reinterpret_cast<const E *>(P.x) + src * P.ldx;
-        float v[UNROLL][4];
+        float v[UNROLL][V];
+        uint32_t a[UNROLL];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            const int c = (b0 + u) * F8_BLOCK + 4 * lane;
-            if constexpr (VEC) {
-                if (c < P.K) {
-                    load4<T>(row + c, v[u]);
-                } else {
-                    v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0.0f;
-                }
+            const int c = (b0 + u * BPL) * F8_BLOCK + V * in_block;
+            a[u] = 0;
+            if (VEC && c < P.K) {
+                a[u] = load_values<T, V>(row + c, v[u]);
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[u][i] = c + i < P.K ? to_f32(row[c + i]) : 0.0f;
+                for (int i = 0; i < V; ++i) {
+                    v[u][i] = !VEC && c + i < P.K ? to_f32(row[c + i]) : 0.0f;
+                    a[u] = max(a[u], __float_as_uint(v[u][i]) & 0x7fffffffu);
+                }
             }
         }
-        uint32_t code[UNROLL];
-        float scale[UNROLL];
+        uint32_t mine = 0;  // lane u of a block's lanes: the maximum of load u
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            uint32_t a = 0;
+            if constexpr (LPB == 32) {
+                a[u] = __reduce_max_sync(0xffffffffu, a[u]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a = max(a, __float_as_uint(v[u][i]) & 0x7fffffffu);
-            a = __reduce_max_sync(0xffffffffu, a);
-            const float s = __fdiv_rn(__uint_as_float(a), 448.0f);
-            scale[u] = s < 1.17549435e-38f ? 1.17549435e-38f : s;  // (keeps a NaN)
-            code[u] = codes4(v[u], __fdiv_rn(1.0f, scale[u]));
+                for (int o = LPB / 2; o > 0; o >>= 1) a[u] = max(a[u], __shfl_xor_sync(0xffffffffu, a[u], o));
+            }
+            if (in_block % UNROLL == u) mine = a[u];
         }
+        float scale = __fdiv_rn(__uint_as_float(mine), 448.0f);
+        scale = scale < 1.17549435e-38f ? 1.17549435e-38f : scale;  // (keeps a NaN)
+        const float inv_mine = __fdiv_rn(1.0f, scale);
+        uint32_t code[UNROLL][V / 4];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const float inv = __shfl_sync(0xffffffffu, inv_mine, (lane & ~(LPB - 1)) + u);
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) code[u][i] = codes4(v[u] + 4 * i, inv);
+        }
+        const int sb = b0 + in_block * BPL;  // the block whose scale this lane stores
         const int copies = P.map && P.k > 0 ? P.k : 1;
         for (int j = 0; j < copies; ++j) {
             int64_t dst = r;
@@ -141,16 +177,19 @@ __global__ void __launch_bounds__(QUANT_THREADS) f8_quantize_kernel(const QuantP
             uint8_t *qr = P.q + dst * P.ld_q;
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u) {
-                const int c = (b0 + u) * F8_BLOCK + 4 * lane;
+                const int c = (b0 + u * BPL) * F8_BLOCK + V * in_block;
                 if constexpr (VEC) {
-                    if (c < P.K) *reinterpret_cast<uint32_t *>(qr + c) = code[u];
+                    if (c < P.K) {
+                        if constexpr (V == 8) *reinterpret_cast<uint2 *>(qr + c) = make_uint2(code[u][0], code[u][1]);
+                        else *reinterpret_cast<uint32_t *>(qr + c) = code[u][0];
+                    }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (c + i < P.K) qr[c + i] = static_cast<uint8_t>(code[u] >> (8 * i));
+                    for (int i = 0; i < V; ++i)
+                        if (c + i < P.K) qr[c + i] = static_cast<uint8_t>(code[u][i / 4] >> (8 * (i % 4)));
                 }
-                if (lane == 0 && b0 + u < P.kb) P.s[dst * P.s_row + (b0 + u) * P.s_blk] = scale[u];
             }
+            if (in_block < UNROLL && sb < P.kb) P.s[dst * P.s_row + sb * P.s_blk] = scale;
         }
     }
 }
@@ -216,15 +255,16 @@ cudaError_t launch_pdl(const void *kern, dim3 grid, dim3 block, void **args, cud
     return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
-template <int T>
-cudaError_t quantize_t(const F8Quant &q, cudaStream_t st, int num_sms) {
+template <int T, int V, bool VEC>
+cudaError_t quantize_v(const F8Quant &q, cudaStream_t st, int num_sms) {
     QuantParams p;
     p.x = static_cast<const uint8_t *>(q.x);
     p.M = q.M;
     p.ldx = q.ldx;
     p.K = static_cast<int>(q.K);
     p.kb = static_cast<int>(f8_blocks(q.K));
-    p.groups = (p.kb + UNROLL - 1) / UNROLL;
+    constexpr int BLOCKS = UNROLL * 32 * V / F8_BLOCK;  // per warp and step
+    p.groups = (p.kb + BLOCKS - 1) / BLOCKS;
     p.q = q.q;
     p.ld_q = q.ld_q;
     p.s = q.s;
@@ -234,25 +274,30 @@ cudaError_t quantize_t(const F8Quant &q, cudaStream_t st, int num_sms) {
     p.k = q.k;
     p.rows_max = q.rows_max;
     p.count = q.count;
-    p.zero = q.zero;
-    p.n_zero = q.n_zero;
     p.status = q.status;
-    p.items = (q.map && q.k == 0 ? q.rows_max : q.M) * p.groups;
-    const int es = f8_size(T);
-    const bool vec = q.K % 4 == 0 && q.ldx % 4 == 0 && q.ld_q % 4 == 0 &&
-                     reinterpret_cast<uintptr_t>(q.x) % (4 * es) == 0 && reinterpret_cast<uintptr_t>(q.q) % 4 == 0;
-    const void *kern = vec ? reinterpret_cast<const void *>(f8_quantize_kernel<T, true>)
-                           : reinterpret_cast<const void *>(f8_quantize_kernel<T, false>);
-    static OncePerDevice ready[2];
-    const cudaError_t e = ready[vec](q.dev, [&] {
-        return vec ? prefer_max_shared(f8_quantize_kernel<T, true>) : prefer_max_shared(f8_quantize_kernel<T, false>);
-    });
+    const int64_t items = (q.map && q.k == 0 ? q.rows_max : q.M) * p.groups;
+    static OncePerDevice ready;
+    const cudaError_t e = ready(q.dev, [] { return prefer_max_shared(f8_quantize_kernel<T, V, VEC>); });
     if (e != cudaSuccess) return e;
-    const int64_t blocks = (p.items + QUANT_THREADS / 32 - 1) / (QUANT_THREADS / 32);
+    const int64_t blocks = (items + QUANT_THREADS / 32 - 1) / (QUANT_THREADS / 32);
     const int64_t cap = static_cast<int64_t>(num_sms) * 8;
     void *args[] = {&p};
-    return launch_pdl(kern, dim3(static_cast<unsigned>(blocks < 1 ? 1 : blocks < cap ? blocks : cap)),
-                      dim3(QUANT_THREADS), args, st);
+    return launch_pdl(reinterpret_cast<const void *>(f8_quantize_kernel<T, V, VEC>),
+                      dim3(static_cast<unsigned>(blocks < 1 ? 1 : blocks < cap ? blocks : cap)), dim3(QUANT_THREADS), args,
+                      st);
+}
+
+// 8 values per lane where 16-byte loads and 8-byte stores are aligned, else 4,
+// else element by element.
+template <int T>
+cudaError_t quantize_t(const F8Quant &q, cudaStream_t st, int num_sms) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(q.x), c = reinterpret_cast<uintptr_t>(q.q);
+    auto fits = [&](int v) {
+        return q.K % v == 0 && q.ldx % v == 0 && q.ld_q % v == 0 && x % (v * f8_size(T)) == 0 && c % v == 0;
+    };
+    if constexpr (T != QMM_F32)
+        if (fits(8)) return quantize_v<T, 8, true>(q, st, num_sms);
+    return fits(4) ? quantize_v<T, 4, true>(q, st, num_sms) : quantize_v<T, 4, false>(q, st, num_sms);
 }
 
 template <int T>

@@ -5,7 +5,7 @@
 // integers (index in expert order on a tie, NaN as -inf, -0 as +0) and takes
 // the largest k times with two warp reductions each.  The pairs are sorted by
 // counting: stable, so the rows of an expert are in token order and the
-// result does not depend on the launch.  Up to TOKENS tokens are one launch of
+// result does not depend on the launch.  Up to FUSED tokens are one launch of
 // one CTA.  More take two: the first leaves a histogram per CTA, and in the
 // second each CTA adds up the histograms before its own.  Bound by latency
 // below a few thousand tokens and by the reading of the logits above.
@@ -20,7 +20,8 @@ namespace qk {
 
 namespace {
 
-constexpr int TOKENS = 128;  // tokens per CTA
+constexpr int TOKENS = 64;  // tokens per CTA when there are several
+constexpr int FUSED = 128;  // most tokens that one CTA sorts by itself
 constexpr int WARPS = 16;
 constexpr int THREADS = 32 * WARPS;
 
@@ -149,14 +150,14 @@ __device__ __forceinline__ int scan_experts(int *cnt, int E, int lane) {
 template <int VPL>
 __global__ void __launch_bounds__(THREADS) route_choose_kernel(const RouteParams P) {
     __shared__ int cnt[QMM_F8_MAX_EXPERTS];
-    __shared__ int chosen[TOKENS * QMM_ROUTE_MAX_K];
+    __shared__ int chosen[FUSED * QMM_ROUTE_MAX_K];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int e = threadIdx.x; e < P.E; e += THREADS) cnt[e] = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * TOKENS;
-    const int nt = static_cast<int>(min(static_cast<int64_t>(TOKENS), P.T - t0));
+    const int nt = P.fused ? static_cast<int>(P.T) : static_cast<int>(min(static_cast<int64_t>(TOKENS), P.T - t0));
     for (int i = warp; i < nt; i += WARPS) {
         const int e = choose<VPL>(P, t0 + i, lane);
         if (lane < P.k) {
@@ -192,15 +193,22 @@ __global__ void __launch_bounds__(THREADS) route_place_kernel(const RouteParams 
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * TOKENS;
     const int n = static_cast<int>(min(static_cast<int64_t>(TOKENS), P.T - t0)) * P.k;
     for (int i = threadIdx.x; i < n; i += THREADS) chosen[i] = P.experts[t0 * P.k + i];
-    const int64_t all = static_cast<int64_t>(gridDim.x) * P.E, mine = static_cast<int64_t>(blockIdx.x) * P.E;
-    for (int64_t i = threadIdx.x; i < all; i += THREADS) {
-        const int h = P.hist[i];
-        if (h) {
-            const int e = static_cast<int>(i % P.E);
-            atomicAdd(cnt + e, h);
-            if (i < mine) atomicAdd(before + e, h);
+    // every thread adds up one expert's column over a share of the CTAs
+    const int wide = min((P.E + 31) & ~31, THREADS), shares = THREADS / wide;
+    const int share = threadIdx.x / wide;
+    if (share < shares)
+        for (int e = threadIdx.x - share * wide; e < P.E; e += wide) {
+            const int32_t *h = P.hist + e;
+            int sum = 0, mine = 0;
+#pragma unroll 8
+            for (int b = share; b < static_cast<int>(gridDim.x); b += shares) {
+                const int v = __ldcg(h + static_cast<int64_t>(b) * P.E);
+                sum += v;
+                mine += b < static_cast<int>(blockIdx.x) ? v : 0;
+            }
+            atomicAdd(cnt + e, sum);
+            atomicAdd(before + e, mine);
         }
-    }
     __syncthreads();
     if (warp == 0) {
         const int total = scan_experts(cnt, P.E, lane);
@@ -241,14 +249,14 @@ cudaError_t launch(Kernel kern, int64_t blocks, RouteParams &p, cudaStream_t st)
 }  // namespace
 
 size_t f8_route_hist_bytes(int64_t T, int E) {
-    return T <= TOKENS ? 0 : static_cast<size_t>((T + TOKENS - 1) / TOKENS) * E * sizeof(int32_t);
+    return T <= FUSED ? 0 : static_cast<size_t>((T + TOKENS - 1) / TOKENS) * E * sizeof(int32_t);
 }
-int f8_route_launches(int64_t T) { return T <= TOKENS ? 1 : 2; }
+int f8_route_launches(int64_t T) { return T <= FUSED ? 1 : 2; }
 
 cudaError_t launch_f8_route(const F8Route &r, cudaStream_t st) {
     RouteParams p = {r.x,      r.T,       r.ldx,     r.x_type,  r.E,    r.k,     r.score, r.normalize,
-                     r.T <= TOKENS, r.factor, r.weights, r.experts, r.offsets, r.rows, r.slots, r.hist};
-    const int64_t blocks = (r.T + TOKENS - 1) / TOKENS;
+                     r.T <= FUSED, r.factor, r.weights, r.experts, r.offsets, r.rows, r.slots, r.hist};
+    const int64_t blocks = p.fused ? 1 : (r.T + TOKENS - 1) / TOKENS;
     static OncePerDevice ready;
     cudaError_t e = ready(r.dev, [] {
         cudaError_t q = prefer_max_shared(route_place_kernel);

@@ -476,6 +476,7 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
                 named_barrier(1, EPI_THREADS);
                 store = *arrived == static_cast<unsigned>(c1 - c0);
                 if (store) {
+                    if (threadIdx.x == 128) P.count[c0 * CG + rank] = 0u;  // zero again for the next launch
                     __threadfence();
 #pragma unroll
                     for (int i = 0; i < OWN; ++i) acc[i] = 0.0f;

@@ -223,6 +223,7 @@ int f8_context(F8Context &c) {
 int f8_workspace(const F8Context &c, cudaStream_t st, size_t bytes, void **ptr) {
     return workspace(c.dev, st, bytes, ptr);
 }
+int f8_counters(const F8Context &c, cudaStream_t st, unsigned **ptr) { return counters(c.dev, st, c.num_sms, ptr); }
 }  // namespace qk
 
 namespace {
@@ -732,6 +733,12 @@ int qmm_device_status(void *stream) {
         if (e != cudaSuccess) return cuda_fail(e, "status clear");
         if (!(word & qk::STATUS_TIMEOUT))
             return fail(QMM_EINDEX, "a row index or an offset was out of range (status word 0x%x)", word);
+        // a launch that gave up may have left completion counters behind
+        e = cudaDeviceSynchronize();
+        std::lock_guard<std::mutex> lk(g_mu);
+        for (auto &c : g_counters)
+            if (e == cudaSuccess && c.first.first == dev && c.second.ptr) e = cudaMemset(c.second.ptr, 0, c.second.bytes);
+        if (e != cudaSuccess) return cuda_fail(e, "counters clear");
         return fail(QMM_ETIMEOUT, "a bounded device wait expired (status word 0x%x)", word);
     }
     return QMM_OK;
