@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int i = 0; i < C::HALF; ++i)
                     if (i < mine) {
                         const float g = acc[0][i];
-                        const float h = n < P.N ? __fdiv_rn(g, 1.0f + expf(-g)) * acc[1][i] : 0.0f;
+                        const float h = n < P.N ? silu(g) * acc[1][i] : 0.0f;
                         acc[0][i] = h;
                         const uint32_t a = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
                         if (lane == 0) amax[quarter * BT + i] = a;

@@ -71,6 +71,12 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// g / (1 + e^-g) with the hardware's exponential and reciprocal: a relative
+// error of a few 2^-24 for g >= 0 and about |g| 2^-24 below, far inside the
+// rounding of h to 8 bits that follows; the exact forms took a third of the
+// gated pair's time (2048 -> 1408, 16372 rows).
+__device__ __forceinline__ float silu(float g) { return g * __fdividef(1.0f, 1.0f + __expf(-g)); }
+
 // A piece of a tile: tokens [row0, row0 + ntok) of expert e against block nblk
 // of weight rows, K blocks [k0, k1).
 struct Piece {

@@ -26,6 +26,7 @@ using namespace f8;
 
 constexpr int TOK = 128;   // tokens per CTA
 constexpr int COLS = 256;  // TMEM columns of a buffer
+constexpr int PIECES = 4;  // pieces the scheduling warp is ahead
 constexpr int BATCH = 4, SC_RING = 3, SC_FLOATS = TOK + 4;  // scales in shared memory
 constexpr int PART = TOK * COLS;              // floats of a partial tile of one CTA
 constexpr long long DRAIN_CYCLES = 1 << 21;   // about a millisecond
@@ -53,7 +54,8 @@ struct Wide {
     static constexpr int OFF_SC = STAGES * STAGE;  // SC_RING batches of BATCH K blocks: xs of the tokens, two of W
     static constexpr int OFF_AMAX = OFF_SC + SC_RING * BATCH * SC_FLOATS * 4;
     static constexpr int OFF_CUM = OFF_AMAX + PARTS * TOK * 4;
-    static constexpr int OFF_ROWS = OFF_CUM + (QMM_F8_MAX_EXPERTS + 4) * 4;
+    static constexpr int OFF_PIECES = OFF_CUM + (QMM_F8_MAX_EXPERTS + 4) * 4;
+    static constexpr int OFF_ROWS = OFF_PIECES + PIECES * 48;
     static constexpr int OFF_BAR = OFF_ROWS + EPI * ROWS_BYTES;
     static constexpr int SMEM = OFF_BAR + 512 + 1024;
     static_assert(SMEM <= 232448, "shared memory");
@@ -239,6 +241,12 @@ __device__ __forceinline__ void store_tile(uint8_t *buf, int lane, const float (
     }
 }
 
+// A piece of work, and when it is part of a cut tile the CTAs (or pairs) that
+// share the tile (else c0 < 0).
+struct Cut {
+    int e, nblk, row0, ntok, k0, k1, c0, c1;
+};
+
 template <int CG, bool DUAL>
 __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
     f8_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2,
@@ -256,6 +264,8 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
     const uint32_t full = bar, empty = full + 8 * C::STAGES;
     const uint32_t d_full = empty + 8 * C::STAGES, d_empty = d_full + 16, done = d_empty + 16;
     const uint32_t sc_full = done + 8, sc_empty = sc_full + 8 * SC_RING;
+    const uint32_t pc_full = sc_empty + 8 * SC_RING, pc_empty = pc_full + 8 * PIECES;
+    int4 *pieces = reinterpret_cast<int4 *>(smem + C::OFF_PIECES);  // three words of 16 bytes each
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 480);
     volatile unsigned *arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 488);
     int *cum = reinterpret_cast<int *>(smem + C::OFF_CUM);
@@ -272,6 +282,10 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
         for (int s = 0; s < SC_RING; ++s) {
             mbar_init(sc_full + 8 * s, 32);
             mbar_init(sc_empty + 8 * s, EPI);
+        }
+        for (int s = 0; s < PIECES; ++s) {
+            mbar_init(pc_full + 8 * s, 1);
+            mbar_init(pc_empty + 8 * s, 2 + (rank == 0) + EPI);  // copies, scales, MMA, epilogue warps
         }
         mbar_init(done, 1);
         fence_mbar_init();
@@ -294,18 +308,26 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    Schedule sch;
-    sch.cum = cum;
-    sch.offsets = P.offsets;
-    sch.E = P.E;
-    sch.R = P.R;
-    sch.kb = P.kb;
-    sch.nb = P.tiles_n;
-    sch.G = static_cast<int>(gridDim.x) / CG;
-    sch.c = static_cast<int>(blockIdx.x) / CG;
-    sch.step = TOK * CG;
-    sch.init();
-    Piece p;
+    // The next piece, from the scheduling warp: the arithmetic that finds it
+    // (divisions, a search over the experts, reads of the offsets) is done ahead
+    // of the roles and out of their registers.  False after the last one, or
+    // when the wait ran out.  With `whole_warp` the caller's lanes are together
+    // and the first arrives for them.
+    Cut p;
+    int np = 0;
+    auto next_piece = [&](bool whole_warp) -> bool {
+        const int s = np % PIECES;
+        bool ok = mbar_spin(pc_full + 8 * s, (np / PIECES) & 1, P.status);
+        if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        const int4 a = pieces[3 * s], b = pieces[3 * s + 1], c = pieces[3 * s + 2];
+        p.row0 = a.x, p.ntok = a.y, p.nblk = a.z, p.e = a.w;
+        p.k0 = b.x, p.k1 = b.y, p.c0 = b.z, p.c1 = b.w;
+        if (whole_warp) __syncwarp();
+        if (!whole_warp || lane == 0) mbar_arrive(pc_empty + 8 * s);
+        ++np;
+        return c.x != 0;
+    };
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_LOW));
@@ -316,7 +338,7 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
             bool ok = true;
             pdl_wait();
             pdl_trigger();
-            while (ok && sch.next(p)) {
+            while (ok && next_piece(false)) {
                 const int tok = p.row0 + rank * TOK;
                 // weight rows of this CTA: all 256, or its half of them
                 const int w0 = p.e * P.N + p.nblk * (DUAL ? 128 : 256);
@@ -355,7 +377,7 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
             int it = 0;
             bool ok = true;
             const uint32_t idesc = (1u << 4) | ((COLS >> 3) << 17) | ((TOK * CG >> 4) << 24);
-            while (ok && sch.next(p)) {
+            while (ok && next_piece(false)) {
                 for (int k = p.k0; k < p.k1; ++k, ++it) {
                     const int s = it % C::STAGES, d = it & 1;
                     if (!mbar_spin(full + 8 * s, (it / C::STAGES) & 1, P.status) ||
@@ -379,7 +401,7 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
             pdl_wait();
             int ib = 0;
             bool ok = true;
-            while (ok && sch.next(p)) {
+            while (ok && next_piece(true)) {
                 const int tok = rank * TOK;
                 const int last = max(p.ntok - 1 - tok, 0);
                 const float *w = P.Ws + (static_cast<int64_t>(p.e) * P.nb + (DUAL ? p.nblk : 2 * p.nblk)) * P.kb;
@@ -402,6 +424,31 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if (warp == 3 && elect_one()) {
+            Schedule sch;
+            sch.cum = cum;
+            sch.offsets = P.offsets;
+            sch.E = P.E;
+            sch.R = P.R;
+            sch.kb = P.kb;
+            sch.nb = P.tiles_n;
+            sch.G = static_cast<int>(gridDim.x) / CG;
+            sch.c = static_cast<int>(blockIdx.x) / CG;
+            sch.step = TOK * CG;
+            sch.init();
+            for (int n = 0;; ++n) {
+                Piece q = {};
+                const bool more = sch.next(q);
+                int c0 = -1, c1 = -1;
+                if (more && q.k1 - q.k0 < P.kb) sch.sharers(q.tile, c0, c1);
+                const int s = n % PIECES;
+                if (n >= PIECES && !mbar_spin(pc_empty + 8 * s, ((n / PIECES) - 1) & 1, P.status)) break;
+                pieces[3 * s] = make_int4(q.row0, q.ntok, q.nblk, q.e);
+                pieces[3 * s + 1] = make_int4(q.k0, q.k1, c0, c1);
+                pieces[3 * s + 2] = make_int4(more, 0, 0, 0);
+                mbar_arrive(pc_full + 8 * s);
+                if (!more) break;
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_HIGH));
@@ -414,7 +461,7 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
         pdl_wait();
         int it = 0, ib = 0;
         bool ok = true;
-        while (ok && sch.next(p)) {
+        while (ok && next_piece(true)) {
             float acc[OWN];
 #pragma unroll
             for (int i = 0; i < OWN; ++i) acc[i] = 0.0f;
@@ -461,10 +508,9 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
             // that gave up, so that none is left at a barrier alone
             if (named_barrier_or(1, EPI_THREADS, !ok)) break;
             bool store = true;
-            if (p.k1 - p.k0 < P.kb) {
+            if (p.c0 >= 0) {
                 // a part of a cut tile, [groups of 4 columns][128 tokens]
-                int c0, c1;
-                sch.sharers(p.tile, c0, c1);
+                const int c0 = p.c0, c1 = p.c1;
                 const int mine = part * (OWN / 4) * TOK + t;
                 float4 *q = reinterpret_cast<float4 *>(P.part + (static_cast<int64_t>(blockIdx.x) * 2 + (p.k0 == 0)) * PART) + mine;
 #pragma unroll
@@ -514,7 +560,7 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < HC; ++i) {
                     const float g = acc[i];
-                    const float h = n0 + i < P.N ? __fdiv_rn(g, 1.0f + expf(-g)) * acc[HC + i] : 0.0f;
+                    const float h = n0 + i < P.N ? silu(g) * acc[HC + i] : 0.0f;
                     acc[i] = h;
                     a = max(a, __float_as_uint(h) & 0x7fffffffu);
                 }
