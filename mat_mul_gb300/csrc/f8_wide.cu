@@ -42,9 +42,9 @@ struct Wide {
     static constexpr int EPI = 4 * PARTS, EPI_THREADS = 32 * EPI, THREADS = 128 + EPI_THREADS;
     static constexpr int OWN = COLS / PARTS;  // accumulators per thread
     // registers per thread at launch, and after the split between the first
-    // four warps and the epilogue (a pair's copies and MMAs need fewer)
+    // four warps and the epilogue
     static constexpr int REGS = DUAL ? 96 : 168;
-    static constexpr int REGS_LOW = DUAL ? 32 : CG == 2 ? 24 : 56, REGS_HIGH = DUAL ? 112 : CG == 2 ? 240 : 224;
+    static constexpr int REGS_LOW = DUAL ? 32 : 56, REGS_HIGH = DUAL ? 112 : 224;
     static_assert(128 * REGS_LOW + EPI_THREADS * REGS_HIGH <= THREADS * REGS, "register split");
     static constexpr int CHUNKS = DUAL ? 2 : 4;              // 16-byte chunks of a row that go to memory together
     static constexpr int ROWS_BYTES = 32 * 16 * CHUNKS;      // a warp's rows on their way to memory
@@ -138,27 +138,6 @@ __device__ __forceinline__ void arrive_cluster(uint32_t a) {
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(a));
-}
-__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                   "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
 }
 
 // acc[0..1] += (a, b) * (s, s)
@@ -480,14 +459,23 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
                     ok = __all_sync(0xffffffffu, mbar_spin(d_full + 8 * d, (it >> 1) & 1, P.status));
                     if (!ok) break;
                     tc_fence_after();
-                    // 32 columns at a time (the gated pair: first half gate, second half up)
-                    constexpr int NC = OWN / 32;
+                    // 16 columns at a time, the next ones on their way meanwhile (the
+                    // gated pair: first half gate, second half up)
+                    constexpr int NC = OWN / 16;
+                    const uint32_t base = my_tmem + d * COLS;
+                    auto column = [](int c) { return 16 * c + (DUAL && c >= NC / 2 ? 128 - OWN / 2 : 0); };
+                    uint32_t r[2][16];
+                    tmem_ld(base, r[0]);
+                    tmem_wait(r[0]);
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        uint32_t r[32];
-                        tmem_ld32(my_tmem + d * COLS + 32 * c + (DUAL && c >= NC / 2 ? 128 - OWN / 2 : 0), r);
-                        tmem_wait32(r);
-                        if (c == NC - 1) {
+                        if (c + 1 < NC) tmem_ld(base + column(c + 1), r[(c + 1) & 1]);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2)
+                            fma2(acc[16 * c + j], acc[16 * c + j + 1], r[c & 1][j], r[c & 1][j + 1],
+                                 f[DUAL && c >= NC / 2 ? NA - 1 : 0]);
+                        if (c + 1 < NC) tmem_wait(r[(c + 1) & 1]);
+                        if (c == NC - 2) {
                             // everything is out of this buffer
                             tc_fence_before();
                             __syncwarp();
@@ -496,9 +484,6 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
                                 else mbar_arrive(d_empty + 8 * d);
                             }
                         }
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2)
-                            fma2(acc[32 * c + j], acc[32 * c + j + 1], r[j], r[j + 1], f[DUAL && c >= NC / 2 ? NA - 1 : 0]);
                     }
                 }
                 __syncwarp();
