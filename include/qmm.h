@@ -284,7 +284,8 @@ QMM_API int qmm_f8_quantize(int x_type, const void *x, int64_t M, int64_t K, int
  * Accuracy against the f64 value of that formula, before the rounding to
  * y's type: |dy| <= 2^-17 * sum_b |sx S| * sum_k |qx code|.
  * Results do not depend on timing: repeated calls agree bit for bit.
- * Two launches (quantiser, product); uses the per-(device, stream) workspace
+ * Two launches (quantiser, product), or one for a few rows (at most 16, fewer
+ * for large matrices: the product quantises x itself, to the same codes); uses the per-(device, stream) workspace
  * of qmm (make one call of the largest size before graph capture).
  * K == 0 writes y = 0.  M*N below 2^31 tiles of 16 x 128.
  */

@@ -92,51 +92,58 @@ int product(const void *W, const float *S, int64_t E, int64_t N, int64_t K, int 
     qk::F8Context c;
     if (int rc = qk::f8_context(c)) return rc;
     if (!qk::f8_available()) return refuse(QMM_ECUDA, "the driver has no tensor map encoder");
-    const Codes q(R, K);
+    // workspace: codes and scales of x (unless the product quantises x itself) |
+    // partial tiles
+    const bool fuse = !offsets && qk::f8_fuses(R, N, K, c.num_sms);
+    const Codes q(fuse ? 0 : R, K);
     char *ws = nullptr;
     const size_t part = qk::f8_part_bytes(R, static_cast<int>(E), false, c.num_sms);
     if (int rc = qk::f8_workspace(c, st, q.q_bytes + q.s_bytes + part, reinterpret_cast<void **>(&ws))) return rc;
-    unsigned *count = nullptr;
-    if (int rc = qk::f8_counters(c, st, &count)) return rc;
-    qk::F8Quant f = {};
-    f.x_type = x_type;
-    f.x = x;
-    f.M = M;
-    f.K = K;
-    f.ldx = ldx;
-    f.q = reinterpret_cast<uint8_t *>(ws);
-    f.ld_q = q.ld;
-    f.s = reinterpret_cast<float *>(ws + q.q_bytes);
-    f.s_row = 1;
-    f.s_blk = q.ld_s;
-    f.map = rows;
-    f.rows_max = R;
-    f.count = rows ? offsets + E : nullptr;
-    f.status = c.status;
-    f.dev = c.dev;
-    cudaError_t e = qk::launch_f8_quantize(f, st, c.num_sms);
-    if (e != cudaSuccess) return cuda_error(e, "quantize launch");
-    qk::count_launches(1);
     qk::F8Gemm g = {};
+    if (int rc = qk::f8_counters(c, st, &g.count)) return rc;
+    if (fuse) {
+        g.x_type = x_type;
+        g.x = x;
+        g.ldx = ldx;
+    } else {
+        qk::F8Quant f = {};
+        f.x_type = x_type;
+        f.x = x;
+        f.M = M;
+        f.K = K;
+        f.ldx = ldx;
+        f.q = reinterpret_cast<uint8_t *>(ws);
+        f.ld_q = q.ld;
+        f.s = reinterpret_cast<float *>(ws + q.q_bytes);
+        f.s_row = 1;
+        f.s_blk = q.ld_s;
+        f.map = rows;
+        f.rows_max = R;
+        f.count = rows ? offsets + E : nullptr;
+        f.status = c.status;
+        f.dev = c.dev;
+        const cudaError_t e = qk::launch_f8_quantize(f, st, c.num_sms);
+        if (e != cudaSuccess) return cuda_error(e, "quantize launch");
+        qk::count_launches(1);
+        g.xq = f.q;
+        g.ld_q = q.ld;
+        g.xs = f.s;
+        g.ld_s = q.ld_s;
+    }
     g.W = static_cast<const uint8_t *>(W);
     g.Ws = S;
     g.E = static_cast<int>(E);
     g.N = N;
     g.K = K;
-    g.xq = f.q;
-    g.ld_q = q.ld;
-    g.xs = f.s;
-    g.ld_s = q.ld_s;
     g.offsets = offsets;
     g.R = R;
     g.y_type = y_type;
     g.y = y;
     g.ldy = ldy;
     g.part = reinterpret_cast<float *>(ws + q.q_bytes + q.s_bytes);
-    g.count = count;
     g.status = c.status;
     g.dev = c.dev;
-    e = qk::launch_f8_gemm(g, st, c.num_sms);
+    const cudaError_t e = qk::launch_f8_gemm(g, st, c.num_sms);
     if (e != cudaSuccess) return cuda_error(e, "product launch");
     qk::count_launches(1);
     return QMM_OK;

@@ -41,27 +41,32 @@ using namespace f8;
 constexpr int BW = 128;
 constexpr int THREADS = 384;
 constexpr int SC_STAGES = 4;
+constexpr int FUSE_BLOCKS = 40;  // most K blocks per CTA with FUSE
+constexpr int FUSE_WARPS = 10, FUSE_ITEMS = 8;  // warps 2 .. 11 quantise, eight (block, row) items each
 constexpr int SMEM_MAX = 232448;
 
-template <int BT, bool DUAL>
+template <int BT, bool DUAL, bool FUSE>
 struct Cfg {
     static constexpr int NA = DUAL ? 2 : 1;            // weight matrices per tile
     // K blocks per step: every wait and hand-over of a step costs the roles a
     // few hundred cycles, about what a 16 KB weight block takes to arrive
-    static constexpr int KS = BT <= (DUAL ? 32 : 64) ? 2 : 1;
+    static constexpr int KS = BT == 16 && !DUAL && !FUSE ? 4 : BT <= (DUAL ? 32 : 64) ? 2 : 1;
     static constexpr int XBOX = BT < 64 ? BT : 64;     // rows per token copy
     static constexpr int W_BYTES = BW * BK, X_BYTES = BT * BK;
-    static constexpr int BLOCK = NA * W_BYTES + X_BYTES, STAGE = KS * BLOCK;
+    static constexpr int BLOCK = NA * W_BYTES + (FUSE ? 0 : X_BYTES), STAGE = KS * BLOCK;
     static constexpr int SC_FLOATS = BT + 4;           // a K block's scales: of the tokens, of the weights
     static constexpr int SC_BYTES = KS * SC_FLOATS * 4;
     static constexpr int HALF = BT / 2;                // token columns per epilogue warp
     static constexpr int CH = HALF < 16 ? HALF : 16;   // columns per TMEM load
     static constexpr int AMAX_BYTES = DUAL ? 4 * BT * 4 : 0;
     static constexpr int CUM_BYTES = (QMM_F8_MAX_EXPERTS + 4) * 4;
-    static constexpr int FIXED = SC_STAGES * SC_BYTES + AMAX_BYTES + CUM_BYTES + 512 + 1024;
+    // FUSE: the codes and the scales of every K block the CTA needs
+    static constexpr int OWN_X = FUSE ? FUSE_BLOCKS * X_BYTES : 0, OWN_SC = FUSE ? FUSE_BLOCKS * SC_FLOATS * 4 : 0;
+    static constexpr int FIXED = OWN_X + OWN_SC + SC_STAGES * SC_BYTES + AMAX_BYTES + CUM_BYTES + 512 + 1024;
     static constexpr int FIT = (SMEM_MAX - FIXED) / STAGE;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;
-    static constexpr int OFF_SC = STAGES * STAGE;
+    static constexpr int OFF_X = STAGES * STAGE, OFF_XS = OFF_X + OWN_X;
+    static constexpr int OFF_SC = OFF_XS + OWN_SC;
     static constexpr int OFF_AMAX = OFF_SC + SC_STAGES * SC_BYTES;
     static constexpr int OFF_CUM = OFF_AMAX + AMAX_BYTES;
     static constexpr int OFF_BAR = OFF_CUM + CUM_BYTES;
@@ -71,7 +76,8 @@ struct Cfg {
     static constexpr int PART = NA * BT * BW;          // floats of a partial tile
     static_assert(STAGES >= 3 && SMEM <= SMEM_MAX, "shared memory");
     static_assert(TMEM_COLS <= 512, "tensor memory");
-    static_assert(8 * (2 * STAGES + 2 * SC_STAGES + 5) + 32 <= 480, "barrier area");
+    static_assert(8 * (2 * STAGES + 2 * SC_STAGES + 6) <= 480, "barrier area");
+    static_assert(!FUSE || (BT == 16 && !DUAL), "FUSE: one tile of tokens, one matrix");
 };
 
 struct Params {
@@ -89,6 +95,9 @@ struct Params {
     float *part;
     unsigned *count;
     int *status;
+    const void *x;  // with FUSE
+    int x_type, x_vec, K;
+    int64_t ldx;
     int stop;  // the first CTA issues no copy from this step on (failure test hook)
 };
 
@@ -111,11 +120,101 @@ __device__ __forceinline__ void store_y(void *y, int type, int64_t i, float v) {
     else static_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
 }
 
-template <int BT, bool DUAL>
+// Four values of x from element c of row r (zeros past K).
+__device__ __forceinline__ void load_x4(const Params &P, int r, int c, float (&v)[4]) {
+    v[0] = v[1] = v[2] = v[3] = 0.0f;
+    if (c >= P.K) return;  // (K is a multiple of 16)
+    const int64_t at = r * P.ldx + c;
+    if (P.x_type == QMM_F32) {
+        const float *x = static_cast<const float *>(P.x) + at;
+        if (P.x_vec) {
+            const float4 a = *reinterpret_cast<const float4 *>(x);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = x[i];
+        }
+        return;
+    }
+    const uint16_t *x = static_cast<const uint16_t *>(P.x) + at;
+    uint32_t a, b;
+    if (P.x_vec) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(x);
+        a = u.x, b = u.y;
+    } else {
+        a = x[0] | static_cast<uint32_t>(x[1]) << 16;
+        b = x[2] | static_cast<uint32_t>(x[3]) << 16;
+    }
+    if (P.x_type == QMM_F16) {
+        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+        const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+        v[0] = p.x, v[1] = p.y, v[2] = q.x, v[3] = q.y;
+    } else {
+        v[0] = __uint_as_float(a << 16), v[1] = __uint_as_float(a & 0xffff0000u);
+        v[2] = __uint_as_float(b << 16), v[3] = __uint_as_float(b & 0xffff0000u);
+    }
+}
+
+// FUSE: the codes of this CTA's K blocks, block b (in the order of its pieces)
+// to codes + b * 2048 in the swizzled rows the MMA reads, its scales to
+// sc + b * pitch (rows, then the scale of W).  Each warp takes up to eight
+// (block, row) items, all of them in flight at once; the same arithmetic as
+// f8_quantize.cu, so the codes are the same.
+__device__ __forceinline__ void quantise_own(const Params &P, const Schedule &s, uint8_t *codes, float *sc, int pitch,
+                                             int warp, int lane) {
+    const int cut = s.u1 - s.u;
+    const int blocks = cut + (s.whole > s.c ? (s.whole - 1 - s.c) / s.G + 1 : 0) * s.kb;
+    const int items = blocks * P.R, i0 = warp * FUSE_ITEMS;  // (at most FUSE_WARPS * FUSE_ITEMS: see f8_fuses)
+    auto block_k = [&](int b) { return b < cut ? (s.u + b) % s.kb : (b - cut) % s.kb; };
+    // lane g: block and row of item g (the divisions once per item)
+    const int i = min(i0 + lane, items - 1), block = i / P.R, row = i - block * P.R, kblk = block_k(block);
+    float v[FUSE_ITEMS][4];
+#pragma unroll
+    for (int g = 0; g < FUSE_ITEMS; ++g) {
+        const int r = __shfl_sync(0xffffffffu, row, g), k = __shfl_sync(0xffffffffu, kblk, g);
+        if (i0 + g < items) load_x4(P, r, k * BK + 4 * lane, v[g]);
+    }
+    for (int b = warp * 32 + lane; b < blocks; b += FUSE_WARPS * 32) {
+        const int tile = b < cut ? s.whole + (s.u + b) / s.kb : s.c + (b - cut) / s.kb * s.G;
+        sc[b * pitch + 16] = __ldg(P.Ws + static_cast<int64_t>(tile) * s.kb + block_k(b));  // (one tile of tokens)
+    }
+    uint32_t mine = 0;  // lane g: the largest |x| of item g
+#pragma unroll
+    for (int g = 0; g < FUSE_ITEMS; ++g) {
+        if (i0 + g >= items) break;
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(v[g][j]) & 0x7fffffffu);
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == g) mine = m;
+    }
+    float scale = __fdiv_rn(__uint_as_float(mine), 448.0f);
+    scale = scale < 1.17549435e-38f ? 1.17549435e-38f : scale;
+    const float inv_mine = __fdiv_rn(1.0f, scale);
+    if (lane < FUSE_ITEMS && i0 + lane < items) sc[block * pitch + row] = scale;
+#pragma unroll
+    for (int g = 0; g < FUSE_ITEMS; ++g) {
+        if (i0 + g >= items) break;
+        const float inv = __shfl_sync(0xffffffffu, inv_mine, g);
+        const int b = __shfl_sync(0xffffffffu, block, g), t = __shfl_sync(0xffffffffu, row, g);
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[g][0] * inv, v[g][1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[g][2] * inv, v[g][3] * inv), __NV_SATFINITE, __NV_E4M3);
+        *reinterpret_cast<uint32_t *>(codes + b * (16 * BK) + t * BK + ((4 * lane) ^ ((t & 7) << 4))) = lo | hi << 16;
+    }
+    // the MMA reads shared memory through the asynchronous proxy
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// FUSE (few rows of one matrix): the kernel quantises x itself, each CTA the K
+// blocks it needs, while its weights stream in: one launch instead of two (13 x
+// 5120 x 1024 from the host 10.4 instead of 14.5 us a call; on the GPU alone 10.0
+// against 9.1, 1 x 4096 x 14336 14.6 against 13.9).  Only where every warp's
+// items are loaded at once: 16 x 4096 x 14336 in five turns took 26 against 14.
+template <int BT, bool DUAL, bool FUSE>
 __global__ void __launch_bounds__(THREADS, 1)
     f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2,
                    const __grid_constant__ CUtensorMap tmX, const Params P) {
-    using C = Cfg<BT, DUAL>;
+    using C = Cfg<BT, DUAL, FUSE>;
     constexpr int NA = C::NA, KS = C::KS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -126,7 +225,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t full = bar, empty = full + 8 * C::STAGES;
     const uint32_t sc_full = empty + 8 * C::STAGES, sc_empty = sc_full + 8 * SC_STAGES;
     const uint32_t d_full = sc_empty + 8 * SC_STAGES, d_empty = d_full + 16;
-    const uint32_t done = d_empty + 16;
+    const uint32_t done = d_empty + 16, x_ready = done + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 480);
     volatile unsigned *arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 488);
     int *cum = reinterpret_cast<int *>(smem + C::OFF_CUM);
@@ -145,6 +244,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(d_empty + 8 * s, 8);
         }
         mbar_init(done, 1);
+        mbar_init(x_ready, FUSE_WARPS);
         fence_mbar_init();
     }
     if (warp == 3) {
@@ -178,9 +278,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp == 0) {
         if (elect_one()) {
-            // Copies.  The weights of the first steps are asked for before the
-            // launch in front is done (it writes only the codes and scales of x),
-            // so that they stream in while x is quantised.
+            // Copies.  The launch in front is the quantiser, which writes only the
+            // codes and scales of x, so the weights of the first steps are asked
+            // for before it is done.  With FUSE it may be any launch: until it is
+            // done the weights are brought as far as L2, which is safe whatever
+            // it writes.
             int stop = NO_STOP;
             if (blockIdx.x == 0 && P.stop != NO_STOP) {  // the failure test hook: at the latest the last step is left out
                 Schedule all = sch;
@@ -193,13 +295,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int kc = min(KS, q.k1 - k), wrow = q.e * P.N + q.nblk * BW;
                 const int boxes = (q.ntok + C::XBOX - 1) / C::XBOX;
                 const uint32_t st = stage0 + s * C::STAGE, b = full + 8 * s;
-                mbar_arrive_expect_tx(b, kc * (NA * C::W_BYTES + boxes * C::XBOX * BK));
+                mbar_arrive_expect_tx(b, kc * (NA * C::W_BYTES + (FUSE ? 0 : boxes * C::XBOX * BK)));
                 for (int j = 0; j < kc; ++j) {
                     tma_2d(st + j * C::BLOCK, &tmW, (k + j) * BK, wrow, b);
                     if constexpr (DUAL) tma_2d(st + j * C::BLOCK + C::W_BYTES, &tmW2, (k + j) * BK, wrow, b);
                 }
             };
-            {
+            if constexpr (FUSE) {
+                Schedule first = sch;
+                while (first.next(p))
+                    for (int k = p.k0; k < p.k1; ++k) prefetch_2d(&tmW, k * BK, p.nblk * BW);
+            } else {
                 Schedule first = sch;
                 while (early < C::STAGES && early < stop && first.next(p))
                     for (int k = p.k0; k < p.k1 && early < C::STAGES && early < stop; k += KS, ++early) weights(p, k, early);
@@ -216,6 +322,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         break;
                     }
                     if (it >= early) weights(p, k, s);
+                    if constexpr (FUSE) continue;
                     const uint32_t st = stage0 + s * C::STAGE + NA * C::W_BYTES, b = full + 8 * s;
                     const int kc = min(KS, p.k1 - k);
                     for (int j = 0; j < kc; ++j)
@@ -229,12 +336,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 1) {
         if (elect_one()) {
-            int it = 0;
-            bool ok = true;
+            int it = 0, blk = 0;
+            bool ok = !FUSE || mbar_spin(x_ready, 0, P.status);
             while (ok && sch.next(p)) {
                 const uint32_t cols = (p.ntok + 15) & ~15;
                 const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((BW >> 4) << 24);
-                for (int k = p.k0; k < p.k1; k += KS, ++it) {
+                for (int k = p.k0; k < p.k1; blk += min(KS, p.k1 - k), k += KS, ++it) {
                     const int s = it % C::STAGES, d = it & 1;
                     if (!mbar_spin(full + 8 * s, (it / C::STAGES) & 1, P.status) ||
                         (it >= 2 && !mbar_spin(d_empty + 8 * d, ((it >> 1) - 1) & 1, P.status))) {
@@ -246,7 +353,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int j = 0; j < KS; ++j) {
                         if (k + j >= p.k1) break;
                         const uint32_t st = stage0 + s * C::STAGE + j * C::BLOCK;
-                        const uint64_t b = smem_desc(st + NA * C::W_BYTES);
+                        const uint64_t b =
+                            smem_desc(FUSE ? stage0 + C::OFF_X + (blk + j) * C::X_BYTES : st + NA * C::W_BYTES);
 #pragma unroll
                         for (int m = 0; m < NA; ++m) {
                             const uint64_t a = smem_desc(st + m * C::W_BYTES);
@@ -261,7 +369,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             mma_commit(done);
         }
-    } else if (warp == 2) {
+    } else if (!FUSE && warp == 2) {
         // Scales of a step, by asynchronous copies straight into shared memory.
         pdl_wait();
         int it = 0;
@@ -286,12 +394,19 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp >= 4) {
+    } else if (FUSE || warp >= 4) {
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + half * C::HALF;
         pdl_wait();
-        int it = 0;
+        if constexpr (FUSE) {
+            quantise_own(P, sch, smem + C::OFF_X, reinterpret_cast<float *>(smem + C::OFF_XS), C::SC_FLOATS, warp - 2, lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_ready);
+        }
+        int it = 0, blk = 0;
         bool ok = true;
+        if constexpr (FUSE) ok = __all_sync(0xffffffffu, mbar_spin(x_ready, 0, P.status));
+        if (FUSE && warp < 4) ok = false;  // (warps 2 and 3 only quantise)
         while (ok && sch.next(p)) {
             float acc[NA][C::HALF];
 #pragma unroll
@@ -299,14 +414,15 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < C::HALF; ++i) acc[m][i] = 0.0f;
             const int mine = min(C::HALF, p.ntok - half * C::HALF);  // this warp's token columns (may be <= 0)
-            for (int k = p.k0; k < p.k1; k += KS, ++it) {
+            for (int k = p.k0; k < p.k1; blk += min(KS, p.k1 - k), k += KS, ++it) {
                 const int d = it & 1, s = it % SC_STAGES;
-                ok = mbar_spin(sc_full + 8 * s, (it / SC_STAGES) & 1, P.status) &&
+                ok = (FUSE || mbar_spin(sc_full + 8 * s, (it / SC_STAGES) & 1, P.status)) &&
                      mbar_spin(d_full + 8 * d, (it >> 1) & 1, P.status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const float *sc = reinterpret_cast<const float *>(smem + C::OFF_SC + s * C::SC_BYTES);
+                const float *sc = reinterpret_cast<const float *>(smem + (FUSE ? C::OFF_XS + blk * C::SC_FLOATS * 4
+                                                                               : C::OFF_SC + s * C::SC_BYTES));
                 if (mine > 0) {
 #pragma unroll
                     for (int j = 0; j < KS; ++j) {
@@ -337,7 +453,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(d_empty + 8 * d);
-                    mbar_arrive(sc_empty + 8 * s);
+                    if (!FUSE) mbar_arrive(sc_empty + 8 * s);
                 }
             }
             // every epilogue warp passes here once per piece, also after a wait
@@ -449,12 +565,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-template <int BT, bool DUAL>
+template <int BT, bool DUAL, bool FUSE = false>
 cudaError_t launch_bt(const F8Gemm &g, cudaStream_t st, int num_sms) {
-    using C = Cfg<BT, DUAL>;
+    using C = Cfg<BT, DUAL, FUSE>;
     CUtensorMap tw = {}, tw2 = {}, tx = {};
     if (!encode_rows(&tw, g.W, g.E * g.N, g.K, g.K, BW) || (DUAL && !encode_rows(&tw2, g.W2, g.E * g.N, g.K, g.K, BW)) ||
-        !encode_rows(&tx, g.xq, g.R, g.K, g.ld_q, C::XBOX))
+        (!FUSE && !encode_rows(&tx, g.xq, g.R, g.K, g.ld_q, C::XBOX)))
         return cudaErrorInvalidValue;
     Params p = {};
     p.Ws = g.Ws;
@@ -477,9 +593,16 @@ cudaError_t launch_bt(const F8Gemm &g, cudaStream_t st, int num_sms) {
     p.part = g.part;
     p.count = g.count;
     p.status = g.status;
+    if (FUSE) {
+        p.x = g.x;
+        p.x_type = g.x_type;
+        p.ldx = g.ldx;
+        p.K = static_cast<int>(g.K);
+        p.x_vec = g.ldx % 4 == 0 && reinterpret_cast<uintptr_t>(g.x) % (4 * f8_size(g.x_type)) == 0;
+    }
     p.stop = inject_stop_stage();
     static OncePerDevice ready;
-    const cudaError_t e = ready(g.dev, [] { return set_smem_attrs(f8_gemm_kernel<BT, DUAL>, C::SMEM); });
+    const cudaError_t e = ready(g.dev, [] { return set_smem_attrs(f8_gemm_kernel<BT, DUAL, FUSE>, C::SMEM); });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
@@ -491,32 +614,43 @@ cudaError_t launch_bt(const F8Gemm &g, cudaStream_t st, int num_sms) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, f8_gemm_kernel<BT, DUAL>, tw, tw2, tx, p);
+    return cudaLaunchKernelEx(&cfg, f8_gemm_kernel<BT, DUAL, FUSE>, tw, tw2, tx, p);
 }
 
 // Tokens per tile: the mean rows of a group, rounded up to a tile width.
 int tile_tokens(int64_t R, int E) {
     const int64_t mean = (R + E - 1) / E;
     int bt = 16;
-    while (bt < mean && bt < 128) bt *= 2;
+    while (bt < mean && bt < 64) bt *= 2;
     return bt;
 }
 
-// Which kernel: 0 this one, 1 f8_wide.cu on single CTAs, 2 on pairs.
+// Which kernel: 0 this one, 1 f8_wide.cu on single CTAs, 2 on pairs.  Measured
+// (bf16, us):
+//   one matrix of 5120 x 5120 / 14336 x 4096 (rows: this, single, pair)
+//     64: 22 28 26 / 23 27 29   96: 34 29 27 / 35 27 30   129: 33 28 26 / 44 31 30
+//     384: 42 29 30 / 69 38 42  1024: 77 40 39 / 147 69 65
+//   32 experts of 2816 x 2048 / the layer of 2048 x 1408 (mean rows: this, single)
+//     16: 40 41 / 69 77   32: 47 44 / 87 83   64: 68 52 / 139 97
+// A pair works on 256 rows at once, so an odd number of 128s costs it half a
+// tile per column of tiles.
 int path_of(int64_t R, int E) {
     const int64_t mean = (R + E - 1) / E;
-    if (mean <= 128) return 0;
-    return E == 1 || mean > 1024 ? 2 : 1;
+    if (mean <= (E == 1 ? 64 : 24)) return 0;
+    if (E > 1) return mean > 1024 ? 2 : 1;
+    const int64_t t = (R + 127) / 128;
+    return t > 8 || t % 2 == 0 ? 2 : 1;
 }
 
 template <bool DUAL>
 cudaError_t launch_any(const F8Gemm &g, cudaStream_t st, int num_sms) {
     if (const int w = path_of(g.R, g.E)) return launch_f8_wide(g, w == 2, st, num_sms);
+    if constexpr (!DUAL)
+        if (!g.xq) return launch_bt<16, false, true>(g, st, num_sms);
     switch (tile_tokens(g.R, g.E)) {
     case 16: return launch_bt<16, DUAL>(g, st, num_sms);
     case 32: return launch_bt<32, DUAL>(g, st, num_sms);
-    case 64: return launch_bt<64, DUAL>(g, st, num_sms);
-    default: return launch_bt<128, DUAL>(g, st, num_sms);
+    default: return launch_bt<64, DUAL>(g, st, num_sms);
     }
 }
 
@@ -525,6 +659,17 @@ cudaError_t launch_any(const F8Gemm &g, cudaStream_t st, int num_sms) {
 size_t f8_part_bytes(int64_t R, int E, bool dual, int num_sms) {
     if (path_of(R, E)) return f8_wide_part_bytes(num_sms);
     return static_cast<size_t>(num_sms) * 2 * (dual ? 2 : 1) * tile_tokens(R, E) * BW * sizeof(float);
+}
+
+bool f8_fuses(int64_t R, int64_t N, int64_t K, int num_sms) {
+    if (R > 16 || R < 1) return false;
+    // the K blocks of the CTA that has most (see Schedule)
+    const int64_t tiles = f8_blocks(N), kb = f8_blocks(K), G = num_sms;
+    const int64_t whole = tiles % G == 0 ? tiles : tiles > G ? (tiles / G - 1) * G : 0;
+    const int64_t units = (tiles - whole) * kb, share = (units + MIN_SHARE - 1) / MIN_SHARE;
+    const int64_t sharing = share < G ? share : G;
+    const int64_t blocks = whole / G * kb + (sharing ? (units + sharing - 1) / sharing : 0);
+    return blocks <= FUSE_BLOCKS && blocks * R <= FUSE_WARPS * FUSE_ITEMS;
 }
 
 bool f8_available() { return tensor_map_encoder() != nullptr; }

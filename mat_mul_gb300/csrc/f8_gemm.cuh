@@ -25,6 +25,13 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int
         : "memory");
 }
 
+// Bring a box into L2.
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap *map, int c0, int c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1)
+                 : "memory");
+}
+
 // One lane of a converged warp, the same one each time.  The compiler knows
 // that a branch on it holds one thread, and feeds the tensor-core and copy
 // instructions their uniform registers directly: behind "lane == 0" four MMAs

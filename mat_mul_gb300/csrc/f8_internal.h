@@ -72,7 +72,12 @@ struct F8Gemm {
     unsigned *count;  // one per CTA, zero before the launch and after it (unless a wait ran out)
     int *status;
     int dev;
+    // xq null (where f8_fuses): one matrix and few rows, quantised by the product
+    int x_type;
+    const void *x;
+    int64_t ldx;
 };
+bool f8_fuses(int64_t R, int64_t N, int64_t K, int num_sms);
 size_t f8_part_bytes(int64_t R, int E, bool dual, int num_sms);
 bool f8_available();
 // The product with the tokens as TMEM lanes (f8_wide.cu), on single CTAs or on

@@ -95,11 +95,35 @@ def test_product_shapes(cuda_lib, M, N, K):
         x, xv = _as(_x(rng, M, K), dtype)
         before = cuda_lib.qmm_launch_count()
         y = cuda_lib.qmm_f8(_t(W), _t(S), x)
-        assert cuda_lib.qmm_launch_count() - before == 2
+        assert cuda_lib.qmm_launch_count() - before == (1 if M <= 16 else 2)
         assert cuda_lib.qmm_device_status() == 0
         assert str(y.dtype) == "torch." + dtype and tuple(y.shape) == (M, N)
         want, A = R.product(W, S, xv)
         _close(_np(y), want, R.bound(K, A), dtype, f"{M}x{N}x{K} {dtype}")
+
+
+@pytest.mark.parametrize("M,N,K,launches", [(1, 14336, 4096, 1), (6, 5120, 5120, 1), (13, 5120, 5120, 2),
+                                            (1, 25600, 4096, 2), (16, 5120, 17408, 2), (5, 17408, 17408, 2),
+                                            (100, 14336, 4096, 2), (64, 5120, 5120, 2), (300, 14336, 1024, 2)])
+def test_product_full_size_matrices(cuda_lib, M, N, K, launches):
+    """Matrices of the size a model has, on sampled columns: few rows with x quantised inside the product and, above
+    the size it can do that for, in front of it."""
+    import torch
+    rng = np.random.default_rng(N + K + M)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    W = torch.randint(0, 0x70, (N, K), generator=g, device="cuda", dtype=torch.uint8)
+    W |= torch.randint(0, 2, (N, K), generator=g, device="cuda", dtype=torch.uint8) << 7
+    S = torch.rand(-(-N // 128), -(-K // 128), generator=g, device="cuda") * 1e-3
+    x, xv = _as(_x(rng, M, K), "bfloat16")
+    before = cuda_lib.qmm_launch_count()
+    y = cuda_lib.qmm_f8(W, S, x, dtype=torch.float32)
+    assert cuda_lib.qmm_launch_count() - before == launches
+    assert cuda_lib.qmm_device_status() == 0
+    blocks = np.unique(np.concatenate([[0, -(-N // 128) - 1], rng.integers(0, -(-N // 128), 6)]))
+    for b in blocks:
+        n = slice(128 * b, min(128 * b + 128, N))
+        want, A = R.product(W[n].cpu().numpy(), S[b:b + 1].cpu().numpy(), xv)
+        _close(_np(y[:, n]), want, R.bound(K, A), "float32", f"block {b}")
 
 
 @pytest.mark.parametrize("xt,yt", [(a, b) for a in TYPES for b in TYPES if a != b])
