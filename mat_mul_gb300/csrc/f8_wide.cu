@@ -3,19 +3,28 @@
 //
 // Here the tokens are the M operand (TMEM lanes) and 256 weight rows the
 // columns, 256 rows of one matrix or 128 of gate and 128 of up.  A thread of
-// the epilogue owns one token, and its 128 columns lie in one scale block of W
-// (two of 64 for the gated pair): the factor xs * Ws of a K block is a scalar
-// per thread, read once, and the K blocks go from TMEM into fp32 registers at
-// one packed fma per two values without touching shared memory, which the
-// operands of the MMA need for themselves.
+// the epilogue owns one token, and its columns lie in one scale block of W (of
+// each matrix, for the gated pair): the factor xs * Ws of a K block is a scalar
+// per thread and the block goes from TMEM into fp32 registers at one packed fma
+// per two values, while in f8_gemm.cu every column has its own factor in shared
+// memory, which the operands of the MMA need for themselves (4096 x 5120 x 17408:
+// 776 us there with 256 token columns, 290 here).
 //
 // With CG = 2 a pair of CTAs works on 256 tokens x 256 columns with one
 // cta_group::2 MMA: each loads its own 128 tokens and half of the weight rows,
-// so the copies and the reads of W are halved.
+// so the copies of W are halved.
 //
-// Warp roles: 0 = copies, 1 = MMA issue (of the pair's first CTA), 2 = idle,
-// 3 = tensor memory, 4..11 = epilogue (TMEM lanes 32*(w%4), columns of half
-// (w-4)/4).  Schedule, cut tiles and waits as in f8_gemm.cu.
+// What bounds it: the two TMEM buffers of 256 columns.  A buffer's round is the
+// MMA of a K block (512 cycles), its commit, the epilogue's reading of it (about
+// 300 cycles for 128 columns per warp) and the hand-back; waits on a completed
+// barrier alone cost 100 to 200 cycles each, so a K block takes about 800 cycles
+// and the tensor pipe is busy about 60 % of them.  Stores of a finished tile are
+// another 6 %.
+//
+// Warp roles: 0 = copies, 1 = MMA issue (of the pair's first CTA), 2 = scales,
+// 3 = schedule (and tensor memory), then the epilogue (warp w: TMEM lanes
+// 32*(w%4), columns of part (w-4)/4).  Schedule of the tiles, cut tiles and
+// bounded waits as in f8_gemm.cu.
 #include "f8_gemm.cuh"
 
 namespace qk {
@@ -34,10 +43,10 @@ constexpr long long DRAIN_CYCLES = 1 << 21;   // about a millisecond
 template <int CG, bool DUAL>
 struct Wide {
     // Epilogue warps per TMEM lane quarter (each has its share of the columns)
-    // and the registers they get.  Two warps of 128 accumulators measured
-    // faster than four of 64 for one matrix, slower for the gated pair, whose
-    // rounding needs more registers beside them (4093 tokens, 32 experts: 327
-    // against 304 us).
+    // and the registers they get.  Two warps of 128 accumulators per thread
+    // measured faster than four of 64 for one matrix (8192 rows of 40 experts 95
+    // against 103 us), slower for the gated pair, whose rounding needs more
+    // registers beside them (4093 tokens, 32 experts: 327 against 304 us).
     static constexpr int PARTS = DUAL ? 4 : 2;
     static constexpr int EPI = 4 * PARTS, EPI_THREADS = 32 * EPI, THREADS = 128 + EPI_THREADS;
     static constexpr int OWN = COLS / PARTS;  // accumulators per thread

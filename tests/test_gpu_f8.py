@@ -443,6 +443,19 @@ def test_moe_bad_slots_are_reported(cuda_lib):
     assert cuda_lib.qmm_device_status() == 0
 
 
+def test_example_layer_agrees_with_grouped_products(cuda_lib):
+    """The layer against its parts: bf16 rounding of the result (2^-9 of it) and of h, whose codes (2^-4 apart) differ
+    where the two SiLUs fall on different sides of a boundary: rarely, so far below 1 % of the norm."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "f8_expert_layer.py")
+    spec = importlib.util.spec_from_file_location("f8_expert_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    for args in ((1, 8, 2, 256, 128), (64, 32, 4, 512, 272), (700, 5, 2, 384, 256)):
+        assert example.main(*args) < 1e-2
+
+
 # ---------------------------------------------------------------------------
 # Failure detection and refusals
 # ---------------------------------------------------------------------------
