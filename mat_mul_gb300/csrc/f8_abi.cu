@@ -97,7 +97,7 @@ int product(const void *W, const float *S, int64_t E, int64_t N, int64_t K, int 
     const bool fuse = !offsets && qk::f8_fuses(R, N, K, c.num_sms);
     const Codes q(fuse ? 0 : R, K);
     char *ws = nullptr;
-    const size_t part = qk::f8_part_bytes(R, static_cast<int>(E), false, c.num_sms);
+    const size_t part = qk::f8_part_bytes(R, static_cast<int>(E), N, false, offsets != nullptr, c.num_sms);
     if (int rc = qk::f8_workspace(c, st, q.q_bytes + q.s_bytes + part, reinterpret_cast<void **>(&ws))) return rc;
     qk::F8Gemm g = {};
     if (int rc = qk::f8_counters(c, st, &g.count)) return rc;
@@ -291,8 +291,8 @@ int qmm_f8_moe(int x_type, const void *x, int64_t T, int64_t H, int64_t ldx, int
     const Codes qx(R, H), qh(R, I);
     const int64_t ldd = up(H, 4);
     const size_t d_bytes = static_cast<size_t>(up(R * ldd * 4, 1024));
-    const size_t part1 = qk::f8_part_bytes(R, static_cast<int>(E), true, c.num_sms);
-    const size_t part2 = qk::f8_part_bytes(R, static_cast<int>(E), false, c.num_sms);
+    const size_t part1 = qk::f8_part_bytes(R, static_cast<int>(E), I, true, true, c.num_sms);
+    const size_t part2 = qk::f8_part_bytes(R, static_cast<int>(E), H, false, true, c.num_sms);
     const size_t part = part1 > part2 ? part1 : part2;
     char *at = nullptr;
     if (int rc = qk::f8_workspace(c, st, qx.q_bytes + qx.s_bytes + qh.q_bytes + qh.s_bytes + d_bytes + part,

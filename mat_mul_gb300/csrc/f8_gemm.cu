@@ -49,7 +49,8 @@ using namespace f8;
 constexpr int BW = 128;
 constexpr int THREADS = 384;
 constexpr int SC_STAGES = 4;
-constexpr int FUSE_BLOCKS = 40;  // most K blocks per CTA with FUSE
+constexpr int LEAST = 4;  // K blocks of cut tiles per CTA (13 x 5120 x 1024: with two 10.1 us, four 9.3, sixteen 12.7)
+constexpr int FUSE_BLOCKS = 8;   // most K blocks per CTA with FUSE
 constexpr int FUSE_WARPS = 10, FUSE_ITEMS = 8;  // warps 2 .. 11 quantise, eight (block, row) items each
 constexpr int SMEM_MAX = 232448;
 
@@ -282,6 +283,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     sch.G = static_cast<int>(gridDim.x);
     sch.c = static_cast<int>(blockIdx.x);
     sch.step = 0;
+    sch.least = LEAST;
     sch.init();
     Piece p;
 
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < C::HALF; ++i) acc[m][i] = 0.0f;
                     // (the parts of a few CTAs at a time, so that their loads overlap)
-                    constexpr int U = NA * C::HALF <= 32 ? 32 / (NA * C::HALF) : 1;
+                    constexpr int U = NA * C::HALF <= 64 ? 64 / (NA * C::HALF) : 1;
                     for (int c = c0; U == 1 && c <= c1; ++c) {
                         const float *q = P.part + (static_cast<int64_t>(c) * 2 + (c == c0)) * C::PART;
 #pragma unroll
@@ -635,27 +637,26 @@ int tile_tokens(int64_t R, int E) {
 }
 
 // Which kernel: 0 this one, 1 f8_wide.cu on single CTAs, 2 on pairs.  Measured
-// (bf16, us):
-//   one matrix of 5120 x 5120 / 14336 x 4096 (rows: this, single, pair)
-//     64: 22 28 26 / 23 27 29   96: 34 29 27 / 35 27 30   129: 33 28 26 / 44 31 30
-//     384: 42 29 30 / 69 38 42  1024: 77 40 39 / 147 69 65
-//   32 experts of 2816 x 2048 / the layer of 2048 x 1408 (mean rows: this, single)
-//     16: 40 41 / 69 77   32: 47 44 / 87 83   64: 68 52 / 139 97
-// A pair works on 256 rows at once, so an odd number of 128s costs it half a
-// tile per column of tiles.
-int path_of(int64_t R, int E) {
-    const int64_t mean = (R + E - 1) / E;
-    if (mean <= (E == 1 ? 64 : 24)) return 0;
-    if (E > 1) return mean > 1024 ? 2 : 1;
-    const int64_t t = (R + 127) / 128;
-    return t > 8 || t % 2 == 0 ? 2 : 1;
+// (bf16, us; this, single, pair):
+//   one matrix of 5120 x 5120: 64 rows 15 22 20, 128 rows 19 23 21, 192 rows 20 21 21,
+//     256 rows 27 21 21, 1024 rows 77 39 38
+//   of 14336 x 4096: 64 rows 17 21 20, 96 rows 26 20 20, 1024 rows 146 55 52
+//   32 experts of 2816 x 2048 (mean rows): 8 22 26 31, 16 32 29 38, 32 43 38 41,
+//     128 92 49 60; 4 experts, 2048: 146 59 64
+//   32 expert layers of 2048 x 1408: 8 41 49 59, 16 55 58 75, 32 75 67 78, 128 185 92 110
+// So this one for as many rows of one matrix as its tiles fit the GPU once (at
+// least 64), else pairs; for row groups single CTAs from a mean of 25 rows, whose
+// ragged ends a pair's 256 rows would waste.
+int path_of(int64_t R, int E, int64_t N, bool grouped, int num_sms) {
+    if (grouped) return (R + E - 1) / E <= 24 ? 0 : 1;
+    return R <= 64 || (R <= 192 && (R + 63) / 64 * f8_blocks(N) <= num_sms) ? 0 : 2;
 }
 
 template <bool DUAL>
 cudaError_t launch_any(const F8Gemm &g, cudaStream_t st, int num_sms) {
-    if (const int w = path_of(g.R, g.E)) return launch_f8_wide(g, w == 2, st, num_sms);
     if constexpr (!DUAL)
         if (!g.xq) return launch_bt<16, false, true>(g, st, num_sms);
+    if (const int w = path_of(g.R, g.E, g.N, g.offsets != nullptr, num_sms)) return launch_f8_wide(g, w == 2, st, num_sms);
     switch (tile_tokens(g.R, g.E)) {
     case 16: return launch_bt<16, DUAL>(g, st, num_sms);
     case 32: return launch_bt<32, DUAL>(g, st, num_sms);
@@ -665,19 +666,19 @@ cudaError_t launch_any(const F8Gemm &g, cudaStream_t st, int num_sms) {
 
 }  // namespace
 
-size_t f8_part_bytes(int64_t R, int E, bool dual, int num_sms) {
-    if (path_of(R, E)) return f8_wide_part_bytes(num_sms);
+size_t f8_part_bytes(int64_t R, int E, int64_t N, bool dual, bool grouped, int num_sms) {
+    if (path_of(R, E, N, grouped, num_sms)) return f8_wide_part_bytes(num_sms);
     return static_cast<size_t>(num_sms) * 2 * (dual ? 2 : 1) * tile_tokens(R, E) * BW * sizeof(float);
 }
 
 bool f8_fuses(int64_t R, int64_t N, int64_t K, int num_sms) {
     if (R > 16 || R < 1) return false;
     // the K blocks of the CTA that has most (see Schedule)
-    const int64_t tiles = f8_blocks(N), kb = f8_blocks(K), G = num_sms;
-    const int64_t whole = tiles % G == 0 ? tiles : tiles > G ? (tiles / G - 1) * G : 0;
-    const int64_t units = (tiles - whole) * kb, share = (units + MIN_SHARE - 1) / MIN_SHARE;
-    const int64_t sharing = share < G ? share : G;
-    const int64_t blocks = whole / G * kb + (sharing ? (units + sharing - 1) / sharing : 0);
+    const int tiles = static_cast<int>(f8_blocks(N)), kb = static_cast<int>(f8_blocks(K));
+    int whole, units, sharing;
+    Schedule::plan(tiles, kb, num_sms, LEAST, whole, units, sharing);
+    const int64_t blocks = static_cast<int64_t>((whole + num_sms - 1) / num_sms) * kb +
+                           (sharing ? (units + sharing - 1) / sharing : 0);
     return blocks <= FUSE_BLOCKS && blocks * R <= FUSE_WARPS * FUSE_ITEMS;
 }
 

@@ -15,7 +15,7 @@ namespace qk {
 namespace f8 {
 
 constexpr int BK = 128;        // values of K per stage: one scale block
-constexpr int MIN_SHARE = 4;   // least K blocks of cut tiles per CTA
+constexpr int CUT_COST = 32;   // see Schedule::plan
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
     asm volatile(
@@ -126,19 +126,34 @@ struct Schedule {
     const int *cum;  // shared memory: tiles before expert e, [E + 1]
     const int32_t *offsets;
     int E, R, kb, nb, G, c;
+    int least;           // K blocks of cut tiles that a CTA has at least
     int step;            // tokens per tile; 0: the rows of an expert split evenly over its tiles
     int tiles, whole;    // tiles [0, whole) go round the CTAs uncut
     int units, sharing;  // K blocks of the cut tiles, and the CTAs that share them
     int u, u1;           // this CTA's of them, counted from tile `whole`
     int next_whole;
 
+    // Which tiles are cut, and how.  Handing partial tiles over costs a CTA about
+    // as much as CUT_COST K blocks, so
+    // - tiles for half of the CTAs or fewer: each among G / tiles CTAs, nobody
+    //   with parts of two tiles;
+    // - else, when the last round would leave CTAs idle for longer than that: the
+    //   tiles of the last round and of the full one before it (so that a cut tile
+    //   has two or three parts) are shared out evenly over all CTAs;
+    // - else none.
+    __host__ __device__ static void plan(int tiles, int kb, int G, int least, int &whole, int &units, int &sharing) {
+        const int last = tiles % G;
+        if (2 * tiles <= G) whole = 0;
+        else if (last == 0 || static_cast<int64_t>(kb) * (G - last) <= static_cast<int64_t>(CUT_COST) * G) whole = tiles;
+        else whole = tiles > G ? (tiles / G - 1) * G : 0;
+        units = (tiles - whole) * kb;
+        const int most = (kb + least - 1) / least;  // parts of a tile
+        if (2 * tiles <= G) sharing = tiles * (G / max(tiles, 1) < most ? G / max(tiles, 1) : most);
+        else sharing = G < units ? G : units;
+    }
     __device__ __forceinline__ void init() {
         tiles = cum[E];
-        // A whole round is kept uncut; the last full round joins the rest, so
-        // that a cut tile has two or three parts.
-        whole = tiles % G == 0 ? tiles : tiles > G ? (tiles / G - 1) * G : 0;
-        units = (tiles - whole) * kb;
-        sharing = min(G, (units + MIN_SHARE - 1) / MIN_SHARE);
+        plan(tiles, kb, G, least, whole, units, sharing);
         u = c < sharing ? static_cast<int>(static_cast<int64_t>(units) * c / sharing) : 0;
         u1 = c < sharing ? static_cast<int>(static_cast<int64_t>(units) * (c + 1) / sharing) : 0;
         next_whole = c;

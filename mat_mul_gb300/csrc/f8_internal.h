@@ -78,7 +78,7 @@ struct F8Gemm {
     int64_t ldx;
 };
 bool f8_fuses(int64_t R, int64_t N, int64_t K, int num_sms);
-size_t f8_part_bytes(int64_t R, int E, bool dual, int num_sms);
+size_t f8_part_bytes(int64_t R, int E, int64_t N, bool dual, bool grouped, int num_sms);
 bool f8_available();
 // The product with the tokens as TMEM lanes (f8_wide.cu), on single CTAs or on
 // pairs; launch_f8_gemm takes it for groups of many rows.

@@ -35,6 +35,7 @@ using namespace f8;
 
 constexpr int TOK = 128;   // tokens per CTA
 constexpr int COLS = 256;  // TMEM columns of a buffer
+constexpr int LEAST = 4;   // K blocks of cut tiles per CTA
 constexpr int PIECES = 4;  // pieces the scheduling warp is ahead
 constexpr int BATCH = 4, SC_RING = 3, SC_FLOATS = TOK + 4;  // scales in shared memory
 constexpr int PART = TOK * COLS;              // floats of a partial tile of one CTA
@@ -423,6 +424,7 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
             sch.G = static_cast<int>(gridDim.x) / CG;
             sch.c = static_cast<int>(blockIdx.x) / CG;
             sch.step = TOK * CG;
+            sch.least = LEAST;
             sch.init();
             for (int n = 0;; ++n) {
                 Piece q = {};

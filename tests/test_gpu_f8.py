@@ -102,7 +102,7 @@ def test_product_shapes(cuda_lib, M, N, K):
         _close(_np(y), want, R.bound(K, A), dtype, f"{M}x{N}x{K} {dtype}")
 
 
-@pytest.mark.parametrize("M,N,K,launches", [(1, 14336, 4096, 1), (6, 5120, 5120, 1), (13, 5120, 5120, 2),
+@pytest.mark.parametrize("M,N,K,launches", [(1, 14336, 4096, 2), (6, 1024, 5120, 1), (13, 5120, 5120, 2),
                                             (1, 25600, 4096, 2), (16, 5120, 17408, 2), (5, 17408, 17408, 2),
                                             (100, 14336, 4096, 2), (64, 5120, 5120, 2), (300, 14336, 1024, 2)])
 def test_product_full_size_matrices(cuda_lib, M, N, K, launches):
