@@ -425,7 +425,9 @@ def qmm_route(logits, k, score="softmax", normalize=True, factor=1.0, stream=Non
     n = k if k > 0 else 0
     ft, device, empty, i32 = f.ftype(logits.dtype, "logits"), logits.device, f.empty, f.int32
     weights = empty((T, n), dtype=f.float32, device=device)
-    experts, slots = empty((2, T, n), dtype=i32, device=device).unbind(0)
+    # (five allocations: views of one buffer cost more than twice as much)
+    experts = empty((T, n), dtype=i32, device=device)
+    slots = empty((T, n), dtype=i32, device=device)
     rows = empty(T * n, dtype=i32, device=device)
     offsets = empty(E + 1, dtype=i32, device=device)
     rc = f.lib.qmm_route(ft, logits.data_ptr(), T, E, ld, k, _SCORES[score], 1 if normalize else 0, factor,
