@@ -282,12 +282,13 @@ QMM_API int qmm_f8_quantize(int x_type, const void *x, int64_t M, int64_t K, int
  * the inner sums on the fp8 tensor cores (exact products, fp32 accumulation
  * over the 128 terms), the outer one in fp32, rounded once to y's type.
  * Accuracy against the f64 value of that formula, before the rounding to
- * y's type: |dy| <= 2^-17 * sum_b |sx S| * sum_k |qx code|.
+ * y's type: |dy| <= (2^-16 + (ceil(K/128) + 3) 2^-24) * sum_b |sx S| * sum_k
+ * |qx code|, whatever the order of the 128 additions; measured 9e-8 of y's norm.
  * Results do not depend on timing: repeated calls agree bit for bit.
  * Two launches (quantiser, product), or one for a few rows (at most 16, fewer
  * for large matrices: the product quantises x itself, to the same codes); uses the per-(device, stream) workspace
  * of qmm (make one call of the largest size before graph capture).
- * K == 0 writes y = 0.  M*N below 2^31 tiles of 16 x 128.
+ * K == 0 writes y = 0.  (M/16 + 1) * ceil(N/128) below 2^31.
  */
 QMM_API int qmm_f8(const void *W, const float *S, int64_t N, int64_t K, int x_type, const void *x, int64_t M,
                    int64_t ldx, int y_type, void *y, int64_t ldy, void *stream);

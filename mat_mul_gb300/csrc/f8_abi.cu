@@ -253,7 +253,7 @@ int qmm_route(int x_type, const void *logits, int64_t T, int64_t E, int64_t ldx,
                            static_cast<int32_t *>(hist), c.dev};
     const cudaError_t e = qk::launch_f8_route(r, st);
     if (e != cudaSuccess) return cuda_error(e, "route launch");
-    qk::count_launches(qk::f8_route_launches(T));
+    qk::count_launches(qk::f8_route_launches(T, static_cast<int>(E)));
     return QMM_OK;
 }
 

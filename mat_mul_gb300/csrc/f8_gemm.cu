@@ -21,18 +21,18 @@
 // lanes of a token are exactly one scale block of h.
 //
 // A tile is 128 weight rows x up to BT tokens.  The grid is one CTA per SM.
-// Whole rounds of tiles go round the CTAs; the tiles that would leave the last
-// round partly empty (all of them when they are fewer than the CTAs) are cut
-// along K so that every CTA has the same number of K blocks.  The CTAs that
+// Whole rounds of tiles go round the CTAs; where the last round would leave too
+// many CTAs idle for too long its tiles are cut along K (Schedule::plan).  The CTAs that
 // share a tile put their fp32 partial tiles into the workspace, and the last
 // one to arrive adds them in K order and stores: no CTA waits for another,
 // and the order of the sum does not depend on which one is last.
 //
 // Measured out of HBM (bf16, a row of calls on different matrices): 1 x 4096 x
-// 14336 17.7 us, 1 x 5120 x 17408 22.4 us, 64 rows of 64 experts of 2048 x 1536
-// (41 of them in use) 27.7 us: about 9 us, the launches and the start and end of
-// the pipeline, plus the weights at 6.6 TB/s.  What bounds it below about 100 MB
-// is therefore latency: the launch, the first weights, then per step the hand-over
+// 14336 14.8 us (4.0 TB/s of the 59 MB, 0.59 of the measured copy rate), 1 x 5120
+// x 17408 19.1 us (4.7 TB/s), 64 rows of 64 experts of 2048 x 1536 (41 of them in
+// use) 26.9 us (4.8 TB/s): about 6 us, the launches and the start and end of the
+// pipeline, plus the weights at 6.8 TB/s.  What bounds it below about 100 MB is
+// therefore latency: the launch, the first weights, then per step the hand-over
 // from the copies to the MMA to the epilogue, and the sum over the CTAs of a tile.
 //
 // Warp roles: 0 = copies (TMA, 128-byte swizzle), 1 = MMA issue, 2 = scales,
@@ -215,11 +215,13 @@ __device__ __forceinline__ void quantise_own(const Params &P, const Schedule &s,
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// FUSE (few rows of one matrix): the kernel quantises x itself, each CTA the K
-// blocks it needs, while its weights stream in: one launch instead of two (13 x
-// 5120 x 1024 from the host 10.4 instead of 14.5 us a call; on the GPU alone 10.0
-// against 9.1, 1 x 4096 x 14336 14.6 against 13.9).  Only where every warp's
-// items are loaded at once: 16 x 4096 x 14336 in five turns took 26 against 14.
+// FUSE (few rows of a small matrix): the kernel quantises x itself, each CTA the K
+// blocks it needs: one launch instead of two, which is what counts where the
+// host's launches take longer than the GPU's work (13 x 5120 x 1024 10.4 instead
+// of 14.5 us a call; on the GPU alone 10.1 against 9.1).  Not where the weights
+// take longer than the quantiser's launch, ahead of which they are asked for (1 x
+// 4096 x 14336 out of HBM 18.2 against 14.6), and only where every warp's items
+// are loaded at once (16 x 4096 x 14336 in five turns took 26 against 14).
 template <int BT, bool DUAL, bool FUSE>
 __global__ void __launch_bounds__(THREADS, 1)
     f8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2,

@@ -99,7 +99,7 @@ struct F8Route {
     int dev;
 };
 size_t f8_route_hist_bytes(int64_t T, int E);
-int f8_route_launches(int64_t T);
+int f8_route_launches(int64_t T, int E);
 cudaError_t launch_f8_route(const F8Route &r, cudaStream_t st);
 
 // y[t] = sum_j w[t*k+j] * d[slots[t*k+j]] in j order, d [R][ldd] fp32; slots

@@ -7,7 +7,8 @@
 // counting: stable, so the rows of an expert are in token order and the
 // result does not depend on the launch.  Up to FUSED tokens are one launch of
 // one CTA.  More take two: the first leaves a histogram per CTA, and in the
-// second each CTA adds up the histograms before its own.  Bound by latency
+// second each CTA adds up the histograms before its own (for many tokens and
+// experts a launch in between does that once).  Bound by latency
 // below a few thousand tokens and by the reading of the logits above.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -28,7 +29,7 @@ constexpr int THREADS = 32 * WARPS;
 struct RouteParams {
     const void *x;
     int64_t T, ldx;
-    int x_type, E, k, score, normalize, fused, tokens;  // tokens per CTA
+    int x_type, E, k, score, normalize, fused, tokens, scanned;  // tokens per CTA; the histograms are running sums
     float factor;
     float *weights;
     int32_t *experts, *offsets, *rows, *slots, *hist;
@@ -193,22 +194,30 @@ __global__ void __launch_bounds__(THREADS) route_place_kernel(const RouteParams 
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * P.tokens;
     const int n = static_cast<int>(min(static_cast<int64_t>(P.tokens), P.T - t0)) * P.k;
     for (int i = threadIdx.x; i < n; i += THREADS) chosen[i] = P.experts[t0 * P.k + i];
-    // every thread adds up one expert's column over a share of the CTAs
-    const int wide = min((P.E + 31) & ~31, THREADS), shares = THREADS / wide;
-    const int share = threadIdx.x / wide;
-    if (share < shares)
-        for (int e = threadIdx.x - share * wide; e < P.E; e += wide) {
-            const int32_t *h = P.hist + e;
-            int sum = 0, mine = 0;
-#pragma unroll 8
-            for (int b = share; b < static_cast<int>(gridDim.x); b += shares) {
-                const int v = __ldcg(h + static_cast<int64_t>(b) * P.E);
-                sum += v;
-                mine += b < static_cast<int>(blockIdx.x) ? v : 0;
-            }
-            atomicAdd(cnt + e, sum);
-            atomicAdd(before + e, mine);
+    if (P.scanned) {
+        // the columns are summed up already: the totals follow the last CTA's row
+        for (int e = threadIdx.x; e < P.E; e += THREADS) {
+            cnt[e] = P.hist[static_cast<int64_t>(gridDim.x) * P.E + e];
+            before[e] = P.hist[static_cast<int64_t>(blockIdx.x) * P.E + e];
         }
+    } else {
+        // every thread adds up one expert's column over a share of the CTAs
+        const int wide = min((P.E + 31) & ~31, THREADS), shares = THREADS / wide;
+        const int share = threadIdx.x / wide;
+        if (share < shares)
+            for (int e = threadIdx.x - share * wide; e < P.E; e += wide) {
+                const int32_t *h = P.hist + e;
+                int sum = 0, mine = 0;
+#pragma unroll 8
+                for (int b = share; b < static_cast<int>(gridDim.x); b += shares) {
+                    const int v = __ldcg(h + static_cast<int64_t>(b) * P.E);
+                    sum += v;
+                    mine += b < static_cast<int>(blockIdx.x) ? v : 0;
+                }
+                atomicAdd(cnt + e, sum);
+                atomicAdd(before + e, mine);
+            }
+    }
     __syncthreads();
     if (warp == 0) {
         const int total = scan_experts(cnt, P.E, lane);
@@ -223,6 +232,36 @@ __global__ void __launch_bounds__(THREADS) route_place_kernel(const RouteParams 
     }
 }
 
+// Between the two for many CTAs: every column of the histograms to its running
+// sums, the total in the row after the last.  32 experts per CTA, 32 shares of
+// the rows.
+__global__ void __launch_bounds__(1024) route_scan_kernel(const RouteParams P, int rows) {
+    __shared__ int part[32][33];
+    const int lane = threadIdx.x & 31, share = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+    const int per = (rows + 31) / 32, a = min(rows, share * per), b = min(rows, a + per);
+    pdl_wait();
+    pdl_trigger();
+    int32_t *h = P.hist + e;
+    int sum = 0;
+    if (e < P.E) {
+#pragma unroll 8
+        for (int r = a; r < b; ++r) sum += h[static_cast<int64_t>(r) * P.E];
+    }
+    part[share][lane] = sum;
+    __syncthreads();
+    int run = 0;
+    for (int q = 0; q < share; ++q) run += part[q][lane];
+    if (e < P.E) {
+#pragma unroll 8
+        for (int r = a; r < b; ++r) {
+            const int v = h[static_cast<int64_t>(r) * P.E];
+            h[static_cast<int64_t>(r) * P.E] = run;
+            run += v;
+        }
+        if (share == 31) h[static_cast<int64_t>(rows) * P.E] = run;
+    }
+}
+
 using Kernel = void (*)(const RouteParams);
 Kernel choose_kernel(int E) {
     if (E <= 32) return route_choose_kernel<1>;
@@ -233,17 +272,18 @@ Kernel choose_kernel(int E) {
     return route_choose_kernel<32>;
 }
 
-cudaError_t launch(Kernel kern, int64_t blocks, RouteParams &p, cudaStream_t st) {
+template <class K, class... A>
+cudaError_t launch(K kern, int64_t blocks, int threads, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(threads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, static_cast<const RouteParams>(p));
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 }  // namespace
@@ -252,25 +292,37 @@ cudaError_t launch(Kernel kern, int64_t blocks, RouteParams &p, cudaStream_t st)
 // of 128 experts: 16.5 -> 10 us with one).
 static int tokens_per_cta(int64_t T) { return T <= FUSED ? FUSED : T <= 2432 ? WARPS : TOKENS; }
 
+static int64_t ctas(int64_t T) { return (T + tokens_per_cta(T) - 1) / tokens_per_cta(T); }
+// Every CTA of the second launch reads all histograms, ctas^2 * E words in all: from
+// 32 MB on a launch in between sums them up once (16384 tokens of 256 experts 67 ->
+// 41 us; of 64 experts, 17 MB, it took 24.7 against 22.3).
+static bool scanned(int64_t T, int E) { return T > FUSED && ctas(T) * ctas(T) * E >= int64_t(1) << 23; }
+
 size_t f8_route_hist_bytes(int64_t T, int E) {
-    return T <= FUSED ? 0 : static_cast<size_t>((T + tokens_per_cta(T) - 1) / tokens_per_cta(T)) * E * sizeof(int32_t);
+    return T <= FUSED ? 0 : static_cast<size_t>(ctas(T) + 1) * E * sizeof(int32_t);
 }
-int f8_route_launches(int64_t T) { return T <= FUSED ? 1 : 2; }
+int f8_route_launches(int64_t T, int E) { return T <= FUSED ? 1 : scanned(T, E) ? 3 : 2; }
 
 cudaError_t launch_f8_route(const F8Route &r, cudaStream_t st) {
     RouteParams p = {r.x,      r.T,       r.ldx,     r.x_type,  r.E,    r.k,     r.score, r.normalize,
-                     r.T <= FUSED, tokens_per_cta(r.T), r.factor, r.weights, r.experts, r.offsets, r.rows, r.slots, r.hist};
-    const int64_t blocks = (r.T + p.tokens - 1) / p.tokens;
+                     r.T <= FUSED, tokens_per_cta(r.T), scanned(r.T, r.E), r.factor, r.weights, r.experts, r.offsets, r.rows, r.slots, r.hist};
+    const int64_t blocks = ctas(r.T);
     static OncePerDevice ready;
     cudaError_t e = ready(r.dev, [] {
         cudaError_t q = prefer_max_shared(route_place_kernel);
+        if (q == cudaSuccess) q = prefer_max_shared(route_scan_kernel);
         for (int n = 32; n <= 1024 && q == cudaSuccess; n *= 2) q = prefer_max_shared(choose_kernel(n));
         return q;
     });
     if (e != cudaSuccess) return e;
-    e = launch(choose_kernel(r.E), blocks, p, st);
+    const RouteParams q = p;
+    e = launch(choose_kernel(r.E), blocks, THREADS, st, q);
     if (e != cudaSuccess || p.fused) return e;
-    return launch(route_place_kernel, blocks, p, st);
+    if (p.scanned) {
+        e = launch(route_scan_kernel, (r.E + 31) / 32, 1024, st, q, static_cast<int>(blocks));
+        if (e != cudaSuccess) return e;
+    }
+    return launch(route_place_kernel, blocks, THREADS, st, q);
 }
 
 }  // namespace qk

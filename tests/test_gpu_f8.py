@@ -356,6 +356,16 @@ def test_route(cuda_lib, T, E, k, score, normalize):
     _check_route(r, xv, k, score, normalize, 2.5)
 
 
+@pytest.mark.parametrize("T,E,k,launches", [(10241, 33, 3, 2), (30001, 64, 6, 3), (70000, 100, 2, 3), (12000, 1024, 4, 3)])
+def test_route_many_tokens(cuda_lib, T, E, k, launches):
+    rng = np.random.default_rng(T)
+    x, xv = _as(rng.standard_normal((T, E)) * 2 + rng.standard_normal(E), "bfloat16")
+    before = cuda_lib.qmm_launch_count()
+    r = cuda_lib.qmm_route(x, k)
+    assert cuda_lib.qmm_launch_count() - before == launches
+    _check_route(r, xv, k, "softmax", True)
+
+
 @pytest.mark.parametrize("T", [1, 40, 700])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_ties_masks_and_nan(cuda_lib, T, score):
