@@ -419,15 +419,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         int it = 0, blk = 0;
         bool ok = true;
         if constexpr (FUSE) ok = __all_sync(0xffffffffu, mbar_spin(x_ready, 0, P.status));
-        if (FUSE && warp < 4) ok = false;  // (warps 2 and 3 only quantise)
-        while (ok && sch.next(p)) {
+        while (warp >= 4 && sch.next(p)) {  // (with FUSE warps 2 and 3 only quantise)
             float acc[NA][C::HALF];
 #pragma unroll
             for (int m = 0; m < NA; ++m)
 #pragma unroll
                 for (int i = 0; i < C::HALF; ++i) acc[m][i] = 0.0f;
             const int mine = min(C::HALF, p.ntok - half * C::HALF);  // this warp's token columns (may be <= 0)
-            for (int k = p.k0; k < p.k1; blk += min(KS, p.k1 - k), k += KS, ++it) {
+            for (int k = p.k0; ok && k < p.k1; blk += min(KS, p.k1 - k), k += KS, ++it) {
                 const int d = it & 1, s = it % SC_STAGES;
                 ok = (FUSE || mbar_spin(sc_full + 8 * s, (it / SC_STAGES) & 1, P.status)) &&
                      mbar_spin(d_full + 8 * d, (it >> 1) & 1, P.status);

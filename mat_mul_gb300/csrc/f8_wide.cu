@@ -502,7 +502,10 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
             }
             // every epilogue warp passes here once per piece, also after a wait
             // that gave up, so that none is left at a barrier alone
-            if (named_barrier_or(1, EPI_THREADS, !ok)) break;
+            if (named_barrier_or(1, EPI_THREADS, !ok)) {
+                ok = false;
+                break;
+            }
             bool store = true;
             if (p.c0 >= 0) {
                 // a part of a cut tile, [groups of 4 columns][128 tokens]
@@ -593,6 +596,9 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
                          });
             }
         }
+        // Every epilogue warp passes one such barrier per record, the closing
+        // record (and one whose wait ran out) too: none is left there alone.
+        if (ok) named_barrier_or(1, EPI_THREADS, true);
     }
     tc_fence_before();
     __syncthreads();
