@@ -114,7 +114,9 @@ QMM_API int qmm_dequant(int type, const void *blocks, int64_t n_elems, float *ou
  * the quantised activations.  It is allocated, or grown, on the first call
  * that needs it, so make one call of the largest M*K on a stream before
  * capturing that stream into a CUDA graph.  Calls on one stream are ordered;
- * calls on different streams use different workspaces.
+ * calls on different streams use different workspaces.  Any number of host
+ * threads may call, on one stream too: the launches of a call follow one
+ * another on its stream, whatever other threads do.
  */
 QMM_API int qmm(int type, const void *W_blocks, int64_t N, int64_t K, const float *x, int64_t M,
         float *y, void *stream);

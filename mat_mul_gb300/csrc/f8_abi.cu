@@ -92,6 +92,7 @@ int product(const void *W, const float *S, int64_t E, int64_t N, int64_t K, int 
     qk::F8Context c;
     if (int rc = qk::f8_context(c)) return rc;
     if (!qk::f8_available()) return refuse(QMM_ECUDA, "the driver has no tensor map encoder");
+    const qk::CallLock lock(c.dev, st);
     // workspace: codes and scales of x (unless the product quantises x itself) |
     // partial tiles
     const bool fuse = !offsets && qk::f8_fuses(R, N, K, c.num_sms);
@@ -245,6 +246,7 @@ int qmm_route(int x_type, const void *logits, int64_t T, int64_t E, int64_t ldx,
     if (int rc = check_words(slots, "slots")) return rc;
     qk::F8Context c;
     if (int rc = qk::f8_context(c)) return rc;
+    const qk::CallLock lock(c.dev, st);
     void *hist = nullptr;
     if (const size_t bytes = qk::f8_route_hist_bytes(T, static_cast<int>(E)))
         if (int rc = qk::f8_workspace(c, st, bytes, &hist)) return rc;
@@ -286,6 +288,7 @@ int qmm_f8_moe(int x_type, const void *x, int64_t T, int64_t H, int64_t ldx, int
     qk::F8Context c;
     if (int rc = qk::f8_context(c)) return rc;
     if (!qk::f8_available()) return refuse(QMM_ECUDA, "the driver has no tensor map encoder");
+    const qk::CallLock lock(c.dev, st);
     // workspace: codes and scales of x per row | of h | the rows of
     // the down product in fp32 | partial tiles
     const Codes qx(R, H), qh(R, I);

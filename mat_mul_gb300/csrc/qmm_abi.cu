@@ -10,6 +10,7 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <shared_mutex>
 #include <utility>
 
 #include "../../include/qmm.h"
@@ -66,7 +67,14 @@ struct Workspace {
     size_t bytes = 0;
 };
 
+// g_mu guards the maps, for the time of a look-up.  A whole call is guarded by
+// qk::CallLock: shared on g_calls, then its stream's mutex in g_stream_mu
+// (entries are never erased).  Locks are taken in the order g_calls, stream,
+// g_mu.
 std::mutex g_mu;
+std::shared_mutex g_calls;
+std::map<std::pair<int, cudaStream_t>, std::mutex> g_stream_mu;
+thread_local int t_calls = 0;  // calls of this thread that hold the locks (qmm_group and qmm_gate_up call qmm)
 std::map<int, DeviceInfo> g_dev;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
 // qmm_t's per-matrix completion counters, per (device, stream): zero between
@@ -97,7 +105,8 @@ int device_info(int dev, DeviceInfo &out) {
 }
 
 // Workspace of at least `bytes` for (dev, stream).  Growing synchronises the
-// stream before the old buffer is released.
+// stream before the old buffer is released.  Callers of this and of the two
+// functions below hold a qk::CallLock of the stream.
 int workspace(int dev, cudaStream_t st, size_t bytes, void **ptr) {
     std::lock_guard<std::mutex> lk(g_mu);
     Workspace &w = g_ws[{dev, st}];
@@ -211,6 +220,22 @@ int inject_stop_stage() {
     return NO_STOP;
 }
 void clear_error() { g_err[0] = 0; }
+CallLock::CallLock(int dev, cudaStream_t st) : stream_mu(nullptr) {
+    if (t_calls++) return;
+    g_calls.lock_shared();
+    std::mutex *m;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        m = &g_stream_mu[{dev, st}];
+    }
+    m->lock();
+    stream_mu = m;
+}
+CallLock::~CallLock() {
+    if (--t_calls) return;
+    stream_mu->unlock();
+    g_calls.unlock_shared();
+}
 int f8_context(F8Context &c) {
     const cudaError_t e = cudaGetDevice(&c.dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -422,6 +447,7 @@ int qmm(int type, const void *W_blocks, int64_t N, int64_t K, const float *x, in
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     DeviceInfo di;
     if (int rc = device_info(dev, di)) return rc;
+    const qk::CallLock lock(dev, st);
 
     // Four paths, chosen by M and by what fits in shared memory:
     //   mma  : decode, Q4_K / Q6_K with QMM_TENSOR_MIN_M <= M <= 8
@@ -551,6 +577,7 @@ int qmm_t(int type, const void *W_blocks, int64_t H, int64_t N, int64_t K, const
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     DeviceInfo di;
     if (int rc = device_info(dev, di)) return rc;
+    const qk::CallLock lock(dev, st);
     void *ws = nullptr;
     if (int rc = workspace(dev, st, qk::qmm_t_part_bytes(H, N, K, di.num_sms), &ws)) return rc;
     unsigned *cnt = nullptr;
@@ -586,12 +613,13 @@ int qmm_group(int n, const int *types, const void *const *Ws, const int64_t *Ns,
     if (!any) return QMM_OK;
     if (K > 0 && (!x || !aligned(x, 4))) return fail(QMM_EINVAL_PTR, "x null or not 4-byte aligned");
 
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    DeviceInfo di;
+    if (int rc = device_info(dev, di)) return rc;
+    const qk::CallLock lock(dev, static_cast<cudaStream_t>(stream));
     if (K > 0 && M <= 8 && !g_force_round_gemv) {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-        DeviceInfo di;
-        if (int rc = device_info(dev, di)) return rc;
         // one launch when the entries take the row-per-lane kernel
         if (group_on_rows(n, types, Ns, K, M, di)) {
             e = qk::launch_gemv_rows_group(n, types, Ws, Ns, K, x, static_cast<int>(M), ys,
@@ -676,6 +704,7 @@ int qmm_gate_up(int type_gate, const void *W_gate, int type_up, const void *W_up
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     DeviceInfo di;
     if (int rc = device_info(dev, di)) return rc;
+    const qk::CallLock lock(dev, st);
 
     // one launch: both matrices of one type on the block-per-lane kernel
     if (type_gate == type_up && M <= 2 && !g_force_round_gemv && !decode_on_tensor_cores(type_gate, M, N, K, di) &&
@@ -733,7 +762,9 @@ int qmm_device_status(void *stream) {
         if (e != cudaSuccess) return cuda_fail(e, "status clear");
         if (!(word & qk::STATUS_TIMEOUT))
             return fail(QMM_EINDEX, "a row index or an offset was out of range (status word 0x%x)", word);
-        // a launch that gave up may have left completion counters behind
+        // a launch that gave up may have left completion counters behind (no
+        // call is between its launches meanwhile)
+        std::unique_lock<std::shared_mutex> calls(g_calls);
         e = cudaDeviceSynchronize();
         std::lock_guard<std::mutex> lk(g_mu);
         for (auto &c : g_counters)
@@ -749,6 +780,7 @@ int qmm_release(void) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    std::unique_lock<std::shared_mutex> calls(g_calls);
     e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "device synchronize");
     std::lock_guard<std::mutex> lk(g_mu);

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 namespace qk {
 
 // Output layout of the quantiser.  q rows have stride q_ld bytes; with
@@ -51,6 +53,23 @@ struct QuantOut {
 // pdl_launch: launch this kernel itself with programmatic dependent launch.
 cudaError_t launch_quantize(const float *x, int64_t M, int64_t K, const QuantOut &o, cudaStream_t st,
                             bool trigger_dependents, int num_sms, bool pdl_launch = false);
+
+// Held by a call from its first look at the stream's workspace, counters or
+// buffers to its last launch.  Those are shared by all calls on a stream: with
+// another thread's launch between a quantiser and its product, the product
+// would read the other call's activations, and a workspace that the other call
+// grows is freed under this one's launches.  Calls on other streams go on.
+// A call made by a call that holds it takes nothing (same thread and stream).
+class CallLock {
+  public:
+    CallLock(int dev, cudaStream_t st);
+    ~CallLock();
+    CallLock(const CallLock &) = delete;
+    CallLock &operator=(const CallLock &) = delete;
+
+  private:
+    std::mutex *stream_mu;  // null in a nested call
+};
 
 // cuTensorMapEncodeTiled from the driver (null when it cannot be found).
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,

@@ -107,6 +107,7 @@ extern "C" QMM_API int qmm_noalloc(int type, const void *W_blocks, int64_t N, in
         }
         d = slot;
     }
+    const qk::CallLock lock(dev, st);
     char *s = static_cast<char *>(d.scratch);
     const size_t q_bytes = round_up(static_cast<size_t>(M * K), 256);
     const size_t d_bytes = round_up(static_cast<size_t>(M * ld) * 4, 256);
