@@ -110,17 +110,44 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
+# The library works on the current device: its workspaces, its status word and
+# its launches are there.  Tensors and streams of another one are refused.
+def _current_device():
+    import torch
+    get = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return get()
+
+
+def _refuse_device(t, current):
+    raise ValueError(f"tensors on cuda:{t.get_device()}, but cuda:{current} is the current device: call under "
+                     f"torch.cuda.device({t.get_device()})")
+
+
+def _require_stream(stream, current):
+    if getattr(stream, "device_index", current) != current:
+        raise ValueError(f"a stream of cuda:{stream.device_index}, but cuda:{current} is the current device")
+
+
 def _stream_handle(stream):
     import torch
     if stream is None:
         stream = torch.cuda.current_stream()
+    else:
+        _require_stream(stream, _current_device())
     return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _require_cuda(*ts):
+    current = None
     for t in ts:
-        if t is not None and not t.is_cuda:
+        if t is None:
+            continue
+        if not t.is_cuda:
             raise ValueError("libqmm takes device tensors; got a tensor on " + str(t.device))
+        if current is None:
+            current = _current_device()
+        if t.get_device() != current:
+            _refuse_device(t, current)
 
 
 def qmm_dequant(qtype: int, blocks, n_elems: int, out=None):
@@ -271,7 +298,15 @@ class _F8:
         self.codes = (torch.float8_e4m3fn, torch.uint8)
         self.ftypes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # qmm_ftype
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self.stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        self.current_stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        self.current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+    def stream(self, dev, stream):
+        """The handle of `stream`, or of the current one, on the current device `dev`."""
+        if stream is None:
+            return self.current_stream(dev)
+        _require_stream(stream, dev)
+        return stream.cuda_stream
 
     def ftype(self, dtype, what):
         t = self.ftypes.get(dtype)
@@ -287,11 +322,13 @@ def _f8_state():
     return _f8
 
 
-def _device_index(first, *others):
-    """The CUDA device of every tensor given (None: left out)."""
+def _device_index(f, first, *others):
+    """The CUDA device of every tensor given (None: left out), the current one."""
     if not first.is_cuda:
         _require_cuda(first)
     dev = first.get_device()
+    if dev != f.current_device():
+        _refuse_device(first, f.current_device())
     for t in others:
         if t is not None and t.get_device() != dev:
             _require_cuda(t)
@@ -344,14 +381,14 @@ def qmm_f8_quantize(x, stream=None):
     """(codes float8_e4m3fn [M, K], scales float32 [M, ceil(K/128)]) of a device
     tensor x [M, K] (or [K]) of float32, float16 or bfloat16 rows."""
     f = _f8_state()
-    dev = _device_index(x)
+    dev = _device_index(f, x)
     M, K, ldx = _rows2d(x, "x")
     ft = f.ftype(x.dtype, "x")
     device = x.device
     c = f.empty((M, K), dtype=f.e4m3, device=device)
     s = f.empty((M, -(-K // F8_BLOCK)), dtype=f.float32, device=device)
     rc = f.lib.qmm_f8_quantize(ft, x.data_ptr(), M, K, ldx, c.data_ptr(), s.data_ptr(),
-                               f.stream(dev) if stream is None else stream.cuda_stream)
+                               f.stream(dev, stream))
     if rc:
         _check(rc)
     return c, s
@@ -363,7 +400,7 @@ def qmm_f8(W, S, x, y=None, dtype=None, stream=None):
     bfloat16; y has x's type unless dtype (or y) says otherwise.  K a multiple
     of 16.  Rows of x and y may be further apart than their length."""
     f = _f8_state()
-    dev = _device_index(x, W, S, y)
+    dev = _device_index(f, x, W, S, y)
     N, K = _f8_weights(f, W, S, 2, "W")
     M, cols, ldx = _rows2d(x, "x")
     if cols != K:
@@ -372,7 +409,7 @@ def qmm_f8(W, S, x, y=None, dtype=None, stream=None):
     ft = f.ftype(xt, "x")
     y, ldy = _f8_out(f, y, M, N, dtype or xt, x.device)
     rc = f.lib.qmm_f8(W.data_ptr(), S.data_ptr(), N, K, ft, x.data_ptr(), M, ldx, f.ftype(y.dtype, "y"), y.data_ptr(),
-                      ldy, f.stream(dev) if stream is None else stream.cuda_stream)
+                      ldy, f.stream(dev, stream))
     if rc:
         _check(rc)
     return y
@@ -384,7 +421,7 @@ def qmm_f8_experts(W, S, x, offsets, rows=None, y=None, dtype=None, stream=None)
     offsets int32 [E+1] and rows int32 on the device.  Returns y [R, N], R the
     length of rows (or of x); rows of y from offsets[E] on are not written."""
     f = _f8_state()
-    dev = _device_index(x, W, S, offsets, rows, y)
+    dev = _device_index(f, x, W, S, offsets, rows, y)
     E, N, K = _f8_weights(f, W, S, 3, "W")
     M, cols, ldx = _rows2d(x, "x")
     if cols != K:
@@ -400,7 +437,7 @@ def qmm_f8_experts(W, S, x, offsets, rows=None, y=None, dtype=None, stream=None)
     y, ldy = _f8_out(f, y, R, N, dtype or xt, x.device)
     rc = f.lib.qmm_f8_experts(W.data_ptr(), S.data_ptr(), E, N, K, ft, x.data_ptr(), M, ldx, offsets.data_ptr(), index, R,
                               f.ftype(y.dtype, "y"), y.data_ptr(), ldy,
-                              f.stream(dev) if stream is None else stream.cuda_stream)
+                              f.stream(dev, stream))
     if rc:
         _check(rc)
     return y
@@ -417,7 +454,7 @@ def qmm_route(logits, k, score="softmax", normalize=True, factor=1.0, stream=Non
     (softmax or sigmoid scores, divided by their sum when normalize), and the
     (token, choice) pairs sorted by expert; see Route."""
     f = _f8_state()
-    dev = _device_index(logits)
+    dev = _device_index(f, logits)
     T, E, ld = _rows2d(logits, "logits")
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, not {score!r}")
@@ -432,7 +469,7 @@ def qmm_route(logits, k, score="softmax", normalize=True, factor=1.0, stream=Non
     offsets = empty(E + 1, dtype=i32, device=device)
     rc = f.lib.qmm_route(ft, logits.data_ptr(), T, E, ld, k, _SCORES[score], 1 if normalize else 0, factor,
                          weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
-                         f.stream(dev) if stream is None else stream.cuda_stream)
+                         f.stream(dev, stream))
     if rc:
         _check(rc)
     return Route(weights, experts, offsets, rows, slots)
@@ -445,7 +482,7 @@ def qmm_f8_moe(x, route, W_gate, S_gate, W_up, S_up, W_down, S_down, y=None, dty
     scales.  H and I multiples of 16."""
     f = _f8_state()
     weights, _, offsets, _, slots = route
-    dev = _device_index(x, W_gate, S_gate, W_up, S_up, W_down, S_down, weights, offsets, slots, y)
+    dev = _device_index(f, x, W_gate, S_gate, W_up, S_up, W_down, S_down, weights, offsets, slots, y)
     E, I, H = shape = _f8_weights(f, W_gate, S_gate, 3, "W_gate")
     if _f8_weights(f, W_up, S_up, 3, "W_up") != shape or _f8_weights(f, W_down, S_down, 3, "W_down") != (E, H, I):
         raise ValueError(f"W_up must be {(E, I, H)} and W_down {(E, H, I)} for W_gate {(E, I, H)}, got "
@@ -465,7 +502,7 @@ def qmm_f8_moe(x, route, W_gate, S_gate, W_up, S_up, W_down, S_down, y=None, dty
     rc = f.lib.qmm_f8_moe(ft, x.data_ptr(), T, H, ldx, k, weights.data_ptr(), offsets.data_ptr(), slots.data_ptr(), E, I,
                           W_gate.data_ptr(), S_gate.data_ptr(), W_up.data_ptr(), S_up.data_ptr(), W_down.data_ptr(),
                           S_down.data_ptr(), f.ftype(y.dtype, "y"), y.data_ptr(), ldy,
-                          f.stream(dev) if stream is None else stream.cuda_stream)
+                          f.stream(dev, stream))
     if rc:
         _check(rc)
     return y
