@@ -11,6 +11,11 @@ library is missing or no GPU is present the calls raise.
     o = q.qmm_t(q.Q8_0, V_cache, H, T, D, p)      # p: [H, M, T] -> [H, M, D]
     w = q.qmm_dequant(q.Q6_K, blocks, n_elems)    # cuda f32 [n_elems]
 
+A call runs on the current stream or on the one given as stream=, as if made
+under torch.cuda.stream(stream): what it allocates belongs to that stream, and
+the caller orders it after the work that makes its inputs and before the
+work that reads its results.
+
 Weights in 8-bit floats (e4m3 codes, one fp32 scale per 128 x 128 block), x and
 y in float32, float16 or bfloat16:
 
@@ -106,6 +111,22 @@ def _check(rc: int):
         raise QmmError(rc, load().qmm_last_error().decode())
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory for a result of a call on `stream` (None: the current one): from
+    that stream's pool, since a block of the current stream's may still be in
+    use there when the other stream writes it; and not handed out again before
+    the current stream, where the caller reads it, is done with it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if stream.cuda_stream != here.cuda_stream:
+        t.record_stream(here)
+    return t
+
+
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
@@ -155,7 +176,7 @@ def qmm_dequant(qtype: int, blocks, n_elems: int, out=None):
     import torch
     _require_cuda(blocks, out)
     if out is None:
-        out = torch.empty(n_elems, dtype=torch.float32, device=blocks.device)
+        out = _empty(n_elems, torch.float32, blocks.device, None)
     _check(load().qmm_dequant(int(qtype), _ptr(blocks), int(n_elems), _ptr(out)))
     return out
 
@@ -171,7 +192,7 @@ def qmm(qtype: int, W, N: int, K: int, x, y=None, stream=None):
     if x.shape[-1] != K:
         raise ValueError(f"x has {x.shape[-1]} columns, K = {K}")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _empty((M, N), torch.float32, x.device, stream)
     elif y.dtype != torch.float32 or not y.is_contiguous() or y.device != x.device or y.numel() < M * N:
         raise ValueError(f"y must be a contiguous float32 tensor on {x.device} with at least M*N = {M * N} elements")
     _check(load().qmm(int(qtype), _ptr(W), int(N), int(K), _ptr(x), int(M), _ptr(y),
@@ -191,7 +212,7 @@ def qmm_t(qtype: int, W, H: int, N: int, K: int, x, y=None, stream=None):
         raise ValueError(f"x has shape {tuple(x.shape)}, expected [H={H}, M, N={N}]")
     M = x.shape[1]
     if y is None:
-        y = torch.empty((H, M, K), dtype=torch.float32, device=x.device)
+        y = _empty((H, M, K), torch.float32, x.device, stream)
     _check(load().qmm_t(int(qtype), _ptr(W), int(H), int(N), int(K), _ptr(x), int(M), _ptr(y),
                         _stream_handle(stream)))
     return y
@@ -210,8 +231,7 @@ def qmm_group(items, K: int, x, stream=None):
     n = len(items)
     ys = []
     for it in items:
-        y = it[3] if len(it) > 3 and it[3] is not None else torch.empty(
-            (M, int(it[2])), dtype=torch.float32, device=x.device)
+        y = it[3] if len(it) > 3 and it[3] is not None else _empty((M, int(it[2])), torch.float32, x.device, stream)
         _require_cuda(it[1], x, y)
         ys.append(y)
     types = (ctypes.c_int * max(n, 1))(*[int(it[0]) for it in items])
@@ -233,7 +253,7 @@ def qmm_gate_up(type_gate: int, W_gate, type_up: int, W_up, N: int, K: int, x, h
     if x.shape[-1] != K:
         raise ValueError(f"x has {x.shape[-1]} columns, K = {K}")
     if h is None:
-        h = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        h = _empty((M, N), torch.float32, x.device, stream)
     elif h.dtype != torch.float32 or not h.is_contiguous() or h.device != x.device or h.numel() < M * N:
         raise ValueError(f"h must be a contiguous float32 tensor on {x.device} with at least M*N = {M * N} elements")
     _check(load().qmm_gate_up(int(type_gate), _ptr(W_gate), int(type_up), _ptr(W_up), int(N), int(K), _ptr(x),
@@ -267,9 +287,9 @@ def qmm_quantize_act(x, stream=None):
     _require_cuda(x)
     x2 = x if x.dim() == 2 else x.reshape(1, -1)
     M, K = x2.shape
-    q = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    d = torch.empty((M, K // 32), dtype=torch.float32, device=x.device)
-    s = torch.empty((M, K // 32), dtype=torch.int32, device=x.device)
+    q = _empty((M, K), torch.int8, x.device, stream)
+    d = _empty((M, K // 32), torch.float32, x.device, stream)
+    s = _empty((M, K // 32), torch.int32, x.device, stream)
     _check(load().qmm_quantize_act(_ptr(x2), int(M), int(K), _ptr(q), _ptr(d), _ptr(s),
                                    _stream_handle(stream)))
     return q, d, s
@@ -307,6 +327,10 @@ class _F8:
             return self.current_stream(dev)
         _require_stream(stream, dev)
         return stream.cuda_stream
+
+    def new(self, shape, dtype, device, stream):
+        """_empty(), without its look-ups where the current stream is meant."""
+        return self.empty(shape, dtype=dtype, device=device) if stream is None else _empty(shape, dtype, device, stream)
 
     def ftype(self, dtype, what):
         t = self.ftypes.get(dtype)
@@ -362,10 +386,10 @@ def _f8_weights(f, W, S, dims, what):
     return shape
 
 
-def _f8_out(f, y, rows, cols, dtype, device):
+def _f8_out(f, y, rows, cols, dtype, device, stream):
     """The result tensor and its row pitch: y checked, or a new one."""
     if y is None:
-        return f.empty((rows, cols), dtype=dtype, device=device), cols
+        return f.new((rows, cols), dtype, device, stream), cols
     r, c, ldy = _rows2d(y, "y")
     if r != rows or c != cols:
         raise ValueError(f"y has shape {tuple(y.shape)}, expected {(rows, cols)}")
@@ -385,8 +409,8 @@ def qmm_f8_quantize(x, stream=None):
     M, K, ldx = _rows2d(x, "x")
     ft = f.ftype(x.dtype, "x")
     device = x.device
-    c = f.empty((M, K), dtype=f.e4m3, device=device)
-    s = f.empty((M, -(-K // F8_BLOCK)), dtype=f.float32, device=device)
+    c = f.new((M, K), f.e4m3, device, stream)
+    s = f.new((M, -(-K // F8_BLOCK)), f.float32, device, stream)
     rc = f.lib.qmm_f8_quantize(ft, x.data_ptr(), M, K, ldx, c.data_ptr(), s.data_ptr(),
                                f.stream(dev, stream))
     if rc:
@@ -407,7 +431,7 @@ def qmm_f8(W, S, x, y=None, dtype=None, stream=None):
         raise ValueError(f"x has {cols} columns, W {K}")
     xt = x.dtype
     ft = f.ftype(xt, "x")
-    y, ldy = _f8_out(f, y, M, N, dtype or xt, x.device)
+    y, ldy = _f8_out(f, y, M, N, dtype or xt, x.device, stream)
     rc = f.lib.qmm_f8(W.data_ptr(), S.data_ptr(), N, K, ft, x.data_ptr(), M, ldx, f.ftype(y.dtype, "y"), y.data_ptr(),
                       ldy, f.stream(dev, stream))
     if rc:
@@ -434,7 +458,7 @@ def qmm_f8_experts(W, S, x, offsets, rows=None, y=None, dtype=None, stream=None)
         index = rows.data_ptr()
     xt = x.dtype
     ft = f.ftype(xt, "x")
-    y, ldy = _f8_out(f, y, R, N, dtype or xt, x.device)
+    y, ldy = _f8_out(f, y, R, N, dtype or xt, x.device, stream)
     rc = f.lib.qmm_f8_experts(W.data_ptr(), S.data_ptr(), E, N, K, ft, x.data_ptr(), M, ldx, offsets.data_ptr(), index, R,
                               f.ftype(y.dtype, "y"), y.data_ptr(), ldy,
                               f.stream(dev, stream))
@@ -460,13 +484,13 @@ def qmm_route(logits, k, score="softmax", normalize=True, factor=1.0, stream=Non
         raise ValueError(f"score must be one of {sorted(_SCORES)}, not {score!r}")
     k = int(k)
     n = k if k > 0 else 0
-    ft, device, empty, i32 = f.ftype(logits.dtype, "logits"), logits.device, f.empty, f.int32
-    weights = empty((T, n), dtype=f.float32, device=device)
+    ft, device, i32 = f.ftype(logits.dtype, "logits"), logits.device, f.int32
+    weights = f.new((T, n), f.float32, device, stream)
     # (five allocations: views of one buffer cost more than twice as much)
-    experts = empty((T, n), dtype=i32, device=device)
-    slots = empty((T, n), dtype=i32, device=device)
-    rows = empty(T * n, dtype=i32, device=device)
-    offsets = empty(E + 1, dtype=i32, device=device)
+    experts = f.new((T, n), i32, device, stream)
+    slots = f.new((T, n), i32, device, stream)
+    rows = f.new(T * n, i32, device, stream)
+    offsets = f.new(E + 1, i32, device, stream)
     rc = f.lib.qmm_route(ft, logits.data_ptr(), T, E, ld, k, _SCORES[score], 1 if normalize else 0, factor,
                          weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
                          f.stream(dev, stream))
@@ -498,7 +522,7 @@ def qmm_f8_moe(x, route, W_gate, S_gate, W_up, S_up, W_down, S_down, y=None, dty
     _int32(f, slots, T * k, "route.slots")
     xt = x.dtype
     ft = f.ftype(xt, "x")
-    y, ldy = _f8_out(f, y, T, H, dtype or xt, x.device)
+    y, ldy = _f8_out(f, y, T, H, dtype or xt, x.device, stream)
     rc = f.lib.qmm_f8_moe(ft, x.data_ptr(), T, H, ldx, k, weights.data_ptr(), offsets.data_ptr(), slots.data_ptr(), E, I,
                           W_gate.data_ptr(), S_gate.data_ptr(), W_up.data_ptr(), S_up.data_ptr(), W_down.data_ptr(),
                           S_down.data_ptr(), f.ftype(y.dtype, "y"), y.data_ptr(), ldy,

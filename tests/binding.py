@@ -30,6 +30,9 @@ def on_gpu(t, index=0):
 
         def get_device(self):
             return index
+
+        def record_stream(self, stream):
+            self.read_on = stream
     return t.as_subclass(OnGpu)
 
 
