@@ -344,6 +344,10 @@ QMM_API int qmm_route(int x_type, const void *logits, int64_t T, int64_t E, int6
  *   h[r] = silu(W_gate[e] . x[t]) * (W_up[e] . x[t]),  r = slots[t,j], e its expert,
  *   y[t] = sum_j weights[t,j] * (W_down[e] . h[slots[t,j]]),
  * x and h rounded as in qmm_f8_quantize, the sum over j in fp32 in order of j.
+ * Accuracy: the three products as in qmm_f8; before its rounding to 8 bits
+ * h is within 2^-21 |h| of silu(g) * u for the g and u computed (|g u| 2^-149
+ * where e^g is subnormal, g < -87.3).  A value of h closer than that to the
+ * boundary between two codes may take either.
  *   x, y                      : device [T] rows of H values, ldx / ldy apart.
  *   weights, offsets, slots   : as qmm_route writes them (k choices per token;
  *                               every row below offsets[E] in exactly one slot).

@@ -107,11 +107,18 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
                  : "memory");
 }
 
-// g / (1 + e^-g) with the hardware's exponential and reciprocal: a relative
-// error of a few 2^-24 for g >= 0 and about |g| 2^-24 below, far inside the
-// rounding of h to 8 bits that follows; expf and the IEEE division took about 40
-// instructions per value of a tile's epilogue, these take 7.
-__device__ __forceinline__ float silu(float g) { return g * __fdividef(1.0f, 1.0f + __expf(-g)); }
+// silu(g) = g / (1 + e^-g), for g < 0 as g e^g / (1 + e^g): the exponential is
+// at most 1, so nothing overflows where the result does not vanish, and the
+// hardware's division has a divisor between 1 and 2.  Over all floats (each one
+// tried against 64 bits) the result is within 5.3 * 2^-24 of its value, an IEEE
+// division 4.8; below -87.3, where e^g is subnormal, within |g| 2^-150.  With
+// __expf it was off by up to 9 * 2^-24 at -8 and 66 at -87, and 0 below.  A layer
+// of 4093 tokens and 32 experts of 2048 x 1408: 239 us, with the IEEE division 252,
+// with __expf 233.
+__device__ __forceinline__ float silu(float g) {
+    const float e = expf(-fabsf(g));
+    return __fdividef(g < 0.0f ? g * e : g, 1.0f + e);
+}
 
 // A piece of a tile: tokens [row0, row0 + ntok) of expert e against block nblk
 // of weight rows, K blocks [k0, k1).
