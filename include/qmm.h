@@ -308,9 +308,9 @@ QMM_API int qmm_f8(const void *W, const float *S, int64_t N, int64_t K, int x_ty
  *             of y is row r of x; then M = R).
  *   R       : rows of y (at least offsets[E]).
  * The sizes are never read on the host: the call can be captured in a graph
- * and replayed with other offsets.  An offset or a row index out of range is
- * skipped, its rows of y are undefined, and qmm_device_status() reports
- * QMM_EINDEX.
+ * and replayed with other offsets.  A row index out of range, and a group whose
+ * offsets are out of range or below one before them, are skipped, their rows of
+ * y are undefined, and qmm_device_status() reports QMM_EINDEX.
  */
 QMM_API int qmm_f8_experts(const void *W, const float *S, int64_t E, int64_t N, int64_t K, int x_type, const void *x,
                            int64_t M, int64_t ldx, const int32_t *offsets, const int32_t *rows, int64_t R, int y_type,

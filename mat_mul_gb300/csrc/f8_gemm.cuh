@@ -1,5 +1,5 @@
 // f8_gemm.cuh -- what the two block-scaled 8-bit-float product kernels share:
-// TMA and tcgen05 wrappers, and the schedule that cuts the work into pieces.
+// TMA and tcgen05 wrappers, and the count of the tiles of every expert.
 #pragma once
 
 #include <cuda.h>
@@ -8,6 +8,7 @@
 #include <cuda_fp8.h>
 
 #include "f8_internal.h"
+#include "f8_schedule.h"
 #include "qmm_device.cuh"
 #include "qmm_internal.h"
 
@@ -15,7 +16,6 @@ namespace qk {
 namespace f8 {
 
 constexpr int BK = 128;        // values of K per stage: one scale block
-constexpr int CUT_COST = 32;   // see Schedule::plan
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
     asm volatile(
@@ -120,107 +120,29 @@ __device__ __forceinline__ float silu(float g) {
     return __fdividef(g < 0.0f ? g * e : g, 1.0f + e);
 }
 
-// A piece of a tile: tokens [row0, row0 + ntok) of expert e against block nblk
-// of weight rows, K blocks [k0, k1).
-struct Piece {
-    int e, nblk, row0, ntok, k0, k1, tile;
-};
-
-// The pieces of this CTA (or pair) in order: first its share of the tiles that
-// are cut along K, then its whole tiles.  (Tiles and K blocks of cut tiles are
-// below 2^31: the caller checks the sizes.)
-struct Schedule {
-    const int *cum;  // shared memory: tiles before expert e, [E + 1]
-    const int32_t *offsets;
-    int E, R, kb, nb, G, c;
-    int least;           // K blocks of cut tiles that a CTA has at least
-    int step;            // tokens per tile; 0: the rows of an expert split evenly over its tiles
-    int tiles, whole;    // tiles [0, whole) go round the CTAs uncut
-    int units, sharing;  // K blocks of the cut tiles, and the CTAs that share them
-    int u, u1;           // this CTA's of them, counted from tile `whole`
-    int next_whole;
-
-    // Which tiles are cut, and how.  Handing partial tiles over costs a CTA about
-    // as much as CUT_COST K blocks, so
-    // - tiles for half of the CTAs or fewer: each among G / tiles CTAs, nobody
-    //   with parts of two tiles;
-    // - else, when the last round would leave CTAs idle for longer than that: the
-    //   tiles of the last round and of the full one before it (so that a cut tile
-    //   has two or three parts) are shared out evenly over all CTAs;
-    // - else none.
-    __host__ __device__ static void plan(int tiles, int kb, int G, int least, int &whole, int &units, int &sharing) {
-        const int last = tiles % G;
-        if (2 * tiles <= G) whole = 0;
-        else if (last == 0 || static_cast<int64_t>(kb) * (G - last) <= static_cast<int64_t>(CUT_COST) * G) whole = tiles;
-        else whole = tiles > G ? (tiles / G - 1) * G : 0;
-        units = (tiles - whole) * kb;
-        const int most = (kb + least - 1) / least;  // parts of a tile
-        if (2 * tiles <= G) sharing = tiles * (G / max(tiles, 1) < most ? G / max(tiles, 1) : most);
-        else sharing = G < units ? G : units;
-    }
-    __device__ __forceinline__ void init() {
-        tiles = cum[E];
-        plan(tiles, kb, G, least, whole, units, sharing);
-        u = c < sharing ? static_cast<int>(static_cast<int64_t>(units) * c / sharing) : 0;
-        u1 = c < sharing ? static_cast<int>(static_cast<int64_t>(units) * (c + 1) / sharing) : 0;
-        next_whole = c;
-    }
-    __device__ __forceinline__ bool next(Piece &p) {
-        if (u < u1) {
-            const int t = u / kb;
-            p.tile = whole + t;
-            p.k0 = u - t * kb;
-            p.k1 = min(kb, p.k0 + (u1 - u));
-            u += p.k1 - p.k0;
-        } else if (next_whole < whole) {
-            p.tile = next_whole;
-            next_whole += G;
-            p.k0 = 0;
-            p.k1 = kb;
-        } else {
-            return false;
-        }
-        int lo = 0, hi = E - 1;  // the expert whose tiles hold p.tile
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (cum[mid] <= p.tile) lo = mid;
-            else hi = mid - 1;
-        }
-        p.e = lo;
-        const int local = p.tile - cum[lo];
-        const int nt = (cum[lo + 1] - cum[lo]) / nb;
-        const int r0 = offsets ? __ldg(offsets + lo) : 0;
-        const int n = offsets ? __ldg(offsets + lo + 1) - r0 : R;
-        // (an even share rounded up to 16 is at most a whole tile, so the last tile is not empty)
-        const int per = step ? step : ((n + nt - 1) / nt + 15) & ~15;
-        p.nblk = local / nt;
-        const int tt = local - p.nblk * nt;
-        p.row0 = r0 + tt * per;
-        p.ntok = min(per, n - tt * per);
-        return true;
-    }
-    // The CTAs [c0, c1] that hold a part of cut tile `tile`.
-    __device__ __forceinline__ void sharers(int tile, int &c0, int &c1) const {
-        const int64_t a = static_cast<int64_t>(tile - whole) * kb;
-        c0 = static_cast<int>(((a + 1) * sharing - 1) / units);
-        c1 = static_cast<int>(((a + kb) * sharing - 1) / units);
-    }
-};
-
 // Tiles before each expert, cum[0 .. E], for tiles of `tokens` rows times nb
-// row blocks of W; one warp.  Offsets out of order or out of [0, R] raise
+// row blocks of W; one warp.  Groups that group_tiles() does not take raise
 // STATUS_INDEX and leave their expert without tiles.
 __device__ __forceinline__ void count_tiles(int *cum, const int32_t *offsets, int E, int R, int tokens, int nb, int lane,
                                             int *status) {
-    int base = 0;
+    int base = 0, highest = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
         const int e = e0 + lane;
+        const int lo = offsets && e < E ? __ldg(offsets + e) : 0;
+        int top = max(lo, highest);  // the largest of offsets[0 .. e]
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, top, o);
+            if (lane >= o) top = max(top, v);
+        }
+        highest = __shfl_sync(0xffffffffu, top, 31);
         int t = 0;
         if (e < E) {
-            const int lo = offsets ? __ldg(offsets + e) : 0;
-            const int hi = offsets ? __ldg(offsets + e + 1) : R;
-            if (lo < 0 || hi < lo || hi > R) atomicOr(status, STATUS_INDEX);
-            else t = (hi - lo + tokens - 1) / tokens * nb;
+            t = group_tiles(lo, offsets ? __ldg(offsets + e + 1) : R, top, R, tokens, nb);
+            if (t < 0) {
+                atomicOr(status, STATUS_INDEX);
+                t = 0;
+            }
         }
         int incl = t;
 #pragma unroll
