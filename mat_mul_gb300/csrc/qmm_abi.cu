@@ -758,19 +758,27 @@ int qmm_device_status(void *stream) {
     e = cudaMemcpy(&word, di.status, sizeof word, cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(e, "status read");
     if (word) {
-        e = cudaMemset(di.status, 0, sizeof word);
-        if (e != cudaSuccess) return cuda_fail(e, "status clear");
-        if (!(word & qk::STATUS_TIMEOUT))
-            return fail(QMM_EINDEX, "a row index or an offset was out of range (status word 0x%x)", word);
-        // a launch that gave up may have left completion counters behind (no
-        // call is between its launches meanwhile)
+        // Nothing may run while the flags go, and the clearing has to be done
+        // when this returns: cudaMemset of device memory comes back before it
+        // is, and streams that do not wait for the default one would not
+        // either.  (No call is between its launches meanwhile.)
         std::unique_lock<std::shared_mutex> calls(g_calls);
         e = cudaDeviceSynchronize();
-        std::lock_guard<std::mutex> lk(g_mu);
-        for (auto &c : g_counters)
-            if (e == cudaSuccess && c.first.first == dev && c.second.ptr) e = cudaMemset(c.second.ptr, 0, c.second.bytes);
-        if (e != cudaSuccess) return cuda_fail(e, "counters clear");
-        return fail(QMM_ETIMEOUT, "a bounded device wait expired (status word 0x%x)", word);
+        int late = 0;
+        if (e == cudaSuccess) e = cudaMemcpy(&late, di.status, sizeof late, cudaMemcpyDeviceToHost);
+        word |= late;
+        if (e == cudaSuccess) e = cudaMemset(di.status, 0, sizeof word);
+        if (word & qk::STATUS_TIMEOUT) {
+            // a launch that gave up may have left completion counters behind
+            std::lock_guard<std::mutex> lk(g_mu);
+            for (auto &c : g_counters)
+                if (e == cudaSuccess && c.first.first == dev && c.second.ptr)
+                    e = cudaMemset(c.second.ptr, 0, c.second.bytes);
+        }
+        if (e == cudaSuccess) e = cudaDeviceSynchronize();
+        if (e != cudaSuccess) return cuda_fail(e, "status clear");
+        if (word & qk::STATUS_TIMEOUT) return fail(QMM_ETIMEOUT, "a bounded device wait expired (status word 0x%x)", word);
+        return fail(QMM_EINDEX, "a row index or an offset was out of range (status word 0x%x)", word);
     }
     return QMM_OK;
 }
