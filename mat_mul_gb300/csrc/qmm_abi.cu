@@ -83,6 +83,18 @@ std::map<std::pair<int, cudaStream_t>, Workspace> g_counters;
 // qmm_gate_up's intermediate products g (and u), per (device, stream)
 std::map<std::pair<int, cudaStream_t>, Workspace> g_gate;
 
+// cudaMalloc; when it fails the runtime keeps no error for whoever asks next
+// (the caller's own check after a launch, say).
+template <class T>
+cudaError_t device_alloc(T **ptr, size_t bytes) {
+    const cudaError_t e = cudaMalloc(ptr, bytes);
+    if (e != cudaSuccess) {
+        *ptr = nullptr;
+        cudaGetLastError();
+    }
+    return e;
+}
+
 int device_info(int dev, DeviceInfo &out) {
     std::lock_guard<std::mutex> lk(g_mu);
     auto it = g_dev.find(dev);
@@ -95,7 +107,7 @@ int device_info(int dev, DeviceInfo &out) {
     if (e == cudaSuccess)
         e = cudaDeviceGetAttribute(&di.max_smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
     if (e != cudaSuccess) return cuda_fail(e, "device query");
-    e = cudaMalloc(&di.status, 256);
+    e = device_alloc(&di.status, 256);
     if (e != cudaSuccess) return fail(QMM_ENOMEM, "status word: %s", cudaGetErrorString(e));
     e = cudaMemset(di.status, 0, 256);
     if (e != cudaSuccess) return cuda_fail(e, "status word init");
@@ -123,11 +135,8 @@ int workspace(int dev, cudaStream_t st, size_t bytes, void **ptr) {
         w.ptr = nullptr;
         w.bytes = 0;
     }
-    cudaError_t e = cudaMalloc(&w.ptr, want);
-    if (e != cudaSuccess) {
-        w.ptr = nullptr;
-        return fail(QMM_ENOMEM, "workspace of %zu bytes: %s", want, cudaGetErrorString(e));
-    }
+    const cudaError_t e = device_alloc(&w.ptr, want);
+    if (e != cudaSuccess) return fail(QMM_ENOMEM, "workspace of %zu bytes: %s", want, cudaGetErrorString(e));
     w.bytes = want;
     *ptr = w.ptr;
     return QMM_OK;
@@ -147,11 +156,8 @@ int gate_buffer(int dev, cudaStream_t st, size_t bytes, float **ptr) {
             w.bytes = 0;
         }
         const size_t want = (bytes + (2u << 20) - 1) & ~size_t((2u << 20) - 1);
-        cudaError_t e = cudaMalloc(&w.ptr, want);
-        if (e != cudaSuccess) {
-            w.ptr = nullptr;
-            return fail(QMM_ENOMEM, "gate buffer of %zu bytes: %s", want, cudaGetErrorString(e));
-        }
+        const cudaError_t e = device_alloc(&w.ptr, want);
+        if (e != cudaSuccess) return fail(QMM_ENOMEM, "gate buffer of %zu bytes: %s", want, cudaGetErrorString(e));
         w.bytes = want;
     }
     *ptr = static_cast<float *>(w.ptr);
@@ -177,11 +183,8 @@ int counters(int dev, cudaStream_t st, int64_t n, unsigned **ptr) {
         w.ptr = nullptr;
         w.bytes = 0;
     }
-    cudaError_t e = cudaMalloc(&w.ptr, want);
-    if (e != cudaSuccess) {
-        w.ptr = nullptr;
-        return fail(QMM_ENOMEM, "counters of %zu bytes: %s", want, cudaGetErrorString(e));
-    }
+    cudaError_t e = device_alloc(&w.ptr, want);
+    if (e != cudaSuccess) return fail(QMM_ENOMEM, "counters of %zu bytes: %s", want, cudaGetErrorString(e));
     e = cudaMemsetAsync(w.ptr, 0, want, st);
     if (e != cudaSuccess) return cuda_fail(e, "counters init");
     w.bytes = want;
