@@ -113,7 +113,9 @@ QMM_API int qmm_dequant(int type, const void *blocks, int64_t n_elems, float *ou
  * The call uses a library-owned device workspace per (device, stream) for
  * the quantised activations.  It is allocated, or grown, on the first call
  * that needs it, so make one call of the largest M*K on a stream before
- * capturing that stream into a CUDA graph.  Calls on one stream are ordered;
+ * capturing that stream into a CUDA graph, and none larger while that graph is
+ * in use: it would free the workspace that the graph's launches address
+ * (another stream's calls do not).  Calls on one stream are ordered;
  * calls on different streams use different workspaces.  Any number of host
  * threads may call, on one stream too: the launches of a call follow one
  * another on its stream, whatever other threads do.

@@ -12,6 +12,7 @@
 #include <mutex>
 #include <shared_mutex>
 #include <utility>
+#include <vector>
 
 #include "../../include/qmm.h"
 #include "qmm_device.cuh"
@@ -77,9 +78,11 @@ std::map<std::pair<int, cudaStream_t>, std::mutex> g_stream_mu;
 thread_local int t_calls = 0;  // calls of this thread that hold the locks (qmm_group and qmm_gate_up call qmm)
 std::map<int, DeviceInfo> g_dev;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
-// qmm_t's per-matrix completion counters, per (device, stream): zero between
-// calls (each call's last CTA of a matrix resets its counter)
+// completion counters of qmm_t's matrices and of the 8-bit-float products' cut
+// tiles, per (device, stream): zero between calls (the last CTA of a matrix or
+// tile resets its counter)
 std::map<std::pair<int, cudaStream_t>, Workspace> g_counters;
+std::vector<std::pair<int, Workspace>> g_old_counters;  // outgrown ones, with their device
 // qmm_gate_up's intermediate products g (and u), per (device, stream)
 std::map<std::pair<int, cudaStream_t>, Workspace> g_gate;
 
@@ -164,8 +167,8 @@ int gate_buffer(int dev, cudaStream_t st, size_t bytes, float **ptr) {
     return QMM_OK;
 }
 
-// At least n zeroed counters for (dev, stream).  Growing synchronises the
-// stream before the old array is released; the new one is zeroed on it.
+// At least n zeroed counters for (dev, stream).  Where they grow the old array
+// stays (a captured graph may hold its address), a few KB until qmm_release.
 int counters(int dev, cudaStream_t st, int64_t n, unsigned **ptr) {
     std::lock_guard<std::mutex> lk(g_mu);
     Workspace &w = g_counters[{dev, st}];
@@ -176,18 +179,15 @@ int counters(int dev, cudaStream_t st, int64_t n, unsigned **ptr) {
     }
     size_t want = 4096;
     while (want < bytes) want *= 2;
-    if (w.ptr) {
-        cudaError_t e = cudaStreamSynchronize(st);
-        if (e != cudaSuccess) return cuda_fail(e, "counters grow (sync)");
-        cudaFree(w.ptr);
-        w.ptr = nullptr;
-        w.bytes = 0;
-    }
-    cudaError_t e = device_alloc(&w.ptr, want);
+    Workspace grown = {nullptr, want};
+    cudaError_t e = device_alloc(&grown.ptr, want);
     if (e != cudaSuccess) return fail(QMM_ENOMEM, "counters of %zu bytes: %s", want, cudaGetErrorString(e));
-    e = cudaMemsetAsync(w.ptr, 0, want, st);
-    if (e != cudaSuccess) return cuda_fail(e, "counters init");
-    w.bytes = want;
+    if ((e = cudaMemsetAsync(grown.ptr, 0, want, st)) != cudaSuccess) {
+        cudaFree(grown.ptr);
+        return cuda_fail(e, "counters init");
+    }
+    if (w.ptr) g_old_counters.push_back({dev, w});
+    w = grown;
     *ptr = static_cast<unsigned *>(w.ptr);
     return QMM_OK;
 }
@@ -777,6 +777,8 @@ int qmm_device_status(void *stream) {
             for (auto &c : g_counters)
                 if (e == cudaSuccess && c.first.first == dev && c.second.ptr)
                     e = cudaMemset(c.second.ptr, 0, c.second.bytes);
+            for (auto &c : g_old_counters)
+                if (e == cudaSuccess && c.first == dev) e = cudaMemset(c.second.ptr, 0, c.second.bytes);
         }
         if (e == cudaSuccess) e = cudaDeviceSynchronize();
         if (e != cudaSuccess) return cuda_fail(e, "status clear");
@@ -803,6 +805,14 @@ int qmm_release(void) {
             } else {
                 ++it;
             }
+        }
+    }
+    for (auto it = g_old_counters.begin(); it != g_old_counters.end();) {
+        if (it->first == dev) {
+            cudaFree(it->second.ptr);
+            it = g_old_counters.erase(it);
+        } else {
+            ++it;
         }
     }
     return QMM_OK;
