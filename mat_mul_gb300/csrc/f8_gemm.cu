@@ -657,12 +657,12 @@ template <bool DUAL>
 cudaError_t launch_any(const F8Gemm &g, cudaStream_t st, int num_sms) {
     if constexpr (!DUAL)
         if (!g.xq) return launch_bt<16, false, true>(g, st, num_sms);
-    if (const int w = path_of(g.R, g.E, g.N, g.offsets != nullptr, num_sms)) return launch_f8_wide(g, w == 2, st, num_sms);
-    switch (tile_tokens(g.R, g.E)) {
-    case 16: return launch_bt<16, DUAL>(g, st, num_sms);
-    case 32: return launch_bt<32, DUAL>(g, st, num_sms);
-    default: return launch_bt<64, DUAL>(g, st, num_sms);
-    }
+    if (const int w = path_of(g.R, g.E, g.N, g.offsets != nullptr, num_sms)) return launch_f8_wide(g, w, st, num_sms);
+    const int bt = tile_tokens(g.R, g.E);
+    if (bt == 16) return launch_bt<16, DUAL>(g, st, num_sms);
+    if constexpr (!DUAL)
+        if (bt == 64) return launch_bt<64, false>(g, st, num_sms);
+    return launch_bt<32, DUAL>(g, st, num_sms);  // (the gated pair always has row groups: a mean of 24 at most)
 }
 
 }  // namespace

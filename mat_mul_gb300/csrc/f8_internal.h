@@ -80,10 +80,10 @@ struct F8Gemm {
 bool f8_fuses(int64_t R, int64_t N, int64_t K, int num_sms);
 size_t f8_part_bytes(int64_t R, int E, int64_t N, bool dual, bool grouped, int num_sms);
 bool f8_available();
-// The product with the tokens as TMEM lanes (f8_wide.cu), on single CTAs or on
-// pairs; launch_f8_gemm takes it for groups of many rows.
+// The product with the tokens as TMEM lanes (f8_wide.cu), on single CTAs or, for
+// one matrix, on pairs; launch_f8_gemm takes it for groups of many rows.
 size_t f8_wide_part_bytes(int num_sms);
-cudaError_t launch_f8_wide(const F8Gemm &g, int pair, cudaStream_t st, int num_sms);
+cudaError_t launch_f8_wide(const F8Gemm &g, int ctas, cudaStream_t st, int num_sms);
 cudaError_t launch_f8_gemm(const F8Gemm &g, cudaStream_t st, int num_sms);
 
 // The router (qmm_route).  hist: f8_route_hist_bytes() of scratch.

@@ -43,6 +43,7 @@ constexpr long long DRAIN_CYCLES = 1 << 21;   // about a millisecond
 
 template <int CG, bool DUAL>
 struct Wide {
+    static_assert(CG == 1 || !DUAL, "the gated pair has row groups, whose ragged ends the 256 rows of CTA pairs would waste");
     // Epilogue warps per TMEM lane quarter (each has its share of the columns)
     // and the registers they get.  Two warps of 128 accumulators per thread
     // measured faster than four of 64 for one matrix (8192 rows of 40 experts 95
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(Wide<CG, DUAL>::THREADS, 1)
                     } else {
                         if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * C::STAGE);
                         tma_2d_pair(st, &tmX, k * BK, tok, b);
-                        tma_2d_pair(st + C::A_BYTES, DUAL && rank ? &tmW2 : &tmW, k * BK, DUAL || !rank ? w0 : w0 + 128, b);
+                        tma_2d_pair(st + C::A_BYTES, &tmW, k * BK, rank ? w0 + 128 : w0, b);
                     }
                 }
             }
@@ -695,9 +696,9 @@ cudaError_t launch_wide(const F8Gemm &g, cudaStream_t st, int num_sms) {
 
 size_t f8_wide_part_bytes(int num_sms) { return static_cast<size_t>(num_sms) * 2 * PART * sizeof(float); }
 
-cudaError_t launch_f8_wide(const F8Gemm &g, int pair, cudaStream_t st, int num_sms) {
-    if (pair) return g.W2 ? launch_wide<2, true>(g, st, num_sms) : launch_wide<2, false>(g, st, num_sms);
-    return g.W2 ? launch_wide<1, true>(g, st, num_sms) : launch_wide<1, false>(g, st, num_sms);
+cudaError_t launch_f8_wide(const F8Gemm &g, int ctas, cudaStream_t st, int num_sms) {
+    if (g.W2) return launch_wide<1, true>(g, st, num_sms);
+    return ctas == 2 ? launch_wide<2, false>(g, st, num_sms) : launch_wide<1, false>(g, st, num_sms);
 }
 
 }  // namespace qk

@@ -39,6 +39,12 @@ static const char *name_of(const void *fun) {
 void fake_set(size_t most_bytes, int status, int us) { limit = most_bytes, status_word = status, launch_us = us; }
 void fake_registers(int n) { registers = n; }
 int fake_last_error(void) { return last_error; }
+/* Names of the library's kernels, one per line. */
+size_t fake_kernels(char *out, size_t n) {
+    size_t m = 0;
+    for (int i = 0; i < n_kernels && m + 161 < n; ++i) m += (size_t)snprintf(out + m, n - m, "%s\n", kernels[i].name);
+    return m;
+}
 size_t fake_log(char *out, size_t n) {
     pthread_mutex_lock(&mu);
     size_t m = used < n ? used : n;

@@ -31,6 +31,13 @@ def log(kind=None):
         out.append((int(w[0]), w[1], w[2], int(w[3], 16), int(w[4], 16)))
     return [e for e in out if kind is None or e[1] == kind]
 
+def kernels():
+    "Every kernel that the library holds."
+    buf = ctypes.create_string_buffer(1 << 18)
+    fake.fake_kernels.restype = ctypes.c_size_t
+    n = fake.fake_kernels(buf, ctypes.c_size_t(len(buf)))
+    return buf.raw[:n].decode().split()
+
 def f8(M, N, K, st=ST):
     return L.qmm_f8(A, A, N, K, 2, A, M, K, 2, A, N, st)
 
