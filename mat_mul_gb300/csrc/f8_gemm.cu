@@ -657,12 +657,16 @@ template <bool DUAL>
 cudaError_t launch_any(const F8Gemm &g, cudaStream_t st, int num_sms) {
     if constexpr (!DUAL)
         if (!g.xq) return launch_bt<16, false, true>(g, st, num_sms);
-    if (const int w = path_of(g.R, g.E, g.N, g.offsets != nullptr, num_sms)) return launch_f8_wide(g, w, st, num_sms);
+    if (const int w = path_of(g.R, g.E, g.N, g.offsets != nullptr, num_sms)) {
+        // (not supported: a build of that kernel with too few registers; its partial tiles take more memory than here)
+        const cudaError_t e = launch_f8_wide(g, w, st, num_sms);
+        if (e != cudaErrorNotSupported) return e;
+    }
     const int bt = tile_tokens(g.R, g.E);
     if (bt == 16) return launch_bt<16, DUAL>(g, st, num_sms);
     if constexpr (!DUAL)
         if (bt == 64) return launch_bt<64, false>(g, st, num_sms);
-    return launch_bt<32, DUAL>(g, st, num_sms);  // (the gated pair always has row groups: a mean of 24 at most)
+    return launch_bt<32, DUAL>(g, st, num_sms);  // (the gated pair always has row groups, of 24 in the mean at most)
 }
 
 }  // namespace

@@ -82,6 +82,7 @@ size_t f8_part_bytes(int64_t R, int E, int64_t N, bool dual, bool grouped, int n
 bool f8_available();
 // The product with the tokens as TMEM lanes (f8_wide.cu), on single CTAs or, for
 // one matrix, on pairs; launch_f8_gemm takes it for groups of many rows.
+// cudaErrorNotSupported where the build gave it too few registers.
 size_t f8_wide_part_bytes(int num_sms);
 cudaError_t launch_f8_wide(const F8Gemm &g, int ctas, cudaStream_t st, int num_sms);
 cudaError_t launch_f8_gemm(const F8Gemm &g, cudaStream_t st, int num_sms);

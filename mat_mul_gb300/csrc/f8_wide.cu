@@ -672,11 +672,11 @@ cudaError_t launch_wide(const F8Gemm &g, cudaStream_t st, int num_sms) {
     const cudaError_t e = ready(g.dev, [&] {
         cudaError_t r = set_smem_attrs(kern, C::SMEM);
         if (r != cudaSuccess) return r;
-        // the register split needs what the launch brings: a build with fewer
-        // registers per thread would wait for them forever
+        // setmaxnreg draws on what the launch brings: with fewer registers than
+        // the split hands out the epilogue would wait for them forever
         cudaFuncAttributes fa;
         if ((r = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return r;
-        if (fa.numRegs != C::REGS) return cudaErrorInvalidConfiguration;
+        if (fa.numRegs * C::THREADS < 128 * C::REGS_LOW + C::EPI_THREADS * C::REGS_HIGH) return cudaErrorNotSupported;
         int groups = num_sms / CG;
         if (CG == 2) {
             int fit = 0;
