@@ -323,9 +323,12 @@ QMM_API int qmm_f8_experts(const void *W, const float *S, int64_t E, int64_t N, 
  * with the largest logits in falling order (ties: the lowest index; NaN counts
  * as -inf; a token may choose experts at -inf when fewer than k others are
  * left, their weight is 0), their weights, and the pairs (t, j) sorted by
- * expert, pairs of one expert in order of t.
+ * expert, pairs of one expert in order of t.  +inf is the largest logit; the
+ * softmax of a row with one has no value, its weights are NaN.
  *   score     : QMM_ROUTE_SOFTMAX over all E logits, or QMM_ROUTE_SIGMOID.
- *   normalize : divide the k weights by their sum (a sum of 0 leaves them 0).
+ *   normalize : divide the k weights by their sum, also where each is below the
+ *               smallest float (all scores 0 leave them 0: logits of -inf, or
+ *               sigmoids below e^-811).
  *   factor    : multiplies the weights.
  *   logits    : device [T] rows of E values of type x_type, ldx apart.
  *   weights, experts : device [T][k] fp32 / int32.

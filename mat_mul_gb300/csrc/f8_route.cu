@@ -82,7 +82,7 @@ __device__ __forceinline__ int choose(const RouteParams &P, int64_t t, int lane)
         }
     }
     int mine = 0;
-    uint32_t mine_key = 0;
+    uint32_t mine_key = 0, first_key = 0;
     for (int j = 0; j < P.k; ++j) {
         uint32_t m = 0;
 #pragma unroll
@@ -97,10 +97,22 @@ __device__ __forceinline__ int choose(const RouteParams &P, int64_t t, int lane)
         for (int i = 0; i < VPL; ++i)
             if (at == static_cast<unsigned>(lane + 32 * i)) key[i] = 0u;
         if (lane == j) mine = static_cast<int>(at), mine_key = m;
+        if (j == 0) first_key = m;
     }
     const float v = key_value(mine_key);
     float w = 0.0f;
-    if (lane < P.k) w = P.score == QMM_ROUTE_SOFTMAX ? expf(v - top) : __fdiv_rn(1.0f, 1.0f + expf(-v));
+    if (lane < P.k) {
+        if (P.score == QMM_ROUTE_SOFTMAX) {
+            w = expf(v - top);
+        } else if (v > 0.0f) {
+            w = __fdiv_rn(1.0f, 1.0f + expf(-v));
+        } else {
+            // e^v / (1 + e^v).  Where all of them are tiny their quotients by the sum need not be: then all are
+            // multiplied by e^-first (a token whose scores are below the smallest 64-bit float keeps weights of 0)
+            const float shift = P.normalize ? fmaxf(fminf(key_value(first_key), 0.0f), -708.0f) : 0.0f;
+            w = __fdiv_rn(expf(v - shift), 1.0f + expf(v));
+        }
+    }
     float total = P.normalize ? warp_sum(w) : P.score == QMM_ROUTE_SOFTMAX ? rest : 1.0f;
     if (total != 0.0f) w = __fdiv_rn(w, total);
     if (lane < P.k) {
