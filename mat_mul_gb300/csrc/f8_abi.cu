@@ -248,14 +248,14 @@ int qmm_route(int x_type, const void *logits, int64_t T, int64_t E, int64_t ldx,
     if (int rc = qk::f8_context(c)) return rc;
     const qk::CallLock lock(c.dev, st);
     void *hist = nullptr;
-    if (const size_t bytes = qk::f8_route_hist_bytes(T, static_cast<int>(E)))
+    if (const size_t bytes = qk::f8_route_hist_bytes(T, static_cast<int>(E), c.num_sms))
         if (int rc = qk::f8_workspace(c, st, bytes, &hist)) return rc;
     const qk::F8Route r = {x_type,  logits,  T,       T > 1 ? ldx : E, static_cast<int>(E), k,
                            score,   normalize, factor, weights, experts, offsets, rows, slots,
                            static_cast<int32_t *>(hist), c.dev};
-    const cudaError_t e = qk::launch_f8_route(r, st);
+    const cudaError_t e = qk::launch_f8_route(r, st, c.num_sms);
     if (e != cudaSuccess) return cuda_error(e, "route launch");
-    qk::count_launches(qk::f8_route_launches(T, static_cast<int>(E)));
+    qk::count_launches(qk::f8_route_launches(T, static_cast<int>(E), c.num_sms));
     return QMM_OK;
 }
 

@@ -99,9 +99,9 @@ struct F8Route {
     int32_t *hist;
     int dev;
 };
-size_t f8_route_hist_bytes(int64_t T, int E);
-int f8_route_launches(int64_t T, int E);
-cudaError_t launch_f8_route(const F8Route &r, cudaStream_t st);
+size_t f8_route_hist_bytes(int64_t T, int E, int num_sms);
+int f8_route_launches(int64_t T, int E, int num_sms);
+cudaError_t launch_f8_route(const F8Route &r, cudaStream_t st, int num_sms);
 
 // y[t] = sum_j w[t*k+j] * d[slots[t*k+j]] in j order, d [R][ldd] fp32; slots
 // outside [0, R) raise STATUS_INDEX and count as zero rows.

@@ -300,25 +300,34 @@ cudaError_t launch(K kern, int64_t blocks, int threads, cudaStream_t st, A... ar
 
 }  // namespace
 
-// One token per warp while that keeps the histograms few, then four (1024 tokens
-// of 128 experts: 16.5 -> 10 us with one).
-static int tokens_per_cta(int64_t T) { return T <= FUSED ? FUSED : T <= 2432 ? WARPS : TOKENS; }
+// One token per warp as long as that gives every SM at most one CTA, so that the
+// histograms stay few, then four (1024 tokens of 128 experts: 16.5 -> 10 us with
+// one).
+static int tokens_per_cta(int64_t T, int num_sms) {
+    return T <= FUSED ? FUSED : T <= static_cast<int64_t>(num_sms) * WARPS ? WARPS : TOKENS;
+}
 
-static int64_t ctas(int64_t T) { return (T + tokens_per_cta(T) - 1) / tokens_per_cta(T); }
+static int64_t ctas(int64_t T, int num_sms) {
+    const int per = tokens_per_cta(T, num_sms);
+    return (T + per - 1) / per;
+}
 // Every CTA of the second launch reads all histograms, ctas^2 * E words in all: from
 // 32 MB on a launch in between sums them up once (16384 tokens of 256 experts 67 ->
 // 41 us; of 64 experts, 17 MB, it took 24.7 against 22.3).
-static bool scanned(int64_t T, int E) { return T > FUSED && ctas(T) * ctas(T) * E >= int64_t(1) << 23; }
-
-size_t f8_route_hist_bytes(int64_t T, int E) {
-    return T <= FUSED ? 0 : static_cast<size_t>(ctas(T) + 1) * E * sizeof(int32_t);
+static bool scanned(int64_t T, int E, int num_sms) {
+    return T > FUSED && ctas(T, num_sms) * ctas(T, num_sms) * E >= int64_t(1) << 23;
 }
-int f8_route_launches(int64_t T, int E) { return T <= FUSED ? 1 : scanned(T, E) ? 3 : 2; }
 
-cudaError_t launch_f8_route(const F8Route &r, cudaStream_t st) {
+size_t f8_route_hist_bytes(int64_t T, int E, int num_sms) {
+    return T <= FUSED ? 0 : static_cast<size_t>(ctas(T, num_sms) + 1) * E * sizeof(int32_t);
+}
+int f8_route_launches(int64_t T, int E, int num_sms) { return T <= FUSED ? 1 : scanned(T, E, num_sms) ? 3 : 2; }
+
+cudaError_t launch_f8_route(const F8Route &r, cudaStream_t st, int num_sms) {
     RouteParams p = {r.x,      r.T,       r.ldx,     r.x_type,  r.E,    r.k,     r.score, r.normalize,
-                     r.T <= FUSED, tokens_per_cta(r.T), scanned(r.T, r.E), r.factor, r.weights, r.experts, r.offsets, r.rows, r.slots, r.hist};
-    const int64_t blocks = ctas(r.T);
+                     r.T <= FUSED, tokens_per_cta(r.T, num_sms), scanned(r.T, r.E, num_sms), r.factor, r.weights, r.experts, r.offsets,
+                     r.rows, r.slots, r.hist};
+    const int64_t blocks = ctas(r.T, num_sms);
     static OncePerDevice ready;
     cudaError_t e = ready(r.dev, [] {
         cudaError_t q = prefer_max_shared(route_place_kernel);

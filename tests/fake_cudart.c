@@ -16,7 +16,7 @@ static char text[1 << 20];
 static size_t used;
 static size_t next_address = 0x700000000000ull;
 static size_t limit = (size_t)1 << 38;
-static int last_error, device, status_word, launch_us, registers = 0;
+static int last_error, device, status_word, launch_us, registers = 0, sms = 152;
 static struct { const void *fun; char name[160]; } kernels[1024];
 static int n_kernels;
 static _Thread_local int thread_id;
@@ -38,6 +38,7 @@ static const char *name_of(const void *fun) {
 /* What a test sets and reads. */
 void fake_set(size_t most_bytes, int status, int us) { limit = most_bytes, status_word = status, launch_us = us; }
 void fake_registers(int n) { registers = n; }
+void fake_multiprocessors(int n) { sms = n; }  /* before the first call */
 int fake_last_error(void) { return last_error; }
 /* Names of the library's kernels, one per line. */
 size_t fake_kernels(char *out, size_t n) {
@@ -72,7 +73,7 @@ void __cudaRegisterVar(void **f, char *h, char *a, const char *n, int e, size_t 
 int cudaGetDevice(int *d) { *d = device; return SUCCESS; }
 int cudaDeviceGetAttribute(int *v, int attr, int d) {
     (void)d;
-    *v = attr == 16 ? 152 : 232448;  /* multiprocessors; opt-in shared memory */
+    *v = attr == 16 ? sms : 232448;  /* multiprocessors; opt-in shared memory */
     return SUCCESS;
 }
 int cudaMalloc(void **p, size_t n) {
