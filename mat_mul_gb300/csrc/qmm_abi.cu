@@ -68,6 +68,16 @@ struct Workspace {
     size_t bytes = 0;
 };
 
+// What the maps know a stream by: its handle, but the per-thread default stream
+// has one handle and another stream in every thread.  (No handle is odd but for
+// the two of the default streams.)
+std::atomic<uintptr_t> g_threads{0};
+cudaStream_t stream_key(cudaStream_t st) {
+    if (st != cudaStreamPerThread) return st;
+    thread_local const uintptr_t mine = 2 * ++g_threads + 1;
+    return reinterpret_cast<cudaStream_t>(mine);
+}
+
 // g_mu guards the maps, for the time of a look-up.  A whole call is guarded by
 // qk::CallLock: shared on g_calls, then its stream's mutex in g_stream_mu
 // (entries are never erased).  Locks are taken in the order g_calls, stream,
@@ -124,7 +134,7 @@ int device_info(int dev, DeviceInfo &out) {
 // functions below hold a qk::CallLock of the stream.
 int workspace(int dev, cudaStream_t st, size_t bytes, void **ptr) {
     std::lock_guard<std::mutex> lk(g_mu);
-    Workspace &w = g_ws[{dev, st}];
+    Workspace &w = g_ws[{dev, stream_key(st)}];
     if (w.bytes >= bytes) {
         *ptr = w.ptr;
         return QMM_OK;
@@ -149,7 +159,7 @@ int workspace(int dev, cudaStream_t st, size_t bytes, void **ptr) {
 // growing synchronises the stream before the old buffer is released.
 int gate_buffer(int dev, cudaStream_t st, size_t bytes, float **ptr) {
     std::lock_guard<std::mutex> lk(g_mu);
-    Workspace &w = g_gate[{dev, st}];
+    Workspace &w = g_gate[{dev, stream_key(st)}];
     if (w.bytes < bytes) {
         if (w.ptr) {
             cudaError_t e = cudaStreamSynchronize(st);
@@ -171,7 +181,7 @@ int gate_buffer(int dev, cudaStream_t st, size_t bytes, float **ptr) {
 // stays (a captured graph may hold its address), a few KB until qmm_release.
 int counters(int dev, cudaStream_t st, int64_t n, unsigned **ptr) {
     std::lock_guard<std::mutex> lk(g_mu);
-    Workspace &w = g_counters[{dev, st}];
+    Workspace &w = g_counters[{dev, stream_key(st)}];
     const size_t bytes = static_cast<size_t>(n) * sizeof(unsigned);
     if (w.bytes >= bytes) {
         *ptr = static_cast<unsigned *>(w.ptr);
@@ -229,7 +239,7 @@ CallLock::CallLock(int dev, cudaStream_t st) : stream_mu(nullptr) {
     std::mutex *m;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        m = &g_stream_mu[{dev, st}];
+        m = &g_stream_mu[{dev, stream_key(st)}];
     }
     m->lock();
     stream_mu = m;
