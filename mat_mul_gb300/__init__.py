@@ -29,6 +29,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import functools
 import os
 
 Q8_0, Q4_K, Q6_K, Q5_K, Q3_K, Q2_K = 0, 1, 2, 3, 4, 5  # Q5_K, Q3_K, Q2_K: qmm_dequant only so far
@@ -133,10 +134,15 @@ def _ptr(t):
 
 # The library works on the current device: its workspaces, its status word and
 # its launches are there.  Tensors and streams of another one are refused.
+_torch = None
+
+
 def _current_device():
-    import torch
-    get = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-    return get()
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch._C._cuda_getDevice()  # (torch.cuda.current_device() without its look-ups: every call comes here)
 
 
 def _refuse_device(t, current):
@@ -144,31 +150,31 @@ def _refuse_device(t, current):
                      f"torch.cuda.device({t.get_device()})")
 
 
-def _require_stream(stream, current):
+def _given_stream(stream, current):
     if getattr(stream, "device_index", current) != current:
         raise ValueError(f"a stream of cuda:{stream.device_index}, but cuda:{current} is the current device")
+    return stream.cuda_stream
 
 
 def _stream_handle(stream):
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
-    else:
-        _require_stream(stream, _current_device())
-    return ctypes.c_void_p(stream.cuda_stream)
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return ctypes.c_void_p(_given_stream(stream, _current_device()))
 
 
 def _require_cuda(*ts):
     current = None
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("libqmm takes device tensors; got a tensor on " + str(t.device))
-        if current is None:
-            current = _current_device()
-        if t.get_device() != current:
-            _refuse_device(t, current)
+        if t is not None:
+            d = t.get_device()
+            if d != current:
+                if d < 0:
+                    raise ValueError("libqmm takes device tensors; got a tensor on " + str(t.device))
+                if current is None:
+                    current = _current_device()
+                if d != current:
+                    _refuse_device(t, current)
 
 
 def qmm_dequant(qtype: int, blocks, n_elems: int, out=None):
@@ -318,19 +324,12 @@ class _F8:
         self.codes = (torch.float8_e4m3fn, torch.uint8)
         self.ftypes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # qmm_ftype
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self.current_stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
-        self.current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        self.stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        self.current_device = torch._C._cuda_getDevice
 
-    def stream(self, dev, stream):
-        """The handle of `stream`, or of the current one, on the current device `dev`."""
-        if stream is None:
-            return self.current_stream(dev)
-        _require_stream(stream, dev)
-        return stream.cuda_stream
-
-    def new(self, shape, dtype, device, stream):
-        """_empty(), without its look-ups where the current stream is meant."""
-        return self.empty(shape, dtype=dtype, device=device) if stream is None else _empty(shape, dtype, device, stream)
+    def on(self, stream):
+        """torch.empty on a call's stream."""
+        return self.empty if stream is None else functools.partial(_empty, stream=stream)
 
     def ftype(self, dtype, what):
         t = self.ftypes.get(dtype)
@@ -389,7 +388,7 @@ def _f8_weights(f, W, S, dims, what):
 def _f8_out(f, y, rows, cols, dtype, device, stream):
     """The result tensor and its row pitch: y checked, or a new one."""
     if y is None:
-        return f.new((rows, cols), dtype, device, stream), cols
+        return f.on(stream)((rows, cols), dtype=dtype, device=device), cols
     r, c, ldy = _rows2d(y, "y")
     if r != rows or c != cols:
         raise ValueError(f"y has shape {tuple(y.shape)}, expected {(rows, cols)}")
@@ -409,10 +408,11 @@ def qmm_f8_quantize(x, stream=None):
     M, K, ldx = _rows2d(x, "x")
     ft = f.ftype(x.dtype, "x")
     device = x.device
-    c = f.new((M, K), f.e4m3, device, stream)
-    s = f.new((M, -(-K // F8_BLOCK)), f.float32, device, stream)
+    empty = f.on(stream)
+    c = empty((M, K), dtype=f.e4m3, device=device)
+    s = empty((M, -(-K // F8_BLOCK)), dtype=f.float32, device=device)
     rc = f.lib.qmm_f8_quantize(ft, x.data_ptr(), M, K, ldx, c.data_ptr(), s.data_ptr(),
-                               f.stream(dev, stream))
+                               f.stream(dev) if stream is None else _given_stream(stream, dev))
     if rc:
         _check(rc)
     return c, s
@@ -433,7 +433,7 @@ def qmm_f8(W, S, x, y=None, dtype=None, stream=None):
     ft = f.ftype(xt, "x")
     y, ldy = _f8_out(f, y, M, N, dtype or xt, x.device, stream)
     rc = f.lib.qmm_f8(W.data_ptr(), S.data_ptr(), N, K, ft, x.data_ptr(), M, ldx, f.ftype(y.dtype, "y"), y.data_ptr(),
-                      ldy, f.stream(dev, stream))
+                      ldy, f.stream(dev) if stream is None else _given_stream(stream, dev))
     if rc:
         _check(rc)
     return y
@@ -461,7 +461,7 @@ def qmm_f8_experts(W, S, x, offsets, rows=None, y=None, dtype=None, stream=None)
     y, ldy = _f8_out(f, y, R, N, dtype or xt, x.device, stream)
     rc = f.lib.qmm_f8_experts(W.data_ptr(), S.data_ptr(), E, N, K, ft, x.data_ptr(), M, ldx, offsets.data_ptr(), index, R,
                               f.ftype(y.dtype, "y"), y.data_ptr(), ldy,
-                              f.stream(dev, stream))
+                              f.stream(dev) if stream is None else _given_stream(stream, dev))
     if rc:
         _check(rc)
     return y
@@ -484,16 +484,16 @@ def qmm_route(logits, k, score="softmax", normalize=True, factor=1.0, stream=Non
         raise ValueError(f"score must be one of {sorted(_SCORES)}, not {score!r}")
     k = int(k)
     n = k if k > 0 else 0
-    ft, device, i32 = f.ftype(logits.dtype, "logits"), logits.device, f.int32
-    weights = f.new((T, n), f.float32, device, stream)
+    ft, device, empty, i32 = f.ftype(logits.dtype, "logits"), logits.device, f.on(stream), f.int32
+    weights = empty((T, n), dtype=f.float32, device=device)
     # (five allocations: views of one buffer cost more than twice as much)
-    experts = f.new((T, n), i32, device, stream)
-    slots = f.new((T, n), i32, device, stream)
-    rows = f.new(T * n, i32, device, stream)
-    offsets = f.new(E + 1, i32, device, stream)
+    experts = empty((T, n), dtype=i32, device=device)
+    slots = empty((T, n), dtype=i32, device=device)
+    rows = empty(T * n, dtype=i32, device=device)
+    offsets = empty(E + 1, dtype=i32, device=device)
     rc = f.lib.qmm_route(ft, logits.data_ptr(), T, E, ld, k, _SCORES[score], 1 if normalize else 0, factor,
                          weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
-                         f.stream(dev, stream))
+                         f.stream(dev) if stream is None else _given_stream(stream, dev))
     if rc:
         _check(rc)
     return Route(weights, experts, offsets, rows, slots)
@@ -526,7 +526,7 @@ def qmm_f8_moe(x, route, W_gate, S_gate, W_up, S_up, W_down, S_down, y=None, dty
     rc = f.lib.qmm_f8_moe(ft, x.data_ptr(), T, H, ldx, k, weights.data_ptr(), offsets.data_ptr(), slots.data_ptr(), E, I,
                           W_gate.data_ptr(), S_gate.data_ptr(), W_up.data_ptr(), S_up.data_ptr(), W_down.data_ptr(),
                           S_down.data_ptr(), f.ftype(y.dtype, "y"), y.data_ptr(), ldy,
-                          f.stream(dev, stream))
+                          f.stream(dev) if stream is None else _given_stream(stream, dev))
     if rc:
         _check(rc)
     return y

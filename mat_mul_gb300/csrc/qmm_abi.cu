@@ -10,7 +10,6 @@
 #include <cstring>
 #include <map>
 #include <mutex>
-#include <shared_mutex>
 #include <utility>
 #include <vector>
 
@@ -79,13 +78,16 @@ cudaStream_t stream_key(cudaStream_t st) {
 }
 
 // g_mu guards the maps, for the time of a look-up.  A whole call is guarded by
-// qk::CallLock: shared on g_calls, then its stream's mutex in g_stream_mu
-// (entries are never erased).  Locks are taken in the order g_calls, stream,
-// g_mu.
+// its stream's mutex (qk::CallLock), taken before g_mu; entries are never erased,
+// so that a thread can remember the one it used last.
 std::mutex g_mu;
-std::shared_mutex g_calls;
 std::map<std::pair<int, cudaStream_t>, std::mutex> g_stream_mu;
-thread_local int t_calls = 0;  // calls of this thread that hold the locks (qmm_group and qmm_gate_up call qmm)
+thread_local struct {
+    int calls = 0;  // calls of this thread that hold the lock (qmm_group and qmm_gate_up call qmm)
+    int dev = -1;
+    cudaStream_t key = nullptr;
+    std::mutex *mu = nullptr;  // of (dev, key)
+} t_lock;
 std::map<int, DeviceInfo> g_dev;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
 // completion counters of qmm_t's matrices and of the 8-bit-float products' cut
@@ -202,6 +204,30 @@ int counters(int dev, cudaStream_t st, int64_t n, unsigned **ptr) {
     return QMM_OK;
 }
 
+// The locks of every stream of a device on which a call was made: none of them
+// is between its launches.  (Taken in the order of the map, g_mu not held.)
+struct AllStreams {
+    std::vector<cudaStream_t> keys;
+    std::vector<std::unique_lock<std::mutex>> locks;
+    explicit AllStreams(int dev) {
+        std::vector<std::mutex *> mus;
+        {
+            std::lock_guard<std::mutex> lk(g_mu);
+            for (auto &m : g_stream_mu)
+                if (m.first.first == dev) {
+                    keys.push_back(m.first.second);
+                    mus.push_back(&m.second);
+                }
+        }
+        for (std::mutex *m : mus) locks.emplace_back(*m);
+    }
+    bool holds(cudaStream_t key) const {
+        for (cudaStream_t k : keys)
+            if (k == key) return true;
+        return false;
+    }
+};
+
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // The products (qmm, qmm_group, qmm_gate_up) take every type of the enum;
@@ -233,21 +259,19 @@ int inject_stop_stage() {
     return NO_STOP;
 }
 void clear_error() { g_err[0] = 0; }
-CallLock::CallLock(int dev, cudaStream_t st) : stream_mu(nullptr) {
-    if (t_calls++) return;
-    g_calls.lock_shared();
-    std::mutex *m;
-    {
+CallLock::CallLock(int dev, cudaStream_t st) {
+    if (t_lock.calls++) return;
+    const cudaStream_t key = stream_key(st);
+    if (!t_lock.mu || t_lock.dev != dev || t_lock.key != key) {
         std::lock_guard<std::mutex> lk(g_mu);
-        m = &g_stream_mu[{dev, stream_key(st)}];
+        t_lock.mu = &g_stream_mu[{dev, key}];
+        t_lock.dev = dev;
+        t_lock.key = key;
     }
-    m->lock();
-    stream_mu = m;
+    t_lock.mu->lock();
 }
 CallLock::~CallLock() {
-    if (--t_calls) return;
-    stream_mu->unlock();
-    g_calls.unlock_shared();
+    if (--t_lock.calls == 0) t_lock.mu->unlock();
 }
 int f8_context(F8Context &c) {
     const cudaError_t e = cudaGetDevice(&c.dev);
@@ -775,7 +799,7 @@ int qmm_device_status(void *stream) {
         // when this returns: cudaMemset of device memory comes back before it
         // is, and streams that do not wait for the default one would not
         // either.  (No call is between its launches meanwhile.)
-        std::unique_lock<std::shared_mutex> calls(g_calls);
+        const AllStreams all(dev);
         e = cudaDeviceSynchronize();
         int late = 0;
         if (e == cudaSuccess) e = cudaMemcpy(&late, di.status, sizeof late, cudaMemcpyDeviceToHost);
@@ -785,7 +809,7 @@ int qmm_device_status(void *stream) {
             // a launch that gave up may have left completion counters behind
             std::lock_guard<std::mutex> lk(g_mu);
             for (auto &c : g_counters)
-                if (e == cudaSuccess && c.first.first == dev && c.second.ptr)
+                if (e == cudaSuccess && c.first.first == dev && c.second.ptr && all.holds(c.first.second))
                     e = cudaMemset(c.second.ptr, 0, c.second.bytes);
             for (auto &c : g_old_counters)
                 if (e == cudaSuccess && c.first == dev) e = cudaMemset(c.second.ptr, 0, c.second.bytes);
@@ -803,13 +827,14 @@ int qmm_release(void) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    std::unique_lock<std::shared_mutex> calls(g_calls);
+    const AllStreams all(dev);
     e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "device synchronize");
     std::lock_guard<std::mutex> lk(g_mu);
     for (auto *m : {&g_ws, &g_counters, &g_gate}) {
         for (auto it = m->begin(); it != m->end();) {
-            if (it->first.first == dev) {
+            // (a stream whose first call came meanwhile keeps its buffers)
+            if (it->first.first == dev && all.holds(it->first.second)) {
                 cudaFree(it->second.ptr);
                 it = m->erase(it);
             } else {

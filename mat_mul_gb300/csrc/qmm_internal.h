@@ -6,8 +6,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <mutex>
-
 namespace qk {
 
 // Output layout of the quantiser.  q rows have stride q_ld bytes; with
@@ -66,9 +64,6 @@ class CallLock {
     ~CallLock();
     CallLock(const CallLock &) = delete;
     CallLock &operator=(const CallLock &) = delete;
-
-  private:
-    std::mutex *stream_mu;  // null in a nested call
 };
 
 // cuTensorMapEncodeTiled from the driver (null when it cannot be found).
