@@ -126,19 +126,25 @@ __device__ __forceinline__ float silu(float g) {
 __device__ __forceinline__ void count_tiles(int *cum, const int32_t *offsets, int E, int R, int tokens, int nb, int lane,
                                             int *status) {
     int base = 0, highest = 0;
+    bool fallen = false;  // an offset below the one before it
     for (int e0 = 0; e0 < E; e0 += 32) {
         const int e = e0 + lane;
         const int lo = offsets && e < E ? __ldg(offsets + e) : 0;
-        int top = max(lo, highest);  // the largest of offsets[0 .. e]
+        const int hi = e >= E ? 0 : offsets ? __ldg(offsets + e + 1) : R;
+        int top = lo;  // the largest of offsets[0 .. e]: the last, as long as they rise
+        fallen = fallen || __any_sync(0xffffffffu, e < E && hi < lo);
+        if (fallen) {
+            top = max(lo, highest);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, top, o);
-            if (lane >= o) top = max(top, v);
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, top, o);
+                if (lane >= o) top = max(top, v);
+            }
+            highest = __shfl_sync(0xffffffffu, top, 31);
         }
-        highest = __shfl_sync(0xffffffffu, top, 31);
         int t = 0;
         if (e < E) {
-            t = group_tiles(lo, offsets ? __ldg(offsets + e + 1) : R, top, R, tokens, nb);
+            t = group_tiles(lo, hi, top, R, tokens, nb);
             if (t < 0) {
                 atomicOr(status, STATUS_INDEX);
                 t = 0;
