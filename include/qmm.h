@@ -290,8 +290,11 @@ QMM_API int qmm_f8_quantize(int x_type, const void *x, int64_t M, int64_t K, int
  * |qx code|, whatever the order of the 128 additions; measured 9e-8 of y's norm.
  * Results do not depend on timing: repeated calls agree bit for bit.
  * Two launches (quantiser, product), or one for a few rows (at most 16, fewer
- * for large matrices: the product quantises x itself, to the same codes); uses the per-(device, stream) workspace
- * of qmm (make one call of the largest size before graph capture).
+ * for large matrices: the product quantises x itself, to the same codes).
+ * Uses the per-(device, stream) workspace of qmm (make one call of the largest
+ * size before graph capture): M (K + K/32) bytes and up to 40 MB of partial
+ * tiles.  A workspace grows to one and a half times what a call needs and stays
+ * until qmm_release.
  * K == 0 writes y = 0.  (M/16 + 1) * ceil(N/128) below 2^31.
  */
 QMM_API int qmm_f8(const void *W, const float *S, int64_t N, int64_t K, int x_type, const void *x, int64_t M,
@@ -360,6 +363,9 @@ QMM_API int qmm_route(int x_type, const void *logits, int64_t T, int64_t E, int6
  *   W_down                    : [E][H][I] codes, scales [E][ceil(H/128)][ceil(I/128)].
  * H and I multiples of 16.  Four launches: quantiser (one row of codes per
  * slot), gate and up with the SiLU and h's rounding, down, weighted sum.
+ * Workspace: T k (5 H + H/32 + I + I/32) bytes, most of it the down product's
+ * rows in fp32, and up to 40 MB of partial tiles: 16384 tokens of 8 choices, H =
+ * 7168, I = 2048, take 5.0 GB, and the workspace that they leave is 7.5 GB.
  * Errors as qmm_f8_experts.
  */
 QMM_API int qmm_f8_moe(int x_type, const void *x, int64_t T, int64_t H, int64_t ldx, int k, const float *weights,

@@ -29,8 +29,8 @@
 //
 // Measured out of HBM (bf16, a row of calls on different matrices): 1 x 4096 x
 // 14336 14.8 us (4.0 TB/s of the 59 MB, 0.59 of the measured copy rate), 1 x 5120
-// x 17408 19.1 us (4.7 TB/s), 64 rows of 64 experts of 2048 x 1536 (41 of them in
-// use) 26.9 us (4.8 TB/s): about 6 us, the launches and the start and end of the
+// x 17408 19.0 us (4.7 TB/s), 64 rows of 64 experts of 2048 x 1536 (41 of them in
+// use) 27.3 us (4.7 TB/s): about 6 us, the launches and the start and end of the
 // pipeline, plus the weights at 6.8 TB/s.  What bounds it below about 100 MB is
 // therefore latency: the launch, the first weights, then per step the hand-over
 // from the copies to the MMA to the epilogue, and the sum over the CTAs of a tile.
@@ -218,7 +218,8 @@ __device__ __forceinline__ void quantise_own(const Params &P, const Schedule &s,
 // FUSE (few rows of a small matrix): the kernel quantises x itself, each CTA the K
 // blocks it needs: one launch instead of two, which is what counts where the
 // host's launches take longer than the GPU's work (13 x 5120 x 1024 10.4 instead
-// of 14.5 us a call; on the GPU alone 10.1 against 9.1).  Not where the weights
+// of 14.5 us a call; on the GPU alone 10.1 against 9.1; a call takes 10 to 15 us,
+// depending on the host).  Not where the weights
 // take longer than the quantiser's launch, ahead of which they are asked for (1 x
 // 4096 x 14336 out of HBM 18.2 against 14.6), and only where every warp's items
 // are loaded at once (16 x 4096 x 14336 in five turns took 26 against 14).
@@ -647,7 +648,12 @@ int tile_tokens(int64_t R, int E) {
 //   32 expert layers of 2048 x 1408: 8 41 49 59, 16 55 58 75, 32 75 67 78, 128 185 92 110
 // So this one for as many rows of one matrix as its tiles fit the GPU once (at
 // least 64), else pairs; for row groups single CTAs from a mean of 25 rows, whose
-// ragged ends a pair's 256 rows would waste.
+// ragged ends a pair's 256 rows would waste.  The mean is over all experts, used
+// or not, since the group sizes are on the device.  A few crowded experts among
+// idle ones then run here, one tile per 16 of their rows, which costs no more as
+// long as the tiles fit the GPU: of 64 experts of 1536 x 2048 one with 64 / 200 / 512 / 1000
+// rows and the others empty 10.8 / 12.8 / 16.6 / 24.2 us, that expert alone (single
+// CTAs) 16.7 / 16.9 / 18.6 / 18.8.
 int path_of(int64_t R, int E, int64_t N, bool grouped, int num_sms) {
     if (grouped) return (R + E - 1) / E <= 24 ? 0 : 1;
     return R <= 64 || (R <= 192 && (R + 63) / 64 * f8_blocks(N) <= num_sms) ? 0 : 2;

@@ -97,7 +97,7 @@ constexpr int UNROLL = 4;  // loads a warp has in flight
 // divisions of a block's scale are done once for all of them, by the lanes
 // that each take one of the warp's blocks, instead of once per block by every
 // lane: with 4 values per lane and the divisions per block the kernel was bound by
-// instruction issue (8191 x 5120 bf16 39 us).  Now 24.3 us, 5.2 TB/s of the 126 MB
+// instruction issue (8191 x 5120 bf16 39 us).  Now 24.4 us, 5.2 TB/s of the 126 MB
 // it reads and writes (0.77 of the measured copy rate); 8191 x 5120 fp32 36.5 us,
 // 5.8 TB/s; 4 x 4096 2.1 us, a launch and two trips to memory.
 // VEC: rows, K and the bases allow whole groups of V values (inside or outside

@@ -13,7 +13,17 @@
 namespace qk {
 namespace f8 {
 
-constexpr int CUT_COST = 32;  // see Schedule::plan
+// See Schedule::plan.  One cost for both kernels, although a partial tile is 8 to
+// 32 KB in f8_gemm.cu and 128 KB per CTA in f8_wide.cu.  Measured (us; a cost of 4,
+// 16, 32, 64, never cut):
+//   f8_gemm: 1 x 4096 x 14336 19.0 15.0 15.0 15.0 15.0; 4 x 9216 x 10000 23.7 23.7 23.7
+//     22.8 22.8; 4 x 5120 x 19800 24.6 24.6 24.6 25.4 25.5; one row for each of 21 experts of
+//     1024 x 2048 16.8 14.1 14.2 14.2 14.3; a layer of 4 tokens of 64 experts 43.2 37.1 37.0 37.0 37.0
+//   f8_wide: 400 x 5120 x 5120 29.2 29.3 22.9 22.9 22.9; 512 x 17408 x 5120 54.1 54.2 54.2
+//     54.1 61.5; 1100 x 17408 x 5120 105 106 105 105 119; 40 rows for each of 8 experts of 2560 x
+//     9216 53.7 53.2 53.2 44.5 44.4, of 5 of 7936 x 5120 54.1 54.2 54.1 55.8 55.6
+// Between 32 and 64 some shapes gain and some lose; 32 was taken.
+constexpr int CUT_COST = 32;
 
 F8_HD int smaller(int a, int b) { return a < b ? a : b; }
 F8_HD int larger(int a, int b) { return a > b ? a : b; }

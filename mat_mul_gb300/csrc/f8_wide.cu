@@ -8,18 +8,20 @@
 // per thread and the block goes from TMEM into fp32 registers at one packed fma
 // per two values, while in f8_gemm.cu every column has its own factor in shared
 // memory, which the operands of the MMA need for themselves (4096 x 5120 x 17408:
-// 776 us there with 256 token columns, 290 here).
+// 776 us there with 256 token columns, 280 to 305 here).
 //
 // With CG = 2 a pair of CTAs works on 256 tokens x 256 columns with one
 // cta_group::2 MMA: each loads its own 128 tokens and half of the weight rows,
 // so the copies of W are halved.
 //
-// What bounds it: the two TMEM buffers of 256 columns.  A buffer's round is the
-// MMA of a K block (512 cycles), its commit, the epilogue's reading of it (about
-// 300 cycles for 128 columns per warp) and the hand-back; waits on a completed
-// barrier alone cost 100 to 200 cycles each, so a K block takes about 800 cycles
-// and the tensor pipe is busy about 60 % of them.  Stores of a finished tile are
-// another 6 %.
+// What bounds it: a K block takes about 800 cycles, of which the tensor pipe is
+// busy 512, about 60 %.  The two TMEM buffers alone would allow a block in about 600
+// (a buffer's round is the MMA, its commit, the epilogue's reading of it, about 300
+// cycles for 128 columns per warp, and the hand-back).  The thread that issues the
+// MMAs takes longer: about 410 cycles for four MMAs and two commits, and 100 to 200
+// for each of its two waits, also when the barrier is complete.  That adds up to
+// the 800; which part could run beside which was not tried.  Stores of a finished
+// tile are another 6 %.
 //
 // Warp roles: 0 = copies, 1 = MMA issue (of the pair's first CTA), 2 = scales,
 // 3 = schedule (and tensor memory), then the epilogue (warp w: TMEM lanes
@@ -48,7 +50,8 @@ struct Wide {
     // and the registers they get.  Two warps of 128 accumulators per thread
     // measured faster than four of 64 for one matrix (8192 rows of 40 experts 95
     // against 103 us), slower for the gated pair, whose rounding needs more
-    // registers beside them (4093 tokens, 32 experts: 327 against 304 us).
+    // registers beside them (4093 tokens, 32 experts: 327 against 304 us).  (Figures
+    // of an earlier state: 81 and 235 us now.)
     static constexpr int PARTS = DUAL ? 4 : 2;
     static constexpr int EPI = 4 * PARTS, EPI_THREADS = 32 * EPI, THREADS = 128 + EPI_THREADS;
     static constexpr int OWN = COLS / PARTS;  // accumulators per thread
