@@ -67,11 +67,12 @@ struct Workspace {
     size_t bytes = 0;
 };
 
-// What the maps know a stream by: its handle, but the per-thread default stream
-// has one handle and another stream in every thread.  (No handle is odd but for
-// the two of the default streams.)
+// What the maps know a stream by: its handle, but the legacy default stream has
+// two handles, and the per-thread default stream has one handle and another
+// stream in every thread.  (No handle is odd but for those of the default streams.)
 std::atomic<uintptr_t> g_threads{0};
 cudaStream_t stream_key(cudaStream_t st) {
+    if (st == cudaStreamLegacy) return nullptr;
     if (st != cudaStreamPerThread) return st;
     thread_local const uintptr_t mine = 2 * ++g_threads + 1;
     return reinterpret_cast<cudaStream_t>(mine);
