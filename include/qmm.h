@@ -373,6 +373,178 @@ QMM_API int qmm_f8_moe(int x_type, const void *x, int64_t T, int64_t H, int64_t 
                        const float *S_gate, const void *W_up, const float *S_up, const void *W_down,
                        const float *S_down, int y_type, void *y, int64_t ldy, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The attention layer between the projections: position rotation, a paged key
+ * and value cache in 8-bit floats, and attention over it
+ * ---------------------------------------------------------------------------
+ * A cache of one layer holds pages of `page` tokens: keys and values as e4m3
+ * codes [pages][heads][page][dim] with one fp32 scale per page and head,
+ * [pages][heads] (key = k_scale * code).  Sequences own pages through a table:
+ * token j of sequence b is in slot j % page of page table[b][j / page].
+ *
+ * A batch has T rows; those of sequence b are offsets[b] .. offsets[b+1) - 1
+ * (offsets null: one row per sequence, B = T), and they are the last of its
+ * lengths[b] tokens: the lengths count the rows of the call.  Rows from
+ * offsets[B] on belong to no sequence: they are not read and their results are
+ * not written.  offsets [B+1], lengths [B] and table (B rows of `width` entries,
+ * ld_table apart) are int32 on the device and never read on the host, so calls
+ * can be captured in a graph and replayed after they changed.  A sequence with
+ * offsets that fall or leave the batch, or a length that its table does not
+ * hold, is skipped, a page that the cache does not have is not touched; their
+ * results are undefined and qmm_device_status() reports QMM_EINDEX.
+ *
+ * Rows of heads (queries, new keys and values, results): element i of head h
+ * of row t at t * ld_t + h * ld_h + i, type QMM_F32, QMM_F16 or QMM_BF16,
+ * aligned to the type.  Results do not depend on timing: repeated calls agree
+ * bit for bit.  The calls take their arguments in a structure (host memory,
+ * read before they return).
+ */
+typedef struct {
+    void *k, *v;              /* device, codes, 16-byte aligned                */
+    float *k_scale, *v_scale; /* device                                        */
+    int64_t pages, heads;     /* 1 <= heads <= 1024, pages < 2^31              */
+    int64_t page;             /* 16, 32, 64 or 128 tokens                      */
+    int64_t dim;              /* a multiple of 16, 16 to 256                   */
+} qmm_kv_cache;
+
+/*
+ * Rotation of the first `rot` values of a head by its position: pair i, the
+ * values (i, i + rot/2) or with `interleaved` (2i, 2i + 1), is turned by
+ *   (a, b) -> factor * (a cos w - b sin w, b cos w + a sin w),  w = position * f_i,
+ * the other values are kept.  turns[i] is f_i / 2 pi as a fraction of 2^64, so
+ * that position * turns[i] is the angle modulo a full turn without rounding:
+ * positions of any size (any int32, negative ones too) keep full precision.
+ */
+typedef struct {
+    const uint64_t *turns; /* device [rot / 2], 8-byte aligned                 */
+    int64_t rot;           /* even, at most the head's size                    */
+    int64_t interleaved;
+    double factor;
+} qmm_rope_table;
+
+/*
+ * qmm_rope_turns -- the table of a rotation, in HOST memory: turns[rot / 2] for
+ * f_i = base^(-2i / rot) (or freqs[i] radians per position where freqs is not
+ * null) and these scalings for contexts longer than the trained one:
+ *   QMM_ROPE_PLAIN  : f_i as it is.
+ *   QMM_ROPE_LINEAR : f_i / scale (interpolated positions).
+ *   QMM_ROPE_NTK    : base * scale^(rot / (rot - 2)) for base (rot >= 4).
+ *   QMM_ROPE_PARTS  : f_i k + f_i / scale (1 - k) with k = (r - low) / (high - low)
+ *                     within 0 .. 1, r = original f_i / 2 pi the turns within the
+ *                     trained length (NTK by parts; with the factor 0.1 ln(scale)
+ *                     + 1, low = 1 and high = 32 this is YaRN).
+ * Needs no GPU.
+ */
+#define QMM_ROPE_PLAIN 0
+#define QMM_ROPE_LINEAR 1
+#define QMM_ROPE_NTK 2
+#define QMM_ROPE_PARTS 3
+QMM_API int qmm_rope_turns(int rot, double base, const double *freqs, int scaling, double scale, double original,
+                           double low, double high, uint64_t *turns);
+
+/*
+ * qmm_rope -- y = the heads of x [T][heads][dim] turned by positions[t].
+ * With `inverse` by the negative angles: the transpose, which is the gradient
+ * of the rotation (of x, given that of y).  y may be x (same pitches and type);
+ * dim even.  One launch.  Against 64 bits: each value of a pair within
+ * 2^-21 factor (|a| + |b|) before the rounding to y's type.
+ */
+typedef struct {
+    const qmm_rope_table *rope; /* host                                        */
+    int64_t inverse;
+    const int32_t *positions; /* device [T]                                    */
+    int64_t T, heads, dim;
+    int64_t x_type;
+    const void *x;
+    int64_t ldx_t, ldx_h;
+    int64_t y_type;
+    void *y;
+    int64_t ldy_t, ldy_h;
+} qmm_rope_args;
+QMM_API int qmm_rope(const qmm_rope_args *args, void *stream);
+
+/*
+ * qmm_kv_append -- the rows' keys and values into the cache, the keys turned on
+ * the way (rope null: not), in one launch; with q also q_out = the rows'
+ * queries turned.  Row r of sequence b is token lengths[b] - (offsets[b+1] - r)
+ * of it, and that is its position unless `positions` [T] says otherwise.
+ * A page's scale is the smallest power of two, at least 2^-100, at which the
+ * largest finite |value| that the call adds to the page and head is at most 448
+ * of it, or the scale that the page has where that is larger and the page holds
+ * earlier tokens of the sequence; those tokens' codes are rounded anew when the
+ * scale grows.  Codes are rounded to nearest, ties to even, from the fp32 value
+ * turned (qmm_rope's accuracy); a NaN or an infinity becomes a NaN code and
+ * changes no scale.  Pages that the call writes to belong to one sequence each:
+ * a page shared by two of them may be read only.
+ *   k, v    : [T][heads of the cache][dim] of x_type.
+ *   q       : [T][q_heads][dim] of x_type, or null; q_out may be q.  Needs rope.
+ */
+typedef struct {
+    const qmm_kv_cache *cache; /* host                                         */
+    const int32_t *table;
+    int64_t width, ld_table;
+    const int32_t *lengths, *offsets;
+    int64_t B, T;
+    int64_t x_type;
+    const void *k;
+    int64_t ldk_t, ldk_h;
+    const void *v;
+    int64_t ldv_t, ldv_h;
+    const qmm_rope_table *rope; /* host                                        */
+    const int32_t *positions;
+    const void *q;
+    int64_t q_heads, ldq_t, ldq_h;
+    void *q_out;
+    int64_t ldo_t, ldo_h;
+} qmm_kv_append_args;
+QMM_API int qmm_kv_append(const qmm_kv_append_args *args, void *stream);
+
+/*
+ * qmm_kv_attention -- y = softmax(scale * q k^T) v of every row and query head
+ * over the tokens of its sequence; query head h reads cache head h / (q_heads /
+ * heads).  The row at position p of its sequence (the last row is at lengths -
+ * 1) sees
+ *   causal : tokens up to p, with window > 0 only the last `window` of them;
+ *   else   : all of them.
+ * A row that sees nothing (no tokens, or more rows than tokens) gets 0, and
+ * lse -inf.  Codes of tokens that no row of the sequence sees are not used.
+ *   q, y    : [T][q_heads][dim] of q_type / y_type.
+ *   lse     : device [T][q_heads] fp32 or null: log of the sum of the exponentials.
+ * Accuracy against the formula in 64 bits, u = 2^-11 for fp16 and bf16 queries,
+ * 2^-20 for fp32: |dy_i| <= (u + (n + dim + 64) 2^-22 (1 + X)) * sum_j p_j |v_ji| / sum_j p_j
+ * before the rounding to y's type, n the tokens seen and X the largest of the
+ * row's |scale| sum_i |q_i k_ji|.
+ * Scales are positive and finite; value scales below 2^-100 count as 2^-100.
+ * scratch null: partial results go to the per-(device, stream) workspace (make
+ * one call of the largest size before capture, and replay graphs that were
+ * captured on one stream one after another).  Otherwise to scratch, device
+ * memory of at least qmm_kv_attention_scratch(args) bytes, 256-byte aligned, that
+ * belongs to the call until its kernels are done: graphs that may run at once
+ * are given one each.
+ */
+typedef struct {
+    const qmm_kv_cache *cache; /* host                                         */
+    const int32_t *table;
+    int64_t width, ld_table;
+    const int32_t *lengths, *offsets;
+    int64_t B, T;
+    int64_t q_type;
+    const void *q;
+    int64_t q_heads, ldq_t, ldq_h;
+    int64_t y_type;
+    void *y;
+    int64_t ldy_t, ldy_h;
+    double scale;
+    int64_t causal, window;
+    float *lse;
+    void *scratch;
+    int64_t scratch_bytes;
+} qmm_kv_attention_args;
+QMM_API int qmm_kv_attention(const qmm_kv_attention_args *args, void *stream);
+/* Bytes of scratch that the call needs at most, or a negative status. */
+QMM_API int64_t qmm_kv_attention_scratch(const qmm_kv_attention_args *args);
+
 /* Name of a status code. */
 QMM_API const char *qmm_strerror(int status);
 

@@ -24,13 +24,23 @@ y in float32, float16 or bfloat16:
     y = q.qmm_f8_experts(W, S, x, r.offsets, rows=r.rows)   # W [E, N, K]: one row per (token, expert)
     y = q.qmm_f8_moe(x, r, Wg, Sg, Wu, Su, Wd, Sd)          # the whole gated expert MLP, [T, H]
     c, s = q.qmm_f8_quantize(x)                   # codes and scales of activations
+
+The attention layer of a step, over a paged cache of 8-bit floats (e4m3 codes, one scale per page and head):
+
+    rope = q.qmm_rope_table(128, base=500000.0, scaling="yarn", scale=8.0, original=8192)
+    cache = q.KvCache.empty(pages, heads, page=64, dim=128)
+    x = q.qmm_rope(x, rope, positions)            # x [T, heads, dim]; inverse=True: its gradient
+    qr = q.qmm_kv_append(cache, k, v, table, lengths, rope=rope, q=qh)   # k turned and stored, queries turned
+    y = q.qmm_kv_attention(cache, qr, table, lengths)                    # [T, heads, dim]
 """
 from __future__ import annotations
 
 import collections
 import ctypes
 import functools
+import math
 import os
+import struct
 
 Q8_0, Q4_K, Q6_K, Q5_K, Q3_K, Q2_K = 0, 1, 2, 3, 4, 5  # Q5_K, Q3_K, Q2_K: qmm_dequant only so far
 BLOCK_BYTES = {Q8_0: 34, Q4_K: 144, Q6_K: 210, Q5_K: 176, Q3_K: 110, Q2_K: 84}
@@ -94,6 +104,13 @@ def load():
     L.qmm_f8_experts.argtypes = [P, P, I64, I64, I64, I, P, I64, I64, P, P, I64, I, P, I64, P]
     L.qmm_route.argtypes = [I, P, I64, I64, I64, I, I, I, ctypes.c_float, P, P, P, P, P, P]
     L.qmm_f8_moe.argtypes = [I, P, I64, I64, I64, I, P, P, P, I64, I64, P, P, P, P, P, P, I, P, I64, P]
+    L.qmm_rope_turns.argtypes = [I, ctypes.c_double, P, I] + [ctypes.c_double] * 4 + [P]
+    L.qmm_kv_attention_scratch.argtypes = [ctypes.c_char_p]
+    L.qmm_kv_attention_scratch.restype = I64
+    for f in ("qmm_rope", "qmm_kv_append", "qmm_kv_attention"):
+        getattr(L, f).argtypes = [ctypes.c_char_p, P]  # the argument structure as packed bytes
+        getattr(L, f).restype = I
+    L.qmm_rope_turns.restype = I
     for f in ("qmm_f8_quantize", "qmm_f8", "qmm_f8_experts", "qmm_route", "qmm_f8_moe"):
         getattr(L, f).restype = I
     for f in ("qmm_dequant", "qmm", "qmm_noalloc", "qmm_quantize_act", "qmm_device_status",
@@ -326,6 +343,16 @@ class _F8:
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self.stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
         self.current_device = torch._C._cuda_getDevice
+        self.uint8 = torch.uint8
+        self._capturing = torch.cuda.is_current_stream_capturing
+        self._use = torch.cuda.stream
+
+    def capturing(self, stream):
+        """Whether a call on the stream goes into a graph."""
+        if stream is None:
+            return self._capturing()
+        with self._use(stream):
+            return self._capturing()
 
     def on(self, stream):
         """torch.empty on a call's stream."""
@@ -530,6 +557,271 @@ def qmm_f8_moe(x, route, W_gate, S_gate, W_up, S_up, W_down, S_down, y=None, dty
     if rc:
         _check(rc)
     return y
+
+
+# ---------------------------------------------------------------------------
+# The attention layer: position rotation, a paged cache of 8-bit floats, and
+# attention over it.  The C calls take a structure of 64-bit fields, packed here
+# in one go: a ctypes call with twenty arguments costs more than the kernel of a
+# decode step.
+# ---------------------------------------------------------------------------
+_ROPE_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "parts": 3, "yarn": 3}
+_ROPE_ARGS = struct.Struct("=QqQqqqqQqqqQqq")
+_APPEND_ARGS = struct.Struct("=QQqqQQqqqQqqQqqQQQqqqQqq")
+_ATTENTION_ARGS = struct.Struct("=QQqqQQqqqQqqqqQqqdqqQQq")
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + \
+               [(n, ctypes.c_int64) for n in ("pages", "heads", "page", "dim")]
+
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int64), ("interleaved", ctypes.c_int64),
+                ("factor", ctypes.c_double)]
+
+
+class RopeTable:
+    """A rotation as qmm_rope_table makes it: turns (int64 [rot / 2], 2^64ths of a
+    full turn per position), rot, interleaved, factor."""
+    __slots__ = ("_turns", "_struct", "_at", "_device")
+
+    def __init__(self, turns, rot, interleaved=False, factor=1.0):
+        import torch
+        _require_cuda(turns)
+        if turns.dtype != torch.int64 or tuple(turns.shape) != (rot // 2,) or not turns.is_contiguous():
+            raise ValueError(f"turns must be a contiguous int64 tensor of {rot // 2} elements, got {turns.dtype} "
+                             f"{tuple(turns.shape)}")
+        self._turns, self._device = turns, turns.get_device()
+        self._struct = _RopeStruct(turns.data_ptr(), rot, 1 if interleaved else 0, factor)
+        self._at = ctypes.addressof(self._struct)
+
+    turns = property(lambda self: self._turns)
+    rot = property(lambda self: self._struct.rot)
+    interleaved = property(lambda self: bool(self._struct.interleaved))
+    factor = property(lambda self: self._struct.factor)
+
+
+def qmm_rope_table(rot, base=10000.0, interleaved=False, scaling=None, scale=1.0, original=None, low=None, high=None,
+                   freqs=None, factor=None, device=None):
+    """The rotation of the first rot values of a head: pairs (i, i + rot/2), or
+    (2i, 2i + 1) when interleaved, at base^(-2i/rot) radians per position (or
+    freqs[i]).  scaling: None, "linear" (positions divided by scale), "ntk" (a
+    larger base), "parts" (frequencies with fewer than `low` turns within the
+    `original` length divided by scale, those with more than `high` kept, 1 and
+    4 unless given) or "yarn" (the same with 1 and 32, and the factor 0.1
+    ln(scale) + 1).  factor multiplies the rotated values."""
+    import torch
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be None, 'linear', 'ntk', 'parts' or 'yarn', not {scaling!r}")
+    if scaling in ("parts", "yarn") and original is None:
+        raise ValueError(f"scaling {scaling!r} needs the original length")
+    rot = int(rot)
+    n = max(rot // 2, 0)
+    if freqs is not None:
+        freqs = [float(f) for f in freqs]
+        if len(freqs) != n:
+            raise ValueError(f"{len(freqs)} frequencies for {n} pairs")
+        freqs = (ctypes.c_double * max(n, 1))(*freqs)
+    if factor is None:
+        factor = 0.1 * math.log(scale) + 1.0 if scaling == "yarn" and scale > 1.0 else 1.0
+    turns = (ctypes.c_uint64 * max(n, 1))()
+    _check(load().qmm_rope_turns(rot, float(base), freqs, _ROPE_SCALINGS[scaling], float(scale), float(original or 0.0),
+                                 float(1.0 if low is None else low),
+                                 float((32.0 if scaling == "yarn" else 4.0) if high is None else high), turns))
+    t = torch.frombuffer(bytearray(bytes(turns)[:8 * n]), dtype=torch.int64) if n else torch.empty(0, dtype=torch.int64)
+    return RopeTable(t.to("cuda" if device is None else device), rot, interleaved, factor)
+
+
+class KvCache:
+    """The cache of one layer: k and v codes (float8_e4m3fn or uint8 [pages,
+    heads, page, dim]) and their scales (float32 [pages, heads]), tensors of the
+    caller that the calls write to."""
+    __slots__ = ("k", "v", "k_scale", "v_scale", "heads", "page", "dim", "_struct", "_at", "_device", "_frozen")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        _require_cuda(k, v, k_scale, v_scale)
+        shape = tuple(k.shape)
+        for t in (k, v):
+            if t.dtype not in (torch.float8_e4m3fn, torch.uint8) or tuple(t.shape) != shape or len(shape) != 4 or \
+                    not t.is_contiguous():
+                raise ValueError("k and v must be contiguous float8_e4m3fn (or uint8) tensors of one shape [pages, heads, "
+                                 f"page, dim], got {tuple(k.shape)} and {tuple(v.shape)}")
+        for t in (k_scale, v_scale):
+            if t.dtype != torch.float32 or tuple(t.shape) != shape[:2] or not t.is_contiguous():
+                raise ValueError(f"scales must be contiguous float32 tensors of shape {shape[:2]}, got {tuple(t.shape)}")
+        if shape[2] not in (16, 32, 64, 128) or shape[3] % 16 or not 16 <= shape[3] <= 256:
+            raise ValueError(f"pages of 16, 32, 64 or 128 tokens, heads of a multiple of 16 up to 256 values, got {shape}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.heads, self.page, self.dim = shape[1:]
+        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *shape)
+        self._at, self._device = ctypes.addressof(self._struct), k.get_device()
+        self._frozen = True
+
+    def __setattr__(self, name, value):
+        # (the calls use the addresses of the tensors that the cache was made of)
+        if getattr(self, "_frozen", False):
+            raise AttributeError("a cache keeps its tensors; make another one")
+        object.__setattr__(self, name, value)
+
+    @classmethod
+    def empty(cls, pages, heads, page=64, dim=128, device=None):
+        """A cache of zeros."""
+        import torch
+        device = "cuda" if device is None else device
+        k, v = (torch.zeros((pages, heads, page, dim), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+                for _ in range(2))
+        ks, vs = (torch.zeros((pages, heads), dtype=torch.float32, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+
+def _row_heads(t, what):
+    """t [T, heads, dim] with adjacent elements of a head: (T, heads, dim, pitch
+    of rows, pitch of heads)."""
+    if t.dim() == 3:
+        T, H, D = t.shape
+        a, b, one = t.stride()
+        if one == 1 or D <= 1:
+            return T, H, D, a, b
+    raise ValueError(f"{what} must be [rows, heads, dim] with the elements of a head adjacent, got shape "
+                     f"{tuple(t.shape)} strides {t.stride()}")
+
+
+def _row_heads_out(f, y, T, H, D, dtype, like, stream, what):
+    if y is None:
+        return f.on(stream)((T, H, D), dtype=dtype, device=like.device), H * D, D
+    r, h, d, a, b = _row_heads(y, what)
+    if (r, h, d) != (T, H, D):
+        raise ValueError(f"{what} has shape {tuple(y.shape)}, expected {(T, H, D)}")
+    return y, a, b
+
+
+def _kv_batch(f, cache, T, table, lengths, offsets):
+    """(sequences, table width, its row pitch, address of the offsets) after the checks of a batch."""
+    shape = table.shape
+    if table.dtype != f.int32 or len(shape) != 2:
+        raise ValueError(f"table must be an int32 matrix [sequences, pages], got {table.dtype} {tuple(shape)}")
+    B, width = shape
+    ld, one = table.stride()
+    if one != 1 and width > 1:
+        raise ValueError("the entries of a row of table must be adjacent")
+    _int32(f, lengths, B, "lengths")
+    if offsets is None:
+        if T != B:
+            raise ValueError(f"{T} rows of {B} sequences: without offsets every sequence has one row")
+        return B, width, ld, 0
+    _int32(f, offsets, B + 1, "offsets")
+    return B, width, ld, offsets.data_ptr()
+
+
+def _kv_device(f, cache, rope, first, *others):
+    dev = _device_index(f, first, *others)
+    if cache is not None and cache._device != dev:
+        raise ValueError(f"a cache on cuda:{cache._device}, rows on {first.device}")
+    if rope is not None and rope._device != dev:
+        raise ValueError(f"a rotation table on cuda:{rope._device}, rows on {first.device}")
+    return dev
+
+
+def qmm_rope(x, rope, positions, y=None, inverse=False, dtype=None, stream=None):
+    """The heads of x [T, heads, dim] turned by rope (a RopeTable) at positions
+    (int32 [T]); with inverse by the negative angles, which is the gradient.  y:
+    the result, which may be x."""
+    f = _f8_state()
+    dev = _kv_device(f, None, rope, x, positions, y)
+    T, H, D, a, b = _row_heads(x, "x")
+    _int32(f, positions, T, "positions")
+    xt = x.dtype
+    ft = f.ftype(xt, "x")
+    y, c, d = _row_heads_out(f, y, T, H, D, dtype or xt, x, stream, "y")
+    rc = f.lib.qmm_rope(_ROPE_ARGS.pack(rope._at, 1 if inverse else 0, positions.data_ptr(), T, H, D, ft, x.data_ptr(), a, b,
+                                        f.ftype(y.dtype, "y"), y.data_ptr(), c, d),
+                        f.stream(dev) if stream is None else _given_stream(stream, dev))
+    if rc:
+        _check(rc)
+    return y
+
+
+def qmm_kv_append(cache, k, v, table, lengths, offsets=None, rope=None, positions=None, q=None, q_out=None, stream=None):
+    """The new keys and values k, v [T, heads, dim] into the cache (a KvCache), the
+    keys turned by rope on the way; with q [T, query heads, dim] returns the
+    queries turned too (q_out may be q), else None.  Rows offsets[b] ..
+    offsets[b+1] (int32 [B+1]; row b without offsets) are the last of the
+    lengths[b] tokens of sequence b, token j of which is in page table[b, j //
+    page]; table int32 [B, width], lengths int32 [B].  positions int32 [T]: other
+    angles than those of a row's place in its sequence."""
+    f = _f8_state()
+    dev = _kv_device(f, cache, rope, k, v, table, lengths, offsets, positions, q, q_out)
+    T, H, D, a, b = _row_heads(k, "k")
+    r, h, d, vc, vd = _row_heads(v, "v")
+    if H != cache.heads or D != cache.dim or (r, h, d) != (T, H, D):
+        raise ValueError(f"k and v must be {(T, cache.heads, cache.dim)}, got {tuple(k.shape)} and {tuple(v.shape)}")
+    xt = k.dtype
+    ft = f.ftype(xt, "k")
+    if v.dtype != xt:
+        raise ValueError(f"k is {xt}, v {v.dtype}")
+    B, width, ld, off = _kv_batch(f, cache, T, table, lengths, offsets)
+    if positions is not None:
+        _int32(f, positions, T, "positions")
+    qp = Hq = qa = qb = op = oa = ob = 0
+    if q is not None:
+        r, Hq, d, qa, qb = _row_heads(q, "q")
+        if (r, d) != (T, D) or q.dtype != xt:
+            raise ValueError(f"q must be [{T}, query heads, {D}] of {xt}, got {tuple(q.shape)} of {q.dtype}")
+        if rope is None:
+            raise ValueError("queries are only turned: q needs rope")
+        qp = q.data_ptr()
+        q_out, oa, ob = _row_heads_out(f, q_out, T, Hq, D, xt, q, stream, "q_out")
+        if q_out.dtype != xt:
+            raise ValueError(f"q_out is {q_out.dtype}, q {xt}")
+        op = q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rc = f.lib.qmm_kv_append(_APPEND_ARGS.pack(cache._at, table.data_ptr(), width, ld, lengths.data_ptr(), off, B, T, ft,
+                                               k.data_ptr(), a, b, v.data_ptr(), vc, vd, 0 if rope is None else rope._at,
+                                               0 if positions is None else positions.data_ptr(), qp, Hq, qa, qb, op, oa, ob),
+                             f.stream(dev) if stream is None else _given_stream(stream, dev))
+    if rc:
+        _check(rc)
+    return q_out
+
+
+def qmm_kv_attention(cache, q, table, lengths, offsets=None, scale=None, causal=True, window=0, y=None, dtype=None,
+                     lse=False, stream=None):
+    """softmax(scale * q k^T) v of the rows q [T, query heads, dim] over the tokens
+    of their sequences in the cache (a KvCache); table, lengths and offsets as in
+    qmm_kv_append, scale 1/sqrt(dim) unless given.  A causal row sees the tokens
+    up to its own (the last `window` of them if that is not 0); a row that sees
+    none gets 0.  Returns y [T, query heads, dim], with lse also the log of the
+    sum of the exponentials, float32 [T, query heads].  Rows from offsets[-1] on
+    are not written."""
+    f = _f8_state()
+    dev = _kv_device(f, cache, None, q, table, lengths, offsets, y)
+    T, H, D, a, b = _row_heads(q, "q")
+    if D != cache.dim:
+        raise ValueError(f"q has heads of {D} values, the cache of {cache.dim}")
+    B, width, ld, off = _kv_batch(f, cache, T, table, lengths, offsets)
+    qt = q.dtype
+    ft = f.ftype(qt, "q")
+    y, c, d = _row_heads_out(f, y, T, H, D, dtype or qt, q, stream, "y")
+    sums = f.on(stream)((T, H), dtype=f.float32, device=q.device) if lse else None
+    head = (cache._at, table.data_ptr(), width, ld, lengths.data_ptr(), off, B, T, ft, q.data_ptr(), H, a, b,
+            f.ftype(y.dtype, "y"), y.data_ptr(), c, d, 1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, window,
+            sums.data_ptr() if lse else 0)
+    if f.capturing(stream):
+        # a graph has its partial results in its own memory, so that two of one stream can run at once
+        n = f.lib.qmm_kv_attention_scratch(_ATTENTION_ARGS.pack(*head, 0, 0))
+        if n < 0:
+            _check(int(n))
+        work = f.on(stream)(n, dtype=f.uint8, device=q.device)
+        args = _ATTENTION_ARGS.pack(*head, work.data_ptr(), n)
+    else:
+        args = _ATTENTION_ARGS.pack(*head, 0, 0)
+    rc = f.lib.qmm_kv_attention(args, f.stream(dev) if stream is None else _given_stream(stream, dev))
+    if rc:
+        _check(rc)
+    return (y, sums) if lse else y
 
 
 def qmm_device_status(stream=None) -> int:

@@ -2,34 +2,10 @@
 // the expert layer: argument checks, workspace layout and launch order.
 #include <cuda_runtime.h>
 
-#include <cstdarg>
-#include <cstdio>
-
-#include "f8_internal.h"
-#include "qmm_internal.h"
+#include "abi_checks.h"
 
 namespace {
 
-int refuse(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
-int refuse(int code, const char *fmt, ...) {
-    char msg[256];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(msg, sizeof msg, fmt, ap);
-    va_end(ap);
-    return qk::record_error(code, msg);
-}
-int cuda_error(cudaError_t e, const char *what) { return refuse(QMM_ECUDA, "%s: %s", what, cudaGetErrorString(e)); }
-
-using ll = long long;
-constexpr int64_t I31 = int64_t(1) << 31;
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-int check_ftype(int t, const char *what) {
-    if (t != QMM_F32 && t != QMM_F16 && t != QMM_BF16) return refuse(QMM_EINVAL_TYPE, "%s: unknown value type %d", what, t);
-    return QMM_OK;
-}
 int check_rows(const void *p, int type, int64_t rows, int64_t cols, int64_t ld, const char *what) {
     if (rows > 1 && ld < cols)
         return refuse(QMM_EINVAL_SHAPE, "%s: a row pitch of %lld is less than the %lld values of a row", what,
@@ -37,11 +13,6 @@ int check_rows(const void *p, int type, int64_t rows, int64_t cols, int64_t ld, 
     if (!p) return refuse(QMM_EINVAL_PTR, "%s is null", what);
     if (!aligned(p, qk::f8_size(type)))
         return refuse(QMM_EINVAL_PTR, "%s must be aligned to its values (%d bytes)", what, qk::f8_size(type));
-    return QMM_OK;
-}
-int check_words(const void *p, const char *what) {
-    if (!p) return refuse(QMM_EINVAL_PTR, "%s is null", what);
-    if (!aligned(p, 4)) return refuse(QMM_EINVAL_PTR, "%s must be 4-byte aligned", what);
     return QMM_OK;
 }
 int check_matrix(const void *W, const float *S, const char *what) {

@@ -1,0 +1,52 @@
+// kv_attention.cu -- which attention kernel takes a call, and what it needs.
+#include "kv_attention.cuh"
+
+namespace qk {
+
+namespace {
+
+// Query rows per block of the kernel for few rows: what the sequences have on
+// the average, so that a decode step does not compute empty rows.
+int row_groups(const KvAttention &a) {
+    const int64_t rows = a.batch.T * (a.q_heads / a.c.heads) / a.batch.B;
+    return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+}
+
+int padded_dim(const KvAttention &a) { return a.c.dim <= 64 ? 64 : a.c.dim <= 128 ? 128 : 256; }
+
+}  // namespace
+
+KvPlan kv_attention_plan(const KvAttention &a, int num_sms) {
+    const int64_t blocks = num_sms * 2, floats = 8 * row_groups(a) * (padded_dim(a) + 2);
+    return {static_cast<size_t>(blocks * 2 * floats * 4), blocks};
+}
+
+cudaError_t launch_kv_attention(const KvAttention &a, cudaStream_t st, int num_sms) {
+    kv::AttnParams p = {};
+    p.codes[0] = static_cast<const uint8_t *>(a.c.k), p.codes[1] = static_cast<const uint8_t *>(a.c.v);
+    p.scales[0] = a.c.k_scale, p.scales[1] = a.c.v_scale;
+    p.pages = a.c.pages;
+    p.heads = static_cast<int>(a.c.heads), p.page = static_cast<int>(a.c.page), p.dim = static_cast<int>(a.c.dim);
+    p.group = a.q_heads / p.heads;
+    p.q = a.q.x, p.ldq_t = a.q.ld_t, p.ldq_h = a.q.ld_h, p.q_type = a.q.type;
+    p.y = const_cast<void *>(a.y.x), p.ldy_t = a.y.ld_t, p.ldy_h = a.y.ld_h, p.y_type = a.y.type;
+    p.offsets = a.batch.offsets, p.lengths = a.batch.lengths, p.table = a.batch.table;
+    p.ld_table = a.batch.ld_table, p.T = a.batch.T, p.width = a.batch.width, p.B = a.batch.B;
+    const double factor = a.scale * 1.4426950408889634074;
+    p.factor = static_cast<float>(factor);
+    p.factor_low = static_cast<float>(factor - p.factor);
+    p.causal = a.causal, p.window = a.window;
+    p.lse = a.lse;
+    p.part = reinterpret_cast<float *>(a.scratch);
+    p.count = a.count;
+    p.status = a.status;
+    const int nb = row_groups(a);
+    const bool hl = a.q.type == QMM_F32;
+    switch (padded_dim(a)) {
+    case 64: return kv::launch_few_64(p, nb, hl, st, num_sms, a.dev);
+    case 128: return kv::launch_few_128(p, nb, hl, st, num_sms, a.dev);
+    default: return kv::launch_few_256(p, nb, hl, st, num_sms, a.dev);
+    }
+}
+
+}  // namespace qk

@@ -17,6 +17,7 @@
 #include "qmm_device.cuh"
 
 #include "f8_internal.h"
+#include "kv_internal.h"
 #include "qmm_internal.h"
 
 namespace {
@@ -287,6 +288,7 @@ int f8_workspace(const F8Context &c, cudaStream_t st, size_t bytes, void **ptr) 
     return workspace(c.dev, st, bytes, ptr);
 }
 int f8_counters(const F8Context &c, cudaStream_t st, unsigned **ptr) { return counters(c.dev, st, c.num_sms, ptr); }
+int f8_counters_n(const F8Context &c, cudaStream_t st, int64_t n, unsigned **ptr) { return counters(c.dev, st, n, ptr); }
 }  // namespace qk
 
 namespace {
