@@ -12,11 +12,18 @@ int row_groups(const KvAttention &a) {
     return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
 
+// Whether the call's rows go to the kernel for many rows: 16-bit queries and
+// sequences of more than 32 rows per cache head on the average.
+bool many_rows(const KvAttention &a) {
+    return a.q.type != QMM_F32 && a.c.dim <= 128 && a.batch.T * (a.q_heads / a.c.heads) > 32 * int64_t(a.batch.B);
+}
+
 int padded_dim(const KvAttention &a) { return a.c.dim <= 64 ? 64 : a.c.dim <= 128 ? 128 : 256; }
 
 }  // namespace
 
 KvPlan kv_attention_plan(const KvAttention &a, int num_sms) {
+    if (many_rows(a)) return {kv::tc_part_bytes(static_cast<int>(a.c.dim), num_sms), 2 * num_sms};
     const int64_t blocks = num_sms * 2, floats = 8 * row_groups(a) * (padded_dim(a) + 2);
     return {static_cast<size_t>(blocks * 2 * floats * 4), blocks};
 }
@@ -40,6 +47,7 @@ cudaError_t launch_kv_attention(const KvAttention &a, cudaStream_t st, int num_s
     p.part = reinterpret_cast<float *>(a.scratch);
     p.count = a.count;
     p.status = a.status;
+    if (many_rows(a)) return kv::launch_tc(p, a.stop, st, num_sms, a.dev);
     const int nb = row_groups(a);
     const bool hl = a.q.type == QMM_F32;
     switch (padded_dim(a)) {

@@ -701,6 +701,11 @@ cudaError_t launch_few_dp(const AttnParams &p, int nb, bool hl, cudaStream_t st,
     if (nb == 2) return hl ? launch_few<DP, 2, true>(p, st, num_sms, dev) : launch_few<DP, 2, false>(p, st, num_sms, dev);
     return hl ? launch_few<DP, 4, true>(p, st, num_sms, dev) : launch_few<DP, 4, false>(p, st, num_sms, dev);
 }
+// The kernel for many rows (kv_attention_tc.cu): 16-bit queries, heads of up to
+// 128 values.  stop: the tile at which the first CTA's copies stop (NO_STOP: none).
+size_t tc_part_bytes(int dim, int num_sms);
+cudaError_t launch_tc(const AttnParams &a, int stop, cudaStream_t st, int num_sms, int dev);
+
 cudaError_t launch_few_64(const AttnParams &p, int nb, bool hl, cudaStream_t st, int num_sms, int dev);
 cudaError_t launch_few_128(const AttnParams &p, int nb, bool hl, cudaStream_t st, int num_sms, int dev);
 cudaError_t launch_few_256(const AttnParams &p, int nb, bool hl, cudaStream_t st, int num_sms, int dev);
