@@ -21,10 +21,13 @@
 // what is cut is joined by the last of its CTAs, in the order of the tokens.
 //
 // Warp roles: 0 = copies, 1 = MMA issue, 2 = schedule, 3 = tensor memory;
-// 4..7 = conversion of queries, keys and values; 8..11 and 12..15 = rows of
-// the first and the second tile (thread = row).
+// 4..7 and 8..11 = conversion of keys and of values, both of queries; 12..19
+// and 20..27 = rows of the first and the second tile, two threads per row
+// (each with half of the tokens, and half of the columns of O).
 // All waits are bounded: a role whose wait ran out stops, the others' then run
 // out too, every copy in flight is waited for and TMEM is freed.
+#include <type_traits>
+
 #include "f8_gemm.cuh"
 #include "kv_attention.cuh"
 
@@ -38,28 +41,33 @@ using f8::mbar_spin;
 using f8::tc_fence_after;
 using f8::tc_fence_before;
 
-constexpr int TC_THREADS = 512, UNIT = 256;
+constexpr int TC_THREADS = 896, UNIT = 256;
 constexpr int TC_LEAST = 4;  // tiles per CTA below which fewer CTAs take part
-constexpr int PIECES = 3, SC_SLOTS = 8, SC_FLOATS = 24;
+constexpr int PIECES = 2, SC_SLOTS = 4, SC_FLOATS = 16;
+// registers per thread at launch, and after the split between roles 0..3, conversion and rows
+constexpr int REGS = 72, REGS_A = 48, REGS_B = 64, REGS_C = 80;
+static_assert(128 * (REGS_A + 2 * REGS_B + 4 * REGS_C) <= TC_THREADS * REGS, "register split");
 constexpr float MOVE = 8.0f;      // growth of the maximum that moves the reference
 constexpr float TC_SHIFT = 6.0f;  // P as fp16 is at most 2^(MOVE + TC_SHIFT)
-constexpr int REGS_A = 56, REGS_B = 56, REGS_C = 200;  // roles 0..3, conversion, rows
-static_assert(128 * (REGS_A + REGS_B + 2 * REGS_C) <= 65536, "register split");
 
 template <int DP>
 struct Tc {
-    static constexpr int ST = 2;               // stages of converted keys and of values
-    static constexpr int TILE_BYTES = TILE * DP * 2;  // converted, and one tile of queries
-    static constexpr int OFF_K = 2 * TILE_BYTES, OFF_V = OFF_K + ST * TILE_BYTES;
-    static constexpr int RAW = TILE * DP;      // codes of a tile
-    static constexpr int OFF_RAW = OFF_V + ST * TILE_BYTES;
-    static constexpr int OFF_ROW = OFF_RAW + 2 * RAW;             // [2 units] power of two of each row's queries
-    static constexpr int OFF_SC = OFF_ROW + 2 * UNIT;              // [SC_SLOTS] key scales, log2 of value scales, their inverses
+    // Converted keys and values take turns in a ring.  Three slots do: a slot is
+    // asked for again two products after its last one, about 1000 cycles.
+    static constexpr int RING = DP == 128 ? 3 : 4;
+    static constexpr int RAW_RING = 4;                // codes on their way, keys and values in turn
+    static constexpr int TILE_BYTES = TILE * DP * 2;  // a slot, and one tile of queries
+    static constexpr int OFF_RING = 2 * TILE_BYTES;
+    static constexpr int RAW = TILE * DP;             // codes of a slot
+    static constexpr int OFF_RAW = OFF_RING + RING * TILE_BYTES;
+    static constexpr int OFF_ROW = OFF_RAW + RAW_RING * RAW;             // power of two of each row's queries
+    static constexpr int OFF_SHARE = OFF_ROW + UNIT;           // [2 halves][UNIT] what the threads of a row tell each other
+    static constexpr int OFF_SC = OFF_SHARE + 2 * UNIT * 4;              // [SC_SLOTS] key scales and log2 of value scales
     static constexpr int OFF_PIECES = OFF_SC + SC_SLOTS * SC_FLOATS * 4;
     static constexpr int OFF_BAR = OFF_PIECES + PIECES * 48;
-    static constexpr int SMEM = OFF_BAR + 256 + 1024;
+    static constexpr int SMEM = OFF_BAR + 288;
     static_assert(SMEM <= 232448, "shared memory");
-    static_assert(2 * RAW >= (TC_THREADS + 1) * 8, "prefix sums lie where the codes will");
+    static_assert(RAW_RING * RAW >= (TC_THREADS + 1) * 8, "prefix sums lie where the codes will");
     static constexpr int PART = UNIT * (DP + 2);  // floats of a partial result
 };
 
@@ -68,6 +76,7 @@ struct TcParams {
     int pairs;  // at most so many (sequence, block of UNIT rows)
     int q_vec, y_vec;
     int stop;
+    uint32_t div_mul, div_shift;  // row / group = row * div_mul >> div_shift for rows below 2^31
 };
 
 // A block of UNIT rows of a sequence and its tiles of tokens.
@@ -160,13 +169,6 @@ __device__ __forceinline__ void tmem_wait32(uint32_t *r) {
                  :
                  : "memory");
 }
-__device__ __forceinline__ void tie32(uint32_t *r) {
-    asm volatile(""
-                 : KV_RW4(r, 0), KV_RW4(r, 4), KV_RW4(r, 8), KV_RW4(r, 12), KV_RW4(r, 16), KV_RW4(r, 20), KV_RW4(r, 24),
-                   KV_RW4(r, 28)
-                 :
-                 : "memory");
-}
 __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
@@ -174,11 +176,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t *r) {
         KV_I4(r, 4), KV_I4(r, 8), KV_I4(r, 12), KV_I4(r, 16), KV_I4(r, 20), KV_I4(r, 24), KV_I4(r, 28), "r"(a)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::KV_I4(r, 0),
-        KV_I4(r, 4), KV_I4(r, 8), KV_I4(r, 12), "r"(a)
-        : "memory");
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : KV_R4(r, 0), KV_R4(r, 4), KV_R4(r, 8), KV_R4(r, 12)
+                 : "r"(a));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : KV_RW4(r, 0), KV_RW4(r, 4), KV_RW4(r, 8), KV_RW4(r, 12) : : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::KV_I4(r, 0), KV_I4(r, 4), "r"(a)
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -202,6 +210,11 @@ __device__ __forceinline__ void add2(float &a, float &b, float c, float d) {
         : "+f"(a), "+f"(b)
         : "f"(c), "f"(d));
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -218,21 +231,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
     using C = Tc<DP>;
     constexpr int KS = DP / 16;
     const AttnParams &P = PP.a;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     const uint32_t bar = base + C::OFF_BAR;
-    const uint32_t raw_full = bar, raw_empty = raw_full + 16;                    // keys, values
-    const uint32_t k_full = raw_empty + 16, k_empty = k_full + 8 * C::ST;
-    const uint32_t v_full = k_empty + 8 * C::ST, v_empty = v_full + 8 * C::ST;
-    const uint32_t q_full = v_empty + 8 * C::ST, q_empty = q_full + 8;
+    const uint32_t raw_full = bar, raw_empty = raw_full + 8 * C::RAW_RING;
+    const uint32_t kv_full = raw_empty + 8 * C::RAW_RING, kv_empty = kv_full + 8 * C::RING;
+    const uint32_t q_full = kv_empty + 8 * C::RING, q_empty = q_full + 8;
     const uint32_t s_full = q_empty + 8, p_full = s_full + 16, pv_done = p_full + 16, o_empty = pv_done + 16;  // per tile
     const uint32_t pc_full = o_empty + 16, pc_empty = pc_full + 8 * PIECES, done = pc_empty + 8 * PIECES;
-    static_assert(32 + 32 * 2 + 16 + 64 + 16 * PIECES + 8 <= 232, "barriers");
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 232);
-    volatile unsigned *const arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 240);  // per tile
+    static_assert(16 * (C::RAW_RING + C::RING) + 16 + 64 + 16 * PIECES + 8 <= 264, "barriers");
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 264);
+    volatile unsigned *const arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 272);  // per tile
     int4 *const pieces = reinterpret_cast<int4 *>(smem + C::OFF_PIECES);
     int8_t *const row_e = reinterpret_cast<int8_t *>(smem + C::OFF_ROW);
     float *const sc = reinterpret_cast<float *>(smem + C::OFF_SC);
@@ -240,24 +251,24 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, 8);
+            mbar_init(pv_done + 8 * i, 1);
+            mbar_init(o_empty + 8 * i, 8);
+        }
+        for (int i = 0; i < C::RAW_RING; ++i) {
             mbar_init(raw_full + 8 * i, 1);
             mbar_init(raw_empty + 8 * i, 4);
-            mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, 4);
-            mbar_init(pv_done + 8 * i, 1);
-            mbar_init(o_empty + 8 * i, 4);
         }
-        for (int i = 0; i < C::ST; ++i) {
-            mbar_init(k_full + 8 * i, 4);
-            mbar_init(k_empty + 8 * i, 1);
-            mbar_init(v_full + 8 * i, 4);
-            mbar_init(v_empty + 8 * i, 1);
+        for (int i = 0; i < C::RING; ++i) {
+            mbar_init(kv_full + 8 * i, 4);
+            mbar_init(kv_empty + 8 * i, 1);
         }
-        mbar_init(q_full, 4);
+        mbar_init(q_full, 8);
         mbar_init(q_empty, 1);
         for (int i = 0; i < PIECES; ++i) {
             mbar_init(pc_full + 8 * i, 1);
-            mbar_init(pc_empty + 8 * i, 1 + 1 + 4 + 8);  // copies, MMA, conversion, rows
+            mbar_init(pc_empty + 8 * i, 1 + 1 + 8 + 16);  // copies, MMA, conversion, rows
         }
         mbar_init(done, 1);
         fence_mbar_init();
@@ -340,6 +351,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
         ++np;
         return c.w != 0;
     };
+    auto token_of = [&](int row) { return static_cast<int>(static_cast<uint64_t>(row) * PP.div_mul >> PP.div_shift); };
     auto rows_of = [&]() { return static_cast<int>(min(static_cast<int64_t>(UNIT), static_cast<int64_t>(pc.n) * P.group - pc.r0)); };
     // first token that some row of the unit sees, and the end of them
     auto end_of = [&](int rows) {
@@ -354,7 +366,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
             const int pages = TILE / P.page;  // of a tile
             const uint32_t page_bytes = static_cast<uint32_t>(P.page * P.dim);
             const int stop = cta == 0 ? PP.stop : NO_STOP;
-            int it = 0, issued[2] = {0, 0};
+            int it = 0, item = 0;  // tiles, and slots filled (keys and values in turn)
             bool ok = true;
             while (ok && next_piece(true)) {
                 const int rows = rows_of(), end = end_of(rows), from = from_of();
@@ -379,8 +391,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                     const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * page_bytes;
 #pragma unroll
                     for (int side = 0; side < 2; ++side) {
+                        const int slot = item % C::RAW_RING;
                         if (it >= stop) ok = false;
-                        if (ok && it > 0) ok = mbar_spin(raw_empty + 8 * side, (it - 1) & 1, P.status);
+                        if (ok && item >= C::RAW_RING) ok = mbar_spin(raw_empty + 8 * slot, ((item / C::RAW_RING) - 1) & 1, P.status);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         if (side == 0) {
@@ -392,33 +405,35 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                                 float *d = sc + (it % SC_SLOTS) * SC_FLOATS + lane;
                                 d[0] = fminf(fmaxf(k, 0x1p-126f), 0x1p127f);
                                 d[8] = log2f(w);
-                                d[16] = __fdiv_rn(1.0f, w) * L_FACTOR;
                             }
                             __syncwarp();
                         }
-                        if (lane == 0) mbar_arrive_expect_tx(raw_full + 8 * side, bytes);
+                        if (lane == 0) mbar_arrive_expect_tx(raw_full + 8 * slot, bytes);
                         __syncwarp();
                         if (id >= 0)
-                            bulk_copy(base + C::OFF_RAW + side * C::RAW + lane * page_bytes, P.codes[side] + tile * page_bytes,
-                                      page_bytes, raw_full + 8 * side);
-                        issued[side] = it + 1;
+                            bulk_copy(base + C::OFF_RAW + slot * C::RAW + lane * page_bytes, P.codes[side] + tile * page_bytes,
+                                      page_bytes, raw_full + 8 * slot);
+                        ++item;
                     }
                     if (!ok) break;
                     id = next;
                 }
             }
             // no CTA ends with copies in flight
-#pragma unroll
-            for (int side = 0; side < 2; ++side)
-                if (issued[side] > 0) mbar_spin(raw_full + 8 * side, (issued[side] - 1) & 1, P.status);
+            for (int i = max(0, item - C::RAW_RING); i < item; ++i)
+                mbar_spin(raw_full + 8 * (i % C::RAW_RING), (i / C::RAW_RING) & 1, P.status);
         } else if (warp == 1 && elect_one()) {
             // ---- MMA issue ----
             constexpr uint32_t ID_S = (1u << 4) | ((TILE >> 3) << 17) | ((128 >> 4) << 24);
             constexpr uint32_t ID_O = (1u << 4) | (1u << 16) | ((DP >> 3) << 17) | ((128 >> 4) << 24);
-            int seg = 0, kit = 0, vit = 0, used[2] = {0, 0}, pit[2] = {0, 0};
+            int seg = 0, used[2] = {0, 0}, pit[2] = {0, 0};
+            int ki = 0, vi = 1;  // items in the ring: keys even, values odd
             bool ok = true;
+            auto slot_of = [&](int item) { return base + C::OFF_RING + (item % C::RING) * C::TILE_BYTES; };
+            auto wait_item = [&](int item) { return mbar_spin(kv_full + 8 * (item % C::RING), (item / C::RING) & 1, P.status); };
+            auto free_item = [&](int item) { commit(kv_empty + 8 * (item % C::RING)); };
             auto scores = [&](int t) {
-                const uint32_t q = base + t * C::TILE_BYTES, k = base + C::OFF_K + (kit % C::ST) * C::TILE_BYTES;
+                const uint32_t q = base + t * C::TILE_BYTES, k = slot_of(ki);
 #pragma unroll
                 for (int i = 0; i < KS; ++i) {
                     const uint32_t at = (i >> 2) * (TILE * 128) + 32 * (i & 3);
@@ -427,10 +442,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                 commit(s_full + 8 * t);
             };
             auto values = [&](int t, bool first) {
-                const uint32_t v = base + C::OFF_V + (vit % C::ST) * C::TILE_BYTES;
+                const uint32_t v = slot_of(vi);
 #pragma unroll
                 for (int i = 0; i < TILE / 16; ++i)
-                    mma_ts(tmem + 256 + t * DP, tmem + t * 128 + 8 * i, desc_mn<DP>(v + 2048 * i), ID_O, first && i == 0 ? 0u : 1u);
+                    mma_ts(tmem + 256 + t * DP, tmem + t * 128 + 8 * i + (i >= TILE / 32 ? 32 : 0), desc_mn<DP>(v + 2048 * i), ID_O, first && i == 0 ? 0u : 1u);
                 commit(pv_done + 8 * t);
             };
             auto wait_p = [&](int t, bool first) {
@@ -445,21 +460,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
             while (ok && next_piece(false)) {
                 const bool two = rows_of() > 128;
                 if (!(ok = mbar_spin(q_full, seg & 1, P.status))) break;
-                if (!(ok = mbar_spin(k_full + 8 * (kit % C::ST), (kit / C::ST) & 1, P.status))) break;
+                if (!(ok = wait_item(ki))) break;
                 tc_fence_after();
                 scores(0);
                 if (two) scores(1);
-                commit(k_empty + 8 * (kit % C::ST));
-                ++kit;
-                if (pc.nt == 1) commit(q_empty);
+                free_item(ki);
+                ki += 2;
                 for (int j = 0; j < pc.nt; ++j) {
                     const bool more = j + 1 < pc.nt;
-                    if (!(ok = mbar_spin(v_full + 8 * (vit % C::ST), (vit / C::ST) & 1, P.status))) break;
+                    if (!(ok = wait_item(vi))) break;
                     if (!(ok = wait_p(0, j == 0))) break;
                     tc_fence_after();
                     values(0, j == 0);
                     if (more) {
-                        if (!(ok = mbar_spin(k_full + 8 * (kit % C::ST), (kit / C::ST) & 1, P.status))) break;
+                        if (!(ok = wait_item(ki))) break;
                         tc_fence_after();
                         scores(0);
                     }
@@ -468,12 +482,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                         tc_fence_after();
                         values(1, j == 0);
                     }
-                    commit(v_empty + 8 * (vit % C::ST));
-                    ++vit;
+                    free_item(vi);
+                    vi += 2;
+                    // (the rows have read what goes with the queries: they have come with P)
+                    if (pc.nt == 1) commit(q_empty);
                     if (more) {
                         if (two) scores(1);
-                        commit(k_empty + 8 * (kit % C::ST));
-                        ++kit;
+                        free_item(ki);
+                        ki += 2;
                         if (j + 2 == pc.nt) commit(q_empty);
                     }
                 }
@@ -527,91 +543,109 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                 if (!more) break;
             }
         }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         // ---- conversion ----
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_B));
-        const int me = tid - 128, w = warp - 4;
-        const int cpr = P.dim / 16;  // 16-code chunks of a token
-        int it = 0, seg = 0;
+        const int side = (warp - 4) >> 2, me = tid & 127, w = warp - 4;  // keys or values
+        const int cpr = P.dim / 16;                                     // 16-code chunks of a token
+        int item = side, seg = 0;
         bool ok = true;
         while (ok && next_piece(true)) {
             const int rows = rows_of(), end = end_of(rows);
             // queries: lanes of 8 values, times a power of two that brings a
             // row's largest to [2^13, 2^14)
-            if (seg > 0) ok = __all_sync(0xffffffffu, mbar_spin(q_empty, (seg - 1) & 1, P.status));
-            if (!ok) break;
             {
-                constexpr int LPR = DP / 8, RPW = 32 / LPR, BATCH = 4;
+                constexpr int LPR = DP / 8, RPW = 32 / LPR, BATCH = 8, NEXT = 8 * RPW;  // rows of a thread are NEXT apart
                 const int d = 8 * (lane % LPR);
-                for (int r = w * RPW + lane / LPR; r < UNIT; r += 4 * RPW * BATCH) {
+                for (int r = w * RPW + lane / LPR; r < UNIT; r += NEXT * BATCH) {
                     uint4 raw[BATCH];
+                    if (PP.q_vec) {
 #pragma unroll
-                    for (int k = 0; k < BATCH; ++k) {
-                        const int rr = r + k * 4 * RPW;
-                        raw[k] = make_uint4(0, 0, 0, 0);
-                        if (rr < rows && d < P.dim) {
-                            const int qr = pc.r0 + rr, i = qr / P.group;
-                            const int64_t at = static_cast<int64_t>(pc.row0 + i) * P.ldq_t +
-                                               static_cast<int64_t>(pc.head * P.group + (qr - i * P.group)) * P.ldq_h + d;
-                            const uint16_t *src = static_cast<const uint16_t *>(P.q) + at;
-                            if (PP.q_vec) raw[k] = __ldg(reinterpret_cast<const uint4 *>(src));
-                            else {
-                                uint32_t v[8];
+                        for (int k = 0; k < BATCH; ++k) {
+                            const int qr = pc.r0 + min(r + k * NEXT, rows - 1), i = token_of(qr);
+                            const uint16_t *src = static_cast<const uint16_t *>(P.q) + static_cast<int64_t>(pc.row0 + i) * P.ldq_t +
+                                                  static_cast<int64_t>(pc.head * P.group + (qr - i * P.group)) * P.ldq_h;
+                            raw[k] = __ldg(reinterpret_cast<const uint4 *>(src + min(d, P.dim - 8)));
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < BATCH; ++k) {
+                            const int qr = pc.r0 + min(r + k * NEXT, rows - 1), i = token_of(qr);
+                            const uint16_t *src = static_cast<const uint16_t *>(P.q) + static_cast<int64_t>(pc.row0 + i) * P.ldq_t +
+                                                  static_cast<int64_t>(pc.head * P.group + (qr - i * P.group)) * P.ldq_h + min(d, P.dim - 8);
+                            uint32_t v[8];
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) v[e] = __ldg(src + e);
-                                raw[k] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-                            }
+                            for (int e = 0; e < 8; ++e) v[e] = __ldg(src + e);
+#pragma unroll
+                            for (int e = 0; e < BATCH - 1; ++e) raw[e] = raw[e + 1];
+                            raw[BATCH - 1] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
                         }
                     }
+                    // (the last unit's scores are done: its queries may go)
+                    if (r < NEXT && seg > 0) ok = __all_sync(0xffffffffu, mbar_spin(q_empty, (seg - 1) & 1, P.status));
+                    if (!ok) break;
+                    // the largest |value| of a row: in either type it is in the order of the bits
+                    const uint32_t inf = P.q_type == QMM_BF16 ? 0x7f80u : 0x7c00u;
+                    uint32_t top[BATCH];
 #pragma unroll
                     for (int k = 0; k < BATCH; ++k) {
-                        const int rr = r + k * 4 * RPW;
+                        const uint32_t m = __vmaxu2(__vmaxu2(raw[k].x & 0x7fff7fffu, raw[k].y & 0x7fff7fffu),
+                                                    __vmaxu2(raw[k].z & 0x7fff7fffu, raw[k].w & 0x7fff7fffu));
+                        top[k] = max(m & 0xffffu, m >> 16);
+                        if (top[k] >= inf) {  // of the finite ones
+                            const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+                            top[k] = 0;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t a = x[e / 2] >> (16 * (e & 1)) & 0x7fffu;
+                                top[k] = a < inf ? max(top[k], a) : top[k];
+                            }
+                        }
+                        if (d >= P.dim) top[k] = 0;
+                    }
+#pragma unroll
+                    for (int o = LPR / 2; o; o >>= 1)
+#pragma unroll
+                        for (int k = 0; k < BATCH; ++k) top[k] = max(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int rr = r + k * NEXT;
                         const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-                        float v[8], top = 0.0f;
+                        const float most = P.q_type == QMM_BF16 ? __uint_as_float(top[k] << 16) : half_bits_to_float(top[k]);
+                        const int e2 = most > 0.0f ? min(max(13 - exponent_of(__float_as_uint(most)), -114), 100) : 0;
+                        // (rows behind the last are zeros; a negative factor goes to the queries)
+                        const float up = rr >= rows ? 0.0f : P.factor < 0.0f ? -pow2f(e2) : pow2f(e2);
+                        uint32_t h[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            if (P.q_type == QMM_BF16) {
-                                v[2 * e] = __uint_as_float(x[e] << 16), v[2 * e + 1] = __uint_as_float(x[e] & 0xffff0000u);
-                            } else {
-                                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x[e]));
-                                v[2 * e] = f.x, v[2 * e + 1] = f.y;
-                            }
+                            float2 v;
+                            if (P.q_type == QMM_BF16) v = make_float2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u));
+                            else v = __half22float2(*reinterpret_cast<const __half2 *>(&x[e]));
+                            h[e] = rr >= rows ? 0 : pack_half(v.x * up, v.y * up);
                         }
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float a = fabsf(v[e]);
-                            top = a <= 3.402823466e38f ? fmaxf(top, a) : top;
-                        }
-#pragma unroll
-                        for (int o = LPR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const int e2 = top > 0.0f ? min(max(13 - exponent_of(__float_as_uint(top)), -114), 100) : 0;
-                        const float up = P.factor < 0.0f ? -pow2f(e2) : pow2f(e2);
-                        if (d < P.dim) {
-                            const uint4 h = make_uint4(pack_half(v[0] * up, v[1] * up), pack_half(v[2] * up, v[3] * up),
-                                                       pack_half(v[4] * up, v[5] * up), pack_half(v[6] * up, v[7] * up));
-                            const int t = rr >> 7, tr = rr & 127;
-                            *reinterpret_cast<uint4 *>(smem + t * C::TILE_BYTES + (d >> 6) * (TILE * 128) + tr * 128 +
-                                                       ((((d & 63) >> 3) ^ (tr & 7)) << 4)) = h;
-                        }
-                        if (d == 0) row_e[(seg & 1) * UNIT + rr] = static_cast<int8_t>(e2);
+                        const int tr = rr & 127;
+                        if (d < P.dim)
+                            *reinterpret_cast<uint4 *>(smem + (rr >> 7) * C::TILE_BYTES + (d >> 6) * (TILE * 128) + tr * 128 +
+                                                       ((((d & 63) >> 3) ^ (tr & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        if (d == 0) row_e[rr] = static_cast<int8_t>(e2);
                     }
                 }
+                if (!ok) break;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full);
                 ++seg;
             }
-            for (int j = 0; ok && j < pc.nt; ++j, ++it) {
-                const int s = it % C::ST, live = end - (pc.tile + j) * TILE;  // tokens below it are in the sequence
-#pragma unroll
-                for (int side = 0; side < 2; ++side) {
-                    const uint32_t full = side ? v_full : k_full, empty = side ? v_empty : k_empty;
-                    bool go = mbar_spin(raw_full + 8 * side, it & 1, P.status);
-                    if (go && it >= C::ST) go = mbar_spin(empty + 8 * s, ((it / C::ST) - 1) & 1, P.status);
+            for (int j = 0; ok && j < pc.nt; ++j, item += 2) {
+                const int live = end - (pc.tile + j) * TILE;  // tokens below it are in the sequence
+                {
+                    const int raw = item % C::RAW_RING, s = item % C::RING;
+                    bool go = mbar_spin(raw_full + 8 * raw, (item / C::RAW_RING) & 1, P.status);
+                    if (go && item >= C::RING) go = mbar_spin(kv_empty + 8 * s, ((item / C::RING) - 1) & 1, P.status);
                     ok = __all_sync(0xffffffffu, go);
                     if (!ok) break;
-                    const uint4 *src = reinterpret_cast<const uint4 *>(smem + C::OFF_RAW + side * C::RAW);
-                    uint8_t *dst = smem + (side ? C::OFF_V : C::OFF_K) + s * C::TILE_BYTES;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(smem + C::OFF_RAW + raw * C::RAW);
+                    uint8_t *dst = smem + C::OFF_RING + s * C::TILE_BYTES;
                     auto one = [&](int row, int c, const uint4 &v) {
                         uint4 a, b;
                         convert16(v, a, b);
@@ -622,7 +656,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                         *reinterpret_cast<uint4 *>(p + (((q + 1 - (h & 1)) ^ x) << 4)) = h & 1 ? a : b;
                     };
                     if (cpr == DP / 16) {
-#pragma unroll 4
+#pragma unroll
                         for (int k = 0; k < DP / 16; ++k) {
                             const int idx = me + 128 * k, row = idx / (DP / 16), c = idx % (DP / 16);
                             uint4 v = src[idx];
@@ -641,8 +675,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(full + 8 * s);
-                        mbar_arrive(raw_empty + 8 * side);
+                        mbar_arrive(kv_full + 8 * s);
+                        mbar_arrive(raw_empty + 8 * raw);
                     }
                 }
             }
@@ -650,64 +684,79 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
     } else {
         // ---- rows ----
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_C));
-        const int t = (warp - 8) >> 2, lane_row = 32 * (warp & 3) + lane;  // tile, and this thread's row (TMEM lane) of it
-        const uint32_t my_s = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + t * 128;
-        const uint32_t my_o = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 256 + t * DP;
-        int it = 0, tiles = 0, seg = 0;  // tiles of this role, tiles and units of the CTA
+        // tile, half of its tokens (and of O's columns), and this thread's row (TMEM lane)
+        const int t = (warp - 12) >> 3, half = (warp - 12) >> 2 & 1, lane_row = 32 * (warp & 3) + lane;
+        constexpr int HT = TILE / 2, HD = DP / 2;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t my_s = tmem + lanes + t * 128 + half * HT, my_p = my_s;  // (P over the scores that this thread has read)
+        const uint32_t my_o = tmem + lanes + 256 + t * DP + half * HD;
+        const int pair_bar = 1 + 4 * t + (warp & 3);  // of the two warps that share 32 rows
+        const int mine = 128 * t + lane_row;
+        float *const tell = reinterpret_cast<float *>(smem + C::OFF_SHARE) + half * UNIT + mine;
+        const float *const told = reinterpret_cast<const float *>(smem + C::OFF_SHARE) + (half ^ 1) * UNIT + mine;
+        int it = 0, tiles = 0;  // tiles of this role, tiles of the CTA
         bool ok = true;
         while (ok && next_piece(true)) {
             const int rows = rows_of();
-            const int mine = 128 * t + lane_row, start = pc.len - pc.n;
+            const int start = pc.len - pc.n;
             bool store = false;
             float ref = -INFINITY, l = 0.0f;
             if (rows > 128 * t) {
                 // tokens that this row sees, and those that all rows see
-                const int i = (pc.r0 + min(mine, rows - 1)) / P.group;
+                const int i = token_of(pc.r0 + min(mine, rows - 1));
                 const int hi = P.causal ? min(pc.len, start + i + 1) : pc.len, lo = P.window ? start + i - P.window + 1 : 0;
-                const int first_i = (pc.r0 + 128 * t) / P.group, last_i = (pc.r0 + min(rows, 128 * t + 128) - 1) / P.group;
+                const int first_i = token_of(pc.r0 + 128 * t), last_i = token_of(pc.r0 + min(rows, 128 * t + 128) - 1);
                 const int all_hi = P.causal ? min(pc.len, start + first_i + 1) : pc.len;
                 const int all_lo = P.window ? start + last_i - P.window + 1 : 0;
                 float f = 0.0f;
                 for (int j = 0; j < pc.nt; ++j, ++it) {
-                    const float4 *scale = reinterpret_cast<const float4 *>(sc + ((tiles + j) % SC_SLOTS) * SC_FLOATS);
+                    // of keys, log2 of values' (groups of 16 tokens)
+                    const float *scale = sc + ((tiles + j) % SC_SLOTS) * SC_FLOATS + half * (HT / 16);
                     ok = __all_sync(0xffffffffu, mbar_spin(s_full + 8 * t, it & 1, P.status));
-                    if (!ok) break;
                     tc_fence_after();
-                    uint32_t s[TILE];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) tmem_ld32(my_s + 32 * k, s + 32 * k);
-                    tmem_wait32(s);
-                    tie32(s + 32), tie32(s + 64), tie32(s + 96);
-                    if (j == 0) f = fabsf(P.factor) * pow2f(-row_e[(seg & 1) * UNIT + mine]);
-                    float x[TILE];
-#pragma unroll
-                    for (int k = 0; k < TILE; ++k) x[k] = __uint_as_float(s[k]);
-                    float fs[8], lv[8];
-                    {
-                        const float4 a = scale[0], b = scale[1], c = scale[2], d = scale[3];
-                        fs[0] = f * a.x, fs[1] = f * a.y, fs[2] = f * a.z, fs[3] = f * a.w;
-                        fs[4] = f * b.x, fs[5] = f * b.y, fs[6] = f * b.z, fs[7] = f * b.w;
-                        lv[0] = c.x, lv[1] = c.y, lv[2] = c.z, lv[3] = c.w, lv[4] = d.x, lv[5] = d.y, lv[6] = d.z, lv[7] = d.w;
-                    }
-                    const int tok = (pc.tile + j) * TILE;
-                    if (tok < all_lo || tok + TILE > all_hi) {
-                        const int from = lo - tok, to = hi - tok;
-#pragma unroll
-                        for (int k = 0; k < TILE; ++k) {
-                            const float v = fmaf(x[k], fs[k / 16], lv[k / 16]);
-                            x[k] = k >= from && k < to ? v : -INFINITY;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) fs[k] = 1.0f, lv[k] = 0.0f;
-                    }
+                    if (j == 0) f = fabsf(P.factor) * pow2f(-row_e[mine]);
+                    const int tok = (pc.tile + j) * TILE + half * HT;
+                    const bool masked = tok < all_lo || tok + HT > all_hi;
+                    const int from = lo - tok, to = hi - tok;
+                    // The scores are read twice, for the maximum and for the
+                    // exponentials: all of them do not fit a thread's registers
+                    // beside the rest.
                     float top = -INFINITY;
+                    auto maximum = [&](auto with_mask) {
+                        uint32_t s[32];
+#pragma unroll 1
+                        for (int h = 0; h < HT / 32; ++h) {
+                            tmem_ld32(my_s + 32 * h, s);
+                            tmem_wait32(s);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float a = x[16 * k];
+                            for (int k = 0; k < 2; ++k) {
+                                const float fk = f * scale[2 * h + k], lv = scale[8 + 2 * h + k];
+                                float a[16];
 #pragma unroll
-                        for (int e = 1; e < 16; ++e) a = fmaxf(a, x[16 * k + e]);
-                        top = fmaxf(top, fmaf(a, fs[k], lv[k]));
+                                for (int e = 0; e < 16; ++e) {
+                                    a[e] = __uint_as_float(s[16 * k + e]);
+                                    if constexpr (with_mask.value) {
+                                        const int c = 32 * h + 16 * k + e;
+                                        a[e] = c >= from && c < to ? fmaf(a[e], fk, lv) : -INFINITY;
+                                    }
+                                }
+                                const float m = max3(max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), max3(a[6], a[7], a[8])),
+                                                     max3(a[9], a[10], a[11]), max3(max3(a[12], a[13], a[14]), a[15], a[0]));
+                                top = fmaxf(top, with_mask.value ? m : fmaf(m, fk, lv));
+                            }
+                        }
+                    };
+                    if (ok) {
+                        if (masked) maximum(std::true_type());
+                        else maximum(std::false_type());
                     }
+                    *tell = top;
+                    // (both warps of the pair take the same way from here)
+                    if (named_barrier_or(pair_bar, 64, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                    top = fmaxf(top, *told);
                     const bool move = top > ref + MOVE;
                     if (__any_sync(0xffffffffu, move)) {
                         const float now = move ? ceilf(top) : ref;
@@ -716,10 +765,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                         l *= down;
                         if (j > 0) {
                             ok = __all_sync(0xffffffffu, mbar_spin(pv_done + 8 * t, (it - 1) & 1, P.status));
-                            if (!ok) break;
                             tc_fence_after();
-#pragma unroll
-                            for (int k = 0; k < DP / 32; ++k) {
+#pragma unroll 1
+                            for (int k = 0; ok && k < HD / 32; ++k) {
                                 uint32_t o[32];
                                 tmem_ld32(my_o + 32 * k, o);
                                 tmem_wait32(o);
@@ -729,28 +777,40 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                             }
                         }
                     }
-                    const float sub = ref == -INFINITY ? 0.0f : ref;
-                    const float4 ia = scale[4], ib = scale[5];
-                    const float iv[8] = {ia.x, ia.y, ia.z, ia.w, ib.x, ib.y, ib.z, ib.w};
+                    const float sub = ref == -INFINITY ? 0.0f : ref;  // (a row that has seen nothing yet: any finite one)
+                    auto exponentials = [&](auto with_mask) {
+                        uint32_t s[2][16];
+                        tmem_ld16(my_s, s[0]);
+                        tmem_wait16(s[0]);
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int k = 2 * h; k < 2 * h + 2; ++k) {
-                            const float d = lv[k] - sub + TC_SHIFT;
-                            float s0 = 0.0f, s1 = 0.0f;
+                        for (int h = 0; h < HT / 16; ++h) {
+                            if (h + 1 < HT / 16) tmem_ld16(my_s + 16 * (h + 1), s[(h + 1) & 1]);
+                            uint32_t p[8];
+                            const float fk = f * scale[h], d = scale[8 + h] - sub + TC_SHIFT;
+                            float v[16];
 #pragma unroll
                             for (int e = 0; e < 16; e += 2) {
-                                float a = x[16 * k + e], b = x[16 * k + e + 1];
-                                fma2(a, b, fs[k], d);
-                                a = ex2(a), b = ex2(b);
-                                add2(s0, s1, a, b);
-                                p[8 * (k & 1) + e / 2] = pack_half(a, b);
+                                float a = __uint_as_float(s[h & 1][e]), b = __uint_as_float(s[h & 1][e + 1]);
+                                fma2(a, b, fk, d);
+                                if constexpr (with_mask.value) {
+                                    const int c = 16 * h + e;
+                                    a = c >= from && c < to ? a : -INFINITY;
+                                    b = c + 1 >= from && c + 1 < to ? b : -INFINITY;
+                                }
+                                v[e] = ex2(a), v[e + 1] = ex2(b);
+                                p[e / 2] = pack_half(v[e], v[e + 1]);
                             }
-                            l = fmaf(s0 + s1, iv[k], l);
+#pragma unroll
+                            for (int o = 8; o >= 2; o >>= 1)
+#pragma unroll
+                                for (int e = 0; e < o; e += 2) add2(v[e], v[e + 1], v[e + o], v[e + o + 1]);
+                            l = fmaf(v[0] + v[1], ex2(-20.0f - scale[8 + h]), l);  // (L_FACTOR / the values' scale)
+                            if (h + 1 < HT / 16) tmem_wait16(s[(h + 1) & 1]);
+                            tmem_st8(my_p + 8 * h, p);
                         }
-                        tmem_st16(my_s + 16 * h, p);
-                    }
+                    };
+                    if (masked) exponentials(std::true_type());
+                    else exponentials(std::false_type());
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -759,23 +819,25 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                 if (ok) ok = __all_sync(0xffffffffu, mbar_spin(pv_done + 8 * t, (it - 1) & 1, P.status));
                 tc_fence_after();
                 store = ok;
+                *tell = l;
             }
             tiles += pc.nt;
-            ++seg;
             // every warp of the tile passes here once per piece, also after a wait
             // that gave up, so that none is left at a barrier alone
-            if (named_barrier_or(1 + t, 128, !ok)) {
+            if (named_barrier_or(9 + t, 256, !ok)) {
                 ok = false;
                 break;
             }
             if (!store) continue;
+            l += *told;
+            named_barrier(pair_bar, 64);  // (it is told the next unit's maxima there)
             auto result = [&](int64_t &at, int64_t &row) {
-                const int qr = pc.r0 + mine, i = qr / P.group, h = pc.head * P.group + (qr - i * P.group);
+                const int qr = pc.r0 + mine, i = token_of(qr), h = pc.head * P.group + (qr - i * P.group);
                 at = static_cast<int64_t>(pc.row0 + i) * P.ldy_t + static_cast<int64_t>(h) * P.ldy_h;
                 row = (static_cast<int64_t>(pc.row0) + i) * P.heads * P.group + h;
             };
             auto put = [&](int64_t at, int d, const float *v, int n) {  // n values from d on
-                const int es = P.y_type == QMM_F32 ? 4 : 2, per = 16 / es;
+                const int es = P.y_type == QMM_F32 ? 4 : 2;
 #pragma unroll
                 for (int k = 0; k < n; k += 4) {
                     if (d + k >= P.dim) break;
@@ -798,7 +860,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                         for (int e = 0; e < 4; ++e) store_typed(P.y, at + d + k + e, P.y_type, v[k + e]);
                     }
                 }
-                (void)per;
             };
             constexpr float LN2 = 0.6931471805599453f, BACK = 20.0f - TC_SHIFT;
             if (pc.c0 < 0) {
@@ -806,11 +867,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                 int64_t at, row;
                 result(at, row);
 #pragma unroll
-                for (int k = 0; k < DP / 32; ++k) {
+                for (int k = 0; k < HD / 32; ++k) {
                     uint32_t o[32];
                     tmem_ld32(my_o + 32 * k, o);
                     tmem_wait32(o);
-                    if (k == DP / 32 - 1) {  // everything is out: the next unit's sums may come
+                    if (k == HD / 32 - 1) {  // everything is out: the next unit's sums may come
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(o_empty + 8 * t);
@@ -818,34 +879,33 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                     float v[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * inv;
-                    if (mine < rows) put(at, 32 * k, v, 32);
+                    if (mine < rows) put(at, half * HD + 32 * k, v, 32);
                 }
-                if (P.lse && mine < rows) P.lse[row] = l != 0.0f ? (ref + log2f(l) + BACK) * LN2 : -INFINITY;
+                if (P.lse && half == 0 && mine < rows) P.lse[row] = l != 0.0f ? (ref + log2f(l) + BACK) * LN2 : -INFINITY;
             } else {
                 // a part of a unit: [groups of four columns][row] sums relative to ref, then ref and l
                 float *const part = P.part + (static_cast<int64_t>(cta) * 2 + pc.begin) * C::PART;
 #pragma unroll
-                for (int k = 0; k < DP / 32; ++k) {
+                for (int k = 0; k < HD / 32; ++k) {
                     uint32_t o[32];
                     tmem_ld32(my_o + 32 * k, o);
                     tmem_wait32(o);
-                    if (k == DP / 32 - 1) {
+                    if (k == HD / 32 - 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(o_empty + 8 * t);
                     }
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        reinterpret_cast<uint4 *>(part)[(8 * k + e / 4) * UNIT + mine] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        reinterpret_cast<uint4 *>(part)[(half * HD / 4 + 8 * k + e / 4) * UNIT + mine] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
-                part[DP * UNIT + mine] = ref;
-                part[(DP + 1) * UNIT + mine] = l;
+                if (half == 0) part[DP * UNIT + mine] = ref, part[(DP + 1) * UNIT + mine] = l;
                 __threadfence();
-                named_barrier(1 + t, 128);
-                if (tid % 128 == 0) arrived[t] = atomicAdd(P.count + 2 * pc.c0 + t, 1u);
-                named_barrier(1 + t, 128);
+                named_barrier(9 + t, 256);
+                if ((warp - 12) % 8 == 0 && lane == 0) arrived[t] = atomicAdd(P.count + 2 * pc.c0 + t, 1u);
+                named_barrier(9 + t, 256);
                 if (arrived[t] == static_cast<unsigned>(pc.c1 - pc.c0)) {
-                    if (tid % 128 == 0) P.count[2 * pc.c0 + t] = 0u;  // zero again for the next launch
+                    if ((warp - 12) % 8 == 0 && lane == 0) P.count[2 * pc.c0 + t] = 0u;  // zero again for the next launch
                     __threadfence();
                     auto part_of = [&](int c) { return P.part + (static_cast<int64_t>(c) * 2 + (c == pc.c0)) * C::PART; };
                     float top = -INFINITY, sum = 0.0f;
@@ -856,28 +916,32 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                     const float inv = sum != 0.0f ? L_FACTOR / sum : 0.0f;
                     int64_t at, row;
                     result(at, row);
-                    for (int k = 0; k < DP / 16; ++k) {
-                        float v[16];
+#pragma unroll 1
+                    for (int k = half * HD / 32; k < (half + 1) * HD / 32; ++k) {
+                        float v[32];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+                        for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+#pragma unroll 1
                         for (int c = pc.c0; c <= pc.c1; ++c) {
-                            const float4 *q = reinterpret_cast<const float4 *>(part_of(c)) + 4 * k * UNIT + mine;
+                            const float4 *q = reinterpret_cast<const float4 *>(part_of(c)) + 8 * k * UNIT + mine;
                             const float w = ex2(__ldcg(part_of(c) + DP * UNIT + mine) - sub) * inv;
+                            float4 o[8];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float4 o = __ldcg(q + e * UNIT);
-                                v[4 * e] = fmaf(o.x, w, v[4 * e]), v[4 * e + 1] = fmaf(o.y, w, v[4 * e + 1]);
-                                v[4 * e + 2] = fmaf(o.z, w, v[4 * e + 2]), v[4 * e + 3] = fmaf(o.w, w, v[4 * e + 3]);
+                            for (int e = 0; e < 8; ++e) o[e] = __ldcg(q + e * UNIT);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                v[4 * e] = fmaf(o[e].x, w, v[4 * e]), v[4 * e + 1] = fmaf(o[e].y, w, v[4 * e + 1]);
+                                v[4 * e + 2] = fmaf(o[e].z, w, v[4 * e + 2]), v[4 * e + 3] = fmaf(o[e].w, w, v[4 * e + 3]);
                             }
                         }
-                        if (mine < rows) put(at, 16 * k, v, 16);
+                        if (mine < rows) put(at, 32 * k, v, 32);
                     }
-                    if (P.lse && mine < rows) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + BACK) * LN2 : -INFINITY;
+                    if (P.lse && half == 0 && mine < rows) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + BACK) * LN2 : -INFINITY;
                 }
             }
         }
         // (a closing record, and one whose wait ran out, counts as a piece at the barrier above)
-        if (ok) named_barrier_or(1 + t, 128, true);
+        if (ok) named_barrier_or(9 + t, 256, true);
     }
     tc_fence_before();
     __syncthreads();
@@ -899,7 +963,7 @@ cudaError_t launch_dp(const TcParams &p, cudaStream_t st, int num_sms, int dev) 
         // setmaxnreg draws on what the launch brings
         cudaFuncAttributes fa;
         if ((r = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return r;
-        return fa.numRegs * TC_THREADS < 128 * (REGS_A + REGS_B + 2 * REGS_C) ? cudaErrorNotSupported : cudaSuccess;
+        return fa.numRegs < REGS ? cudaErrorNotSupported : cudaSuccess;
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -936,6 +1000,8 @@ cudaError_t launch_tc(const AttnParams &a, int stop, cudaStream_t st, int num_sm
     p.q_vec = vec(a.q, a.q_type, a.ldq_t, a.ldq_h);
     p.y_vec = vec(a.y, a.y_type, a.ldy_t, a.ldy_h);
     p.stop = stop;
+    for (p.div_shift = 31; (int64_t(1) << (p.div_shift - 31)) < a.group;) ++p.div_shift;
+    p.div_mul = static_cast<uint32_t>(((uint64_t(1) << p.div_shift) + a.group - 1) / a.group);
     return a.dim <= 64 ? launch_dp<64>(p, st, num_sms, dev) : launch_dp<128>(p, st, num_sms, dev);
 }
 
