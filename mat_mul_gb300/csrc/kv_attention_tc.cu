@@ -5,25 +5,31 @@
 // The formulas are those of kv_attention.cuh.  A unit is 256 query rows (rows
 // of the batch times query heads of one cache head, two TMEM tiles of 128)
 // over the tokens that some of them see, 128 at a time:
-//   S_t [128 rows x 128 tokens] = Q_t K^T        operands in shared memory
-//   P_t = 2^(x - reference) as fp16              over S_t's columns in TMEM
-//   O_t [128 rows x dim]       += P_t V          A in TMEM, V as it lies in
-//                                                the cache (tokens x dim)
-// While the tensor cores work on one tile, the other's warps take the
-// exponentials.  The codes arrive by bulk copies, page by page, and four warps
-// turn them into fp16 (exactly) in the 128-byte swizzle that the products read.
+//   S_t [128 rows x 128 tokens] = Q_t K^T       kind::f8f6f4, both in shared memory
+//   P_t = 2^(x - reference) as fp16             over S_t's columns in TMEM
+//   O_t [128 rows x dim]       += P_t V         kind::f16, A in TMEM, V as it lies
+//                                               in the cache (tokens x dim)
+// Keys go from the cache to the tensor cores as they are: TMA brings their codes
+// in the 128-byte swizzle, and a query is the sum of e4m3 parts, two for bf16 (4
+// bits each: its 8 bits) and three for fp16, in one power of two per row.  Parts
+// are cut off at 2^-10 of a scale at which the row's largest value is 2^7 to 2^8, so
+// values below 2^-9 of it lose bits of theirs (an error of 2^-17 of the largest at
+// most).  Two parts at the rate of 8-bit codes cost what one fp16 operand
+// costs.  Values have to meet P in fp16: four warps convert them (exactly).
 //
-// The reference of a row is its running maximum, but only moved when the
-// maximum has grown by more than 2^8 of it: fp16 holds P up to 2^14 then, and O
+// While the tensor cores work on one tile, the other's warps take the
+// exponentials.  The reference of a row is its running maximum, but only moved when
+// the maximum has grown by more than 2^8 of it: fp16 holds P up to 2^14 then, and O
 // is scaled anew a few times per row instead of once per tile.
 //
-// All units' tiles form one list that is cut into equal shares, one per CTA;
-// what is cut is joined by the last of its CTAs, in the order of the tokens.
+// All units' tiles form one list that is cut into equal shares, one per CTA, a
+// unit counting UNIT_COST tiles more than it has; what is cut is joined by the
+// last of its CTAs, in the order of the tokens.
 //
 // Warp roles: 0 = copies, 1 = MMA issue, 2 = schedule, 3 = tensor memory;
-// 4..7 and 8..11 = conversion of keys and of values, both of queries; 12..19
-// and 20..27 = rows of the first and the second tile, two threads per row
-// (each with half of the tokens, and half of the columns of O).
+// 4..7 = conversion of values; 8..15 and 16..23 = rows of the first and the
+// second tile, two threads per row (each with half of the tokens, and half of the
+// columns of O).
 // All waits are bounded: a role whose wait ran out stops, the others' then run
 // out too, every copy in flight is waited for and TMEM is freed.
 #include <type_traits>
@@ -41,33 +47,35 @@ using f8::mbar_spin;
 using f8::tc_fence_after;
 using f8::tc_fence_before;
 
-constexpr int TC_THREADS = 896, UNIT = 256;
-constexpr int TC_LEAST = 4;  // tiles per CTA below which fewer CTAs take part
-constexpr int PIECES = 2, SC_SLOTS = 4, SC_FLOATS = 16;
+constexpr int TC_THREADS = 768, UNIT = 256;
+constexpr int TC_LEAST = 6;   // tiles (and unit costs) per CTA below which fewer CTAs take part
+constexpr int UNIT_COST = 2;  // what a unit costs beside its tiles, in tiles
+constexpr int PIECES = 3, SC_SLOTS = 4, SC_FLOATS = 16;
 // registers per thread at launch, and after the split between roles 0..3, conversion and rows
-constexpr int REGS = 72, REGS_A = 48, REGS_B = 64, REGS_C = 80;
-static_assert(128 * (REGS_A + 2 * REGS_B + 4 * REGS_C) <= TC_THREADS * REGS, "register split");
+constexpr int REGS = 80, REGS_A = 56, REGS_B = 64, REGS_C = 88;
+static_assert(128 * (REGS_A + REGS_B + 4 * REGS_C) <= TC_THREADS * REGS, "register split");
 constexpr float MOVE = 8.0f;      // growth of the maximum that moves the reference
 constexpr float TC_SHIFT = 6.0f;  // P as fp16 is at most 2^(MOVE + TC_SHIFT)
 
-template <int DP>
+// Where P of token group g (16 tokens) of a tile lies, from its first column on:
+// over the scores of its thread's half, columns that were read before it is written.
+__device__ __forceinline__ constexpr int p_column(int g) { return 64 * (g >> 2) + 32 * (g >> 1 & 1) + 8 * (g & 1); }
+
+// NQ: e4m3 parts of a query.
+template <int DP, int NQ>
 struct Tc {
-    // Converted keys and values take turns in a ring.  Three slots do: a slot is
-    // asked for again two products after its last one, about 1000 cycles.
-    static constexpr int RING = DP == 128 ? 3 : 4;
-    static constexpr int RAW_RING = 4;                // codes on their way, keys and values in turn
-    static constexpr int TILE_BYTES = TILE * DP * 2;  // a slot, and one tile of queries
-    static constexpr int OFF_RING = 2 * TILE_BYTES;
-    static constexpr int RAW = TILE * DP;             // codes of a slot
-    static constexpr int OFF_RAW = OFF_RING + RING * TILE_BYTES;
-    static constexpr int OFF_ROW = OFF_RAW + RAW_RING * RAW;             // power of two of each row's queries
-    static constexpr int OFF_SHARE = OFF_ROW + UNIT;           // [2 halves][UNIT] what the threads of a row tell each other
-    static constexpr int OFF_SC = OFF_SHARE + 2 * UNIT * 4;              // [SC_SLOTS] key scales and log2 of value scales
+    static constexpr int KEYS = TILE * 128;                  // a tile of keys, and a part of a tile of queries: rows of 128 bytes
+    static constexpr int KR = DP == 128 && NQ == 3 ? 2 : 4;  // tiles of keys on their way
+    static constexpr int VR = 2;                             // tiles of values on their way, and converted
+    static constexpr int RAW = TILE * DP, TILE_BYTES = TILE * DP * 2;
+    static constexpr int OFF_K = 2 * NQ * KEYS, OFF_V = OFF_K + KR * KEYS, OFF_RAW = OFF_V + VR * TILE_BYTES;
+    static constexpr int OFF_SHARE = OFF_RAW + VR * RAW;          // [2 halves][UNIT] what the threads of a row tell each other
+    static constexpr int OFF_SC = OFF_SHARE + 2 * UNIT * 4;       // [SC_SLOTS] key scales and log2 of value scales
     static constexpr int OFF_PIECES = OFF_SC + SC_SLOTS * SC_FLOATS * 4;
     static constexpr int OFF_BAR = OFF_PIECES + PIECES * 48;
-    static constexpr int SMEM = OFF_BAR + 288;
+    static constexpr int SMEM = OFF_BAR + 312;
     static_assert(SMEM <= 232448, "shared memory");
-    static_assert(RAW_RING * RAW >= (TC_THREADS + 1) * 8, "prefix sums lie where the codes will");
+    static_assert(VR * RAW >= (TC_THREADS + 1) * 8, "prefix sums lie where the codes will");
     static constexpr int PART = UNIT * (DP + 2);  // floats of a partial result
 };
 
@@ -114,6 +122,13 @@ __device__ __forceinline__ bool load_pair(const AttnParams &P, int p, Pair &q) {
     return true;
 }
 
+// A page of one head: box of `page` rows of 128 bytes (zeros behind dim).
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, int tile, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(0), "r"(tile), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
@@ -126,7 +141,7 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
@@ -153,33 +168,21 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
 
 #define KV_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
 #define KV_RW4(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])
+#define KV_RWF4(m) "+f"(m[0]), "+f"(m[1]), "+f"(m[2]), "+f"(m[3])
 #define KV_I4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
-__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t *r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : KV_R4(r, 0), KV_R4(r, 4), KV_R4(r, 8), KV_R4(r, 12), KV_R4(r, 16), KV_R4(r, 20), KV_R4(r, 24), KV_R4(r, 28)
-        : "r"(a));
-}
-// Wait for the loads issued; the registers are operands so that no use moves before.
-__device__ __forceinline__ void tmem_wait32(uint32_t *r) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : KV_RW4(r, 0), KV_RW4(r, 4), KV_RW4(r, 8), KV_RW4(r, 12), KV_RW4(r, 16), KV_RW4(r, 20), KV_RW4(r, 24),
-                   KV_RW4(r, 28)
-                 :
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::KV_I4(r, 0),
-        KV_I4(r, 4), KV_I4(r, 8), KV_I4(r, 12), KV_I4(r, 16), KV_I4(r, 20), KV_I4(r, 24), KV_I4(r, 28), "r"(a)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t *r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                  : KV_R4(r, 0), KV_R4(r, 4), KV_R4(r, 8), KV_R4(r, 12)
                  : "r"(a));
+}
+// 16 columns and the largest of them.
+__device__ __forceinline__ float tmem_max16(uint32_t a, uint32_t *r) {
+    float m;
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, [%17];"
+        : KV_R4(r, 0), KV_R4(r, 4), KV_R4(r, 8), KV_R4(r, 12), "=f"(m)
+        : "r"(a));
+    return m;
 }
 __device__ __forceinline__ void tmem_wait16(uint32_t *r) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : KV_RW4(r, 0), KV_RW4(r, 4), KV_RW4(r, 8), KV_RW4(r, 12) : : "memory");
@@ -187,6 +190,12 @@ __device__ __forceinline__ void tmem_wait16(uint32_t *r) {
 __device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t *r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::KV_I4(r, 0), KV_I4(r, 4), "r"(a)
                  : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::KV_I4(r, 0),
+        KV_I4(r, 4), KV_I4(r, 8), KV_I4(r, 12), "r"(a)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -226,49 +235,63 @@ __device__ __forceinline__ void convert16(const uint4 &w, uint4 &a, uint4 &b) {
     b = make_uint4(halves(w.z), halves_hi(w.z), halves(w.w), halves_hi(w.w));
 }
 
-template <int DP>
-__global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const TcParams PP) {
-    using C = Tc<DP>;
-    constexpr int KS = DP / 16;
+// Four values as codes, and what the codes leave of them.
+__device__ __forceinline__ uint32_t part4(float (&v)[4]) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        v[2 * i] -= f.x, v[2 * i + 1] -= f.y;
+        w |= static_cast<uint32_t>(c) << (16 * i);
+    }
+    return w;
+}
+
+template <int DP, int NQ>
+__global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const TcParams PP) {
+    using C = Tc<DP, NQ>;
     const AttnParams &P = PP.a;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    const uint32_t bar = base + C::OFF_BAR;
-    const uint32_t raw_full = bar, raw_empty = raw_full + 8 * C::RAW_RING;
-    const uint32_t kv_full = raw_empty + 8 * C::RAW_RING, kv_empty = kv_full + 8 * C::RING;
-    const uint32_t q_full = kv_empty + 8 * C::RING, q_empty = q_full + 8;
-    const uint32_t s_full = q_empty + 8, p_full = s_full + 16, pv_done = p_full + 16, o_empty = pv_done + 16;  // per tile
-    const uint32_t pc_full = o_empty + 16, pc_empty = pc_full + 8 * PIECES, done = pc_empty + 8 * PIECES;
-    static_assert(16 * (C::RAW_RING + C::RING) + 16 + 64 + 16 * PIECES + 8 <= 264, "barriers");
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 264);
-    volatile unsigned *const arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 272);  // per tile
+    const uint32_t k_full = base + C::OFF_BAR, k_empty = k_full + 8 * C::KR;
+    const uint32_t raw_full = k_empty + 8 * C::KR, raw_empty = raw_full + 8 * C::VR;
+    const uint32_t v_full = raw_empty + 8 * C::VR, v_empty = v_full + 8 * C::VR;
+    const uint32_t q_full = v_empty + 8 * C::VR, s_full = q_full + 16, pv_done = s_full + 16, o_empty = pv_done + 16;  // per tile
+    const uint32_t p_full = o_empty + 16;  // per tile, two halves of its groups of tokens
+    const uint32_t pc_full = p_full + 32, pc_empty = pc_full + 8 * PIECES, done = pc_empty + 8 * PIECES;
+    static_assert(16 * C::KR + 32 * C::VR + 64 + 32 + 16 * PIECES + 8 <= 296, "barriers");
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 296);
+    volatile unsigned *const arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 304);  // per tile
     int4 *const pieces = reinterpret_cast<int4 *>(smem + C::OFF_PIECES);
-    int8_t *const row_e = reinterpret_cast<int8_t *>(smem + C::OFF_ROW);
     float *const sc = reinterpret_cast<float *>(smem + C::OFF_SC);
     long long *const pre = reinterpret_cast<long long *>(smem + C::OFF_RAW);
 
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, 8);
-            mbar_init(pv_done + 8 * i, 1);
-            mbar_init(o_empty + 8 * i, 8);
+        for (int i = 0; i < C::KR; ++i) {
+            mbar_init(k_full + 8 * i, 1);
+            mbar_init(k_empty + 8 * i, 1);
         }
-        for (int i = 0; i < C::RAW_RING; ++i) {
+        for (int i = 0; i < C::VR; ++i) {
             mbar_init(raw_full + 8 * i, 1);
             mbar_init(raw_empty + 8 * i, 4);
+            mbar_init(v_full + 8 * i, 4);
+            mbar_init(v_empty + 8 * i, 1);
         }
-        for (int i = 0; i < C::RING; ++i) {
-            mbar_init(kv_full + 8 * i, 4);
-            mbar_init(kv_empty + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + 8 * i, 8);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(pv_done + 8 * i, 1);
+            mbar_init(o_empty + 8 * i, 8);
+            mbar_init(p_full + 16 * i, 8);
+            mbar_init(p_full + 16 * i + 8, 8);
         }
-        mbar_init(q_full, 8);
-        mbar_init(q_empty, 1);
         for (int i = 0; i < PIECES; ++i) {
             mbar_init(pc_full + 8 * i, 1);
-            mbar_init(pc_empty + 8 * i, 1 + 1 + 8 + 16);  // copies, MMA, conversion, rows
+            mbar_init(pc_empty + 8 * i, 1 + 1 + 4 + 16);  // copies, MMA, conversion, rows
         }
         mbar_init(done, 1);
         fence_mbar_init();
@@ -277,22 +300,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (DP > P.dim) {  // columns that no conversion writes
-        uint4 *z = reinterpret_cast<uint4 *>(smem);
-        for (int i = tid; i < C::OFF_RAW / 16; i += TC_THREADS) z[i] = make_uint4(0, 0, 0, 0);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
     pdl_wait();
     pdl_trigger();
 
-    // the tiles of the pairs before each thread's share of them
+    // what the pairs before each thread's share of them cost
     const int share = (PP.pairs + TC_THREADS - 1) / TC_THREADS;
     {
         long long sum = 0;
         for (int p = tid * share; p < min(PP.pairs, (tid + 1) * share); ++p) {
             Pair q;
             if (!load_pair(P, p, q)) atomicOr(P.status, STATUS_INDEX);
-            sum += q.tiles;
+            if (q.tiles > 0) sum += q.tiles + UNIT_COST;
         }
         sum *= P.heads;
         long long incl = sum;
@@ -332,44 +350,53 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // The next piece of work, from the scheduling warp.
-    struct {
-        int row0, n, len, r0, head, b, tile, nt, c0, c1, begin;
-    } pc;
-    int np = 0;
-    auto next_piece = [&](bool whole_warp) -> bool {
-        const int s = np % PIECES;
-        bool ok = mbar_spin(pc_full + 8 * s, (np / PIECES) & 1, P.status);
-        if (whole_warp) ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return false;
-        const int4 a = pieces[3 * s], b = pieces[3 * s + 1], c = pieces[3 * s + 2];
-        pc.row0 = a.x, pc.n = a.y, pc.len = a.z, pc.r0 = a.w;
-        pc.head = b.x, pc.b = b.y, pc.tile = b.z, pc.nt = b.w;
-        pc.c0 = c.x, pc.c1 = c.y, pc.begin = c.z;
-        if (whole_warp) __syncwarp();
-        if (!whole_warp || lane == 0) mbar_arrive(pc_empty + 8 * s);
-        ++np;
-        return c.w != 0;
+    // A piece of work, from the scheduling warp.
+    struct Piece {
+        int row0, n, len, r0, head, b, tile, nt, c0, c1, begin, more;
+    };
+    auto read_piece = [&](int n) {
+        const int4 a = pieces[3 * (n % PIECES)], b = pieces[3 * (n % PIECES) + 1], c = pieces[3 * (n % PIECES) + 2];
+        return Piece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+    };
+    auto piece_bar = [&](int n) { return pc_full + 8 * (n % PIECES); };
+    auto piece_parity = [&](int n) { return static_cast<uint32_t>(n / PIECES) & 1; };
+    auto free_piece = [&](int n) { mbar_arrive(pc_empty + 8 * (n % PIECES)); };
+    // Waits of warps that share a role: the first tests, the others sleep at the
+    // named barrier `id` (a testing warp takes eight issue slots per test, which with
+    // all of them testing was most of what this kernel executed).  One answer
+    // for all of them.
+    auto group_wait = [&](bool first, int id, int threads, uint32_t b, uint32_t parity) -> bool {
+        bool go = true;
+        if (first) go = mbar_spin(b, parity, P.status);
+        return !named_barrier_or(id, threads, !go);
     };
     auto token_of = [&](int row) { return static_cast<int>(static_cast<uint64_t>(row) * PP.div_mul >> PP.div_shift); };
-    auto rows_of = [&]() { return static_cast<int>(min(static_cast<int64_t>(UNIT), static_cast<int64_t>(pc.n) * P.group - pc.r0)); };
-    // first token that some row of the unit sees, and the end of them
-    auto end_of = [&](int rows) {
-        return P.causal ? min(pc.len, pc.len - pc.n + (pc.r0 + rows - 1) / P.group + 1) : pc.len;
+    auto rows_of = [&](const Piece &p) {
+        return static_cast<int>(min(static_cast<int64_t>(UNIT), static_cast<int64_t>(p.n) * P.group - p.r0));
     };
-    auto from_of = [&]() { return P.window ? max(0, pc.len - pc.n + pc.r0 / P.group - P.window + 1) : 0; };
+    // first token that some row of the unit sees, and the end of them
+    auto end_of = [&](const Piece &p) {
+        return P.causal ? min(p.len, p.len - p.n + token_of(p.r0 + rows_of(p) - 1) + 1) : p.len;
+    };
+    auto from_of = [&](const Piece &p) { return P.window ? max(0, p.len - p.n + token_of(p.r0) - P.window + 1) : 0; };
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_A));
         if (warp == 0) {
             // ---- copies ----
             const int pages = TILE / P.page;  // of a tile
-            const uint32_t page_bytes = static_cast<uint32_t>(P.page * P.dim);
+            const uint32_t page_bytes = static_cast<uint32_t>(P.page * P.dim), key_bytes = static_cast<uint32_t>(P.page) * 128;
             const int stop = cta == 0 ? PP.stop : NO_STOP;
-            int it = 0, item = 0;  // tiles, and slots filled (keys and values in turn)
+            int it = 0;
             bool ok = true;
-            while (ok && next_piece(true)) {
-                const int rows = rows_of(), end = end_of(rows), from = from_of();
+            for (int np = 0; ok; ++np) {
+                ok = __all_sync(0xffffffffu, mbar_spin(piece_bar(np), piece_parity(np), P.status));
+                if (!ok) break;
+                const Piece pc = read_piece(np);
+                __syncwarp();
+                if (lane == 0) free_piece(np);
+                if (!pc.more) break;
+                const int end = end_of(pc), from = from_of(pc);
                 const int32_t *tab = P.table + static_cast<int64_t>(pc.b) * P.ld_table;
                 auto page_of = [&](int j) {
                     const int tok = (pc.tile + j) * TILE + lane * P.page;
@@ -388,112 +415,115 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                     const int next = page_of(j + 1);
                     const int64_t tile = static_cast<int64_t>(max(id, 0)) * P.heads + pc.head;
                     const float ks = __ldg(P.scales[0] + tile), vs = __ldg(P.scales[1] + tile);
-                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id >= 0)) * page_bytes;
-#pragma unroll
-                    for (int side = 0; side < 2; ++side) {
-                        const int slot = item % C::RAW_RING;
-                        if (it >= stop) ok = false;
-                        if (ok && item >= C::RAW_RING) ok = mbar_spin(raw_empty + 8 * slot, ((item / C::RAW_RING) - 1) & 1, P.status);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        if (side == 0) {
-                            // scales of the groups of 16 tokens
-                            const int src = 16 * lane / P.page;
-                            const float k = __shfl_sync(0xffffffffu, ks, src), v = __shfl_sync(0xffffffffu, vs, src);
-                            if (lane < 8) {
-                                const float w = fminf(fmaxf(v, 0x1p-100f), 0x1p127f);
-                                float *d = sc + (it % SC_SLOTS) * SC_FLOATS + lane;
-                                d[0] = fminf(fmaxf(k, 0x1p-126f), 0x1p127f);
-                                d[8] = log2f(w);
-                            }
-                            __syncwarp();
-                        }
-                        if (lane == 0) mbar_arrive_expect_tx(raw_full + 8 * slot, bytes);
-                        __syncwarp();
-                        if (id >= 0)
-                            bulk_copy(base + C::OFF_RAW + slot * C::RAW + lane * page_bytes, P.codes[side] + tile * page_bytes,
-                                      page_bytes, raw_full + 8 * slot);
-                        ++item;
-                    }
+                    const uint32_t live = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                    const int k = it % C::KR, v = it % C::VR;
+                    if (it >= stop) ok = false;
+                    if (ok && it >= C::KR) ok = mbar_spin(k_empty + 8 * k, ((it / C::KR) - 1) & 1, P.status);
+                    if (ok && it >= C::VR) ok = mbar_spin(raw_empty + 8 * v, ((it / C::VR) - 1) & 1, P.status);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
+                    // scales of the groups of 16 tokens (the values of tile it - 2 are
+                    // converted, so their slot had been freed by tile it - 4, whose
+                    // rows are done with the scales that these replace)
+                    const int src = 16 * lane / P.page;
+                    const float kg = __shfl_sync(0xffffffffu, ks, src), vg = __shfl_sync(0xffffffffu, vs, src);
+                    if (lane < 8) {
+                        float *d = sc + (it % SC_SLOTS) * SC_FLOATS + lane;
+                        d[0] = fminf(fmaxf(kg, 0x1p-126f), 0x1p127f);
+                        d[8] = log2f(fminf(fmaxf(vg, 0x1p-100f), 0x1p127f));
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(k_full + 8 * k, live * key_bytes);
+                        mbar_arrive_expect_tx(raw_full + 8 * v, live * page_bytes);
+                    }
+                    __syncwarp();
+                    if (id >= 0) {
+                        tma_page(base + C::OFF_K + k * C::KEYS + lane * key_bytes, &tmK, static_cast<int>(tile), k_full + 8 * k);
+                        bulk_copy(base + C::OFF_RAW + v * C::RAW + lane * page_bytes, P.codes[1] + tile * page_bytes, page_bytes,
+                                  raw_full + 8 * v);
+                    }
                     id = next;
                 }
             }
             // no CTA ends with copies in flight
-            for (int i = max(0, item - C::RAW_RING); i < item; ++i)
-                mbar_spin(raw_full + 8 * (i % C::RAW_RING), (i / C::RAW_RING) & 1, P.status);
+            for (int i = max(0, it - C::KR); i < it; ++i) mbar_spin(k_full + 8 * (i % C::KR), (i / C::KR) & 1, P.status);
+            for (int i = max(0, it - C::VR); i < it; ++i) mbar_spin(raw_full + 8 * (i % C::VR), (i / C::VR) & 1, P.status);
         } else if (warp == 1 && elect_one()) {
             // ---- MMA issue ----
             constexpr uint32_t ID_S = (1u << 4) | ((TILE >> 3) << 17) | ((128 >> 4) << 24);
             constexpr uint32_t ID_O = (1u << 4) | (1u << 16) | ((DP >> 3) << 17) | ((128 >> 4) << 24);
-            int seg = 0, used[2] = {0, 0}, pit[2] = {0, 0};
-            int ki = 0, vi = 1;  // items in the ring: keys even, values odd
+            const uint64_t dq0 = f8::smem_desc(base), dk0 = f8::smem_desc(base + C::OFF_K), dv0 = desc_mn<DP>(base + C::OFF_V);
+            const int ks = (P.dim + 31) / 32;
+            int units[2] = {0, 0}, it[2] = {0, 0};  // of each tile: units with rows in it, P taken
+            int ki = 0, vi = 0;
             bool ok = true;
-            auto slot_of = [&](int item) { return base + C::OFF_RING + (item % C::RING) * C::TILE_BYTES; };
-            auto wait_item = [&](int item) { return mbar_spin(kv_full + 8 * (item % C::RING), (item / C::RING) & 1, P.status); };
-            auto free_item = [&](int item) { commit(kv_empty + 8 * (item % C::RING)); };
+            auto wait_keys = [&]() { return mbar_spin(k_full + 8 * (ki % C::KR), (ki / C::KR) & 1, P.status); };
+            auto free_keys = [&]() { commit(k_empty + 8 * (ki % C::KR)), ++ki; };
             auto scores = [&](int t) {
-                const uint32_t q = base + t * C::TILE_BYTES, k = slot_of(ki);
+                const uint64_t dk = dk0 + static_cast<uint64_t>((ki % C::KR) * (C::KEYS >> 4));
 #pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    const uint32_t at = (i >> 2) * (TILE * 128) + 32 * (i & 3);
-                    mma_ss(tmem + t * 128, f8::smem_desc(q + at), f8::smem_desc(k + at), ID_S, i ? 1u : 0u);
-                }
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int i = 0; i < DP / 32; ++i)
+                        if (i < ks)
+                            mma_ss(tmem + t * 128, dq0 + (t * NQ + n) * (C::KEYS >> 4) + 2 * i, dk + 2 * i, ID_S, n || i ? 1u : 0u);
                 commit(s_full + 8 * t);
             };
-            auto values = [&](int t, bool first) {
-                const uint32_t v = slot_of(vi);
+            // the first half of P: token groups 2, 3, 6 and 7, then the others
+            auto values = [&](int t, int half, bool first) {
+                const uint64_t dv = dv0 + static_cast<uint64_t>((vi % C::VR) * (C::TILE_BYTES >> 4));
 #pragma unroll
-                for (int i = 0; i < TILE / 16; ++i)
-                    mma_ts(tmem + 256 + t * DP, tmem + t * 128 + 8 * i + (i >= TILE / 32 ? 32 : 0), desc_mn<DP>(v + 2048 * i), ID_O, first && i == 0 ? 0u : 1u);
-                commit(pv_done + 8 * t);
-            };
-            auto wait_p = [&](int t, bool first) {
-                if (!mbar_spin(p_full + 8 * t, pit[t] & 1, P.status)) return false;
-                ++pit[t];
-                if (first) {
-                    if (used[t] > 0 && !mbar_spin(o_empty + 8 * t, (used[t] - 1) & 1, P.status)) return false;
-                    ++used[t];
+                for (int i = 0; i < 4; ++i) {
+                    const int g = (half ? 0 : 2) + (i & 1) + 4 * (i >> 1);
+                    mma_ts(tmem + 256 + t * DP, tmem + t * 128 + p_column(g), dv + (2048 >> 4) * g, ID_O, first && i == 0 ? 0u : 1u);
                 }
+            };
+            // P of tile t, and the product with the values
+            auto product = [&](int t, bool first) {
+                if (first && units[t] > 1 && !mbar_spin(o_empty + 8 * t, units[t] & 1, P.status)) return false;
+                if (!mbar_spin(p_full + 16 * t, it[t] & 1, P.status)) return false;
+                tc_fence_after();
+                values(t, 0, first);
+                if (!mbar_spin(p_full + 16 * t + 8, it[t] & 1, P.status)) return false;
+                tc_fence_after();
+                values(t, 1, false);
+                commit(pv_done + 8 * t);
+                ++it[t];
                 return true;
             };
-            while (ok && next_piece(false)) {
-                const bool two = rows_of() > 128;
-                if (!(ok = mbar_spin(q_full, seg & 1, P.status))) break;
-                if (!(ok = wait_item(ki))) break;
-                tc_fence_after();
-                scores(0);
-                if (two) scores(1);
-                free_item(ki);
-                ki += 2;
+            for (int np = 0; ok; ++np) {
+                if (!(ok = mbar_spin(piece_bar(np), piece_parity(np), P.status))) break;
+                const Piece pc = read_piece(np);
+                free_piece(np);
+                if (!pc.more) break;
+                const bool two = rows_of(pc) > 128;
+                if (!(ok = wait_keys())) break;
+                for (int t = 0; t < 1 + two; ++t) {
+                    if (!(ok = ok && mbar_spin(q_full + 8 * t, units[t] & 1, P.status))) break;
+                    ++units[t];
+                    tc_fence_after();
+                    scores(t);
+                }
+                if (!ok) break;
+                free_keys();
                 for (int j = 0; j < pc.nt; ++j) {
                     const bool more = j + 1 < pc.nt;
-                    if (!(ok = wait_item(vi))) break;
-                    if (!(ok = wait_p(0, j == 0))) break;
-                    tc_fence_after();
-                    values(0, j == 0);
+                    if (!(ok = mbar_spin(v_full + 8 * (vi % C::VR), (vi / C::VR) & 1, P.status))) break;
+                    if (!(ok = product(0, j == 0))) break;
                     if (more) {
-                        if (!(ok = wait_item(ki))) break;
+                        if (!(ok = wait_keys())) break;
                         tc_fence_after();
                         scores(0);
                     }
-                    if (two) {
-                        if (!(ok = wait_p(1, j == 0))) break;
-                        tc_fence_after();
-                        values(1, j == 0);
-                    }
-                    free_item(vi);
-                    vi += 2;
-                    // (the rows have read what goes with the queries: they have come with P)
-                    if (pc.nt == 1) commit(q_empty);
+                    if (two && !(ok = product(1, j == 0))) break;
+                    commit(v_empty + 8 * (vi % C::VR));
+                    ++vi;
                     if (more) {
                         if (two) scores(1);
-                        free_item(ki);
-                        ki += 2;
-                        if (j + 2 == pc.nt) commit(q_empty);
+                        free_keys();
                     }
                 }
-                ++seg;
             }
             commit(done);
         } else if (warp == 2 && elect_one()) {
@@ -503,259 +533,271 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
             Pair q;
             q.tiles = 0;
             long long off = 0;  // of t in the pair
+            auto cost = [&]() { return q.tiles > 0 ? static_cast<long long>(q.tiles + UNIT_COST) * P.heads : 0; };
             if (any)
                 for (;; ++p) {
                     load_pair(P, p, q);
-                    const long long all = static_cast<long long>(q.tiles) * P.heads;
-                    if (t < before + all) {
+                    if (t < before + cost()) {
                         off = t - before;
                         break;
                     }
-                    before += all;
+                    before += cost();
                 }
-            for (;; ++n) {
+            for (;;) {
                 const bool more = t < t_end;
-                const int s = n % PIECES;
-                if (n >= PIECES && !mbar_spin(pc_empty + 8 * s, ((n / PIECES) - 1) & 1, P.status)) break;
+                int at = 0, nt = 0, head = 0, c0 = -1, c1 = -1;
                 if (more) {
-                    const int head = static_cast<int>(off / q.tiles), at = static_cast<int>(off - static_cast<long long>(head) * q.tiles);
-                    const int nt = static_cast<int>(min(static_cast<long long>(q.tiles - at), t_end - t));
-                    const long long u0 = before + static_cast<long long>(head) * q.tiles, u1 = u0 + q.tiles - 1;
-                    int c0 = -1, c1 = -1;
-                    if (nt < q.tiles) {
+                    // this CTA's part of the unit: what of its cost is behind UNIT_COST
+                    const int all = q.tiles + UNIT_COST;
+                    head = static_cast<int>(off / all);
+                    const int from = static_cast<int>(off - static_cast<long long>(head) * all);
+                    const int to = static_cast<int>(min(static_cast<long long>(all), from + (t_end - t)));
+                    at = max(0, from - UNIT_COST);
+                    nt = max(0, to - UNIT_COST) - at;
+                    if (nt > 0 && nt < q.tiles) {
+                        const long long u0 = before + static_cast<long long>(head) * all + UNIT_COST, u1 = u0 + q.tiles - 1;
                         c0 = static_cast<int>(((u0 + 1) * ctas - 1) / W);
                         c1 = static_cast<int>(((u1 + 1) * ctas - 1) / W);
                     }
+                    t += to - from, off += to - from;
+                }
+                if (nt > 0 || !more) {
+                    const int s = n % PIECES;
+                    if (n >= PIECES && !mbar_spin(pc_empty + 8 * s, ((n / PIECES) - 1) & 1, P.status)) break;
                     pieces[3 * s] = make_int4(q.row0, q.n, q.len, q.r0);
                     pieces[3 * s + 1] = make_int4(head, q.b, q.tile + at, nt);
-                    pieces[3 * s + 2] = make_int4(c0, c1, at == 0, 1);
-                    t += nt, off += nt;
-                    if (t < t_end && off == static_cast<long long>(q.tiles) * P.heads) {
-                        before += off;
-                        off = 0;
-                        do load_pair(P, ++p, q);
-                        while (q.tiles == 0);
-                    }
-                } else {
-                    pieces[3 * s + 2] = make_int4(0, 0, 0, 0);
+                    pieces[3 * s + 2] = make_int4(c0, c1, at == 0, more);
+                    mbar_arrive(pc_full + 8 * s);
+                    ++n;
                 }
-                mbar_arrive(pc_full + 8 * s);
                 if (!more) break;
+                if (t < t_end && off == cost()) {
+                    before += off;
+                    off = 0;
+                    do load_pair(P, ++p, q);
+                    while (q.tiles == 0);
+                }
             }
         }
-    } else if (warp < 12) {
-        // ---- conversion ----
+    } else if (warp < 8) {
+        // ---- conversion of values ----
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_B));
-        const int side = (warp - 4) >> 2, me = tid & 127, w = warp - 4;  // keys or values
-        const int cpr = P.dim / 16;                                     // 16-code chunks of a token
-        int item = side, seg = 0;
+        const int me = tid - 128;
+        const int cpr = P.dim / 16;  // 16-code chunks of a token
+        int it = 0;
         bool ok = true;
-        while (ok && next_piece(true)) {
-            const int rows = rows_of(), end = end_of(rows);
-            // queries: lanes of 8 values, times a power of two that brings a
-            // row's largest to [2^13, 2^14)
-            {
-                constexpr int LPR = DP / 8, RPW = 32 / LPR, BATCH = 8, NEXT = 8 * RPW;  // rows of a thread are NEXT apart
-                const int d = 8 * (lane % LPR);
-                for (int r = w * RPW + lane / LPR; r < UNIT; r += NEXT * BATCH) {
-                    uint4 raw[BATCH];
-                    if (PP.q_vec) {
+        for (int np = 0; ok; ++np) {
+            ok = group_wait(warp == 4, 11, 128, piece_bar(np), piece_parity(np));
+            if (!ok) break;
+            const Piece pc = read_piece(np);
+            __syncwarp();
+            if (lane == 0) free_piece(np);
+            if (!pc.more) break;
+            const int end = end_of(pc), from = from_of(pc);
+            for (int j = 0; j < pc.nt; ++j, ++it) {
+                const int s = it % C::VR, live0 = from - (pc.tile + j) * TILE, live1 = end - (pc.tile + j) * TILE;
+                bool go = true;
+                if (warp == 4) {
+                    go = mbar_spin(raw_full + 8 * s, (it / C::VR) & 1, P.status);
+                    if (go && it >= C::VR) go = mbar_spin(v_empty + 8 * s, ((it / C::VR) - 1) & 1, P.status);
+                }
+                if (named_barrier_or(11, 128, !go)) {
+                    ok = false;
+                    break;
+                }
+                const uint4 *src = reinterpret_cast<const uint4 *>(smem + C::OFF_RAW + s * C::RAW);
+                uint8_t *dst = smem + C::OFF_V + s * C::TILE_BYTES;
+                auto one = [&](int row, int c, uint4 v) {
+                    // (what no row sees may be anything, and is not even there where a
+                    // whole page is: its probabilities are 0)
+                    if (row < live0 || row >= live1) v = make_uint4(0, 0, 0, 0);
+                    uint4 a, b;
+                    convert16(v, a, b);
+                    // (odd halves store their second part first: no two of eight lanes on one bank)
+                    const int h = c >> 2, q = 2 * (c & 3), x = row & 7;
+                    uint8_t *p = dst + h * (TILE * 128) + row * 128;
+                    *reinterpret_cast<uint4 *>(p + (((q + (h & 1)) ^ x) << 4)) = h & 1 ? b : a;
+                    *reinterpret_cast<uint4 *>(p + (((q + 1 - (h & 1)) ^ x) << 4)) = h & 1 ? a : b;
+                };
+                if (cpr == DP / 16) {
+                    uint4 v[DP / 16];
 #pragma unroll
-                        for (int k = 0; k < BATCH; ++k) {
-                            const int qr = pc.r0 + min(r + k * NEXT, rows - 1), i = token_of(qr);
-                            const uint16_t *src = static_cast<const uint16_t *>(P.q) + static_cast<int64_t>(pc.row0 + i) * P.ldq_t +
-                                                  static_cast<int64_t>(pc.head * P.group + (qr - i * P.group)) * P.ldq_h;
-                            raw[k] = __ldg(reinterpret_cast<const uint4 *>(src + min(d, P.dim - 8)));
-                        }
-                    } else {
-#pragma unroll 1
-                        for (int k = 0; k < BATCH; ++k) {
-                            const int qr = pc.r0 + min(r + k * NEXT, rows - 1), i = token_of(qr);
-                            const uint16_t *src = static_cast<const uint16_t *>(P.q) + static_cast<int64_t>(pc.row0 + i) * P.ldq_t +
-                                                  static_cast<int64_t>(pc.head * P.group + (qr - i * P.group)) * P.ldq_h + min(d, P.dim - 8);
-                            uint32_t v[8];
+                    for (int k = 0; k < DP / 16; ++k) v[k] = src[me + 128 * k];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) v[e] = __ldg(src + e);
-#pragma unroll
-                            for (int e = 0; e < BATCH - 1; ++e) raw[e] = raw[e + 1];
-                            raw[BATCH - 1] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-                        }
-                    }
-                    // (the last unit's scores are done: its queries may go)
-                    if (r < NEXT && seg > 0) ok = __all_sync(0xffffffffu, mbar_spin(q_empty, (seg - 1) & 1, P.status));
-                    if (!ok) break;
-                    // the largest |value| of a row: in either type it is in the order of the bits
-                    const uint32_t inf = P.q_type == QMM_BF16 ? 0x7f80u : 0x7c00u;
-                    uint32_t top[BATCH];
-#pragma unroll
-                    for (int k = 0; k < BATCH; ++k) {
-                        const uint32_t m = __vmaxu2(__vmaxu2(raw[k].x & 0x7fff7fffu, raw[k].y & 0x7fff7fffu),
-                                                    __vmaxu2(raw[k].z & 0x7fff7fffu, raw[k].w & 0x7fff7fffu));
-                        top[k] = max(m & 0xffffu, m >> 16);
-                        if (top[k] >= inf) {  // of the finite ones
-                            const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-                            top[k] = 0;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const uint32_t a = x[e / 2] >> (16 * (e & 1)) & 0x7fffu;
-                                top[k] = a < inf ? max(top[k], a) : top[k];
-                            }
-                        }
-                        if (d >= P.dim) top[k] = 0;
-                    }
-#pragma unroll
-                    for (int o = LPR / 2; o; o >>= 1)
-#pragma unroll
-                        for (int k = 0; k < BATCH; ++k) top[k] = max(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
-#pragma unroll
-                    for (int k = 0; k < BATCH; ++k) {
-                        const int rr = r + k * NEXT;
-                        const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-                        const float most = P.q_type == QMM_BF16 ? __uint_as_float(top[k] << 16) : half_bits_to_float(top[k]);
-                        const int e2 = most > 0.0f ? min(max(13 - exponent_of(__float_as_uint(most)), -114), 100) : 0;
-                        // (rows behind the last are zeros; a negative factor goes to the queries)
-                        const float up = rr >= rows ? 0.0f : P.factor < 0.0f ? -pow2f(e2) : pow2f(e2);
-                        uint32_t h[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float2 v;
-                            if (P.q_type == QMM_BF16) v = make_float2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u));
-                            else v = __half22float2(*reinterpret_cast<const __half2 *>(&x[e]));
-                            h[e] = rr >= rows ? 0 : pack_half(v.x * up, v.y * up);
-                        }
-                        const int tr = rr & 127;
-                        if (d < P.dim)
-                            *reinterpret_cast<uint4 *>(smem + (rr >> 7) * C::TILE_BYTES + (d >> 6) * (TILE * 128) + tr * 128 +
-                                                       ((((d & 63) >> 3) ^ (tr & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                        if (d == 0) row_e[rr] = static_cast<int8_t>(e2);
+                    for (int k = 0; k < DP / 16; ++k) one((me + 128 * k) / (DP / 16), me % (DP / 16), v[k]);
+                } else {
+                    for (int k = 0; k < cpr; ++k) {
+                        const int idx = me + 128 * k, row = idx / cpr;
+                        one(row, idx - row * cpr, src[idx]);
                     }
                 }
-                if (!ok) break;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
-                ++seg;
-            }
-            for (int j = 0; ok && j < pc.nt; ++j, item += 2) {
-                const int live = end - (pc.tile + j) * TILE;  // tokens below it are in the sequence
-                {
-                    const int raw = item % C::RAW_RING, s = item % C::RING;
-                    bool go = mbar_spin(raw_full + 8 * raw, (item / C::RAW_RING) & 1, P.status);
-                    if (go && item >= C::RING) go = mbar_spin(kv_empty + 8 * s, ((item / C::RING) - 1) & 1, P.status);
-                    ok = __all_sync(0xffffffffu, go);
-                    if (!ok) break;
-                    const uint4 *src = reinterpret_cast<const uint4 *>(smem + C::OFF_RAW + raw * C::RAW);
-                    uint8_t *dst = smem + C::OFF_RING + s * C::TILE_BYTES;
-                    auto one = [&](int row, int c, const uint4 &v) {
-                        uint4 a, b;
-                        convert16(v, a, b);
-                        // (odd halves store their second part first: no two of eight lanes on one bank)
-                        const int h = c >> 2, q = 2 * (c & 3), x = row & 7;
-                        uint8_t *p = dst + h * (TILE * 128) + row * 128;
-                        *reinterpret_cast<uint4 *>(p + (((q + (h & 1)) ^ x) << 4)) = h & 1 ? b : a;
-                        *reinterpret_cast<uint4 *>(p + (((q + 1 - (h & 1)) ^ x) << 4)) = h & 1 ? a : b;
-                    };
-                    if (cpr == DP / 16) {
-#pragma unroll
-                        for (int k = 0; k < DP / 16; ++k) {
-                            const int idx = me + 128 * k, row = idx / (DP / 16), c = idx % (DP / 16);
-                            uint4 v = src[idx];
-                            // (what is not in the sequence may be anything: its probabilities are 0)
-                            if (side && row >= live) v = make_uint4(0, 0, 0, 0);
-                            one(row, c, v);
-                        }
-                    } else {
-                        for (int k = 0; k < cpr; ++k) {
-                            const int idx = me + 128 * k, row = idx / cpr, c = idx - row * cpr;
-                            uint4 v = src[idx];
-                            if (side && row >= live) v = make_uint4(0, 0, 0, 0);
-                            one(row, c, v);
-                        }
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(kv_full + 8 * s);
-                        mbar_arrive(raw_empty + 8 * raw);
-                    }
+                if (lane == 0) {
+                    mbar_arrive(v_full + 8 * s);
+                    mbar_arrive(raw_empty + 8 * s);
                 }
             }
         }
     } else {
         // ---- rows ----
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_C));
-        // tile, half of its tokens (and of O's columns), and this thread's row (TMEM lane)
-        const int t = (warp - 12) >> 3, half = (warp - 12) >> 2 & 1, lane_row = 32 * (warp & 3) + lane;
+        // tile, half of its tokens (and of the row's values), and this thread's row (TMEM lane)
+        const int t = (warp - 8) >> 3, half = (warp - 8) >> 2 & 1, lane_row = 32 * (warp & 3) + lane;
         constexpr int HT = TILE / 2, HD = DP / 2;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t my_s = tmem + lanes + t * 128 + half * HT, my_p = my_s;  // (P over the scores that this thread has read)
-        const uint32_t my_o = tmem + lanes + 256 + t * DP + half * HD;
+        const uint32_t my_s = tmem + lanes + t * 128 + half * HT, my_o = tmem + lanes + 256 + t * DP + half * HD;
         const int pair_bar = 1 + 4 * t + (warp & 3);  // of the two warps that share 32 rows
+        const int tile_bar = 9 + t;                   // of the tile's eight
+        const bool first = ((warp - 8) & 7) == 0;
         const int mine = 128 * t + lane_row;
         float *const tell = reinterpret_cast<float *>(smem + C::OFF_SHARE) + half * UNIT + mine;
-        const float *const told = reinterpret_cast<const float *>(smem + C::OFF_SHARE) + (half ^ 1) * UNIT + mine;
+        const volatile float *const told = reinterpret_cast<const float *>(smem + C::OFF_SHARE) + (half ^ 1) * UNIT + mine;
         int it = 0, tiles = 0;  // tiles of this role, tiles of the CTA
         bool ok = true;
-        while (ok && next_piece(true)) {
-            const int rows = rows_of();
-            const int start = pc.len - pc.n;
-            bool store = false;
+        float f = 0.0f;  // scale log2 e over the power of two of the row's queries
+
+        // The queries of piece p as e4m3 parts, in a power of two that brings a row's
+        // largest to [2^7, 2^8).
+        auto load_queries = [&](const Piece &p) {
+            const int rows = rows_of(p);
+            const int qr = p.r0 + min(mine, rows - 1), i = token_of(qr);
+            const uint16_t *src = static_cast<const uint16_t *>(P.q) + static_cast<int64_t>(p.row0 + i) * P.ldq_t +
+                                  static_cast<int64_t>(p.head * P.group + (qr - i * P.group)) * P.ldq_h + half * HD;
+            const bool in = mine < rows;
+            uint4 raw[HD / 8];
+#pragma unroll
+            for (int k = 0; k < HD / 8; ++k) {
+                raw[k] = make_uint4(0, 0, 0, 0);
+                if (in && half * HD + 8 * k < P.dim) {
+                    if (PP.q_vec) raw[k] = __ldg(reinterpret_cast<const uint4 *>(src) + k);
+                    else {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = __ldg(src + 8 * k + e);
+                        raw[k] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+                    }
+                }
+            }
+            // the largest |value|: in either type it is in the order of the bits
+            constexpr uint32_t INF = NQ == 2 ? 0x7f80u : 0x7c00u;
+            uint32_t m = 0;
+#pragma unroll
+            for (int k = 0; k < HD / 8; ++k)
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(raw[k].x & 0x7fff7fffu, raw[k].y & 0x7fff7fffu),
+                                         __vmaxu2(raw[k].z & 0x7fff7fffu, raw[k].w & 0x7fff7fffu)));
+            uint32_t top = max(m & 0xffffu, m >> 16);
+            if (top >= INF) {  // of the finite ones
+                top = 0;
+#pragma unroll
+                for (int k = 0; k < HD / 8; ++k) {
+                    const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t a = x[e / 2] >> (16 * (e & 1)) & 0x7fffu;
+                        top = a < INF ? max(top, a) : top;
+                    }
+                }
+            }
+            *tell = __uint_as_float(top);
+            named_barrier(pair_bar, 64);
+            top = max(top, __float_as_uint(*told));
+            const float most = NQ == 2 ? __uint_as_float(top << 16) : half_bits_to_float(top);
+            const int e2 = most > 0.0f ? min(max(7 - exponent_of(__float_as_uint(most)), -120), 100) : 0;
+            const float up = P.factor < 0.0f ? -pow2f(e2) : pow2f(e2);
+            f = fabsf(P.factor) * pow2f(-e2);
+            uint8_t *dst = smem + t * NQ * C::KEYS + lane_row * 128;
+#pragma unroll
+            for (int c = 0; c < HD / 16; ++c) {
+                uint32_t w[NQ][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint4 r = raw[2 * c + (e >> 1)];
+                    const uint32_t x0 = e & 1 ? r.z : r.x, x1 = e & 1 ? r.w : r.y;
+                    float v[4];
+                    if constexpr (NQ == 2) {
+                        v[0] = __uint_as_float(x0 << 16), v[1] = __uint_as_float(x0 & 0xffff0000u);
+                        v[2] = __uint_as_float(x1 << 16), v[3] = __uint_as_float(x1 & 0xffff0000u);
+                    } else {
+                        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&x0));
+                        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&x1));
+                        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        v[k] *= up;
+                        v[k] = fabsf(v[k]) <= 448.0f ? v[k] : __uint_as_float(0x7fffffffu);  // (infinities: there is no code)
+                    }
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) w[n][e] = part4(v);
+                }
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+                    *reinterpret_cast<uint4 *>(dst + n * C::KEYS + (((half * (HD / 16) + c) ^ (lane_row & 7)) << 4)) =
+                        make_uint4(w[n][0], w[n][1], w[n][2], w[n][3]);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full + 8 * t);
+        };
+
+        int np = 0;
+        ok = group_wait(first, tile_bar, 256, piece_bar(np), piece_parity(np));
+        Piece pc = read_piece(np);
+        if (ok && pc.more && rows_of(pc) > 128 * t) load_queries(pc);
+        while (ok && pc.more) {
+            __syncwarp();
+            if (lane == 0) free_piece(np);
+            ++np;
+            const int rows = rows_of(pc);
+            const bool have = rows > 128 * t;  // rows in this tile
             float ref = -INFINITY, l = 0.0f;
-            if (rows > 128 * t) {
+            if (have) {
                 // tokens that this row sees, and those that all rows see
-                const int i = token_of(pc.r0 + min(mine, rows - 1));
+                const int start = pc.len - pc.n, i = token_of(pc.r0 + min(mine, rows - 1));
                 const int hi = P.causal ? min(pc.len, start + i + 1) : pc.len, lo = P.window ? start + i - P.window + 1 : 0;
-                const int first_i = token_of(pc.r0 + 128 * t), last_i = token_of(pc.r0 + min(rows, 128 * t + 128) - 1);
-                const int all_hi = P.causal ? min(pc.len, start + first_i + 1) : pc.len;
-                const int all_lo = P.window ? start + last_i - P.window + 1 : 0;
-                float f = 0.0f;
+                const int all_hi = P.causal ? min(pc.len, start + token_of(pc.r0 + 128 * t) + 1) : pc.len;
+                const int all_lo = P.window ? start + token_of(pc.r0 + min(rows, 128 * t + 128) - 1) - P.window + 1 : 0;
                 for (int j = 0; j < pc.nt; ++j, ++it) {
-                    // of keys, log2 of values' (groups of 16 tokens)
-                    const float *scale = sc + ((tiles + j) % SC_SLOTS) * SC_FLOATS + half * (HT / 16);
-                    ok = __all_sync(0xffffffffu, mbar_spin(s_full + 8 * t, it & 1, P.status));
+                    ok = group_wait(first, tile_bar, 256, s_full + 8 * t, it & 1);
+                    if (!ok) break;
                     tc_fence_after();
-                    if (j == 0) f = fabsf(P.factor) * pow2f(-row_e[mine]);
                     const int tok = (pc.tile + j) * TILE + half * HT;
                     const bool masked = tok < all_lo || tok + HT > all_hi;
                     const int from = lo - tok, to = hi - tok;
-                    // The scores are read twice, for the maximum and for the
-                    // exponentials: all of them do not fit a thread's registers
-                    // beside the rest.
-                    float top = -INFINITY;
-                    auto maximum = [&](auto with_mask) {
-                        uint32_t s[32];
-#pragma unroll 1
-                        for (int h = 0; h < HT / 32; ++h) {
-                            tmem_ld32(my_s + 32 * h, s);
-                            tmem_wait32(s);
+                    // The scores are read twice, for the maximum, which the load itself
+                    // finds, and for the exponentials: all of them do not fit a
+                    // thread's registers beside the rest.
+                    uint32_t s[2][16];
+                    float fk[4], lv[4], m[4];  // of the thread's groups of 16 tokens
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const float fk = f * scale[2 * h + k], lv = scale[8 + 2 * h + k];
-                                float a[16];
+                    for (int h = 0; h < 4; ++h) m[h] = tmem_max16(my_s + 16 * h, s[h & 1]);
+                    {
+                        const float *scale = sc + ((tiles + j) % SC_SLOTS) * SC_FLOATS + half * 4;
+                        const float4 a = *reinterpret_cast<const float4 *>(scale), b = *reinterpret_cast<const float4 *>(scale + 8);
+                        fk[0] = f * a.x, fk[1] = f * a.y, fk[2] = f * a.z, fk[3] = f * a.w;
+                        lv[0] = b.x, lv[1] = b.y, lv[2] = b.z, lv[3] = b.w;
+                    }
+                    tmem_wait16(s[0]);
+                    asm volatile("" : KV_RW4(s[1], 0), KV_RW4(s[1], 4), KV_RW4(s[1], 8), KV_RW4(s[1], 12), KV_RWF4(m) : : "memory");
+                    float top = max3(fmaxf(fmaf(m[0], fk[0], lv[0]), fmaf(m[1], fk[1], lv[1])), fmaf(m[2], fk[2], lv[2]),
+                                     fmaf(m[3], fk[3], lv[3]));
+                    if (masked) {  // of what the row sees
+                        top = -INFINITY;
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    a[e] = __uint_as_float(s[16 * k + e]);
-                                    if constexpr (with_mask.value) {
-                                        const int c = 32 * h + 16 * k + e;
-                                        a[e] = c >= from && c < to ? fmaf(a[e], fk, lv) : -INFINITY;
-                                    }
-                                }
-                                const float m = max3(max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), max3(a[6], a[7], a[8])),
-                                                     max3(a[9], a[10], a[11]), max3(max3(a[12], a[13], a[14]), a[15], a[0]));
-                                top = fmaxf(top, with_mask.value ? m : fmaf(m, fk, lv));
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t r[16];
+                            tmem_ld16(my_s + 16 * h, r);
+                            tmem_wait16(r);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float v = fmaf(__uint_as_float(r[e]), fk[h], lv[h]);
+                                top = 16 * h + e >= from && 16 * h + e < to ? fmaxf(top, v) : top;
                             }
                         }
-                    };
-                    if (ok) {
-                        if (masked) maximum(std::true_type());
-                        else maximum(std::false_type());
                     }
                     *tell = top;
-                    // (both warps of the pair take the same way from here)
-                    if (named_barrier_or(pair_bar, 64, !ok)) {
-                        ok = false;
-                        break;
-                    }
+                    named_barrier(pair_bar, 64);
                     top = fmaxf(top, *told);
                     const bool move = top > ref + MOVE;
                     if (__any_sync(0xffffffffu, move)) {
@@ -764,34 +806,33 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                         ref = now;
                         l *= down;
                         if (j > 0) {
-                            ok = __all_sync(0xffffffffu, mbar_spin(pv_done + 8 * t, (it - 1) & 1, P.status));
+                            // (one that runs out has raised the status; the tile's warps go on together)
+                            mbar_spin(pv_done + 8 * t, (it - 1) & 1, P.status);
+                            __syncwarp();
                             tc_fence_after();
 #pragma unroll 1
-                            for (int k = 0; ok && k < HD / 32; ++k) {
-                                uint32_t o[32];
-                                tmem_ld32(my_o + 32 * k, o);
-                                tmem_wait32(o);
+                            for (int k = 0; k < HD / 16; ++k) {
+                                uint32_t o[16];
+                                tmem_ld16(my_o + 16 * k, o);
+                                tmem_wait16(o);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
-                                tmem_st32(my_o + 32 * k, o);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
+                                tmem_st16(my_o + 16 * k, o);
                             }
                         }
                     }
-                    const float sub = ref == -INFINITY ? 0.0f : ref;  // (a row that has seen nothing yet: any finite one)
+                    const float sub = (ref == -INFINITY ? 0.0f : ref) - TC_SHIFT;  // (a row that has seen nothing yet: any finite one)
+                    // Groups 2 and 3, whose scores are here from the maximum, then 0 and 1.
                     auto exponentials = [&](auto with_mask) {
-                        uint32_t s[2][16];
-                        tmem_ld16(my_s, s[0]);
-                        tmem_wait16(s[0]);
 #pragma unroll
-                        for (int h = 0; h < HT / 16; ++h) {
-                            if (h + 1 < HT / 16) tmem_ld16(my_s + 16 * (h + 1), s[(h + 1) & 1]);
+                        for (int i2 = 0; i2 < 4; ++i2) {
+                            const int h = (i2 + 2) & 3;
                             uint32_t p[8];
-                            const float fk = f * scale[h], d = scale[8 + h] - sub + TC_SHIFT;
                             float v[16];
 #pragma unroll
                             for (int e = 0; e < 16; e += 2) {
-                                float a = __uint_as_float(s[h & 1][e]), b = __uint_as_float(s[h & 1][e + 1]);
-                                fma2(a, b, fk, d);
+                                float a = __uint_as_float(s[i2 & 1][e]), b = __uint_as_float(s[i2 & 1][e + 1]);
+                                fma2(a, b, fk[h], lv[h] - sub);
                                 if constexpr (with_mask.value) {
                                     const int c = 16 * h + e;
                                     a = c >= from && c < to ? a : -INFINITY;
@@ -800,148 +841,154 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
                                 v[e] = ex2(a), v[e + 1] = ex2(b);
                                 p[e / 2] = pack_half(v[e], v[e + 1]);
                             }
+                            if (i2 < 2) tmem_ld16(my_s + 16 * i2, s[i2 & 1]);
 #pragma unroll
                             for (int o = 8; o >= 2; o >>= 1)
 #pragma unroll
                                 for (int e = 0; e < o; e += 2) add2(v[e], v[e + 1], v[e + o], v[e + o + 1]);
-                            l = fmaf(v[0] + v[1], ex2(-20.0f - scale[8 + h]), l);  // (L_FACTOR / the values' scale)
-                            if (h + 1 < HT / 16) tmem_wait16(s[(h + 1) & 1]);
-                            tmem_st8(my_p + 8 * h, p);
+                            l = fmaf(v[0] + v[1], ex2(-20.0f - lv[h]), l);  // (L_FACTOR / the values' scale)
+                            if (i2 == 1 || i2 == 2) tmem_wait16(s[(i2 + 1) & 1]);
+                            tmem_st8(my_s + p_column(h), p);
+                            if (i2 & 1) {
+                                tmem_wait_st();
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * (i2 >> 1));
+                            }
                         }
                     };
                     if (masked) exponentials(std::true_type());
                     else exponentials(std::false_type());
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_full + 8 * t);
                 }
-                if (ok) ok = __all_sync(0xffffffffu, mbar_spin(pv_done + 8 * t, (it - 1) & 1, P.status));
-                tc_fence_after();
-                store = ok;
-                *tell = l;
             }
             tiles += pc.nt;
-            // every warp of the tile passes here once per piece, also after a wait
-            // that gave up, so that none is left at a barrier alone
-            if (named_barrier_or(9 + t, 256, !ok)) {
-                ok = false;
-                break;
+            // the next piece's queries before this one's results (the tile's warps
+            // agree on every wait, also on one that ran out)
+            if (ok) ok = group_wait(first, tile_bar, 256, piece_bar(np), piece_parity(np));
+            if (!ok) break;
+            {
+                const Piece next = read_piece(np);
+                if (next.more && rows_of(next) > 128 * t) load_queries(next);
             }
-            if (!store) continue;
-            l += *told;
-            named_barrier(pair_bar, 64);  // (it is told the next unit's maxima there)
-            auto result = [&](int64_t &at, int64_t &row) {
-                const int qr = pc.r0 + mine, i = token_of(qr), h = pc.head * P.group + (qr - i * P.group);
-                at = static_cast<int64_t>(pc.row0 + i) * P.ldy_t + static_cast<int64_t>(h) * P.ldy_h;
-                row = (static_cast<int64_t>(pc.row0) + i) * P.heads * P.group + h;
-            };
-            auto put = [&](int64_t at, int d, const float *v, int n) {  // n values from d on
-                const int es = P.y_type == QMM_F32 ? 4 : 2;
+            if (have) {
+                ok = group_wait(first, tile_bar, 256, pv_done + 8 * t, (it - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                *tell = l;
+                named_barrier(pair_bar, 64);
+                l += *told;
+                auto result = [&](int64_t &at, int64_t &row) {
+                    const int qr = pc.r0 + mine, i = token_of(qr), h = pc.head * P.group + (qr - i * P.group);
+                    at = static_cast<int64_t>(pc.row0 + i) * P.ldy_t + static_cast<int64_t>(h) * P.ldy_h;
+                    row = (static_cast<int64_t>(pc.row0) + i) * P.heads * P.group + h;
+                };
+                auto put = [&](int64_t at, int d, const float *v, int n) {  // n values from d on
+                    const int es = P.y_type == QMM_F32 ? 4 : 2;
 #pragma unroll
-                for (int k = 0; k < n; k += 4) {
-                    if (d + k >= P.dim) break;
-                    if (PP.y_vec && es == 4) {
-                        *reinterpret_cast<float4 *>(static_cast<float *>(P.y) + at + d + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-                    } else if (PP.y_vec) {
-                        if (k % 8) continue;
-                        uint32_t w[4];
+                    for (int k = 0; k < n; k += 4) {
+                        if (d + k >= P.dim) break;
+                        if (PP.y_vec && es == 4) {
+                            *reinterpret_cast<float4 *>(static_cast<float *>(P.y) + at + d + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                        } else if (PP.y_vec) {
+                            if (k % 8) continue;
+                            uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (P.y_type == QMM_F16) w[e] = pack_half(v[k + 2 * e], v[k + 2 * e + 1]);
-                            else {
-                                const __nv_bfloat162 b = __floats2bfloat162_rn(v[k + 2 * e], v[k + 2 * e + 1]);
-                                w[e] = *reinterpret_cast<const uint32_t *>(&b);
+                            for (int e = 0; e < 4; ++e) {
+                                if (P.y_type == QMM_F16) w[e] = pack_half(v[k + 2 * e], v[k + 2 * e + 1]);
+                                else {
+                                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[k + 2 * e], v[k + 2 * e + 1]);
+                                    w[e] = *reinterpret_cast<const uint32_t *>(&b);
+                                }
                             }
+                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(P.y) + at + d + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) store_typed(P.y, at + d + k + e, P.y_type, v[k + e]);
                         }
-                        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(P.y) + at + d + k) = make_uint4(w[0], w[1], w[2], w[3]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) store_typed(P.y, at + d + k + e, P.y_type, v[k + e]);
                     }
-                }
-            };
-            constexpr float LN2 = 0.6931471805599453f, BACK = 20.0f - TC_SHIFT;
-            if (pc.c0 < 0) {
-                const float inv = l != 0.0f ? L_FACTOR / l : 0.0f;
-                int64_t at, row;
-                result(at, row);
-#pragma unroll
-                for (int k = 0; k < HD / 32; ++k) {
-                    uint32_t o[32];
-                    tmem_ld32(my_o + 32 * k, o);
-                    tmem_wait32(o);
-                    if (k == HD / 32 - 1) {  // everything is out: the next unit's sums may come
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(o_empty + 8 * t);
-                    }
-                    float v[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * inv;
-                    if (mine < rows) put(at, half * HD + 32 * k, v, 32);
-                }
-                if (P.lse && half == 0 && mine < rows) P.lse[row] = l != 0.0f ? (ref + log2f(l) + BACK) * LN2 : -INFINITY;
-            } else {
-                // a part of a unit: [groups of four columns][row] sums relative to ref, then ref and l
-                float *const part = P.part + (static_cast<int64_t>(cta) * 2 + pc.begin) * C::PART;
-#pragma unroll
-                for (int k = 0; k < HD / 32; ++k) {
-                    uint32_t o[32];
-                    tmem_ld32(my_o + 32 * k, o);
-                    tmem_wait32(o);
-                    if (k == HD / 32 - 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(o_empty + 8 * t);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        reinterpret_cast<uint4 *>(part)[(half * HD / 4 + 8 * k + e / 4) * UNIT + mine] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                }
-                if (half == 0) part[DP * UNIT + mine] = ref, part[(DP + 1) * UNIT + mine] = l;
-                __threadfence();
-                named_barrier(9 + t, 256);
-                if ((warp - 12) % 8 == 0 && lane == 0) arrived[t] = atomicAdd(P.count + 2 * pc.c0 + t, 1u);
-                named_barrier(9 + t, 256);
-                if (arrived[t] == static_cast<unsigned>(pc.c1 - pc.c0)) {
-                    if ((warp - 12) % 8 == 0 && lane == 0) P.count[2 * pc.c0 + t] = 0u;  // zero again for the next launch
-                    __threadfence();
-                    auto part_of = [&](int c) { return P.part + (static_cast<int64_t>(c) * 2 + (c == pc.c0)) * C::PART; };
-                    float top = -INFINITY, sum = 0.0f;
-                    for (int c = pc.c0; c <= pc.c1; ++c) top = fmaxf(top, __ldcg(part_of(c) + DP * UNIT + mine));
-                    const float sub = top == -INFINITY ? 0.0f : top;
-                    for (int c = pc.c0; c <= pc.c1; ++c)
-                        sum = fmaf(__ldcg(part_of(c) + (DP + 1) * UNIT + mine), ex2(__ldcg(part_of(c) + DP * UNIT + mine) - sub), sum);
-                    const float inv = sum != 0.0f ? L_FACTOR / sum : 0.0f;
+                };
+                constexpr float LN2 = 0.6931471805599453f, BACK = 20.0f - TC_SHIFT;
+                if (pc.c0 < 0) {
+                    const float inv = l != 0.0f ? L_FACTOR / l : 0.0f;
                     int64_t at, row;
                     result(at, row);
-#pragma unroll 1
-                    for (int k = half * HD / 32; k < (half + 1) * HD / 32; ++k) {
-                        float v[32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = 0.0f;
-#pragma unroll 1
-                        for (int c = pc.c0; c <= pc.c1; ++c) {
-                            const float4 *q = reinterpret_cast<const float4 *>(part_of(c)) + 8 * k * UNIT + mine;
-                            const float w = ex2(__ldcg(part_of(c) + DP * UNIT + mine) - sub) * inv;
-                            float4 o[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] = __ldcg(q + e * UNIT);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                v[4 * e] = fmaf(o[e].x, w, v[4 * e]), v[4 * e + 1] = fmaf(o[e].y, w, v[4 * e + 1]);
-                                v[4 * e + 2] = fmaf(o[e].z, w, v[4 * e + 2]), v[4 * e + 3] = fmaf(o[e].w, w, v[4 * e + 3]);
-                            }
+                    for (int k = 0; k < HD / 16; ++k) {
+                        uint32_t o[16];
+                        tmem_ld16(my_o + 16 * k, o);
+                        tmem_wait16(o);
+                        if (k == HD / 16 - 1) {  // everything is out: the next unit's sums may come
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(o_empty + 8 * t);
                         }
-                        if (mine < rows) put(at, 32 * k, v, 32);
+                        float v[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * inv;
+                        if (mine < rows) put(at, half * HD + 16 * k, v, 16);
                     }
-                    if (P.lse && half == 0 && mine < rows) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + BACK) * LN2 : -INFINITY;
+                    if (P.lse && half == 0 && mine < rows) P.lse[row] = l != 0.0f ? (ref + log2f(l) + BACK) * LN2 : -INFINITY;
+                } else {
+                    // a part of a unit: [groups of four columns][row] sums relative to ref, then ref and l
+                    float *const part = P.part + (static_cast<int64_t>(cta) * 2 + pc.begin) * C::PART;
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k) {
+                        uint32_t o[16];
+                        tmem_ld16(my_o + 16 * k, o);
+                        tmem_wait16(o);
+                        if (k == HD / 16 - 1) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(o_empty + 8 * t);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            reinterpret_cast<uint4 *>(part)[(half * HD / 4 + 4 * k + e / 4) * UNIT + mine] =
+                                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                    if (half == 0) part[DP * UNIT + mine] = ref, part[(DP + 1) * UNIT + mine] = l;
+                    __threadfence();
+                    named_barrier(tile_bar, 256);
+                    if (first && lane == 0) arrived[t] = atomicAdd(P.count + 2 * pc.c0 + t, 1u);
+                    named_barrier(tile_bar, 256);
+                    if (arrived[t] == static_cast<unsigned>(pc.c1 - pc.c0)) {
+                        if (first && lane == 0) P.count[2 * pc.c0 + t] = 0u;  // zero again for the next launch
+                        __threadfence();
+                        auto part_of = [&](int c) { return P.part + (static_cast<int64_t>(c) * 2 + (c == pc.c0)) * C::PART; };
+                        float top = -INFINITY, sum = 0.0f;
+                        for (int c = pc.c0; c <= pc.c1; ++c) top = fmaxf(top, __ldcg(part_of(c) + DP * UNIT + mine));
+                        const float sub = top == -INFINITY ? 0.0f : top;
+                        for (int c = pc.c0; c <= pc.c1; ++c)
+                            sum = fmaf(__ldcg(part_of(c) + (DP + 1) * UNIT + mine), ex2(__ldcg(part_of(c) + DP * UNIT + mine) - sub), sum);
+                        const float inv = sum != 0.0f ? L_FACTOR / sum : 0.0f;
+                        int64_t at, row;
+                        result(at, row);
+#pragma unroll 1
+                        for (int k = half * HD / 16; k < (half + 1) * HD / 16; ++k) {
+                            float v[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+#pragma unroll 2
+                            for (int c = pc.c0; c <= pc.c1; ++c) {
+                                const float4 *q = reinterpret_cast<const float4 *>(part_of(c)) + 4 * k * UNIT + mine;
+                                const float w = ex2(__ldcg(part_of(c) + DP * UNIT + mine) - sub) * inv;
+                                float4 o[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[e] = __ldcg(q + e * UNIT);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    v[4 * e] = fmaf(o[e].x, w, v[4 * e]), v[4 * e + 1] = fmaf(o[e].y, w, v[4 * e + 1]);
+                                    v[4 * e + 2] = fmaf(o[e].z, w, v[4 * e + 2]), v[4 * e + 3] = fmaf(o[e].w, w, v[4 * e + 3]);
+                                }
+                            }
+                            if (mine < rows) put(at, 16 * k, v, 16);
+                        }
+                        if (P.lse && half == 0 && mine < rows) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + BACK) * LN2 : -INFINITY;
+                    }
                 }
             }
+            pc = read_piece(np);
         }
-        // (a closing record, and one whose wait ran out, counts as a piece at the barrier above)
-        if (ok) named_barrier_or(9 + t, 256, true);
     }
     tc_fence_before();
     __syncthreads();
@@ -952,10 +999,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const Tc
     }
 }
 
-template <int DP>
+template <int DP, int NQ>
 cudaError_t launch_dp(const TcParams &p, cudaStream_t st, int num_sms, int dev) {
-    using C = Tc<DP>;
-    const auto kern = kv_attention_tc_kernel<DP>;
+    using C = Tc<DP, NQ>;
+    const auto kern = kv_attention_tc_kernel<DP, NQ>;
     static OncePerDevice ready;
     const cudaError_t e = ready(dev, [&] {
         cudaError_t r = set_smem_attrs(kern, C::SMEM);
@@ -966,6 +1013,16 @@ cudaError_t launch_dp(const TcParams &p, cudaStream_t st, int num_sms, int dev) 
         return fa.numRegs < REGS ? cudaErrorNotSupported : cudaSuccess;
     });
     if (e != cudaSuccess) return e;
+    // keys: [pages * heads][page][dim] codes, boxes of a page and 128 bytes
+    CUtensorMap tm = {};
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.a.dim), static_cast<cuuint64_t>(p.a.page),
+                                static_cast<cuuint64_t>(p.a.pages * p.a.heads)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.a.dim), static_cast<cuuint64_t>(p.a.dim) * p.a.page};
+    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(p.a.page), 1}, es[3] = {1, 1, 1};
+    if (tensor_map_encoder()(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(p.a.codes[0]), dims, strides, box, es,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
     cfg.blockDim = dim3(TC_THREADS);
@@ -976,14 +1033,16 @@ cudaError_t launch_dp(const TcParams &p, cudaStream_t st, int num_sms, int dev) 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return cudaLaunchKernelEx(&cfg, kern, tm, p);
 }
 
 }  // namespace
 
 size_t tc_part_bytes(int dim, int num_sms) {
-    return static_cast<size_t>(num_sms) * 2 * (dim <= 64 ? Tc<64>::PART : Tc<128>::PART) * sizeof(float);
+    return static_cast<size_t>(num_sms) * 2 * (dim <= 64 ? Tc<64, 2>::PART : Tc<128, 2>::PART) * sizeof(float);
 }
+
+bool tc_available() { return tensor_map_encoder() != nullptr; }
 
 cudaError_t launch_tc(const AttnParams &a, int stop, cudaStream_t st, int num_sms, int dev) {
     TcParams p = {};
@@ -1002,7 +1061,8 @@ cudaError_t launch_tc(const AttnParams &a, int stop, cudaStream_t st, int num_sm
     p.stop = stop;
     for (p.div_shift = 31; (int64_t(1) << (p.div_shift - 31)) < a.group;) ++p.div_shift;
     p.div_mul = static_cast<uint32_t>(((uint64_t(1) << p.div_shift) + a.group - 1) / a.group);
-    return a.dim <= 64 ? launch_dp<64>(p, st, num_sms, dev) : launch_dp<128>(p, st, num_sms, dev);
+    if (a.q_type == QMM_BF16) return a.dim <= 64 ? launch_dp<64, 2>(p, st, num_sms, dev) : launch_dp<128, 2>(p, st, num_sms, dev);
+    return a.dim <= 64 ? launch_dp<64, 3>(p, st, num_sms, dev) : launch_dp<128, 3>(p, st, num_sms, dev);
 }
 
 }  // namespace kv
