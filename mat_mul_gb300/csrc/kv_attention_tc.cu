@@ -49,10 +49,10 @@ using f8::tc_fence_before;
 
 constexpr int TC_THREADS = 768, UNIT = 256;
 constexpr int TC_LEAST = 6;   // tiles (and unit costs) per CTA below which fewer CTAs take part
-constexpr int UNIT_COST = 2;  // what a unit costs beside its tiles, in tiles
+constexpr int UNIT_COST = 5;  // what a unit costs beside its tiles, in tiles
 constexpr int PIECES = 3, SC_SLOTS = 4, SC_FLOATS = 16;
 // registers per thread at launch, and after the split between roles 0..3, conversion and rows
-constexpr int REGS = 80, REGS_A = 56, REGS_B = 64, REGS_C = 88;
+constexpr int REGS = 80, REGS_A = 48, REGS_B = 48, REGS_C = 96;
 static_assert(128 * (REGS_A + REGS_B + 4 * REGS_C) <= TC_THREADS * REGS, "register split");
 constexpr float MOVE = 8.0f;      // growth of the maximum that moves the reference
 constexpr float TC_SHIFT = 6.0f;  // P as fp16 is at most 2^(MOVE + TC_SHIFT)
@@ -235,15 +235,14 @@ __device__ __forceinline__ void convert16(const uint4 &w, uint4 &a, uint4 &b) {
     b = make_uint4(halves(w.z), halves_hi(w.z), halves(w.w), halves_hi(w.w));
 }
 
-// Four values as codes, and what the codes leave of them.
-__device__ __forceinline__ uint32_t part4(float (&v)[4]) {
+// Four values (fp16) as codes, and what the codes leave of them (exact).
+__device__ __forceinline__ uint32_t part4(__half2 (&v)[2]) {
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+        const __nv_fp8x2_storage_t c = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(v[i]), __NV_SATFINITE, __NV_E4M3);
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        v[2 * i] -= f.x, v[2 * i + 1] -= f.y;
+        v[i] = __hsub2(v[i], *reinterpret_cast<const __half2 *>(&h));
         w |= static_cast<uint32_t>(c) << (16 * i);
     }
     return w;
@@ -255,15 +254,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
     const AttnParams &P = PP.a;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     const uint32_t k_full = base + C::OFF_BAR, k_empty = k_full + 8 * C::KR;
     const uint32_t raw_full = k_empty + 8 * C::KR, raw_empty = raw_full + 8 * C::VR;
     const uint32_t v_full = raw_empty + 8 * C::VR, v_empty = v_full + 8 * C::VR;
     const uint32_t q_full = v_empty + 8 * C::VR, s_full = q_full + 16, pv_done = s_full + 16, o_empty = pv_done + 16;  // per tile
-    const uint32_t p_full = o_empty + 16;  // per tile, two halves of its groups of tokens
-    const uint32_t pc_full = p_full + 32, pc_empty = pc_full + 8 * PIECES, done = pc_empty + 8 * PIECES;
-    static_assert(16 * C::KR + 32 * C::VR + 64 + 32 + 16 * PIECES + 8 <= 296, "barriers");
+    const uint32_t p_full = o_empty + 16, pc_full = p_full + 16, pc_empty = pc_full + 8 * PIECES, done = pc_empty + 8 * PIECES;
+    static_assert(16 * C::KR + 32 * C::VR + 64 + 16 + 16 * PIECES + 8 <= 296, "barriers");
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 296);
     volatile unsigned *const arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 304);  // per tile
     int4 *const pieces = reinterpret_cast<int4 *>(smem + C::OFF_PIECES);
@@ -286,8 +284,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
             mbar_init(s_full + 8 * i, 1);
             mbar_init(pv_done + 8 * i, 1);
             mbar_init(o_empty + 8 * i, 8);
-            mbar_init(p_full + 16 * i, 8);
-            mbar_init(p_full + 16 * i + 8, 8);
+            mbar_init(p_full + 8 * i, 8);
         }
         for (int i = 0; i < PIECES; ++i) {
             mbar_init(pc_full + 8 * i, 1);
@@ -348,15 +345,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     // A piece of work, from the scheduling warp.
     struct Piece {
         int row0, n, len, r0, head, b, tile, nt, c0, c1, begin, more;
     };
+    // (volatile: read again where it is needed again, instead of kept in registers)
     auto read_piece = [&](int n) {
-        const int4 a = pieces[3 * (n % PIECES)], b = pieces[3 * (n % PIECES) + 1], c = pieces[3 * (n % PIECES) + 2];
-        return Piece{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+        const uint32_t at = base + C::OFF_PIECES + 48 * (n % PIECES);
+        Piece p;
+        asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(p.row0), "=r"(p.n), "=r"(p.len), "=r"(p.r0) : "r"(at));
+        asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(p.head), "=r"(p.b), "=r"(p.tile), "=r"(p.nt) : "r"(at + 16));
+        asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(p.c0), "=r"(p.c1), "=r"(p.begin), "=r"(p.more) : "r"(at + 32));
+        return p;
     };
     auto piece_bar = [&](int n) { return pc_full + 8 * (n % PIECES); };
     auto piece_parity = [&](int n) { return static_cast<uint32_t>(n / PIECES) & 1; };
@@ -449,83 +451,84 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
             // no CTA ends with copies in flight
             for (int i = max(0, it - C::KR); i < it; ++i) mbar_spin(k_full + 8 * (i % C::KR), (i / C::KR) & 1, P.status);
             for (int i = max(0, it - C::VR); i < it; ++i) mbar_spin(raw_full + 8 * (i % C::VR), (i / C::VR) & 1, P.status);
-        } else if (warp == 1 && elect_one()) {
+        } else if (warp == 1) {
             // ---- MMA issue ----
+            // This warp's own instructions were the bottleneck: seven waits, at 300
+            // cycles each also where the barrier is complete, and 32 MMAs per tile took
+            // 4400 cycles.  Hence one wait for the values and the next keys (the
+            // conversion looks after the keys as well), one per tile for P, and a
+            // whole warp that stays together, so that the addresses stay in uniform registers.
             constexpr uint32_t ID_S = (1u << 4) | ((TILE >> 3) << 17) | ((128 >> 4) << 24);
             constexpr uint32_t ID_O = (1u << 4) | (1u << 16) | ((DP >> 3) << 17) | ((128 >> 4) << 24);
             const uint64_t dq0 = f8::smem_desc(base), dk0 = f8::smem_desc(base + C::OFF_K), dv0 = desc_mn<DP>(base + C::OFF_V);
             const int ks = (P.dim + 31) / 32;
-            int units[2] = {0, 0}, it[2] = {0, 0};  // of each tile: units with rows in it, P taken
+            int units0 = 0, units1 = 0, it0 = 0, it1 = 0;  // of each tile: units with rows in it, P taken
             int ki = 0, vi = 0;
             bool ok = true;
-            auto wait_keys = [&]() { return mbar_spin(k_full + 8 * (ki % C::KR), (ki / C::KR) & 1, P.status); };
-            auto free_keys = [&]() { commit(k_empty + 8 * (ki % C::KR)), ++ki; };
-            auto scores = [&](int t) {
+            auto wait = [&](uint32_t b, int phase) { return __all_sync(0xffffffffu, mbar_spin(b, phase & 1, P.status)); };
+            auto scores = [&](int t, bool last) {
                 const uint64_t dk = dk0 + static_cast<uint64_t>((ki % C::KR) * (C::KEYS >> 4));
+                if (elect_one()) {
 #pragma unroll
-                for (int n = 0; n < NQ; ++n)
+                    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                    for (int i = 0; i < DP / 32; ++i)
-                        if (i < ks)
-                            mma_ss(tmem + t * 128, dq0 + (t * NQ + n) * (C::KEYS >> 4) + 2 * i, dk + 2 * i, ID_S, n || i ? 1u : 0u);
-                commit(s_full + 8 * t);
-            };
-            // the first half of P: token groups 2, 3, 6 and 7, then the others
-            auto values = [&](int t, int half, bool first) {
-                const uint64_t dv = dv0 + static_cast<uint64_t>((vi % C::VR) * (C::TILE_BYTES >> 4));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int g = (half ? 0 : 2) + (i & 1) + 4 * (i >> 1);
-                    mma_ts(tmem + 256 + t * DP, tmem + t * 128 + p_column(g), dv + (2048 >> 4) * g, ID_O, first && i == 0 ? 0u : 1u);
+                        for (int i = 0; i < DP / 32; ++i)
+                            if (i < ks)
+                                mma_ss(tmem + t * 128, dq0 + (t * NQ + n) * (C::KEYS >> 4) + 2 * i, dk + 2 * i, ID_S, n || i ? 1u : 0u);
+                    commit(s_full + 8 * t);
+                    if (last) commit(k_empty + 8 * (ki % C::KR));
                 }
+                __syncwarp();
+                if (last) ++ki;
             };
-            // P of tile t, and the product with the values
-            auto product = [&](int t, bool first) {
-                if (first && units[t] > 1 && !mbar_spin(o_empty + 8 * t, units[t] & 1, P.status)) return false;
-                if (!mbar_spin(p_full + 16 * t, it[t] & 1, P.status)) return false;
-                tc_fence_after();
-                values(t, 0, first);
-                if (!mbar_spin(p_full + 16 * t + 8, it[t] & 1, P.status)) return false;
-                tc_fence_after();
-                values(t, 1, false);
-                commit(pv_done + 8 * t);
-                ++it[t];
-                return true;
+            auto values = [&](int t, bool first, bool last) {
+                const uint64_t dv = dv0 + static_cast<uint64_t>((vi % C::VR) * (C::TILE_BYTES >> 4));
+                if (elect_one()) {
+#pragma unroll
+                    for (int g = 0; g < TILE / 16; ++g)
+                        mma_ts(tmem + 256 + t * DP, tmem + t * 128 + p_column(g), dv + (2048 >> 4) * g, ID_O, first && g == 0 ? 0u : 1u);
+                    commit(pv_done + 8 * t);
+                    if (last) commit(v_empty + 8 * (vi % C::VR));
+                }
+                __syncwarp();
+                if (last) ++vi;
             };
             for (int np = 0; ok; ++np) {
-                if (!(ok = mbar_spin(piece_bar(np), piece_parity(np), P.status))) break;
+                if (!(ok = wait(piece_bar(np), np / PIECES))) break;
                 const Piece pc = read_piece(np);
-                free_piece(np);
-                if (!pc.more) break;
-                const bool two = rows_of(pc) > 128;
-                if (!(ok = wait_keys())) break;
-                for (int t = 0; t < 1 + two; ++t) {
-                    if (!(ok = ok && mbar_spin(q_full + 8 * t, units[t] & 1, P.status))) break;
-                    ++units[t];
+                __syncwarp();
+                if (lane == 0) free_piece(np);
+                const int nt = __shfl_sync(0xffffffffu, pc.more ? pc.nt : 0, 0);
+                if (nt == 0) break;
+                const bool two = __shfl_sync(0xffffffffu, rows_of(pc) > 128, 0);
+                if (!(ok = wait(k_full + 8 * (ki % C::KR), ki / C::KR))) break;
+                if (!(ok = wait(q_full, units0++))) break;
+                tc_fence_after();
+                scores(0, !two);
+                if (two) {
+                    if (!(ok = wait(q_full + 8, units1++))) break;
                     tc_fence_after();
-                    scores(t);
+                    scores(1, true);
                 }
-                if (!ok) break;
-                free_keys();
-                for (int j = 0; j < pc.nt; ++j) {
-                    const bool more = j + 1 < pc.nt;
-                    if (!(ok = mbar_spin(v_full + 8 * (vi % C::VR), (vi / C::VR) & 1, P.status))) break;
-                    if (!(ok = product(0, j == 0))) break;
-                    if (more) {
-                        if (!(ok = wait_keys())) break;
+                for (int j = 0; j < nt; ++j) {
+                    const bool more = j + 1 < nt;
+                    if (!(ok = wait(v_full + 8 * (vi % C::VR), vi / C::VR))) break;
+                    if (j == 0 && units0 > 1 && !(ok = wait(o_empty, units0))) break;
+                    if (!(ok = wait(p_full, it0++))) break;
+                    tc_fence_after();
+                    values(0, j == 0, !two);
+                    if (more) scores(0, !two);
+                    if (two) {
+                        if (j == 0 && units1 > 1 && !(ok = wait(o_empty + 8, units1))) break;
+                        if (!(ok = wait(p_full + 8, it1++))) break;
                         tc_fence_after();
-                        scores(0);
-                    }
-                    if (two && !(ok = product(1, j == 0))) break;
-                    commit(v_empty + 8 * (vi % C::VR));
-                    ++vi;
-                    if (more) {
-                        if (two) scores(1);
-                        free_keys();
+                        values(1, j == 0, true);
+                        if (more) scores(1, true);
                     }
                 }
             }
-            commit(done);
+            if (elect_one()) commit(done);
+            __syncwarp();
         } else if (warp == 2 && elect_one()) {
             // ---- schedule ----
             long long t = t_begin, before = before0;
@@ -600,6 +603,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                 if (warp == 4) {
                     go = mbar_spin(raw_full + 8 * s, (it / C::VR) & 1, P.status);
                     if (go && it >= C::VR) go = mbar_spin(v_empty + 8 * s, ((it / C::VR) - 1) & 1, P.status);
+                    // (who waits for these values needs the next keys as well)
+                    if (go && j + 1 < pc.nt) go = mbar_spin(k_full + 8 * ((it + 1) % C::KR), ((it + 1) / C::KR) & 1, P.status);
                 }
                 if (named_barrier_or(11, 128, !go)) {
                     ok = false;
@@ -620,11 +625,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                     *reinterpret_cast<uint4 *>(p + (((q + 1 - (h & 1)) ^ x) << 4)) = h & 1 ? a : b;
                 };
                 if (cpr == DP / 16) {
-                    uint4 v[DP / 16];
+#pragma unroll 1
+                    for (int g = 0; g < DP / 16; g += 4) {
+                        uint4 v[4];
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) v[k] = src[me + 128 * k];
+                        for (int k = 0; k < 4; ++k) v[k] = src[me + 128 * (g + k)];
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) one((me + 128 * k) / (DP / 16), me % (DP / 16), v[k]);
+                        for (int k = 0; k < 4; ++k) one((me + 128 * (g + k)) / (DP / 16), me % (DP / 16), v[k]);
+                    }
                 } else {
                     for (int k = 0; k < cpr; ++k) {
                         const int idx = me + 128 * k, row = idx / cpr;
@@ -658,111 +666,129 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
         float f = 0.0f;  // scale log2 e over the power of two of the row's queries
 
         // The queries of piece p as e4m3 parts, in a power of two that brings a row's
-        // largest to [2^7, 2^8).
+        // largest to [2^7, 2^8).  A row goes to DP / 8 lanes, 16 bytes each (with a
+        // row per thread every load touched 32 lines: 8000 cycles per unit).
         auto load_queries = [&](const Piece &p) {
-            const int rows = rows_of(p);
-            const int qr = p.r0 + min(mine, rows - 1), i = token_of(qr);
-            const uint16_t *src = static_cast<const uint16_t *>(P.q) + static_cast<int64_t>(p.row0 + i) * P.ldq_t +
-                                  static_cast<int64_t>(p.head * P.group + (qr - i * P.group)) * P.ldq_h + half * HD;
-            const bool in = mine < rows;
-            uint4 raw[HD / 8];
+            constexpr int LPR = DP / 8, RPW = 32 / LPR, N = 16 / RPW;  // lanes per row, rows per load, loads of a warp's 16 rows
+            const int rows = rows_of(p), d = 8 * (lane % LPR);
+            const int r0 = 16 * ((warp - 8) & 7) + lane / LPR;  // of the tile's rows, RPW apart
+            auto source = [&](int k) {
+                const int qr = p.r0 + min(128 * t + r0 + RPW * k, rows - 1), i = token_of(qr);
+                return static_cast<const uint16_t *>(P.q) + static_cast<int64_t>(p.row0 + i) * P.ldq_t +
+                       static_cast<int64_t>(p.head * P.group + (qr - i * P.group)) * P.ldq_h + min(d, P.dim - 8);
+            };
+            uint4 raw[N];
+            if (PP.q_vec) {  // (all of them on their way at once)
 #pragma unroll
-            for (int k = 0; k < HD / 8; ++k) {
-                raw[k] = make_uint4(0, 0, 0, 0);
-                if (in && half * HD + 8 * k < P.dim) {
-                    if (PP.q_vec) raw[k] = __ldg(reinterpret_cast<const uint4 *>(src) + k);
-                    else {
-                        uint32_t v[8];
+                for (int k = 0; k < N; ++k) raw[k] = __ldg(reinterpret_cast<const uint4 *>(source(k)));
+            } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = __ldg(src + 8 * k + e);
-                        raw[k] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-                    }
+                for (int k = 0; k < N; ++k) {
+                    const uint16_t *src = source(k);
+                    uint32_t v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = __ldg(src + e);
+                    raw[k] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
                 }
             }
             // the largest |value|: in either type it is in the order of the bits
             constexpr uint32_t INF = NQ == 2 ? 0x7f80u : 0x7c00u;
-            uint32_t m = 0;
+            uint32_t top[N];
+            bool special = false;
 #pragma unroll
-            for (int k = 0; k < HD / 8; ++k)
-                m = __vmaxu2(m, __vmaxu2(__vmaxu2(raw[k].x & 0x7fff7fffu, raw[k].y & 0x7fff7fffu),
-                                         __vmaxu2(raw[k].z & 0x7fff7fffu, raw[k].w & 0x7fff7fffu)));
-            uint32_t top = max(m & 0xffffu, m >> 16);
-            if (top >= INF) {  // of the finite ones
-                top = 0;
+            for (int k = 0; k < N; ++k) {
+                if (r0 + RPW * k + 128 * t >= rows || d >= P.dim) raw[k] = make_uint4(0, 0, 0, 0);
+                const uint32_t m = __vmaxu2(__vmaxu2(raw[k].x & 0x7fff7fffu, raw[k].y & 0x7fff7fffu),
+                                            __vmaxu2(raw[k].z & 0x7fff7fffu, raw[k].w & 0x7fff7fffu));
+                top[k] = max(m & 0xffffu, m >> 16);
+                special = special || top[k] >= INF;
+            }
+            special = __any_sync(0xffffffffu, special);
+            if (special) {  // of the finite ones
 #pragma unroll
-                for (int k = 0; k < HD / 8; ++k) {
+                for (int k = 0; k < N; ++k) {
                     const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+                    top[k] = 0;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const uint32_t a = x[e / 2] >> (16 * (e & 1)) & 0x7fffu;
-                        top = a < INF ? max(top, a) : top;
+                        top[k] = a < INF ? max(top[k], a) : top[k];
                     }
                 }
             }
-            *tell = __uint_as_float(top);
-            named_barrier(pair_bar, 64);
-            top = max(top, __float_as_uint(*told));
-            const float most = NQ == 2 ? __uint_as_float(top << 16) : half_bits_to_float(top);
-            const int e2 = most > 0.0f ? min(max(7 - exponent_of(__float_as_uint(most)), -120), 100) : 0;
-            const float up = P.factor < 0.0f ? -pow2f(e2) : pow2f(e2);
-            f = fabsf(P.factor) * pow2f(-e2);
-            uint8_t *dst = smem + t * NQ * C::KEYS + lane_row * 128;
 #pragma unroll
-            for (int c = 0; c < HD / 16; ++c) {
-                uint32_t w[NQ][4];
+            for (int o = LPR / 2; o; o >>= 1)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint4 r = raw[2 * c + (e >> 1)];
-                    const uint32_t x0 = e & 1 ? r.z : r.x, x1 = e & 1 ? r.w : r.y;
-                    float v[4];
-                    if constexpr (NQ == 2) {
-                        v[0] = __uint_as_float(x0 << 16), v[1] = __uint_as_float(x0 & 0xffff0000u);
-                        v[2] = __uint_as_float(x1 << 16), v[3] = __uint_as_float(x1 & 0xffff0000u);
-                    } else {
-                        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&x0));
-                        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&x1));
-                        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
-                    }
+                for (int k = 0; k < N; ++k) top[k] = max(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
+            float *const factors = reinterpret_cast<float *>(smem + C::OFF_SHARE) + 128 * t;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        v[k] *= up;
-                        v[k] = fabsf(v[k]) <= 448.0f ? v[k] : __uint_as_float(0x7fffffffu);  // (infinities: there is no code)
+            for (int k = 0; k < N; ++k) {
+                const int r = r0 + RPW * k;
+                const float most = NQ == 2 ? __uint_as_float(top[k] << 16) : half_bits_to_float(top[k]);
+                const int e2 = most > 0.0f ? min(max(7 - exponent_of(__float_as_uint(most)), -120), 100) : 0;
+                const float up = P.factor < 0.0f ? -pow2f(e2) : pow2f(e2);
+                if (d == 0) factors[r] = fabsf(P.factor) * pow2f(-e2);
+                const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+                uint32_t w[NQ][2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    __half2 v[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t y = x[2 * e + i];
+                        float2 z;
+                        if constexpr (NQ == 2) z = make_float2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
+                        else z = __half22float2(*reinterpret_cast<const __half2 *>(&y));
+                        z.x *= up, z.y *= up;
+                        if (special) {  // (infinities: there is no code)
+                            z.x = fabsf(z.x) <= 448.0f ? z.x : __uint_as_float(0x7fffffffu);
+                            z.y = fabsf(z.y) <= 448.0f ? z.y : __uint_as_float(0x7fffffffu);
+                        }
+                        v[i] = __floats2half2_rn(z.x, z.y);
                     }
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) w[n][e] = part4(v);
                 }
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
-                    *reinterpret_cast<uint4 *>(dst + n * C::KEYS + (((half * (HD / 16) + c) ^ (lane_row & 7)) << 4)) =
-                        make_uint4(w[n][0], w[n][1], w[n][2], w[n][3]);
+                    *reinterpret_cast<uint2 *>(smem + (t * NQ + n) * C::KEYS + r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 8)) =
+                        make_uint2(w[n][0], w[n][1]);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full + 8 * t);
+            named_barrier(tile_bar, 256);  // (of all 128 rows)
+            f = factors[lane_row];
         };
 
         int np = 0;
+        bool more = false;
         ok = group_wait(first, tile_bar, 256, piece_bar(np), piece_parity(np));
-        Piece pc = read_piece(np);
-        if (ok && pc.more && rows_of(pc) > 128 * t) load_queries(pc);
-        while (ok && pc.more) {
-            __syncwarp();
-            if (lane == 0) free_piece(np);
-            ++np;
-            const int rows = rows_of(pc);
-            const bool have = rows > 128 * t;  // rows in this tile
+        if (ok) {
+            const Piece pc = read_piece(np);
+            more = pc.more;
+            if (more && rows_of(pc) > 128 * t) load_queries(pc);
+        }
+        while (ok && more) {
+            int tile0, nt, hi, lo, all_hi, all_lo;  // tokens that this row sees, and those that all rows see
+            bool have;                              // rows in this tile
+            {
+                const Piece pc = read_piece(np);
+                const int rows = rows_of(pc);
+                have = rows > 128 * t;
+                tile0 = pc.tile, nt = pc.nt;
+                const int start = pc.len - pc.n, i = token_of(pc.r0 + min(mine, rows - 1));
+                hi = P.causal ? min(pc.len, start + i + 1) : pc.len, lo = P.window ? start + i - P.window + 1 : 0;
+                all_hi = P.causal ? min(pc.len, start + token_of(pc.r0 + min(rows - 1, 128 * t)) + 1) : pc.len;
+                all_lo = P.window ? start + token_of(pc.r0 + min(rows, 128 * t + 128) - 1) - P.window + 1 : 0;
+            }
             float ref = -INFINITY, l = 0.0f;
             if (have) {
-                // tokens that this row sees, and those that all rows see
-                const int start = pc.len - pc.n, i = token_of(pc.r0 + min(mine, rows - 1));
-                const int hi = P.causal ? min(pc.len, start + i + 1) : pc.len, lo = P.window ? start + i - P.window + 1 : 0;
-                const int all_hi = P.causal ? min(pc.len, start + token_of(pc.r0 + 128 * t) + 1) : pc.len;
-                const int all_lo = P.window ? start + token_of(pc.r0 + min(rows, 128 * t + 128) - 1) - P.window + 1 : 0;
-                for (int j = 0; j < pc.nt; ++j, ++it) {
+                for (int j = 0; j < nt; ++j, ++it) {
                     ok = group_wait(first, tile_bar, 256, s_full + 8 * t, it & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    const int tok = (pc.tile + j) * TILE + half * HT;
+                    const int tok = (tile0 + j) * TILE + half * HT;
                     const bool masked = tok < all_lo || tok + HT > all_hi;
                     const int from = lo - tok, to = hi - tok;
                     // The scores are read twice, for the maximum, which the load itself
@@ -782,7 +808,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                     asm volatile("" : KV_RW4(s[1], 0), KV_RW4(s[1], 4), KV_RW4(s[1], 8), KV_RW4(s[1], 12), KV_RWF4(m) : : "memory");
                     float top = max3(fmaxf(fmaf(m[0], fk[0], lv[0]), fmaf(m[1], fk[1], lv[1])), fmaf(m[2], fk[2], lv[2]),
                                      fmaf(m[3], fk[3], lv[3]));
-                    if (masked) {  // of what the row sees
+                    // (the maximum of all tokens will do where it moves nothing)
+                    if (masked && __any_sync(0xffffffffu, top > ref + MOVE)) {  // of what the row sees
                         top = -INFINITY;
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
@@ -828,47 +855,48 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                         for (int i2 = 0; i2 < 4; ++i2) {
                             const int h = (i2 + 2) & 3;
                             uint32_t p[8];
-                            float v[16];
+                            float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
+                            for (int e = 0; e < 16; e += 4) {
                                 float a = __uint_as_float(s[i2 & 1][e]), b = __uint_as_float(s[i2 & 1][e + 1]);
+                                float c = __uint_as_float(s[i2 & 1][e + 2]), d = __uint_as_float(s[i2 & 1][e + 3]);
                                 fma2(a, b, fk[h], lv[h] - sub);
+                                fma2(c, d, fk[h], lv[h] - sub);
                                 if constexpr (with_mask.value) {
-                                    const int c = 16 * h + e;
-                                    a = c >= from && c < to ? a : -INFINITY;
-                                    b = c + 1 >= from && c + 1 < to ? b : -INFINITY;
+                                    const int k = 16 * h + e;
+                                    a = k >= from && k < to ? a : -INFINITY;
+                                    b = k + 1 >= from && k + 1 < to ? b : -INFINITY;
+                                    c = k + 2 >= from && k + 2 < to ? c : -INFINITY;
+                                    d = k + 3 >= from && k + 3 < to ? d : -INFINITY;
                                 }
-                                v[e] = ex2(a), v[e + 1] = ex2(b);
-                                p[e / 2] = pack_half(v[e], v[e + 1]);
+                                a = ex2(a), b = ex2(b), c = ex2(c), d = ex2(d);
+                                p[e / 2] = pack_half(a, b), p[e / 2 + 1] = pack_half(c, d);
+                                add2(s0, s1, a, b);
+                                add2(s2, s3, c, d);
                             }
                             if (i2 < 2) tmem_ld16(my_s + 16 * i2, s[i2 & 1]);
-#pragma unroll
-                            for (int o = 8; o >= 2; o >>= 1)
-#pragma unroll
-                                for (int e = 0; e < o; e += 2) add2(v[e], v[e + 1], v[e + o], v[e + o + 1]);
-                            l = fmaf(v[0] + v[1], ex2(-20.0f - lv[h]), l);  // (L_FACTOR / the values' scale)
+                            l = fmaf((s0 + s1) + (s2 + s3), ex2(-20.0f - lv[h]), l);  // (L_FACTOR / the values' scale)
                             if (i2 == 1 || i2 == 2) tmem_wait16(s[(i2 + 1) & 1]);
                             tmem_st8(my_s + p_column(h), p);
-                            if (i2 & 1) {
-                                tmem_wait_st();
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * (i2 >> 1));
-                            }
                         }
                     };
                     if (masked) exponentials(std::true_type());
                     else exponentials(std::false_type());
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full + 8 * t);
                 }
             }
-            tiles += pc.nt;
+            tiles += nt;
             // the next piece's queries before this one's results (the tile's warps
             // agree on every wait, also on one that ran out)
-            if (ok) ok = group_wait(first, tile_bar, 256, piece_bar(np), piece_parity(np));
+            if (ok) ok = group_wait(first, tile_bar, 256, piece_bar(np + 1), piece_parity(np + 1));
             if (!ok) break;
             {
-                const Piece next = read_piece(np);
-                if (next.more && rows_of(next) > 128 * t) load_queries(next);
+                const Piece next = read_piece(np + 1);
+                more = next.more;
+                if (more && rows_of(next) > 128 * t) load_queries(next);
             }
             if (have) {
                 ok = group_wait(first, tile_bar, 256, pv_done + 8 * t, (it - 1) & 1);
@@ -877,34 +905,40 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                 *tell = l;
                 named_barrier(pair_bar, 64);
                 l += *told;
+                const Piece pc = read_piece(np);
+                const int rows = rows_of(pc);
                 auto result = [&](int64_t &at, int64_t &row) {
                     const int qr = pc.r0 + mine, i = token_of(qr), h = pc.head * P.group + (qr - i * P.group);
                     at = static_cast<int64_t>(pc.row0 + i) * P.ldy_t + static_cast<int64_t>(h) * P.ldy_h;
                     row = (static_cast<int64_t>(pc.row0) + i) * P.heads * P.group + h;
                 };
-                auto put = [&](int64_t at, int d, const float *v, int n) {  // n values from d on
-                    const int es = P.y_type == QMM_F32 ? 4 : 2;
+                auto put = [&](int64_t at, int d, const float *v) {  // 16 values from d on
+                    if (d >= P.dim) return;
+                    if (PP.y_vec && P.y_type == QMM_F32) {
+                        float *p = static_cast<float *>(P.y) + at + d;
 #pragma unroll
-                    for (int k = 0; k < n; k += 4) {
-                        if (d + k >= P.dim) break;
-                        if (PP.y_vec && es == 4) {
-                            *reinterpret_cast<float4 *>(static_cast<float *>(P.y) + at + d + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-                        } else if (PP.y_vec) {
-                            if (k % 8) continue;
-                            uint32_t w[4];
+                        for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4 *>(p + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                    } else if (PP.y_vec) {
+                        uint32_t w[8];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (P.y_type == QMM_F16) w[e] = pack_half(v[k + 2 * e], v[k + 2 * e + 1]);
-                                else {
-                                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[k + 2 * e], v[k + 2 * e + 1]);
-                                    w[e] = *reinterpret_cast<const uint32_t *>(&b);
-                                }
+                        for (int e = 0; e < 8; ++e) {
+                            if (P.y_type == QMM_F16) w[e] = pack_half(v[2 * e], v[2 * e + 1]);
+                            else {
+                                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+                                w[e] = *reinterpret_cast<const uint32_t *>(&b);
                             }
-                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(P.y) + at + d + k) = make_uint4(w[0], w[1], w[2], w[3]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) store_typed(P.y, at + d + k + e, P.y_type, v[k + e]);
                         }
+                        uint16_t *p = static_cast<uint16_t *>(P.y) + at + d;
+                        if (PP.y_vec == 2) {  // whole sectors of 32 bytes
+                            asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::KV_I4(w, 0), KV_I4(w, 4), "l"(p)
+                                         : "memory");
+                        } else {
+                            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4 *>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) store_typed(P.y, at + d + e, P.y_type, v[e]);
                     }
                 };
                 constexpr float LN2 = 0.6931471805599453f, BACK = 20.0f - TC_SHIFT;
@@ -925,7 +959,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                         float v[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * inv;
-                        if (mine < rows) put(at, half * HD + 16 * k, v, 16);
+                        if (mine < rows) put(at, half * HD + 16 * k, v);
                     }
                     if (P.lse && half == 0 && mine < rows) P.lse[row] = l != 0.0f ? (ref + log2f(l) + BACK) * LN2 : -INFINITY;
                 } else {
@@ -981,13 +1015,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                                     v[4 * e + 2] = fmaf(o[e].z, w, v[4 * e + 2]), v[4 * e + 3] = fmaf(o[e].w, w, v[4 * e + 3]);
                                 }
                             }
-                            if (mine < rows) put(at, 16 * k, v, 16);
+                            if (mine < rows) put(at, 16 * k, v);
                         }
                         if (P.lse && half == 0 && mine < rows) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + BACK) * LN2 : -INFINITY;
                     }
                 }
             }
-            pc = read_piece(np);
+            __syncwarp();
+            if (lane == 0) free_piece(np);
+            ++np;
         }
     }
     tc_fence_before();
@@ -1051,13 +1087,13 @@ cudaError_t launch_tc(const AttnParams &a, int stop, cudaStream_t st, int num_sm
     const float least = 1e-30f;
     if (a.factor > -least && a.factor < least) p.a.factor = a.factor < 0 ? -least : least;
     p.pairs = static_cast<int>(a.T * a.group / UNIT + a.B);
-    auto vec = [&](const void *x, int type, int64_t ld_t, int64_t ld_h) {
+    auto vec = [&](const void *x, int type, int64_t ld_t, int64_t ld_h, int bytes) {
         const int es = f8_size(type);
-        return reinterpret_cast<uintptr_t>(x) % 16 == 0 && (a.T == 1 || ld_t * es % 16 == 0) &&
-               (a.heads * a.group == 1 || ld_h * es % 16 == 0);
+        return reinterpret_cast<uintptr_t>(x) % bytes == 0 && (a.T == 1 || ld_t * es % bytes == 0) &&
+               (a.heads * a.group == 1 || ld_h * es % bytes == 0);
     };
-    p.q_vec = vec(a.q, a.q_type, a.ldq_t, a.ldq_h);
-    p.y_vec = vec(a.y, a.y_type, a.ldy_t, a.ldy_h);
+    p.q_vec = vec(a.q, a.q_type, a.ldq_t, a.ldq_h, 16);
+    p.y_vec = vec(a.y, a.y_type, a.ldy_t, a.ldy_h, 16) + vec(a.y, a.y_type, a.ldy_t, a.ldy_h, 32);
     p.stop = stop;
     for (p.div_shift = 31; (int64_t(1) << (p.div_shift - 31)) < a.group;) ++p.div_shift;
     p.div_mul = static_cast<uint32_t>(((uint64_t(1) << p.div_shift) + a.group - 1) / a.group);
