@@ -111,7 +111,7 @@ int check_attention(const qmm_kv_attention_args *args, qk::KvAttention &out) {
     if (!std::isfinite(a.scale) || std::fabs(a.scale) > 1e30)
         return refuse(QMM_EINVAL_SHAPE, "scale=%g: finite, at most 1e30", a.scale);
     if (int rc = check_batch(a, out.batch)) return rc;
-    if (a.T * (a.q_heads / a.cache->heads) >= I31)
+    if (a.T * (a.q_heads / a.cache->heads) >= I31 - 256)
         return refuse(QMM_EINVAL_SHAPE, "T=%lld rows of %lld heads: too large", static_cast<ll>(a.T), static_cast<ll>(a.q_heads));
     out.c = *a.cache;
     out.q = {a.q, a.ldq_t, a.ldq_h, static_cast<int>(a.q_type)};
@@ -265,6 +265,7 @@ int qmm_kv_attention(const qmm_kv_attention_args *args, void *stream) {
     if (a.lse && !aligned(a.lse, 4)) return refuse(QMM_EINVAL_PTR, "lse must be 4-byte aligned");
     qk::F8Context c;
     if (int rc = qk::f8_context(c)) return rc;
+    if (!qk::f8_available()) return refuse(QMM_ECUDA, "the driver has no tensor map encoder");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const qk::CallLock lock(c.dev, st);
     const qk::KvPlan plan = qk::kv_attention_plan(r, c.num_sms);

@@ -43,6 +43,8 @@ cudaError_t launch_kv_attention(const KvAttention &a, cudaStream_t st, int num_s
     p.factor = static_cast<float>(factor);
     p.factor_low = static_cast<float>(factor - p.factor);
     p.causal = a.causal, p.window = a.window;
+    for (p.div_shift = 31; (int64_t(1) << (p.div_shift - 31)) < p.group;) ++p.div_shift;
+    p.div_mul = static_cast<uint32_t>(((uint64_t(1) << p.div_shift) + p.group - 1) / p.group);
     p.lse = a.lse;
     p.part = reinterpret_cast<float *>(a.scratch);
     p.count = a.count;

@@ -17,8 +17,12 @@
 //   O^T [16 dims x 8 rows]   += V^T [16 x 128 tokens] P^T.
 // Eight warps share a tile of 128 tokens: each takes 16 tokens of S, and after
 // the probabilities went through shared memory 16 (or 32) dims of O, so nobody
-// has to add up accumulators but across cut units.
+// has to add up accumulators but across cut units.  A ninth warp brings the tiles
+// by TMA, page by page, in the swizzle that the loads of the fragments want, and
+// runs ahead across units.
 #pragma once
+
+#include <cuda.h>
 
 #include "kv_device.cuh"
 #include "qmm_internal.h"
@@ -28,8 +32,9 @@ namespace qk {
 namespace kv {
 
 constexpr int TILE = 128;     // tokens of a tile
-constexpr int THREADS = 256;  // 8 warps
+constexpr int THREADS = 256;  // 8 warps, and one for the copies
 constexpr int LEAST = 2;      // tiles per block below which fewer blocks take part
+constexpr int SHORT = 4;      // tiles of a unit that is not cut: it goes to the block where it begins
 
 // A power of two on p', so that its low part in fp16 keeps 2^-38 of the largest.
 constexpr float P_SHIFT = 14.0f;
@@ -52,6 +57,7 @@ struct AttnParams {
     int width, B;
     float factor, factor_low;  // scale * log2 e, and what that loses in 32 bits
     int causal, window;
+    uint32_t div_mul, div_shift;  // row / group = row * div_mul >> div_shift for rows below 2^31
     float *lse;
     float *part;
     unsigned *count;
@@ -64,6 +70,16 @@ struct Seq {
     int row0, n, len, lo, tiles, blocks;
     int64_t units;
 };
+
+// a / b of what is mostly below 2^32 (a 64-bit division takes hundreds of cycles).
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+// The row of the batch (within its sequence) of query row r < 2^31.
+__device__ __forceinline__ int token_of(const AttnParams &P, int r) {
+    return static_cast<int>(static_cast<uint64_t>(r) * P.div_mul >> P.div_shift);
+}
 
 template <int R>
 __device__ __forceinline__ bool load_seq(const AttnParams &P, int b, Seq &s) {
@@ -80,23 +96,18 @@ __device__ __forceinline__ bool load_seq(const AttnParams &P, int b, Seq &s) {
     s.lo = 0;
     if (P.window) s.lo = max(0, len - s.n - P.window + 1) & ~(TILE - 1);
     s.tiles = max(1, (len - s.lo + TILE - 1) / TILE);
-    const int64_t blocks = (static_cast<int64_t>(s.n) * P.group + R - 1) / R;
-    s.blocks = static_cast<int>(blocks);
-    s.units = blocks * P.heads;
+    s.blocks = (s.n * P.group + R - 1) / R;  // (the call's rows times group are below 2^31 - R)
+    s.units = static_cast<int64_t>(s.blocks) * P.heads;
     return true;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
-    const int n = live ? 16 : 0;  // the rest is filled with zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// A box of one page and head: up to 128 bytes of `page` rows from column c on (zeros
+// behind dim).
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, int c, int tile, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(0), "r"(tile), "r"(bar)
+        : "memory");
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -150,7 +161,9 @@ __device__ __forceinline__ void store_typed(void *p, int64_t i, int type, float 
 template <int DP, int NB, bool HL>
 struct Few {
     static constexpr int R = 8 * NB, PARTS = HL ? 2 : 1;
-    static constexpr int STAGES = DP == 256 ? 2 : 3;
+    static constexpr int CTAS = DP == 256 ? 1 : 2;  // per multiprocessor
+    static constexpr int STAGES = DP == 64 ? 4 : DP == 128 && NB * PARTS <= 2 ? 3 : 2;  // (two CTAs per multiprocessor up to 128)
+    static constexpr int ROW = DP == 64 ? 64 : 128, COLS = DP / ROW;  // bytes of a row of a box, boxes side by side
     static constexpr int SIDE = TILE * DP, STAGE = 2 * SIDE;
     static constexpr int QP = DP + 16, PP = TILE + 16;  // pitches in halves: 8 banks between rows, as 8-byte reads want
     static constexpr int OFF_Q = STAGES * STAGE;
@@ -158,178 +171,205 @@ struct Few {
     static constexpr int OFF_RED = OFF_P + PARTS * R * PP * 2;       // [8 warps][R]
     static constexpr int OFF_ROW = OFF_RED + 8 * R * 4;              // [R] factor of the row, [R] first, [R] end, [R] the factor's low part
     static constexpr int OFF_SC = OFF_ROW + 4 * R * 4;               // [STAGES][2][8] scales
-    static constexpr int OFF_ID = OFF_SC + STAGES * 16 * 4;          // [STAGES + 1][8] page ids
-    static constexpr int OFF_PRE = (OFF_ID + (STAGES + 1) * 8 * 4 + 7) / 8 * 8;  // prefix sums
-    static constexpr int SMEM = OFF_PRE + (THREADS + 1) * 8 + 64;
+    static constexpr int OFF_BAR = (OFF_SC + STAGES * 16 * 4 + 7) / 8 * 8;
+    static constexpr int SMEM = OFF_BAR + 16 * STAGES + 16;
+    static_assert(CTAS == 1 ? SMEM <= 232448 : 2 * (SMEM + 1024) <= 233472, "shared memory");
     static constexpr int PART = R * (DP + 2);  // floats of a partial result
+    // byte of 16-byte chunk c of a row of a tile
+    static __device__ __forceinline__ int at(int row, int c) {
+        if constexpr (DP == 64) return row * 64 + ((c ^ (row >> 1 & 3)) << 4);
+        else return (c >> 3) * (TILE * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+    }
 };
 
+// Where a CTA's share of the tiles lies: sequence, unit of it, tile of that.
+struct Walk {
+    int b, tile;
+    int64_t unit;
+    long long seq0, t;  // tiles before the sequence, and before this one
+    Seq s;
+};
+// On to the next unit, nt tiles further.
+template <int R>
+__device__ __forceinline__ void advance(const AttnParams &P, Walk &w, int nt, long long t1) {
+    w.t += nt;
+    w.tile = 0;
+    if (w.t < t1 && ++w.unit == w.s.units) {
+        w.seq0 += w.s.units * w.s.tiles;
+        w.unit = 0;
+        do load_seq<R>(P, ++w.b, w.s);
+        while (w.s.units == 0);
+    }
+}
+// The rows of a unit, and the tokens and tiles that some of them see.
+struct Span {
+    int head, nt, r0, rows, i0, lo, hi, all_lo, all_hi, jb, je;
+};
+template <int R>
+__device__ __forceinline__ Span span_of(const AttnParams &P, const Walk &w, long long t1) {
+    Span u;
+    const Seq &s = w.s;
+    u.head = static_cast<int>(s.blocks == 1 ? w.unit : divide(w.unit, s.blocks));
+    const int block = static_cast<int>(w.unit - static_cast<int64_t>(u.head) * s.blocks);
+    u.nt = s.tiles <= SHORT ? s.tiles : static_cast<int>(min(static_cast<long long>(s.tiles - w.tile), t1 - w.t));
+    u.r0 = block * R;
+    u.rows = min(R, s.n * P.group - u.r0);
+    const int start = s.len - s.n;
+    u.i0 = token_of(P, u.r0);
+    const int i1 = token_of(P, u.r0 + u.rows - 1);
+    u.hi = P.causal ? min(s.len, start + i1 + 1) : s.len;
+    u.all_hi = P.causal ? min(s.len, start + u.i0 + 1) : s.len;
+    u.lo = P.window ? max(0, start + u.i0 - P.window + 1) : 0;
+    u.all_lo = P.window ? max(0, start + i1 - P.window + 1) : 0;
+    u.jb = max(w.tile, (u.lo - s.lo) / TILE);
+    u.je = min(w.tile + u.nt, u.hi > s.lo ? (u.hi - s.lo + TILE - 1) / TILE : 0);
+    return u;
+}
+
 template <int DP, int NB, bool HL>
-__global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kernel(const AttnParams P) {
+__global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
+    kv_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams P) {
     using C = Few<DP, NB, HL>;
     constexpr int R = C::R, STAGES = C::STAGES, KS = DP / 16;
     constexpr int MT = DP / 16 >= 8 ? DP / 128 : 1;  // groups of 16 dims per warp
     constexpr int HALVES = DP == 64 ? 2 : 1;          // warps that share a group of dims, each with its tokens
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, c = lane & 3;
     __half *const sq = reinterpret_cast<__half *>(smem + C::OFF_Q);
     __half *const sp = reinterpret_cast<__half *>(smem + C::OFF_P);
     float *const red = reinterpret_cast<float *>(smem + C::OFF_RED);
     float *const row_f = reinterpret_cast<float *>(smem + C::OFF_ROW);
     int *const row_lo = reinterpret_cast<int *>(row_f + R), *const row_hi = row_lo + R;
-    const float *const sc = reinterpret_cast<const float *>(smem + C::OFF_SC);
-    int *const ids = reinterpret_cast<int *>(smem + C::OFF_ID);
-    long long *const pre = reinterpret_cast<long long *>(smem + C::OFF_PRE);
-    __shared__ unsigned arrived;
+    float *const sc = reinterpret_cast<float *>(smem + C::OFF_SC);
+    const uint32_t full = base + C::OFF_BAR, empty = full + 8 * STAGES;
+    volatile unsigned *const arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 16 * STAGES);
 
+    if (tid == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 8);
+        }
+        fence_mbar_init();
+    }
     pdl_wait();
     pdl_trigger();
 
-    // the tiles of the sequences before each thread's share of them
-    const int share = (P.B + THREADS - 1) / THREADS;
-    {
-        long long sum = 0;
-        for (int b = tid * share; b < min(P.B, (tid + 1) * share); ++b) {
-            Seq s;
-            if (!load_seq<R>(P, b, s)) atomicOr(P.status, STATUS_INDEX);
-            sum += s.units * s.tiles;
-        }
-        long long incl = sum;
+    // Where this CTA's share of the tiles begins.  Every warp finds it by itself:
+    // nobody waits for a barrier in the first microseconds, which a small call is made of.
+    const int share = (P.B + 31) / 32;
+    long long sum = 0;
+    for (int b = lane * share; b < min(P.B, (lane + 1) * share); ++b) {
+        Seq s;
+        if (!load_seq<R>(P, b, s)) atomicOr(P.status, STATUS_INDEX);
+        sum += s.units * s.tiles;
+    }
+    long long before = sum;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) pre[warp] = incl;
-        __syncthreads();
-        long long before = 0;
-        for (int w = 0; w < warp; ++w) before += pre[w];
-        __syncthreads();
-        pre[tid] = before + incl - sum;
-        if (tid == THREADS - 1) pre[THREADS] = before + incl;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
     }
-    if (DP > P.dim) {  // the columns that no copy writes
-        uint4 *z = reinterpret_cast<uint4 *>(smem);
-        for (int i = tid; i < STAGES * C::STAGE / 16; i += THREADS) z[i] = make_uint4(0, 0, 0, 0);
-    }
-    __syncthreads();
-    const long long W = pre[THREADS];
+    const long long W = __shfl_sync(0xffffffffu, before, 31);
+    before -= sum;
     if (W == 0) return;
-    const long long most = max(1ll, W / LEAST);
-    const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), most));
+    const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, W / LEAST)));
     const int cta = blockIdx.x;
     if (cta >= blocks) return;
-    long long t = cta * W / blocks;
-    const long long t1 = (cta + 1) * W / blocks;
-
-    int b, tile;
-    int64_t unit;
-    Seq s;
-    long long seq0;  // tiles before sequence b
+    const long long t1 = divide((cta + 1) * W, blocks);
+    Walk w;
+    w.t = divide(cta * W, blocks);
     {
-        int first = 0, last = THREADS - 1;
-        while (first < last) {
-            const int mid = (first + last + 1) >> 1;
-            if (pre[mid] <= t) first = mid;
-            else last = mid - 1;
+        const int from = __ffs(__ballot_sync(0xffffffffu, before <= w.t && w.t < before + sum)) - 1;
+        w.b = from * share;
+        w.seq0 = __shfl_sync(0xffffffffu, before, from);
+        for (;; ++w.b) {
+            load_seq<R>(P, w.b, w.s);
+            if (w.t < w.seq0 + w.s.units * w.s.tiles) break;
+            w.seq0 += w.s.units * w.s.tiles;
         }
-        b = first * share;
-        seq0 = pre[first];
-        for (;; ++b) {
-            load_seq<R>(P, b, s);
-            if (t < seq0 + s.units * s.tiles) break;
-            seq0 += s.units * s.tiles;
-        }
-        unit = (t - seq0) / s.tiles;
-        tile = static_cast<int>((t - seq0) - unit * s.tiles);
+        w.unit = divide(w.t - w.seq0, w.s.tiles);
+        w.tile = static_cast<int>((w.t - w.seq0) - w.unit * w.s.tiles);
+        if (w.tile && w.s.tiles <= SHORT) advance<R>(P, w, w.s.tiles - w.tile, t1);
     }
+    __syncthreads();  // (the barriers are ready)
 
-    // copies: this thread's 16-byte column and rows of a tile
-    constexpr int CPR = DP / 16, STEP = THREADS / CPR;
-    const int my_c = tid % CPR, my_r = tid / CPR;
-    const bool copies = my_c < P.dim / 16;
-    auto swz = [](int row) { return DP == 64 ? (row >> 1) & 3 : row & 7; };
-
-    while (t < t1) {
-        const int head = static_cast<int>(unit / s.blocks), block = static_cast<int>(unit - static_cast<int64_t>(head) * s.blocks);
-        const int nt = static_cast<int>(min(static_cast<long long>(s.tiles - tile), t1 - t));
-        const int64_t r0 = static_cast<int64_t>(block) * R;
-        const int rows = static_cast<int>(min(static_cast<int64_t>(R), static_cast<int64_t>(s.n) * P.group - r0));
-        // tokens that some row of the block sees, and those that all of them see
-        const int start = s.len - s.n;
-        const int i0 = static_cast<int>(r0 / P.group), i1 = static_cast<int>((r0 + rows - 1) / P.group);
-        const int hi = P.causal ? min(s.len, start + i1 + 1) : s.len;
-        const int all_hi = P.causal ? min(s.len, start + i0 + 1) : s.len;
-        const int lo = P.window ? max(0, start + i0 - P.window + 1) : 0;
-        const int all_lo = P.window ? max(0, start + i1 - P.window + 1) : 0;
-        const int jb = max(tile, (lo - s.lo) / TILE), je = min(tile + nt, hi > s.lo ? (hi - s.lo + TILE - 1) / TILE : 0);
-
-        __syncthreads();  // nobody reads what the last segment left in shared memory
-        const int32_t *ptab = P.table + static_cast<int64_t>(b) * P.ld_table;
-        // ids of the eight groups of 16 tokens of tile j, -1 where there is nothing to read
-        auto page_of = [&](int j) {
-            const int tok = s.lo + j * TILE + 16 * tid;
-            int id = -1;
-            if (tid < 8 && j < je && tok < hi && tok + 15 >= lo) {
-                id = __ldg(ptab + tok / P.page);
-                if (id < 0 || id >= P.pages) {
-                    atomicOr(P.status, STATUS_INDEX);
-                    id = -1;
-                }
-            }
-            return id;
-        };
-        auto copy_tile = [&](int j) {
-            if (j < je) {
-                const int slot = (j - jb) % STAGES;
-                const int *id = ids + ((j - jb) % (STAGES + 1)) * 8;
-                const uint32_t dst = base + slot * C::STAGE;
-                const int tok0 = s.lo + j * TILE;
-#pragma unroll
-                for (int i = 0; i < TILE / STEP; ++i) {
-                    const int r = my_r + i * STEP;
-                    const int page = id[r >> 4];
-                    const bool live = page >= 0 && tok0 + r < hi;
-                    const int64_t at =
-                        live ? ((static_cast<int64_t>(page) * P.heads + head) * P.page + ((tok0 + r) & (P.page - 1))) * P.dim + 16 * my_c
-                             : 0;
-                    const uint32_t d = dst + r * DP + ((my_c ^ swz(r)) << 4);
-                    if (copies) {
-                        cp16(d, P.codes[0] + at, live);
-                        cp16(d + C::SIDE, P.codes[1] + at, live);
+    if (warp == 8) {
+        // ---- copies ----
+        const int pages = TILE / P.page;  // of a tile
+        const uint32_t box = static_cast<uint32_t>(P.page) * C::ROW;
+        int it = 0;
+        bool ok = true;
+        while (ok && w.t < t1) {
+            const Span u = span_of<R>(P, w, t1);
+            const int32_t *tab = P.table + static_cast<int64_t>(w.b) * P.ld_table;
+            auto page_of = [&](int j) {  // of lane's page of tile j, -1 where there is nothing to read
+                const int tok = w.s.lo + j * TILE + lane * P.page;
+                int id = -1;
+                if (lane < pages && j < u.je && tok < u.hi && tok + P.page > u.lo) {
+                    id = __ldg(tab + tok / P.page);
+                    if (id < 0 || id >= P.pages) {
+                        atomicOr(P.status, STATUS_INDEX);
+                        id = -1;
                     }
                 }
-                if (tid < 16) {
-                    const int page = max(id[tid & 7], 0);
-                    cp4(base + C::OFF_SC + (slot * 16 + tid) * 4, P.scales[tid >> 3] + static_cast<int64_t>(page) * P.heads + head);
+                return id;
+            };
+            int id = page_of(u.jb);
+            for (int j = u.jb; j < u.je; ++j, ++it) {
+                const int64_t tile = static_cast<int64_t>(max(id, 0)) * P.heads + u.head;
+                const float ks = __ldg(P.scales[0] + tile), vs = __ldg(P.scales[1] + tile);
+                const int next = page_of(j + 1);
+                const int s = it % STAGES;
+                if (it >= STAGES) ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * s, ((it / STAGES) - 1) & 1, P.status));
+                if (!ok) break;
+                const int src = 16 * lane / P.page;  // scales of the groups of 16 tokens
+                const float kg = __shfl_sync(0xffffffffu, ks, src), vg = __shfl_sync(0xffffffffu, vs, src);
+                if (lane < 8) sc[16 * s + lane] = kg, sc[16 * s + 8 + lane] = fmaxf(vg, 0x1p-100f);
+                const uint32_t live = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * C::COLS * live * box);
+                __syncwarp();
+                if (id >= 0) {
+                    const uint32_t dst = base + s * C::STAGE + lane * box;
+#pragma unroll
+                    for (int k = 0; k < C::COLS; ++k) {
+                        tma_page(dst + k * TILE * 128, &tmK, 128 * k, static_cast<int>(tile), full + 8 * s);
+                        tma_page(dst + C::SIDE + k * TILE * 128, &tmV, 128 * k, static_cast<int>(tile), full + 8 * s);
+                    }
                 }
+                id = next;
             }
-            cp_commit();
-        };
-        if (tid < 8) {
-#pragma unroll
-            for (int j = 0; j < STAGES; ++j) ids[j * 8 + tid] = page_of(jb + j);
+            advance<R>(P, w, u.nt, t1);
         }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < STAGES - 1; ++j) copy_tile(jb + j);
+        // no CTA ends with copies in flight
+        for (int i = max(0, it - STAGES); i < it; ++i) mbar_wait(full + 8 * (i % STAGES), (i / STAGES) & 1, P.status);
+        return;
+    }
+
+    int it = 0;
+    while (w.t < t1) {
+        const Span u = span_of<R>(P, w, t1);
+        const Seq &s = w.s;
+        const int r0 = u.r0, rows = u.rows, head = u.head, start = s.len - s.n;
 
         // queries: one warp per row, times a power of two that brings the largest to [2^13, 2^14)
+        // (the last unit's barriers lie between its reading of them and this)
+        float v[NB][DP / 32];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            const int r = warp + 8 * n;
-            float v[DP / 32];
+            const int qr = r0 + min(warp + 8 * n, rows - 1), i = token_of(P, qr);
+            const int64_t at = (static_cast<int64_t>(s.row0) + i) * P.ldq_t + static_cast<int64_t>(head * P.group + (qr - i * P.group)) * P.ldq_h;
+#pragma unroll
+            for (int k = 0; k < DP / 32; ++k) v[n][k] = load_typed(P.q, at + min(lane + 32 * k, P.dim - 1), P.q_type);
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const int r = warp + 8 * n, i = token_of(P, r0 + min(r, rows - 1));
             float top = 0.0f;
-            const bool live = r < rows;
-            const int64_t qr = r0 + (live ? r : 0);
-            const int i = static_cast<int>(qr / P.group);
-            const int64_t at = (s.row0 + i) * P.ldq_t + (head * P.group + (qr - static_cast<int64_t>(i) * P.group)) * P.ldq_h;
 #pragma unroll
             for (int k = 0; k < DP / 32; ++k) {
-                const int d = lane + 32 * k;
-                v[k] = live && d < P.dim ? load_typed(P.q, at + d, P.q_type) : 0.0f;
-                const float a = fabsf(v[k]);
+                if (r >= rows || lane + 32 * k >= P.dim) v[n][k] = 0.0f;
+                const float a = fabsf(v[n][k]);
                 top = a <= 3.402823466e38f ? fmaxf(top, a) : top;
             }
 #pragma unroll
@@ -339,10 +379,10 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
             const float up = pow2f(e);
 #pragma unroll
             for (int k = 0; k < DP / 32; ++k) {
-                const float w = v[k] * up;
-                const __half h = __float2half_rn(w);
+                const float x = v[n][k] * up;
+                const __half h = __float2half_rn(x);
                 sq[r * C::QP + lane + 32 * k] = h;
-                if constexpr (HL) sq[(R + r) * C::QP + lane + 32 * k] = __float2half_rn(w - __half2float(h));
+                if constexpr (HL) sq[(R + r) * C::QP + lane + 32 * k] = __float2half_rn(x - __half2float(h));
             }
             if (lane == 0) {
                 row_f[r] = P.factor * pow2f(-e);
@@ -350,6 +390,14 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
                 row_hi[r] = P.causal ? min(s.len, start + i + 1) : s.len;
                 row_lo[r] = P.window ? start + i - P.window + 1 : 0;
             }
+        }
+        named_barrier(1, THREADS);
+        // one group of rows in one part: its fragments stay in registers
+        constexpr bool KEEP = NB == 1 && !HL && DP <= 128;
+        uint2 qf[KEEP ? KS : 1];
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const uint2 *>(sq + g * C::QP + 16 * k + 4 * c);
         }
 
         float o[MT][NB][4];
@@ -364,13 +412,24 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
                 for (int i = 0; i < 4; ++i) o[k][n][i] = 0.0f;
         }
 
-        for (int j = jb; j < je; ++j) {
-            const int slot = (j - jb) % STAGES;
-            cp_wait<STAGES - 2>();
-            __syncthreads();
-            copy_tile(j + STAGES - 1);
-            const int next_id = page_of(j + STAGES);
+        for (int j = u.jb; j < u.je; ++j, ++it) {
+            const int slot = it % STAGES;
+            // (a wait that ran out has raised the status; the warps go on together)
+            mbar_wait(full + 8 * slot, (it / STAGES) & 1, P.status);
+            __syncwarp();
             const uint32_t sk = base + slot * C::STAGE, sv = sk + C::SIDE;
+            const int tok0 = s.lo + j * TILE;
+            const bool whole = tok0 >= u.all_lo && tok0 + TILE <= u.all_hi;
+            if (tok0 < u.lo || tok0 + TILE > u.hi) {
+                // what no row sees may be anything, a page that nobody sees is not even
+                // there: P of them is 0, and so are their values from here on
+                for (int i = lane; i < 16 * KS; i += 32) {
+                    const int row = 16 * warp + i / KS;
+                    if (tok0 + row < u.lo || tok0 + row >= u.hi)
+                        *reinterpret_cast<uint4 *>(smem + slot * C::STAGE + C::SIDE + C::at(row, i % KS)) = make_uint4(0, 0, 0, 0);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (before the next copy into the slot)
+            }
 
             // S^T of this warp's 16 tokens
             float x[NB][4];
@@ -380,18 +439,21 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
                 for (int i = 0; i < 4; ++i) x[n][i] = 0.0f;
             {
                 const int row = 16 * warp + (lane & 15);
-                const uint32_t ra = sk + row * DP;
 #pragma unroll
                 for (int k = 0; k < KS; k += 2) {
-                    uint32_t w[4];
-                    ldsm4(ra + (((k + (lane >> 4)) ^ swz(row)) << 4), w);
+                    uint32_t f[4];
+                    ldsm4(sk + C::at(row, k + (lane >> 4)), f);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t a[4] = {halves(w[2 * h]), halves(w[2 * h + 1]), halves_hi(w[2 * h]), halves_hi(w[2 * h + 1])};
+                        const uint32_t a[4] = {halves(f[2 * h]), halves(f[2 * h + 1]), halves_hi(f[2 * h]), halves_hi(f[2 * h + 1])};
 #pragma unroll
                         for (int n = 0; n < NB; ++n) {
-                            const uint2 q = *reinterpret_cast<const uint2 *>(sq + (8 * n + g) * C::QP + 16 * (k + h) + 4 * c);
-                            mma16816(x[n], a, q.x, q.y);
+                            if constexpr (KEEP) {
+                                mma16816(x[n], a, qf[k + h].x, qf[k + h].y);
+                            } else {
+                                const uint2 q = *reinterpret_cast<const uint2 *>(sq + (8 * n + g) * C::QP + 16 * (k + h) + 4 * c);
+                                mma16816(x[n], a, q.x, q.y);
+                            }
                             if constexpr (HL) {
                                 const uint2 ql =
                                     *reinterpret_cast<const uint2 *>(sq + (R + 8 * n + g) * C::QP + 16 * (k + h) + 4 * c);
@@ -401,15 +463,15 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
                     }
                 }
             }
-            const int tok = s.lo + j * TILE + 16 * warp + g;  // this lane's tokens: tok, tok + 8
-            const float ks = sc[slot * 16 + warp], vs = fmaxf(sc[slot * 16 + 8 + warp], 0x1p-100f);
+            const int tok = tok0 + 16 * warp + g;  // this lane's tokens: tok, tok + 8
+            const float ks = sc[slot * 16 + warp], vs = sc[slot * 16 + 8 + warp];
             const float lv = log2f(vs), iv = __fdiv_rn(1.0f, vs);
             uint32_t hidden = 0;  // bit 4 n + i: x[n][i] is masked
-            const bool whole = s.lo + j * TILE >= all_lo && s.lo + (j + 1) * TILE <= all_hi;
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
                 const int r = 8 * n + 2 * c;
-                const float f0 = row_f[r] * ks, f1 = row_f[r + 1] * ks;
+                const float2 f = *reinterpret_cast<const float2 *>(row_f + r);
+                const float f0 = f.x * ks, f1 = f.y * ks;
                 float y[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] = fmaf(x[n][i], i & 1 ? f1 : f0, lv);
@@ -432,16 +494,15 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
                 }
                 if (g == 0) *reinterpret_cast<float2 *>(red + warp * R + r) = make_float2(a, d);
             }
-            __syncthreads();
-            if (tid < 8) ids[((j + STAGES - jb) % (STAGES + 1)) * 8 + tid] = next_id;
+            named_barrier(1, THREADS);
             float alpha[NB][2];
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
                 const int r = 8 * n + 2 * c;
                 float2 top = make_float2(m[n][0], m[n][1]);
 #pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                    const float2 v = *reinterpret_cast<const float2 *>(red + w * R + r);
+                for (int k = 0; k < 8; ++k) {
+                    const float2 v = *reinterpret_cast<const float2 *>(red + k * R + r);
                     top.x = fmaxf(top.x, v.x), top.y = fmaxf(top.y, v.y);
                 }
                 // The reference is a whole number: log2 of the value scales is one
@@ -478,7 +539,7 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
                     if constexpr (HL) d[R * C::PP] = __float2half_rn(p[i] - __half2float(h));
                 }
             }
-            __syncthreads();
+            named_barrier(1, THREADS);
             // O^T += V^T P^T; for fp32 a tile's products are summed apart and added
             // with a rounding to nearest (the tensor cores cut off what an addition loses)
             const int wd = HALVES == 2 ? warp & 3 : warp, wt = HALVES == 2 ? warp >> 2 : 0;
@@ -507,12 +568,11 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
                             pb[h][n][q] = *reinterpret_cast<const uint2 *>(sp + (q * R + 8 * n + g) * C::PP + 16 * (t16 + h) + 4 * c);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const int chunk = wd * MT + mt;
-                    uint32_t w[4];
-                    ldsm4_t(sv + row * DP + ((chunk ^ swz(row)) << 4), w);
+                    uint32_t f[4];
+                    ldsm4_t(sv + C::at(row, wd * MT + mt), f);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t u0 = __byte_perm(w[2 * h], 0, 0x3120), u1 = __byte_perm(w[2 * h + 1], 0, 0x3120);
+                        const uint32_t u0 = __byte_perm(f[2 * h], 0, 0x3120), u1 = __byte_perm(f[2 * h + 1], 0, 0x3120);
                         const uint32_t a[4] = {halves(u0), halves_hi(u0), halves(u1), halves_hi(u1)};
 #pragma unroll
                         for (int n = 0; n < NB; ++n)
@@ -524,6 +584,8 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
                     }
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + 8 * slot);
             if constexpr (HL) {
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
@@ -533,8 +595,7 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
                         for (int i = 0; i < 4; ++i) o[k][n][i] = fmaf(o[k][n][i], alpha[n][i & 1], part[k][n][i]);
             }
         }
-        cp_wait<0>();
-        __syncthreads();
+        named_barrier(1, THREADS);
 
         // sums over the lanes and warps that share a row
 #pragma unroll
@@ -556,7 +617,7 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
                     for (int i = 0; i < 4; ++i) half_o[((warp - 4) * NB * 4 + n * 4 + i) * 32 + lane] = o[0][n][i];
             }
         }
-        __syncthreads();
+        named_barrier(1, THREADS);
         if constexpr (HALVES == 2) {
             if (warp < 4) {
 #pragma unroll
@@ -569,21 +630,19 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
         for (int n = 0; n < NB; ++n) {
             l[n][0] = l[n][1] = 0.0f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const float2 v = *reinterpret_cast<const float2 *>(red + w * R + 8 * n + 2 * c);
+            for (int k = 0; k < 8; ++k) {
+                const float2 v = *reinterpret_cast<const float2 *>(red + k * R + 8 * n + 2 * c);
                 l[n][0] += v.x, l[n][1] += v.y;
             }
         }
 
         auto out = [&](int r, int64_t &at, int64_t &row) {
-            const int64_t qr = r0 + r;
-            const int i = static_cast<int>(qr / P.group);
-            const int h = head * P.group + static_cast<int>(qr - static_cast<int64_t>(i) * P.group);
-            at = (s.row0 + i) * P.ldy_t + h * P.ldy_h;
+            const int i = token_of(P, r0 + r), h = head * P.group + (r0 + r - i * P.group);
+            at = (static_cast<int64_t>(s.row0) + i) * P.ldy_t + static_cast<int64_t>(h) * P.ldy_h;
             row = (static_cast<int64_t>(s.row0) + i) * P.heads * P.group + h;
         };
-        const bool cut = nt < s.tiles;
-        if (!cut) {
+        constexpr float LN2 = 0.6931471805599453f, BACK = 20.0f - P_SHIFT;
+        if (u.nt == s.tiles) {
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -603,12 +662,11 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
                             }
                         }
                     }
-                    if (P.lse && warp == 0 && g == 0)
-                        P.lse[row] = l[n][h] != 0.0f ? (m[n][h] + log2f(l[n][h]) + 20.0f - P_SHIFT) * 0.6931471805599453f : -INFINITY;
+                    if (P.lse && warp == 0 && g == 0) P.lse[row] = l[n][h] != 0.0f ? (m[n][h] + log2f(l[n][h]) + BACK) * LN2 : -INFINITY;
                 }
         } else {
             // a part of a unit: [row][dim] sums relative to m, then m and l
-            float *const mine = P.part + (static_cast<int64_t>(cta) * 2 + (tile == 0)) * C::PART;
+            float *const mine = P.part + (static_cast<int64_t>(cta) * 2 + (w.tile == 0)) * C::PART;
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -625,29 +683,45 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
                     if (warp == 0 && g == 0) mine[R * DP + r] = m[n][h], mine[R * DP + R + r] = l[n][h];
                 }
             __threadfence();
-            __syncthreads();
-            const long long u0 = seq0 + unit * s.tiles, u1 = u0 + s.tiles - 1;  // first and last tile of the unit
-            const int c0 = static_cast<int>(((u0 + 1) * blocks - 1) / W), c1 = static_cast<int>(((u1 + 1) * blocks - 1) / W);
-            if (tid == 0) arrived = atomicAdd(P.count + c0, 1u);
-            __syncthreads();
-            if (arrived == static_cast<unsigned>(c1 - c0)) {
+            named_barrier(1, THREADS);
+            const long long u0 = w.seq0 + w.unit * s.tiles, u1 = u0 + s.tiles - 1;  // first and last tile of the unit
+            const int c0 = static_cast<int>(divide((u0 + 1) * blocks - 1, W)), c1 = static_cast<int>(divide((u1 + 1) * blocks - 1, W));
+            if (tid == 0) *arrived = atomicAdd(P.count + c0, 1u);
+            named_barrier(1, THREADS);
+            if (*arrived == static_cast<unsigned>(c1 - c0)) {
                 if (tid == 0) P.count[c0] = 0u;  // zero again for the next launch
                 __threadfence();
-                // the last one joins them, in their order
+                // the last one joins them, in their order, eight at a time on their way
                 for (int i = tid; i < rows * (DP / 4); i += THREADS) {
                     const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
-                    float top = -INFINITY;
-                    for (int k = c0; k <= c1; ++k)
-                        top = fmaxf(top, __ldcg(P.part + (static_cast<int64_t>(k) * 2 + (k == c0)) * C::PART + R * DP + r));
-                    const float ref = top == -INFINITY ? 0.0f : top;
-                    float sum = 0.0f;
+                    float top = -INFINITY, sum = 0.0f;
                     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int k = c0; k <= c1; ++k) {
-                        const float *q = P.part + (static_cast<int64_t>(k) * 2 + (k == c0)) * C::PART;
-                        const float w = ex2(__ldcg(q + R * DP + r) - ref);
-                        sum = fmaf(__ldcg(q + R * DP + R + r), w, sum);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(q + r * DP + d));
-                        y.x = fmaf(v.x, w, y.x), y.y = fmaf(v.y, w, y.y), y.z = fmaf(v.z, w, y.z), y.w = fmaf(v.w, w, y.w);
+                    for (int k0 = c0; k0 <= c1; k0 += 8) {
+                        float pm[8], pl[8];
+                        float4 pv[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int cc = min(k0 + k, c1);
+                            const float *q = P.part + (static_cast<int64_t>(cc) * 2 + (cc == c0)) * C::PART;
+                            pm[k] = __ldcg(q + R * DP + r);
+                            pl[k] = __ldcg(q + R * DP + R + r);
+                            pv[k] = __ldcg(reinterpret_cast<const float4 *>(q + r * DP + d));
+                        }
+                        float now = top;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) now = fmaxf(now, pm[k]);
+                        const float ref = now == -INFINITY ? 0.0f : now, down = ex2(top - ref);
+                        top = now;
+                        sum *= down, y.x *= down, y.y *= down, y.z *= down, y.w *= down;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float f = k0 + k <= c1 ? ex2(pm[k] - ref) : 0.0f;
+                            if (k0 + k <= c1) {
+                                sum = fmaf(pl[k], f, sum);
+                                y.x = fmaf(pv[k].x, f, y.x), y.y = fmaf(pv[k].y, f, y.y);
+                                y.z = fmaf(pv[k].z, f, y.z), y.w = fmaf(pv[k].w, f, y.w);
+                            }
+                        }
                     }
                     const float inv = sum != 0.0f ? L_FACTOR / sum : 0.0f;
                     int64_t at, row;
@@ -658,21 +732,23 @@ __global__ void __launch_bounds__(THREADS, DP == 256 ? 1 : 2) kv_attention_kerne
                         store_typed(P.y, at + d + 2, P.y_type, y.z * inv);
                         store_typed(P.y, at + d + 3, P.y_type, y.w * inv);
                     }
-                    if (P.lse && d == 0) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + 20.0f - P_SHIFT) * 0.6931471805599453f : -INFINITY;
+                    if (P.lse && d == 0) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + BACK) * LN2 : -INFINITY;
                 }
             }
         }
-
-        // the next unit
-        t += nt;
-        tile = 0;
-        if (t < t1 && ++unit == s.units) {
-            seq0 += s.units * s.tiles;
-            unit = 0;
-            do load_seq<R>(P, ++b, s);
-            while (s.units == 0);
-        }
+        advance<R>(P, w, u.nt, t1);
     }
+}
+
+// The tensor map of codes [pages * heads][page][dim], boxes of a page and `cols` bytes.
+inline bool encode_pages(CUtensorMap *m, const uint8_t *codes, const AttnParams &p, int cols) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.dim), static_cast<cuuint64_t>(p.page),
+                                static_cast<cuuint64_t>(p.pages * p.heads)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.dim), static_cast<cuuint64_t>(p.dim) * p.page};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(p.page), 1}, es[3] = {1, 1, 1};
+    return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(codes), dims, strides, box, es,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // One instance (a translation unit of its own per DP, as they take long to compile).
@@ -683,9 +759,11 @@ cudaError_t launch_few(const AttnParams &p, cudaStream_t st, int num_sms, int de
     static OncePerDevice ready;
     const cudaError_t e = ready(dev, [&] { return set_smem_attrs(kern, C::SMEM); });
     if (e != cudaSuccess) return e;
+    CUtensorMap tk = {}, tv = {};
+    if (!encode_pages(&tk, p.codes[0], p, C::ROW) || !encode_pages(&tv, p.codes[1], p, C::ROW)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(num_sms * (DP == 256 ? 1 : 2)));
-    cfg.blockDim = dim3(THREADS);
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms * C::CTAS));
+    cfg.blockDim = dim3(THREADS + 32);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -693,7 +771,7 @@ cudaError_t launch_few(const AttnParams &p, cudaStream_t st, int num_sms, int de
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return cudaLaunchKernelEx(&cfg, kern, tk, tv, p);
 }
 template <int DP>
 cudaError_t launch_few_dp(const AttnParams &p, int nb, bool hl, cudaStream_t st, int num_sms, int dev) {

@@ -84,7 +84,6 @@ struct TcParams {
     int pairs;  // at most so many (sequence, block of UNIT rows)
     int q_vec, y_vec;
     int stop;
-    uint32_t div_mul, div_shift;  // row / group = row * div_mul >> div_shift for rows below 2^31
 };
 
 // A block of UNIT rows of a sequence and its tiles of tokens.
@@ -122,13 +121,6 @@ __device__ __forceinline__ bool load_pair(const AttnParams &P, int p, Pair &q) {
     return true;
 }
 
-// A page of one head: box of `page` rows of 128 bytes (zeros behind dim).
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, int tile, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(0), "r"(tile), "r"(bar)
-        : "memory");
-}
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
@@ -372,7 +364,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
         if (first) go = mbar_spin(b, parity, P.status);
         return !named_barrier_or(id, threads, !go);
     };
-    auto token_of = [&](int row) { return static_cast<int>(static_cast<uint64_t>(row) * PP.div_mul >> PP.div_shift); };
+    auto token_of = [&](int row) { return kv::token_of(P, row); };
     auto rows_of = [&](const Piece &p) {
         return static_cast<int>(min(static_cast<int64_t>(UNIT), static_cast<int64_t>(p.n) * P.group - p.r0));
     };
@@ -441,7 +433,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                     }
                     __syncwarp();
                     if (id >= 0) {
-                        tma_page(base + C::OFF_K + k * C::KEYS + lane * key_bytes, &tmK, static_cast<int>(tile), k_full + 8 * k);
+                        tma_page(base + C::OFF_K + k * C::KEYS + lane * key_bytes, &tmK, 0, static_cast<int>(tile), k_full + 8 * k);
                         bulk_copy(base + C::OFF_RAW + v * C::RAW + lane * page_bytes, P.codes[1] + tile * page_bytes, page_bytes,
                                   raw_full + 8 * v);
                     }
@@ -1049,16 +1041,8 @@ cudaError_t launch_dp(const TcParams &p, cudaStream_t st, int num_sms, int dev) 
         return fa.numRegs < REGS ? cudaErrorNotSupported : cudaSuccess;
     });
     if (e != cudaSuccess) return e;
-    // keys: [pages * heads][page][dim] codes, boxes of a page and 128 bytes
     CUtensorMap tm = {};
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.a.dim), static_cast<cuuint64_t>(p.a.page),
-                                static_cast<cuuint64_t>(p.a.pages * p.a.heads)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.a.dim), static_cast<cuuint64_t>(p.a.dim) * p.a.page};
-    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(p.a.page), 1}, es[3] = {1, 1, 1};
-    if (tensor_map_encoder()(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(p.a.codes[0]), dims, strides, box, es,
-                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
+    if (!encode_pages(&tm, p.a.codes[0], p.a, 128)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
     cfg.blockDim = dim3(TC_THREADS);
@@ -1078,8 +1062,6 @@ size_t tc_part_bytes(int dim, int num_sms) {
     return static_cast<size_t>(num_sms) * 2 * (dim <= 64 ? Tc<64, 2>::PART : Tc<128, 2>::PART) * sizeof(float);
 }
 
-bool tc_available() { return tensor_map_encoder() != nullptr; }
-
 cudaError_t launch_tc(const AttnParams &a, int stop, cudaStream_t st, int num_sms, int dev) {
     TcParams p = {};
     p.a = a;
@@ -1095,8 +1077,6 @@ cudaError_t launch_tc(const AttnParams &a, int stop, cudaStream_t st, int num_sm
     p.q_vec = vec(a.q, a.q_type, a.ldq_t, a.ldq_h, 16);
     p.y_vec = vec(a.y, a.y_type, a.ldy_t, a.ldy_h, 16) + vec(a.y, a.y_type, a.ldy_t, a.ldy_h, 32);
     p.stop = stop;
-    for (p.div_shift = 31; (int64_t(1) << (p.div_shift - 31)) < a.group;) ++p.div_shift;
-    p.div_mul = static_cast<uint32_t>(((uint64_t(1) << p.div_shift) + a.group - 1) / a.group);
     if (a.q_type == QMM_BF16) return a.dim <= 64 ? launch_dp<64, 2>(p, st, num_sms, dev) : launch_dp<128, 2>(p, st, num_sms, dev);
     return a.dim <= 64 ? launch_dp<64, 3>(p, st, num_sms, dev) : launch_dp<128, 3>(p, st, num_sms, dev);
 }
