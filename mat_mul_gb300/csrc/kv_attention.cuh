@@ -505,9 +505,10 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
                     const float2 v = *reinterpret_cast<const float2 *>(red + k * R + r);
                     top.x = fmaxf(top.x, v.x), top.y = fmaxf(top.y, v.y);
                 }
-                // The reference is a whole number: log2 of the value scales is one
-                // too, so its difference to x has no error of its own.
-                top.x = ceilf(top.x), top.y = ceilf(top.y);
+                // For fp32 the reference is a whole number: log2 of the value scales is
+                // one too, so its difference to x has no error of its own.  Otherwise it
+                // is the maximum, whose p then is exact in fp16.
+                if constexpr (HL) top.x = ceilf(top.x), top.y = ceilf(top.y);
                 // (a row that has seen nothing yet: any finite reference)
                 const float m0 = top.x == -INFINITY ? 0.0f : top.x, m1 = top.y == -INFINITY ? 0.0f : top.y;
                 alpha[n][0] = ex2(m[n][0] - m0), alpha[n][1] = ex2(m[n][1] - m1);

@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                     top = fmaxf(top, *told);
                     const bool move = top > ref + MOVE;
                     if (__any_sync(0xffffffffu, move)) {
-                        const float now = move ? ceilf(top) : ref;
+                        const float now = move ? top : ref;  // (whose P is exact in fp16)
                         const float down = move ? ex2(ref - now) : 1.0f;
                         ref = now;
                         l *= down;

@@ -21,13 +21,13 @@ struct RopeParams {
     RopeArgs rope;
 };
 
-constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_THREADS = 128;
 
 template <int TX, int TY, int V>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams P) {
     using X = typename KvElem<TX>::type;
     using Y = typename KvElem<TY>::type;
-    constexpr int BATCH = V == 8 ? 2 : 4;
+    constexpr int BATCH = 4;
     pdl_wait();
     pdl_trigger();
     const int parts = (P.heads + P.per - 1) / P.per;
@@ -42,23 +42,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeParams P) 
     group.angles(P.rope, __ldg(P.positions + t), cs);
     const X *x = static_cast<const X *>(P.x) + t * P.ldx_t + h0 * P.ldx_h;
     Y *y = static_cast<Y *>(P.y) + t * P.ldy_t + h0 * P.ldy_h;
-    // (x and y may be the same rows: a batch of heads is read before any of it is written)
-    for (int h = h0; h < h1; h += BATCH, x += BATCH * P.ldx_h, y += BATCH * P.ldy_h) {
-        float v[BATCH][2 * V];
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i)
-            if (h + i < h1) {
-                load_v<X, V>(x + i * P.ldx_h + group.first, v[i]);
-                load_v<X, V>(x + i * P.ldx_h + group.second, v[i] + V);
-            }
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i)
-            if (h + i < h1) {
-                group.turn(v[i], cs);
-                store_v<Y, V>(y + i * P.ldy_h + group.first, v[i]);
-                store_v<Y, V>(y + i * P.ldy_h + group.second, v[i] + V);
-            }
-    }
+    turn_heads<X, Y, V, BATCH>(x, P.ldx_h, y, P.ldy_h, h1 - h0, group, cs);
 }
 
 bool runs_of(const Heads &a, int64_t T, int heads, int v) {
