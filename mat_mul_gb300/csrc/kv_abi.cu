@@ -288,7 +288,7 @@ int qmm_kv_attention(const qmm_kv_attention_args *args, void *stream) {
     }
     r.status = c.status;
     r.dev = c.dev;
-    r.stop = qk::NO_STOP;
+    r.stop = qk::inject_stop_stage();
     const cudaError_t e = qk::launch_kv_attention(r, st, c.num_sms);
     if (e != cudaSuccess) return cuda_error(e, "attention launch");
     qk::count_launches(1);

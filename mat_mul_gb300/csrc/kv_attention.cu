@@ -49,7 +49,8 @@ cudaError_t launch_kv_attention(const KvAttention &a, cudaStream_t st, int num_s
     p.part = reinterpret_cast<float *>(a.scratch);
     p.count = a.count;
     p.status = a.status;
-    if (many_rows(a)) return kv::launch_tc(p, a.stop, st, num_sms, a.dev);
+    p.stop = a.stop;
+    if (many_rows(a)) return kv::launch_tc(p, st, num_sms, a.dev);
     const int nb = row_groups(a);
     const bool hl = a.q.type == QMM_F32;
     switch (padded_dim(a)) {

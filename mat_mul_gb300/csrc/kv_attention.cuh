@@ -62,6 +62,7 @@ struct AttnParams {
     float *part;
     unsigned *count;
     int *status;
+    int stop;  // the tile at which the first CTA's copies stop (NO_STOP: none)
 };
 
 // A sequence of the batch and its share of the work: `units` = heads x row
@@ -121,6 +122,11 @@ __device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(a)
                  : "memory");
+}
+// Whether one of 16 codes is a NaN.
+__device__ __forceinline__ bool has_nan(const uint4 &v) {
+    auto nan = [](uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; };  // bit 7 of a byte is set if it was 0x7f
+    return ((nan(v.x) | nan(v.y) | nan(v.z) | nan(v.w)) & 0x80808080u) != 0;
 }
 // Two codes as exact fp16 values.
 __device__ __forceinline__ uint32_t halves(uint32_t w) {
@@ -298,6 +304,7 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
         // ---- copies ----
         const int pages = TILE / P.page;  // of a tile
         const uint32_t box = static_cast<uint32_t>(P.page) * C::ROW;
+        const int stop = cta == 0 ? P.stop : NO_STOP;
         int it = 0;
         bool ok = true;
         while (ok && w.t < t1) {
@@ -321,7 +328,8 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
                 const float ks = __ldg(P.scales[0] + tile), vs = __ldg(P.scales[1] + tile);
                 const int next = page_of(j + 1);
                 const int s = it % STAGES;
-                if (it >= STAGES) ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * s, ((it / STAGES) - 1) & 1, P.status));
+                if (it >= stop) ok = false;
+                if (ok && it >= STAGES) ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * s, ((it / STAGES) - 1) & 1, P.status));
                 if (!ok) break;
                 const int src = 16 * lane / P.page;  // scales of the groups of 16 tokens
                 const float kg = __shfl_sync(0xffffffffu, ks, src), vg = __shfl_sync(0xffffffffu, vs, src);
@@ -414,19 +422,30 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
 
         for (int j = u.jb; j < u.je; ++j, ++it) {
             const int slot = it % STAGES;
-            // (a wait that ran out has raised the status; the warps go on together)
-            mbar_wait(full + 8 * slot, (it / STAGES) & 1, P.status);
-            __syncwarp();
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * slot, (it / STAGES) & 1, P.status));
             const uint32_t sk = base + slot * C::STAGE, sv = sk + C::SIDE;
             const int tok0 = s.lo + j * TILE;
             const bool whole = tok0 >= u.all_lo && tok0 + TILE <= u.all_hi;
-            if (tok0 < u.lo || tok0 + TILE > u.hi) {
-                // what no row sees may be anything, a page that nobody sees is not even
-                // there: P of them is 0, and so are their values from here on
-                for (int i = lane; i < 16 * KS; i += 32) {
-                    const int row = 16 * warp + i / KS;
-                    if (tok0 + row < u.lo || tok0 + row >= u.hi)
-                        *reinterpret_cast<uint4 *>(smem + slot * C::STAGE + C::SIDE + C::at(row, i % KS)) = make_uint4(0, 0, 0, 0);
+            uint32_t nans = 0;  // of this warp's tokens those with a NaN among their values
+            if (ok && !whole) {
+                // What no row sees may be anything, a page that nobody sees is not even
+                // there: P of them is 0, and so are their values from here on.  A token
+                // that some rows see and some do not: 0 times a NaN would reach the
+                // others, so the NaN goes to the scores of those that see it.
+#pragma unroll 1
+                for (int i = 0; i < 16 * KS / 32; ++i) {
+                    const int row = 16 * warp + (32 * i + lane) / KS;
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + slot * C::STAGE + C::SIDE + C::at(row, (32 * i + lane) % KS));
+                    const bool seen = tok0 + row >= u.lo && tok0 + row < u.hi, bad = seen && has_nan(*v);
+                    if (!seen) *v = make_uint4(0, 0, 0, 0);
+                    if (__any_sync(0xffffffffu, bad)) nans |= __reduce_or_sync(0xffffffffu, bad ? 1u << (row & 15) : 0u);
+                }
+                if (nans) {
+#pragma unroll 1
+                    for (int i = lane; i < 16 * KS; i += 32)
+                        if (nans >> (i / KS) & 1)
+                            *reinterpret_cast<uint4 *>(smem + slot * C::STAGE + C::SIDE + C::at(16 * warp + i / KS, i % KS)) =
+                                make_uint4(0, 0, 0, 0);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (before the next copy into the slot)
             }
@@ -473,6 +492,11 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
                 const float2 f = *reinterpret_cast<const float2 *>(row_f + r);
                 const float f0 = f.x * ks, f1 = f.y * ks;
                 float y[4];
+                if (nans) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (nans >> (g + (i >> 1) * 8) & 1) x[n][i] = __uint_as_float(0x7fffffffu);
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] = fmaf(x[n][i], i & 1 ? f1 : f0, lv);
                 if (!whole) {
@@ -494,7 +518,7 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
                 }
                 if (g == 0) *reinterpret_cast<float2 *>(red + warp * R + r) = make_float2(a, d);
             }
-            named_barrier(1, THREADS);
+            if (named_barrier_or(1, THREADS, !ok)) return;  // (a wait ran out: nothing more of this CTA)
             float alpha[NB][2];
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
@@ -781,9 +805,9 @@ cudaError_t launch_few_dp(const AttnParams &p, int nb, bool hl, cudaStream_t st,
     return hl ? launch_few<DP, 4, true>(p, st, num_sms, dev) : launch_few<DP, 4, false>(p, st, num_sms, dev);
 }
 // The kernel for many rows (kv_attention_tc.cu): 16-bit queries, heads of up to
-// 128 values.  stop: the tile at which the first CTA's copies stop (NO_STOP: none).
+// 128 values.
 size_t tc_part_bytes(int dim, int num_sms);
-cudaError_t launch_tc(const AttnParams &a, int stop, cudaStream_t st, int num_sms, int dev);
+cudaError_t launch_tc(const AttnParams &a, cudaStream_t st, int num_sms, int dev);
 
 cudaError_t launch_few_64(const AttnParams &p, int nb, bool hl, cudaStream_t st, int num_sms, int dev);
 cudaError_t launch_few_128(const AttnParams &p, int nb, bool hl, cudaStream_t st, int num_sms, int dev);

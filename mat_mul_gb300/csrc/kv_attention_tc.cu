@@ -73,7 +73,8 @@ struct Tc {
     static constexpr int OFF_SC = OFF_SHARE + 2 * UNIT * 4;       // [SC_SLOTS] key scales and log2 of value scales
     static constexpr int OFF_PIECES = OFF_SC + SC_SLOTS * SC_FLOATS * 4;
     static constexpr int OFF_BAR = OFF_PIECES + PIECES * 48;
-    static constexpr int SMEM = OFF_BAR + 312;
+    static constexpr int OFF_NANS = OFF_BAR + 320;  // [VR][4] bits of the tokens with a NaN among their values
+    static constexpr int SMEM = OFF_NANS + VR * 16;
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(VR * RAW >= (TC_THREADS + 1) * 8, "prefix sums lie where the codes will");
     static constexpr int PART = UNIT * (DP + 2);  // floats of a partial result
@@ -83,7 +84,6 @@ struct TcParams {
     AttnParams a;
     int pairs;  // at most so many (sequence, block of UNIT rows)
     int q_vec, y_vec;
-    int stop;
 };
 
 // A block of UNIT rows of a sequence and its tiles of tokens.
@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
     static_assert(16 * C::KR + 32 * C::VR + 64 + 16 + 16 * PIECES + 8 <= 296, "barriers");
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 296);
     volatile unsigned *const arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 304);  // per tile
+    uint32_t *const nans = reinterpret_cast<uint32_t *>(smem + C::OFF_NANS);
     int4 *const pieces = reinterpret_cast<int4 *>(smem + C::OFF_PIECES);
     float *const sc = reinterpret_cast<float *>(smem + C::OFF_SC);
     long long *const pre = reinterpret_cast<long long *>(smem + C::OFF_RAW);
@@ -372,6 +373,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
     auto end_of = [&](const Piece &p) {
         return P.causal ? min(p.len, p.len - p.n + token_of(p.r0 + rows_of(p) - 1) + 1) : p.len;
     };
+    // the tokens from one on that all rows of the unit see, and the end of them
+    auto all_end_of = [&](const Piece &p) { return P.causal ? min(p.len, p.len - p.n + token_of(p.r0) + 1) : p.len; };
+    auto all_from_of = [&](const Piece &p) {
+        return P.window ? p.len - p.n + token_of(p.r0 + rows_of(p) - 1) - P.window + 1 : 0;
+    };
     auto from_of = [&](const Piece &p) { return P.window ? max(0, p.len - p.n + token_of(p.r0) - P.window + 1) : 0; };
 
     if (warp < 4) {
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
             // ---- copies ----
             const int pages = TILE / P.page;  // of a tile
             const uint32_t page_bytes = static_cast<uint32_t>(P.page * P.dim), key_bytes = static_cast<uint32_t>(P.page) * 128;
-            const int stop = cta == 0 ? PP.stop : NO_STOP;
+            const int stop = cta == 0 ? P.stop : NO_STOP;
             int it = 0;
             bool ok = true;
             for (int np = 0; ok; ++np) {
@@ -588,8 +594,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
             __syncwarp();
             if (lane == 0) free_piece(np);
             if (!pc.more) break;
-            const int end = end_of(pc), from = from_of(pc);
+            const int end = end_of(pc), from = from_of(pc), all_end = all_end_of(pc), all_from = all_from_of(pc);
             for (int j = 0; j < pc.nt; ++j, ++it) {
+                const int tok0 = (pc.tile + j) * TILE;
+                const bool whole = tok0 >= all_from && tok0 + TILE <= all_end;
                 const int s = it % C::VR, live0 = from - (pc.tile + j) * TILE, live1 = end - (pc.tile + j) * TILE;
                 bool go = true;
                 if (warp == 4) {
@@ -604,10 +612,22 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                 }
                 const uint4 *src = reinterpret_cast<const uint4 *>(smem + C::OFF_RAW + s * C::RAW);
                 uint8_t *dst = smem + C::OFF_V + s * C::TILE_BYTES;
+                if (!whole) {
+                    // A token that some rows see and some do not: 0 times a NaN would reach
+                    // the others, so its values go, and the rows that see it are told.
+                    uint32_t *const bits = nans + 4 * s;
+                    if (me < 4) bits[me] = 0;
+                    named_barrier(11, 128);
+                    for (int k = me; k < TILE * cpr; k += 128) {
+                        const int row = k / cpr;
+                        if (row >= live0 && row < live1 && has_nan(src[k])) atomicOr(bits + row / 32, 1u << (row & 31));
+                    }
+                    named_barrier(11, 128);
+                }
                 auto one = [&](int row, int c, uint4 v) {
                     // (what no row sees may be anything, and is not even there where a
                     // whole page is: its probabilities are 0)
-                    if (row < live0 || row >= live1) v = make_uint4(0, 0, 0, 0);
+                    if (row < live0 || row >= live1 || (!whole && nans[4 * s + row / 32] >> (row & 31) & 1)) v = make_uint4(0, 0, 0, 0);
                     uint4 a, b;
                     convert16(v, a, b);
                     // (odd halves store their second part first: no two of eight lanes on one bank)
@@ -762,7 +782,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
             if (more && rows_of(pc) > 128 * t) load_queries(pc);
         }
         while (ok && more) {
-            int tile0, nt, hi, lo, all_hi, all_lo;  // tokens that this row sees, and those that all rows see
+            int tile0, nt, hi, lo, all_hi, all_lo;  // tokens that this row sees, and those that all rows of the unit see
             bool have;                              // rows in this tile
             {
                 const Piece pc = read_piece(np);
@@ -771,8 +791,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                 tile0 = pc.tile, nt = pc.nt;
                 const int start = pc.len - pc.n, i = token_of(pc.r0 + min(mine, rows - 1));
                 hi = P.causal ? min(pc.len, start + i + 1) : pc.len, lo = P.window ? start + i - P.window + 1 : 0;
-                all_hi = P.causal ? min(pc.len, start + token_of(pc.r0 + min(rows - 1, 128 * t)) + 1) : pc.len;
-                all_lo = P.window ? start + token_of(pc.r0 + min(rows, 128 * t + 128) - 1) - P.window + 1 : 0;
+                all_hi = all_end_of(pc), all_lo = all_from_of(pc);
             }
             float ref = -INFINITY, l = 0.0f;
             if (have) {
@@ -780,9 +799,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                     ok = group_wait(first, tile_bar, 256, s_full + 8 * t, it & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    const int tok = (tile0 + j) * TILE + half * HT;
-                    const bool masked = tok < all_lo || tok + HT > all_hi;
-                    const int from = lo - tok, to = hi - tok;
+                    const int tok = (tile0 + j) * TILE;
+                    const bool masked = tok < all_lo || tok + TILE > all_hi;  // (as the conversion has it)
+                    const int from = lo - tok - half * HT, to = hi - tok - half * HT;
                     // The scores are read twice, for the maximum, which the load itself
                     // finds, and for the exponentials: all of them do not fit a
                     // thread's registers beside the rest.
@@ -841,6 +860,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                         }
                     }
                     const float sub = (ref == -INFINITY ? 0.0f : ref) - TC_SHIFT;  // (a row that has seen nothing yet: any finite one)
+                    uint32_t bad0 = 0, bad1 = 0;
+                    if (masked) {  // (the conversion of the tile's values has found them)
+                        const int v = tiles + j;
+                        mbar_spin(v_full + 8 * (v % C::VR), (v / C::VR) & 1, P.status);
+                        __syncwarp();
+                        bad0 = nans[4 * (v % C::VR) + 2 * half], bad1 = nans[4 * (v % C::VR) + 2 * half + 1];
+                    }
                     // Groups 2 and 3, whose scores are here from the maximum, then 0 and 1.
                     auto exponentials = [&](auto with_mask) {
 #pragma unroll
@@ -854,7 +880,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                                 float c = __uint_as_float(s[i2 & 1][e + 2]), d = __uint_as_float(s[i2 & 1][e + 3]);
                                 fma2(a, b, fk[h], lv[h] - sub);
                                 fma2(c, d, fk[h], lv[h] - sub);
-                                if constexpr (with_mask.value) {
+                                    if constexpr (with_mask.value) {
+                                    if (bad0 | bad1) {  // tokens with a NaN among their values
+                                        const float nan = __uint_as_float(0x7fffffffu);
+                                        const uint32_t w = (h < 2 ? bad0 : bad1) >> (16 * (h & 1) + e);
+                                        a = w & 1 ? nan : a, b = w & 2 ? nan : b, c = w & 4 ? nan : c, d = w & 8 ? nan : d;
+                                    }
                                     const int k = 16 * h + e;
                                     a = k >= from && k < to ? a : -INFINITY;
                                     b = k + 1 >= from && k + 1 < to ? b : -INFINITY;
@@ -1062,7 +1093,7 @@ size_t tc_part_bytes(int dim, int num_sms) {
     return static_cast<size_t>(num_sms) * 2 * (dim <= 64 ? Tc<64, 2>::PART : Tc<128, 2>::PART) * sizeof(float);
 }
 
-cudaError_t launch_tc(const AttnParams &a, int stop, cudaStream_t st, int num_sms, int dev) {
+cudaError_t launch_tc(const AttnParams &a, cudaStream_t st, int num_sms, int dev) {
     TcParams p = {};
     p.a = a;
     // a negative factor goes to the queries; one that vanishes would lose the masks
@@ -1076,7 +1107,6 @@ cudaError_t launch_tc(const AttnParams &a, int stop, cudaStream_t st, int num_sm
     };
     p.q_vec = vec(a.q, a.q_type, a.ldq_t, a.ldq_h, 16);
     p.y_vec = vec(a.y, a.y_type, a.ldy_t, a.ldy_h, 16) + vec(a.y, a.y_type, a.ldy_t, a.ldy_h, 32);
-    p.stop = stop;
     if (a.q_type == QMM_BF16) return a.dim <= 64 ? launch_dp<64, 2>(p, st, num_sms, dev) : launch_dp<128, 2>(p, st, num_sms, dev);
     return a.dim <= 64 ? launch_dp<64, 3>(p, st, num_sms, dev) : launch_dp<128, 3>(p, st, num_sms, dev);
 }

@@ -404,3 +404,38 @@ def test_attention_with_scales_far_apart(cuda_lib, dtype, new):
     rng = np.random.default_rng(2)
     _attend(cuda_lib, rng, [new, new], [400, 77], 16, 2, 4, 64, dtype, spread=30, qscale=2.0 ** -28)
     _attend(cuda_lib, rng, [new, new], [400, 77], 16, 2, 4, 64, dtype, qscale=50.0)
+
+
+def test_nan_in_the_values_of_a_masked_token(cuda_lib):
+    """A NaN among the values of a token makes the rows that see it NaN and no other, whatever tile they share; behind
+    the end of a sequence, on a page that only other sequences know and outside the window it reaches nobody."""
+    import torch
+    q = cuda_lib
+    rng = np.random.default_rng(12)
+    for dtype, new, window in (("float32", 40, 0), ("bfloat16", 3, 0), ("bfloat16", 200, 0), ("float16", 200, 50), ("bfloat16", 200, 50)):
+        batch = R.Batch(rng, [new, new], [300, 260], 64)
+        cache, codes, scales = _cache(q, rng, batch, 2, 64)
+        x = _as(rng.standard_normal((batch.T, 4, 64)), dtype)[0]
+        args = (x, _t(batch.table), _t(np.array(batch.lengths, np.int32)), _t(batch.offsets))
+        run = lambda c: _np(q.qmm_kv_attention(c, args[0], args[1], args[2], offsets=args[3], window=window))
+        want = run(cache)
+        v = cache.v.view(torch.uint8)
+        k = cache.k.view(torch.uint8)
+        spots = [298, 299] if new < 100 else [150, 297]     # tokens of the first sequence, of the second none
+        for j in spots:
+            v[int(batch.table[0, j // 64]), 1, j % 64, 5] = 127 if j % 2 else 255
+        for c in (k, v):                                    # behind the ends, and pages of nobody
+            c[int(batch.table[0, 4]), :, 300 - 256:] = 127
+            c[int(batch.table[1, 4]), :, 260 - 256:] = 255
+            c[[p for p in range(batch.pages) if p not in set(batch.table[batch.table >= 0].tolist())]] = 127
+        got = run(cache)
+        pos = np.arange(300 - new, 300)
+        sees = np.zeros(batch.T, bool)
+        for j in spots:
+            sees[:new] |= (pos >= j) & ((pos < j + window) if window else True)
+        assert sees.any() and not sees[:new].all()
+        poisoned = np.zeros(got.shape, bool)
+        poisoned[sees, 2:] = True                           # the query heads of cache head 1
+        assert np.array_equal(got[~poisoned], want[~poisoned])
+        assert np.isnan(got[poisoned].reshape(-1, 64)[:, 5]).all()
+        assert q.qmm_device_status() == 0
