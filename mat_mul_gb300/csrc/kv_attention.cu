@@ -23,9 +23,13 @@ int padded_dim(const KvAttention &a) { return a.c.dim <= 64 ? 64 : a.c.dim <= 12
 }  // namespace
 
 KvPlan kv_attention_plan(const KvAttention &a, int num_sms) {
-    if (many_rows(a)) return {kv::tc_part_bytes(static_cast<int>(a.c.dim), num_sms), 2 * num_sms};
     const int64_t blocks = num_sms * 2, floats = 8 * row_groups(a) * (padded_dim(a) + 2);
-    return {static_cast<size_t>(blocks * 2 * floats * 4), blocks};
+    size_t bytes = static_cast<size_t>(blocks * 2 * floats * 4);
+    if (many_rows(a)) {
+        const size_t many = kv::tc_part_bytes(static_cast<int>(a.c.dim), num_sms);
+        bytes = many > bytes ? many : bytes;
+    }
+    return {bytes, blocks};
 }
 
 cudaError_t launch_kv_attention(const KvAttention &a, cudaStream_t st, int num_sms) {
@@ -50,7 +54,10 @@ cudaError_t launch_kv_attention(const KvAttention &a, cudaStream_t st, int num_s
     p.count = a.count;
     p.status = a.status;
     p.stop = a.stop;
-    if (many_rows(a)) return kv::launch_tc(p, st, num_sms, a.dev);
+    if (many_rows(a)) {
+        const cudaError_t e = kv::launch_tc(p, st, num_sms, a.dev);
+        if (e != cudaErrorNotSupported) return e;  // (else the build gave it too few registers)
+    }
     const int nb = row_groups(a);
     const bool hl = a.q.type == QMM_F32;
     switch (padded_dim(a)) {

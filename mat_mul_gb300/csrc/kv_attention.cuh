@@ -805,7 +805,7 @@ cudaError_t launch_few_dp(const AttnParams &p, int nb, bool hl, cudaStream_t st,
     return hl ? launch_few<DP, 4, true>(p, st, num_sms, dev) : launch_few<DP, 4, false>(p, st, num_sms, dev);
 }
 // The kernel for many rows (kv_attention_tc.cu): 16-bit queries, heads of up to
-// 128 values.
+// 128 values; cudaErrorNotSupported where the build gave it too few registers.
 size_t tc_part_bytes(int dim, int num_sms);
 cudaError_t launch_tc(const AttnParams &a, cudaStream_t st, int num_sms, int dev);
 
