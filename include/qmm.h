@@ -514,7 +514,13 @@ QMM_API int qmm_kv_append(const qmm_kv_append_args *args, void *stream);
  * Accuracy against the formula in 64 bits, u = 2^-11 for fp16 and bf16 queries,
  * 2^-20 for fp32: |dy_i| <= (u + (n + dim + 64) 2^-22 (1 + X)) * sum_j p_j |v_ji| / sum_j p_j
  * before the rounding to y's type, n the tokens seen and X the largest of the
- * row's |scale| sum_i |q_i k_ji|.
+ * row's |scale| sum_i |q_i k_ji|; 16-bit query values below 2^-13 of their head's
+ * largest, m, may besides be off by 2^-21 m.
+ * A NaN or an infinity among a head's query values makes its results NaN, a NaN
+ * code those of the rows that see its token: of a value in its own element, of a
+ * key in all of them.
+ * y must not be q, nor overlap it.  How a sequence's tokens are shared out, and with
+ * it the last bits of its rows, depends on the other sequences of the call.
  * Scales are positive and finite; value scales below 2^-100 count as 2^-100.
  * scratch null: partial results go to the per-(device, stream) workspace (make
  * one call of the largest size before capture, and replay graphs that were
@@ -619,9 +625,9 @@ QMM_API int qmm_set_prefill_path(int path);
 /*
  * qmm_inject_stall -- test hook for failure detection (no counterpart in
  * the pages).  The next `launches` launches of the weight-streaming product
- * kernels (block-per-lane and tensor-core decode, tcgen05 prefill) are
- * launched with their first CTA's weight producer stopping after its first
- * stage, so a consumer's bounded wait (about 2^31 SM cycles, one second at
+ * kernels (block-per-lane and tensor-core decode, tcgen05 prefill) and of the
+ * attention kernels are launched with their first CTA's producer (of weights, or
+ * of keys and values) stopping after its first stage, so a consumer's bounded wait (about 2^31 SM cycles, one second at
  * full clock) expires: the kernel records the timeout in the device status
  * word, stops, waits for the copies it did issue, releases its tensor memory
  * and returns.  That call returns QMM_OK with y incomplete, and the next

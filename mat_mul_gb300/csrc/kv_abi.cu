@@ -62,6 +62,9 @@ int check_cache(const qmm_kv_cache *c) {
 // What a call with rows needs besides.
 int check_pages(const qmm_kv_cache *c) {
     if (c->pages < 1) return refuse(QMM_EINVAL_SHAPE, "a cache without pages");
+    if (c->pages * c->heads >= I31)    // (page, head) is one coordinate of a tensor map
+        return refuse(QMM_EINVAL_SHAPE, "cache of %lld pages and %lld heads: pages * heads must be below 2^31",
+                      static_cast<ll>(c->pages), static_cast<ll>(c->heads));
     if (!c->k || !c->v) return refuse(QMM_EINVAL_PTR, "cache: codes are null");
     if (!aligned(c->k, 16) || !aligned(c->v, 16)) return refuse(QMM_EINVAL_PTR, "cache: codes must be 16-byte aligned");
     if (int rc = check_words(c->k_scale, "cache: key scales")) return rc;
@@ -262,6 +265,7 @@ int qmm_kv_attention(const qmm_kv_attention_args *args, void *stream) {
     if (int rc = check_values(a.q, r.q.type, "q")) return rc;
     if (int rc = check_values(a.y, r.y.type, "y")) return rc;
     if (int rc = check_apart(a.T, a.q_heads, a.cache->dim, a.ldy_t, a.ldy_h, "y")) return rc;
+    if (a.q == a.y) return refuse(QMM_EINVAL_PTR, "y is q: blocks that share a row's tokens read q while others write y");
     if (a.lse && !aligned(a.lse, 4)) return refuse(QMM_EINVAL_PTR, "lse must be 4-byte aligned");
     qk::F8Context c;
     if (int rc = qk::f8_context(c)) return rc;

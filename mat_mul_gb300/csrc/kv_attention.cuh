@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
             const float up = pow2f(e);
 #pragma unroll
             for (int k = 0; k < DP / 32; ++k) {
-                const float x = v[n][k] * up;
+                const float x = v[n][k] * up + (v[n][k] - v[n][k]);  // (an infinity as NaN: its scores may all be -inf, as if nothing was seen)
                 const __half h = __float2half_rn(x);
                 sq[r * C::QP + lane + 32 * k] = h;
                 if constexpr (HL) sq[(R + r) * C::QP + lane + 32 * k] = __float2half_rn(x - __half2float(h));

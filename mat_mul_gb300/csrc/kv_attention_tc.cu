@@ -10,12 +10,15 @@
 //   O_t [128 rows x dim]       += P_t V         kind::f16, A in TMEM, V as it lies
 //                                               in the cache (tokens x dim)
 // Keys go from the cache to the tensor cores as they are: TMA brings their codes
-// in the 128-byte swizzle, and a query is the sum of e4m3 parts, two for bf16 (4
-// bits each: its 8 bits) and three for fp16, in one power of two per row.  Parts
-// are cut off at 2^-10 of a scale at which the row's largest value is 2^7 to 2^8, so
-// values below 2^-9 of it lose bits of theirs (an error of 2^-17 of the largest at
-// most).  Two parts at the rate of 8-bit codes cost what one fp16 operand
-// costs.  Values have to meet P in fp16: four warps convert them (exactly).
+// in the 128-byte swizzle, and a query is the sum of 8-bit parts, two for bf16 and
+// three for fp16, in a power of two that brings its row's largest value to 2^7 to 2^8.
+// The first part is e4m3.  Its 4 bits leave at most half a step, 8 units of the last
+// of bf16's 8 bits: 3 bits hold that, so the second part is e5m2, whose steps reach
+// down to 2^-16 (e4m3's end at 2^-9).  fp16's 11 bits leave 64 units, then 4, and the
+// third part is e5m2 as well.  So values down to 2^-6 (at least 2^-13 of the largest)
+// are exact; smaller ones are off by at most 2^-14 (bf16) or 2^-17 (fp16), that is
+// 2^-21 and 2^-24 of the largest.  Two parts at the rate of 8-bit codes cost what one
+// fp16 operand costs.  Values have to meet P in fp16: four warps convert them (exactly).
 //
 // While the tensor cores work on one tile, the other's warps take the
 // exponentials.  The reference of a row is its running maximum, but only moved when
@@ -61,7 +64,7 @@ constexpr float TC_SHIFT = 6.0f;  // P as fp16 is at most 2^(MOVE + TC_SHIFT)
 // over the scores of its thread's half, columns that were read before it is written.
 __device__ __forceinline__ constexpr int p_column(int g) { return 64 * (g >> 2) + 32 * (g >> 1 & 1) + 8 * (g & 1); }
 
-// NQ: e4m3 parts of a query.
+// NQ: 8-bit parts of a query.
 template <int DP, int NQ>
 struct Tc {
     static constexpr int KEYS = TILE * 128;                  // a tile of keys, and a part of a tile of queries: rows of 128 bytes
@@ -228,12 +231,13 @@ __device__ __forceinline__ void convert16(const uint4 &w, uint4 &a, uint4 &b) {
 }
 
 // Four values (fp16) as codes, and what the codes leave of them (exact).
+template <__nv_fp8_interpretation_t TYPE>
 __device__ __forceinline__ uint32_t part4(__half2 (&v)[2]) {
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const __nv_fp8x2_storage_t c = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(v[i]), __NV_SATFINITE, __NV_E4M3);
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3);
+        const __nv_fp8x2_storage_t c = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(v[i]), __NV_SATFINITE, TYPE);
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(c, TYPE);
         v[i] = __hsub2(v[i], *reinterpret_cast<const __half2 *>(&h));
         w |= static_cast<uint32_t>(c) << (16 * i);
     }
@@ -457,6 +461,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
             // conversion looks after the keys as well), one per tile for P, and a
             // whole warp that stays together, so that the addresses stay in uniform registers.
             constexpr uint32_t ID_S = (1u << 4) | ((TILE >> 3) << 17) | ((128 >> 4) << 24);
+            constexpr uint32_t ID_S5 = ID_S | (1u << 7);  // A in e5m2
             constexpr uint32_t ID_O = (1u << 4) | (1u << 16) | ((DP >> 3) << 17) | ((128 >> 4) << 24);
             const uint64_t dq0 = f8::smem_desc(base), dk0 = f8::smem_desc(base + C::OFF_K), dv0 = desc_mn<DP>(base + C::OFF_V);
             const int ks = (P.dim + 31) / 32;
@@ -472,7 +477,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
 #pragma unroll
                         for (int i = 0; i < DP / 32; ++i)
                             if (i < ks)
-                                mma_ss(tmem + t * 128, dq0 + (t * NQ + n) * (C::KEYS >> 4) + 2 * i, dk + 2 * i, ID_S, n || i ? 1u : 0u);
+                                mma_ss(tmem + t * 128, dq0 + (t * NQ + n) * (C::KEYS >> 4) + 2 * i, dk + 2 * i, n ? ID_S5 : ID_S, n || i ? 1u : 0u);
                     commit(s_full + 8 * t);
                     if (last) commit(k_empty + 8 * (ki % C::KR));
                 }
@@ -677,7 +682,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
         bool ok = true;
         float f = 0.0f;  // scale log2 e over the power of two of the row's queries
 
-        // The queries of piece p as e4m3 parts, in a power of two that brings a row's
+        // The queries of piece p as 8-bit parts, in a power of two that brings a row's
         // largest to [2^7, 2^8).  A row goes to DP / 8 lanes, 16 bytes each (with a
         // row per thread every load touched 32 lines: 8000 cycles per unit).
         auto load_queries = [&](const Piece &p) {
@@ -759,7 +764,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                         v[i] = __floats2half2_rn(z.x, z.y);
                     }
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n) w[n][e] = part4(v);
+                    for (int n = 0; n < NQ; ++n) w[n][e] = n ? part4<__NV_E5M2>(v) : part4<__NV_E4M3>(v);
                 }
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)

@@ -126,9 +126,10 @@ def append(codes, scales, x, batch):
     return codes, scales
 
 
-def attention(q, k, ks, v, vs, batch, scale, causal=True, window=0):
+def attention(q, k, ks, v, vs, batch, scale, causal=True, window=0, small=False):
     """(y, lse, bound of y before its rounding, bound of lse) in 64 bits; q [T, query heads, dim] as the values it holds,
-    fp32 queries (u32) or 16-bit ones."""
+    fp32 queries (u32) or 16-bit ones.  small: some 16-bit values are below 2^-13 of their head's largest, m, and may be
+    off by 2^-21 m.  A score is then off by at most d = |scale| 2^-21 m sum |k_ji|, and p_j / sum p by exp(2 d) - 1 of it."""
     T, Hq, D = q.shape
     H, P = k.shape[1], batch.page
     y, e = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
@@ -161,6 +162,9 @@ def attention(q, k, ks, v, vs, batch, scale, causal=True, window=0):
                 spread = np.where(some[:, None], (w @ np.abs(V[g])) / total[:, None], 0)
                 lse[rows, h] = np.where(some, top + np.log(total), -np.inf)
             c = (seen.sum(axis=1) + D + 64) * 2.0 ** -22 * (1 + X)
+            if small and q.dtype != np.float32:
+                d = abs(scale) * 2.0 ** -21 * np.abs(q[rows, h]).max(axis=1) * np.where(seen, np.abs(K[g]).sum(axis=1), 0).max(axis=1)
+                c = c + np.expm1(2 * d)
             y[rows, h], e[rows, h] = r, c[:, None] * spread
             le[rows, h] = c + 2.0 ** -22 * np.where(some, np.abs(lse[rows, h]), 0)
             e[rows, h] += 2.0 ** -11 * spread if q.dtype != np.float32 else 2.0 ** -20 * spread

@@ -439,3 +439,59 @@ def test_nan_in_the_values_of_a_masked_token(cuda_lib):
         assert np.array_equal(got[~poisoned], want[~poisoned])
         assert np.isnan(got[poisoned].reshape(-1, 64)[:, 5]).all()
         assert q.qmm_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+@pytest.mark.parametrize("new", [1, 200])
+def test_one_large_query_value_leaves_the_others_theirs(cuda_lib, dtype, new):
+    """A channel with queries 2^12 times the others' and keys of 0: no share in any score, and the others keep their bits
+    but for those that are smaller still."""
+    q = cuda_lib
+    rng = np.random.default_rng(61)
+    H, D = 2, 64
+    batch = R.Batch(rng, [new], [500], 64)
+    cache, codes, scales = _cache(q, rng, batch, H, D)
+    codes[0][..., 5] = 0
+    cache.k.view(__import__("torch").uint8).copy_(_t(codes[0]))
+    values = rng.standard_normal((batch.T, 4, D))
+    values[..., 5] = 4096.0 * np.where(values[..., 5] < 0, -1, 1)
+    x, xv = _as(values, dtype)
+    y, lse = q.qmm_kv_attention(cache, x, _t(batch.table), _t(np.array([500], np.int32)), offsets=_t(batch.offsets), lse=True)
+    wy, wl, e, le = R.attention(xv, codes[0], scales[0], codes[1], scales[1], batch, D ** -0.5, small=True)
+    _within(_np(y), wy, R.rounded(wy, e, dtype), "y")
+    _within(_np(lse), wl, le, "lse")
+    assert q.qmm_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("new", [1, 200])
+def test_nan_and_infinities_in_queries_and_keys(cuda_lib, dtype, new):
+    """In a head's query: its results are NaN (also where every score is -inf).  In a key: those of the rows that see the
+    token.  All others are as they should be."""
+    q = cuda_lib
+    rng = np.random.default_rng(62)
+    H, D, lengths = 2, 64, [500, 300]
+    batch = R.Batch(rng, [new, new], lengths, 64)
+    cache, codes, scales = _cache(q, rng, batch, H, D)
+    codes[0][..., 7] = 0x38                       # 1, so that one infinite query value decides all scores
+    at = 300 - new // 2 - 1                       # of the second sequence: seen by half of its rows (by its only one)
+    codes[0][batch.table[1, at // 64], 1, at % 64, 9] = 0x7f
+    cache.k.view(__import__("torch").uint8).copy_(_t(codes[0]))
+    values = rng.standard_normal((batch.T, 4, D))
+    bad = np.zeros((batch.T, 4), bool)
+    for row, head, i, v in ((0, 1, 3, np.nan), (0, 2, 7, np.inf), (0, 3, 7, -np.inf), (batch.T - 1, 0, 0, np.nan), (new // 3, 0, 63, np.inf)):
+        values[row, head, i] = v
+        bad[row, head] = True
+    if new == 1:
+        bad[1, 2:] = True
+    else:
+        bad[batch.T - 1 - new // 2:, 2:] = True   # rows from position `at` on, heads of cache head 1
+    x, xv = _as(values, dtype)
+    y, lse = q.qmm_kv_attention(cache, x, _t(batch.table), _t(np.array(lengths, np.int32)), offsets=_t(batch.offsets), lse=True)
+    assert q.qmm_device_status() == 0
+    codes[0][codes[0] == 0x7f] = 0
+    wy, wl, e, le = R.attention(np.where(np.isfinite(xv), xv, 0).astype(xv.dtype), codes[0], scales[0], codes[1], scales[1], batch, D ** -0.5)
+    y, lse = _np(y), _np(lse)
+    assert np.isnan(y[bad]).all() and np.isnan(lse[bad]).all()
+    _within(y[~bad], wy[~bad], R.rounded(wy, e, dtype)[~bad], "y")
+    _within(lse[~bad], wl[~bad], le[~bad], "lse")

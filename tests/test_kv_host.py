@@ -22,7 +22,7 @@ def append(c=cache(), tab=A, width=8, ld=8, lens=A, off=0, B=3, T=3, t=2, k=A, k
            pos=0, qp=A, Hq=8, qa=1024, qb=128, op=A + (1 << 20), oa=1024, ob=128):
     return L.qmm_kv_append(q._APPEND_ARGS.pack(at(c), tab, width, ld, lens, off, B, T, t, k, ka, kb, v, va, vb, at(r), pos, qp, Hq,
                                                qa, qb, op, oa, ob), ST)
-def args(c=cache(), tab=A, width=8, ld=8, lens=A, off=0, B=3, T=3, t=2, x=A, Hq=8, xa=1024, xb=128, yt=2, y=A, ya=1024, yb=128,
+def args(c=cache(), tab=A, width=8, ld=8, lens=A, off=0, B=3, T=3, t=2, x=A, Hq=8, xa=1024, xb=128, yt=2, y=A + 4096, ya=1024, yb=128,
          scale=0.1, causal=1, window=0, lse=0, work=0, n=0):
     return q._ATTENTION_ARGS.pack(at(c), tab, width, ld, lens, off, B, T, t, x, Hq, xa, xb, yt, y, ya, yb, scale, causal, window,
                                   lse, work, n)
@@ -58,7 +58,8 @@ refused(attend, TYPE, dict(t=3), dict(yt=7))
 refused(attend, SHAPE, dict(Hq=6), dict(Hq=0), dict(Hq=1 << 15), dict(window=-1), dict(window=5, causal=0), dict(scale=float('nan')),
         dict(scale=float('inf')), dict(scale=1e31), dict(ya=1023), dict(yb=64), dict(T=1 << 30, off=A, B=1),
         dict(work=A, n=100), dict(work=A, n=-1))
-refused(attend, PTR, dict(x=0), dict(y=0), dict(x=A + 1), dict(y=A + 1), dict(lse=A + 2), dict(work=A + 128, n=1 << 30))
+refused(attend, PTR, dict(x=0), dict(y=0), dict(x=A + 1), dict(y=A + 1), dict(lse=A + 2), dict(work=A + 128, n=1 << 30), dict(x=A, y=A))
+refused(attend, SHAPE, dict(c=cache(pages=I31 >> 10, heads=1024), Hq=1024, xa=1 << 17, ya=1 << 17))
 assert L.qmm_rope(None, ST) == PTR and L.qmm_kv_append(None, ST) == PTR and L.qmm_kv_attention(None, ST) == PTR
 assert L.qmm_kv_attention_scratch(None) == PTR and L.qmm_kv_attention_scratch(args(Hq=6)) == SHAPE
 assert not log('launch')
@@ -71,7 +72,7 @@ assert not log('launch')
 # and what is at the edge of it
 for rc in (rope(r=table(0)), rope(x=A, y=A), rope(ya=128, yb=128 * 3, xa=128, xb=384), append(r=None, qp=0, op=0), append(r=table(0)), append(qp=A, op=A),
            append(qp=0), attend(window=1 << 40), attend(causal=0), attend(width=0, tab=0), attend(scale=0.0), attend(scale=-1.0),
-           attend(c=cache(pages=I31 - 1, heads=1024), Hq=1024, xa=1 << 17, ya=1 << 17)):
+           attend(c=cache(pages=(I31 >> 10) - 1, heads=1024), Hq=1024, xa=1 << 17, ya=1 << 17)):
     assert rc == 0, L.qmm_last_error()
 assert len(log('launch')) == 13
 """)
