@@ -12,10 +12,14 @@ int row_groups(const KvAttention &a) {
     return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
 
-// Whether the call's rows go to the kernel for many rows: 16-bit queries and
-// sequences of more than 32 rows per cache head on the average.
+// Whether the call's rows go to a kernel for many rows (of 256 on tcgen05 for 16-bit
+// queries, of 128 on mma.sync for fp32): heads of up to 128 values, sequences of more than 32
+// rows per cache head on the average.  Measured, the kernel for few rows against the
+// other, 8 sequences, 8 heads of 128: 16-bit, 20 rows over 1024, 4096, 16384 tokens 22, 45, 117
+// against 27, 43, 112 us; fp32, 40 rows over 4096 96 against 77, 64 rows over 1024 44
+// against 42.
 bool many_rows(const KvAttention &a) {
-    return a.q.type != QMM_F32 && a.c.dim <= 128 && a.batch.T * (a.q_heads / a.c.heads) > 32 * int64_t(a.batch.B);
+    return a.c.dim <= 128 && a.batch.T * (a.q_heads / a.c.heads) > 32 * int64_t(a.batch.B);
 }
 
 int padded_dim(const KvAttention &a) { return a.c.dim <= 64 ? 64 : a.c.dim <= 128 ? 128 : 256; }
@@ -26,7 +30,8 @@ KvPlan kv_attention_plan(const KvAttention &a, int num_sms) {
     const int64_t blocks = num_sms * 2, floats = 8 * row_groups(a) * (padded_dim(a) + 2);
     size_t bytes = static_cast<size_t>(blocks * 2 * floats * 4);
     if (many_rows(a)) {
-        const size_t many = kv::tc_part_bytes(static_cast<int>(a.c.dim), num_sms);
+        const int dim = static_cast<int>(a.c.dim);
+        const size_t many = a.q.type == QMM_F32 ? kv::rows_part_bytes(dim, num_sms) : kv::tc_part_bytes(dim, num_sms);
         bytes = many > bytes ? many : bytes;
     }
     return {bytes, blocks};
@@ -55,7 +60,7 @@ cudaError_t launch_kv_attention(const KvAttention &a, cudaStream_t st, int num_s
     p.status = a.status;
     p.stop = a.stop;
     if (many_rows(a)) {
-        const cudaError_t e = kv::launch_tc(p, st, num_sms, a.dev);
+        const cudaError_t e = a.q.type == QMM_F32 ? kv::launch_rows(p, st, num_sms, a.dev) : kv::launch_tc(p, st, num_sms, a.dev);
         if (e != cudaErrorNotSupported) return e;  // (else the build gave it too few registers)
     }
     const int nb = row_groups(a);

@@ -34,6 +34,7 @@ namespace kv {
 constexpr int TILE = 128;     // tokens of a tile
 constexpr int THREADS = 256;  // 8 warps, and one for the copies
 constexpr int LEAST = 2;      // tiles per block below which fewer blocks take part
+constexpr int SCALES = 24;    // floats of a tile's scales
 constexpr int SHORT = 4;      // tiles of a unit that is not cut: it goes to the block where it begins
 
 // A power of two on p', so that its low part in fp16 keeps 2^-38 of the largest.
@@ -41,6 +42,7 @@ constexpr float P_SHIFT = 14.0f;
 // and one on the sum of p' / sv, which then stays within fp32 for 2^31 tokens
 // of any scale from 2^-100 to 2^120
 constexpr float L_FACTOR = 0x1p-20f;
+constexpr float LN2 = 0.6931471805599453f, BACK = 20.0f - P_SHIFT;  // of log2 of the sum as it is held
 
 struct AttnParams {
     const uint8_t *codes[2];
@@ -166,7 +168,7 @@ __device__ __forceinline__ void store_typed(void *p, int64_t i, int type, float 
 // block; HL: queries and probabilities as two fp16 parts.
 template <int DP, int NB, bool HL>
 struct Few {
-    static constexpr int R = 8 * NB, PARTS = HL ? 2 : 1;
+    static constexpr int R = 8 * NB, PARTS = HL ? 2 : 1, CONSUMERS = THREADS;
     static constexpr int CTAS = DP == 256 ? 1 : 2;  // per multiprocessor
     static constexpr int STAGES = DP == 64 ? 4 : DP == 128 && NB * PARTS <= 2 ? 3 : 2;  // (two CTAs per multiprocessor up to 128)
     static constexpr int ROW = DP == 64 ? 64 : 128, COLS = DP / ROW;  // bytes of a row of a box, boxes side by side
@@ -176,8 +178,8 @@ struct Few {
     static constexpr int OFF_P = OFF_Q + PARTS * R * QP * 2;
     static constexpr int OFF_RED = OFF_P + PARTS * R * PP * 2;       // [8 warps][R]
     static constexpr int OFF_ROW = OFF_RED + 8 * R * 4;              // [R] factor of the row, [R] first, [R] end, [R] the factor's low part
-    static constexpr int OFF_SC = OFF_ROW + 4 * R * 4;               // [STAGES][2][8] scales
-    static constexpr int OFF_BAR = (OFF_SC + STAGES * 16 * 4 + 7) / 8 * 8;
+    static constexpr int OFF_SC = OFF_ROW + 4 * R * 4;               // [STAGES][3][8]: key scales, log2 and inverse of value scales
+    static constexpr int OFF_BAR = (OFF_SC + STAGES * SCALES * 4 + 7) / 8 * 8;
     static constexpr int SMEM = OFF_BAR + 16 * STAGES + 16;
     static_assert(CTAS == 1 ? SMEM <= 232448 : 2 * (SMEM + 1024) <= 233472, "shared memory");
     static constexpr int PART = R * (DP + 2);  // floats of a partial result
@@ -209,7 +211,8 @@ __device__ __forceinline__ void advance(const AttnParams &P, Walk &w, int nt, lo
 }
 // The rows of a unit, and the tokens and tiles that some of them see.
 struct Span {
-    int head, nt, r0, rows, i0, lo, hi, all_lo, all_hi, jb, je;
+    int head, nt, r0, rows, lo, hi, all_lo, all_hi;
+    int from, jb, je;  // tiles jb .. je - 1 from token `from` on
 };
 template <int R>
 __device__ __forceinline__ Span span_of(const AttnParams &P, const Walk &w, long long t1) {
@@ -221,15 +224,162 @@ __device__ __forceinline__ Span span_of(const AttnParams &P, const Walk &w, long
     u.r0 = block * R;
     u.rows = min(R, s.n * P.group - u.r0);
     const int start = s.len - s.n;
-    u.i0 = token_of(P, u.r0);
-    const int i1 = token_of(P, u.r0 + u.rows - 1);
+    const int i0 = token_of(P, u.r0), i1 = token_of(P, u.r0 + u.rows - 1);
     u.hi = P.causal ? min(s.len, start + i1 + 1) : s.len;
-    u.all_hi = P.causal ? min(s.len, start + u.i0 + 1) : s.len;
-    u.lo = P.window ? max(0, start + u.i0 - P.window + 1) : 0;
+    u.all_hi = P.causal ? min(s.len, start + i0 + 1) : s.len;
+    u.lo = P.window ? max(0, start + i0 - P.window + 1) : 0;
     u.all_lo = P.window ? max(0, start + i1 - P.window + 1) : 0;
+    u.from = s.lo;
     u.jb = max(w.tile, (u.lo - s.lo) / TILE);
     u.je = min(w.tile + u.nt, u.hi > s.lo ? (u.hi - s.lo + TILE - 1) / TILE : 0);
     return u;
+}
+
+// Where this CTA's share of the tiles begins (w.t) and ends (t1), of W tiles in `blocks`
+// shares; false: it has none.  Every warp finds it by itself: nobody waits for a
+// barrier in the first microseconds, which a small call is made of.
+template <int R>
+__device__ __forceinline__ bool begin_walk(const AttnParams &P, int lane, Walk &w, long long &t1, long long &W, int &blocks) {
+    const int share = (P.B + 31) / 32;
+    long long sum = 0;
+    for (int b = lane * share; b < min(P.B, (lane + 1) * share); ++b) {
+        Seq s;
+        if (!load_seq<R>(P, b, s)) atomicOr(P.status, STATUS_INDEX);
+        sum += s.units * s.tiles;
+    }
+    long long before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+    }
+    W = __shfl_sync(0xffffffffu, before, 31);
+    before -= sum;
+    if (W == 0) return false;
+    blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, W / LEAST)));
+    const int cta = blockIdx.x;
+    if (cta >= blocks) return false;
+    t1 = divide((cta + 1) * W, blocks);
+    w.t = divide(cta * W, blocks);
+    const int from = __ffs(__ballot_sync(0xffffffffu, before <= w.t && w.t < before + sum)) - 1;
+    w.b = from * share;
+    w.seq0 = __shfl_sync(0xffffffffu, before, from);
+    for (;; ++w.b) {
+        load_seq<R>(P, w.b, w.s);
+        if (w.t < w.seq0 + w.s.units * w.s.tiles) break;
+        w.seq0 += w.s.units * w.s.tiles;
+    }
+    w.unit = divide(w.t - w.seq0, w.s.tiles);
+    w.tile = static_cast<int>((w.t - w.seq0) - w.unit * w.s.tiles);
+    if (w.tile && w.s.tiles <= SHORT) advance<R>(P, w, w.s.tiles - w.tile, t1);
+    return true;
+}
+
+// The copies of a CTA's tiles, by one warp.  W: the walk over its units, span_of and
+// advance for it.
+template <class C, class W>
+__device__ __forceinline__ void copy_tiles(const AttnParams &P, const CUtensorMap &tmK, const CUtensorMap &tmV, W w, long long t1,
+                                           int stop, uint32_t base, float *sc, uint32_t full, uint32_t empty, int lane) {
+    const int pages = TILE / P.page;  // of a tile
+    const uint32_t box = static_cast<uint32_t>(P.page) * C::ROW;
+    int it = 0;
+    bool ok = true;
+    while (ok && w.t < t1) {
+        const Span u = span_of<C::R>(P, w, t1);
+        const int32_t *tab = P.table + static_cast<int64_t>(w.b) * P.ld_table;
+        auto page_of = [&](int j) {  // of lane's page of tile j, -1 where there is nothing to read
+            const int tok = u.from + j * TILE + lane * P.page;
+            int id = -1;
+            if (lane < pages && j < u.je && tok < u.hi && tok + P.page > u.lo) {
+                id = __ldg(tab + tok / P.page);
+                if (id < 0 || id >= P.pages) {
+                    atomicOr(P.status, STATUS_INDEX);
+                    id = -1;
+                }
+            }
+            return id;
+        };
+        int id = page_of(u.jb);
+        for (int j = u.jb; j < u.je; ++j, ++it) {
+            const int64_t tile = static_cast<int64_t>(max(id, 0)) * P.heads + u.head;
+            const float ks = __ldg(P.scales[0] + tile), vs = __ldg(P.scales[1] + tile);
+            const int next = page_of(j + 1);
+            const int s = it % C::STAGES;
+            if (it >= stop) ok = false;
+            if (ok && it >= C::STAGES) ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * s, ((it / C::STAGES) - 1) & 1, P.status));
+            if (!ok) break;
+            const int src = 16 * lane / P.page;  // scales of the groups of 16 tokens
+            const float kg = __shfl_sync(0xffffffffu, ks, src), vg = __shfl_sync(0xffffffffu, vs, src);
+            if (lane < 8) {
+                const float v = fmaxf(vg, 0x1p-100f);
+                float *const d = sc + SCALES * s + lane;
+                d[0] = kg, d[8] = log2f(v), d[16] = __fdiv_rn(1.0f, v);
+            }
+            const uint32_t live = __popc(__ballot_sync(0xffffffffu, id >= 0));
+            if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * C::COLS * live * box);
+            __syncwarp();
+            if (id >= 0) {
+                const uint32_t dst = base + s * C::STAGE + lane * box;
+#pragma unroll
+                for (int k = 0; k < C::COLS; ++k) {
+                    tma_page(dst + k * TILE * 128, &tmK, 128 * k, static_cast<int>(tile), full + 8 * s);
+                    tma_page(dst + C::SIDE + k * TILE * 128, &tmV, 128 * k, static_cast<int>(tile), full + 8 * s);
+                }
+            }
+            id = next;
+        }
+        advance<C::R>(P, w, u.nt, t1);
+    }
+    // no CTA ends with copies in flight
+    for (int i = max(0, it - C::STAGES); i < it; ++i) mbar_wait(full + 8 * (i % C::STAGES), (i / C::STAGES) & 1, P.status);
+}
+
+// The parts of a unit, of the CTAs c0 .. c1, joined in their order, eight at a time on
+// their way; out(r, at, row) says where row r goes.
+template <class C, int DP, class Out>
+__device__ __forceinline__ void join_parts(const AttnParams &P, int c0, int c1, int rows, int tid, const Out &out) {
+    for (int i = tid; i < rows * (DP / 4); i += C::CONSUMERS) {
+        const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
+        float top = -INFINITY, sum = 0.0f;
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k0 = c0; k0 <= c1; k0 += 8) {
+            float pm[8], pl[8];
+            float4 pv[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int cc = min(k0 + k, c1);
+                const float *q = P.part + (static_cast<int64_t>(cc) * 2 + (cc == c0)) * C::PART;
+                pm[k] = __ldcg(q + C::R * DP + r);
+                pl[k] = __ldcg(q + C::R * (DP + 1) + r);
+                pv[k] = __ldcg(reinterpret_cast<const float4 *>(q + r * DP + d));
+            }
+            float now = top;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) now = fmaxf(now, pm[k]);
+            const float ref = now == -INFINITY ? 0.0f : now, down = ex2(top - ref);
+            top = now;
+            sum *= down, y.x *= down, y.y *= down, y.z *= down, y.w *= down;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float f = k0 + k <= c1 ? ex2(pm[k] - ref) : 0.0f;
+                if (k0 + k <= c1) {
+                    sum = fmaf(pl[k], f, sum);
+                    y.x = fmaf(pv[k].x, f, y.x), y.y = fmaf(pv[k].y, f, y.y);
+                    y.z = fmaf(pv[k].z, f, y.z), y.w = fmaf(pv[k].w, f, y.w);
+                }
+            }
+        }
+        const float inv = sum != 0.0f ? L_FACTOR / sum : 0.0f;
+        int64_t at, row;
+        out(r, at, row);
+        if (d < P.dim) {
+            store_typed(P.y, at + d, P.y_type, y.x * inv);
+            store_typed(P.y, at + d + 1, P.y_type, y.y * inv);
+            store_typed(P.y, at + d + 2, P.y_type, y.z * inv);
+            store_typed(P.y, at + d + 3, P.y_type, y.w * inv);
+        }
+        if (P.lse && d == 0) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + BACK) * LN2 : -INFINITY;
+    }
 }
 
 template <int DP, int NB, bool HL>
@@ -261,96 +411,14 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
     pdl_wait();
     pdl_trigger();
 
-    // Where this CTA's share of the tiles begins.  Every warp finds it by itself:
-    // nobody waits for a barrier in the first microseconds, which a small call is made of.
-    const int share = (P.B + 31) / 32;
-    long long sum = 0;
-    for (int b = lane * share; b < min(P.B, (lane + 1) * share); ++b) {
-        Seq s;
-        if (!load_seq<R>(P, b, s)) atomicOr(P.status, STATUS_INDEX);
-        sum += s.units * s.tiles;
-    }
-    long long before = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
-    }
-    const long long W = __shfl_sync(0xffffffffu, before, 31);
-    before -= sum;
-    if (W == 0) return;
-    const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), max(1ll, W / LEAST)));
-    const int cta = blockIdx.x;
-    if (cta >= blocks) return;
-    const long long t1 = divide((cta + 1) * W, blocks);
     Walk w;
-    w.t = divide(cta * W, blocks);
-    {
-        const int from = __ffs(__ballot_sync(0xffffffffu, before <= w.t && w.t < before + sum)) - 1;
-        w.b = from * share;
-        w.seq0 = __shfl_sync(0xffffffffu, before, from);
-        for (;; ++w.b) {
-            load_seq<R>(P, w.b, w.s);
-            if (w.t < w.seq0 + w.s.units * w.s.tiles) break;
-            w.seq0 += w.s.units * w.s.tiles;
-        }
-        w.unit = divide(w.t - w.seq0, w.s.tiles);
-        w.tile = static_cast<int>((w.t - w.seq0) - w.unit * w.s.tiles);
-        if (w.tile && w.s.tiles <= SHORT) advance<R>(P, w, w.s.tiles - w.tile, t1);
-    }
+    long long t1, W;
+    int blocks;
+    if (!begin_walk<R>(P, lane, w, t1, W, blocks)) return;
     __syncthreads();  // (the barriers are ready)
 
     if (warp == 8) {
-        // ---- copies ----
-        const int pages = TILE / P.page;  // of a tile
-        const uint32_t box = static_cast<uint32_t>(P.page) * C::ROW;
-        const int stop = cta == 0 ? P.stop : NO_STOP;
-        int it = 0;
-        bool ok = true;
-        while (ok && w.t < t1) {
-            const Span u = span_of<R>(P, w, t1);
-            const int32_t *tab = P.table + static_cast<int64_t>(w.b) * P.ld_table;
-            auto page_of = [&](int j) {  // of lane's page of tile j, -1 where there is nothing to read
-                const int tok = w.s.lo + j * TILE + lane * P.page;
-                int id = -1;
-                if (lane < pages && j < u.je && tok < u.hi && tok + P.page > u.lo) {
-                    id = __ldg(tab + tok / P.page);
-                    if (id < 0 || id >= P.pages) {
-                        atomicOr(P.status, STATUS_INDEX);
-                        id = -1;
-                    }
-                }
-                return id;
-            };
-            int id = page_of(u.jb);
-            for (int j = u.jb; j < u.je; ++j, ++it) {
-                const int64_t tile = static_cast<int64_t>(max(id, 0)) * P.heads + u.head;
-                const float ks = __ldg(P.scales[0] + tile), vs = __ldg(P.scales[1] + tile);
-                const int next = page_of(j + 1);
-                const int s = it % STAGES;
-                if (it >= stop) ok = false;
-                if (ok && it >= STAGES) ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * s, ((it / STAGES) - 1) & 1, P.status));
-                if (!ok) break;
-                const int src = 16 * lane / P.page;  // scales of the groups of 16 tokens
-                const float kg = __shfl_sync(0xffffffffu, ks, src), vg = __shfl_sync(0xffffffffu, vs, src);
-                if (lane < 8) sc[16 * s + lane] = kg, sc[16 * s + 8 + lane] = fmaxf(vg, 0x1p-100f);
-                const uint32_t live = __popc(__ballot_sync(0xffffffffu, id >= 0));
-                if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * C::COLS * live * box);
-                __syncwarp();
-                if (id >= 0) {
-                    const uint32_t dst = base + s * C::STAGE + lane * box;
-#pragma unroll
-                    for (int k = 0; k < C::COLS; ++k) {
-                        tma_page(dst + k * TILE * 128, &tmK, 128 * k, static_cast<int>(tile), full + 8 * s);
-                        tma_page(dst + C::SIDE + k * TILE * 128, &tmV, 128 * k, static_cast<int>(tile), full + 8 * s);
-                    }
-                }
-                id = next;
-            }
-            advance<R>(P, w, u.nt, t1);
-        }
-        // no CTA ends with copies in flight
-        for (int i = max(0, it - STAGES); i < it; ++i) mbar_wait(full + 8 * (i % STAGES), (i / STAGES) & 1, P.status);
+        copy_tiles<C>(P, tmK, tmV, w, t1, blockIdx.x == 0 ? P.stop : NO_STOP, base, sc, full, empty, lane);
         return;
     }
 
@@ -483,8 +551,8 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
                 }
             }
             const int tok = tok0 + 16 * warp + g;  // this lane's tokens: tok, tok + 8
-            const float ks = sc[slot * 16 + warp], vs = sc[slot * 16 + 8 + warp];
-            const float lv = log2f(vs), iv = __fdiv_rn(1.0f, vs);
+            const float *const scales = sc + SCALES * slot + warp;
+            const float ks = scales[0], lv = scales[8], iv = scales[16];
             uint32_t hidden = 0;  // bit 4 n + i: x[n][i] is masked
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
@@ -666,7 +734,6 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
             at = (static_cast<int64_t>(s.row0) + i) * P.ldy_t + static_cast<int64_t>(h) * P.ldy_h;
             row = (static_cast<int64_t>(s.row0) + i) * P.heads * P.group + h;
         };
-        constexpr float LN2 = 0.6931471805599453f, BACK = 20.0f - P_SHIFT;
         if (u.nt == s.tiles) {
 #pragma unroll
             for (int n = 0; n < NB; ++n)
@@ -691,7 +758,7 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
                 }
         } else {
             // a part of a unit: [row][dim] sums relative to m, then m and l
-            float *const mine = P.part + (static_cast<int64_t>(cta) * 2 + (w.tile == 0)) * C::PART;
+            float *const mine = P.part + (static_cast<int64_t>(blockIdx.x) * 2 + (w.tile == 0)) * C::PART;
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -716,49 +783,7 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
             if (*arrived == static_cast<unsigned>(c1 - c0)) {
                 if (tid == 0) P.count[c0] = 0u;  // zero again for the next launch
                 __threadfence();
-                // the last one joins them, in their order, eight at a time on their way
-                for (int i = tid; i < rows * (DP / 4); i += THREADS) {
-                    const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
-                    float top = -INFINITY, sum = 0.0f;
-                    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int k0 = c0; k0 <= c1; k0 += 8) {
-                        float pm[8], pl[8];
-                        float4 pv[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int cc = min(k0 + k, c1);
-                            const float *q = P.part + (static_cast<int64_t>(cc) * 2 + (cc == c0)) * C::PART;
-                            pm[k] = __ldcg(q + R * DP + r);
-                            pl[k] = __ldcg(q + R * DP + R + r);
-                            pv[k] = __ldcg(reinterpret_cast<const float4 *>(q + r * DP + d));
-                        }
-                        float now = top;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) now = fmaxf(now, pm[k]);
-                        const float ref = now == -INFINITY ? 0.0f : now, down = ex2(top - ref);
-                        top = now;
-                        sum *= down, y.x *= down, y.y *= down, y.z *= down, y.w *= down;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float f = k0 + k <= c1 ? ex2(pm[k] - ref) : 0.0f;
-                            if (k0 + k <= c1) {
-                                sum = fmaf(pl[k], f, sum);
-                                y.x = fmaf(pv[k].x, f, y.x), y.y = fmaf(pv[k].y, f, y.y);
-                                y.z = fmaf(pv[k].z, f, y.z), y.w = fmaf(pv[k].w, f, y.w);
-                            }
-                        }
-                    }
-                    const float inv = sum != 0.0f ? L_FACTOR / sum : 0.0f;
-                    int64_t at, row;
-                    out(r, at, row);
-                    if (d < P.dim) {
-                        store_typed(P.y, at + d, P.y_type, y.x * inv);
-                        store_typed(P.y, at + d + 1, P.y_type, y.y * inv);
-                        store_typed(P.y, at + d + 2, P.y_type, y.z * inv);
-                        store_typed(P.y, at + d + 3, P.y_type, y.w * inv);
-                    }
-                    if (P.lse && d == 0) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + BACK) * LN2 : -INFINITY;
-                }
+                join_parts<C, DP>(P, c0, c1, rows, tid, out);
             }
         }
         advance<R>(P, w, u.nt, t1);
@@ -808,6 +833,9 @@ cudaError_t launch_few_dp(const AttnParams &p, int nb, bool hl, cudaStream_t st,
 // 128 values; cudaErrorNotSupported where the build gave it too few registers.
 size_t tc_part_bytes(int dim, int num_sms);
 cudaError_t launch_tc(const AttnParams &a, cudaStream_t st, int num_sms, int dev);
+// The kernel for many fp32 rows (kv_attention_rows.cu).
+size_t rows_part_bytes(int dim, int num_sms);
+cudaError_t launch_rows(const AttnParams &a, cudaStream_t st, int num_sms, int dev);
 
 cudaError_t launch_few_64(const AttnParams &p, int nb, bool hl, cudaStream_t st, int num_sms, int dev);
 cudaError_t launch_few_128(const AttnParams &p, int nb, bool hl, cudaStream_t st, int num_sms, int dev);

@@ -124,10 +124,12 @@ def test_rows_go_to_the_other_kernel_where_the_compiler_gave_too_few_registers(t
 def names(n):
     log()
     fake.fake_registers(n)
-    assert attend(off=A, T=600) == 0, L.qmm_last_error()
+    assert attend(off=A, T=600) == 0 and attend(off=A, T=600, t=0) == 0, L.qmm_last_error()
     return [e[2] for e in log('launch')]
-assert 'kv_attention_kernel' in names(64)[0]
-assert 'kv_attention_tc' in names(80)[0] and 'kv_attention_tc' in names(0)[0]
+assert all('kv_attention_kernel' in n for n in names(64))
+assert 'kv_attention_tc' in names(80)[0] and 'kv_attention_kernel' in names(80)[1]
+for n in (0, 168):
+    assert 'kv_attention_tc' in names(n)[0] and 'kv_attention_rows' in names(n)[1]
 """)
 
 
