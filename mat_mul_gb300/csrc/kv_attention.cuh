@@ -42,7 +42,7 @@ constexpr float P_SHIFT = 14.0f;
 // and one on the sum of p' / sv, which then stays within fp32 for 2^31 tokens
 // of any scale from 2^-100 to 2^120
 constexpr float L_FACTOR = 0x1p-20f;
-constexpr float LN2 = 0.6931471805599453f, BACK = 20.0f - P_SHIFT;  // of log2 of the sum as it is held
+constexpr float LN2 = 0.6931471805599453f;
 
 struct AttnParams {
     const uint8_t *codes[2];
@@ -169,6 +169,7 @@ __device__ __forceinline__ void store_typed(void *p, int64_t i, int type, float 
 template <int DP, int NB, bool HL>
 struct Few {
     static constexpr int R = 8 * NB, PARTS = HL ? 2 : 1, CONSUMERS = THREADS;
+    static constexpr float SHIFT = P_SHIFT;
     static constexpr int CTAS = DP == 256 ? 1 : 2;  // per multiprocessor
     static constexpr int STAGES = DP == 64 ? 4 : DP == 128 && NB * PARTS <= 2 ? 3 : 2;  // (two CTAs per multiprocessor up to 128)
     static constexpr int ROW = DP == 64 ? 64 : 128, COLS = DP / ROW;  // bytes of a row of a box, boxes side by side
@@ -378,7 +379,7 @@ __device__ __forceinline__ void join_parts(const AttnParams &P, int c0, int c1, 
             store_typed(P.y, at + d + 2, P.y_type, y.z * inv);
             store_typed(P.y, at + d + 3, P.y_type, y.w * inv);
         }
-        if (P.lse && d == 0) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + BACK) * LN2 : -INFINITY;
+        if (P.lse && d == 0) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + 20.0f - C::SHIFT) * LN2 : -INFINITY;
     }
 }
 
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
                             }
                         }
                     }
-                    if (P.lse && warp == 0 && g == 0) P.lse[row] = l[n][h] != 0.0f ? (m[n][h] + log2f(l[n][h]) + BACK) * LN2 : -INFINITY;
+                    if (P.lse && warp == 0 && g == 0) P.lse[row] = l[n][h] != 0.0f ? (m[n][h] + log2f(l[n][h]) + 20.0f - C::SHIFT) * LN2 : -INFINITY;
                 }
         } else {
             // a part of a unit: [row][dim] sums relative to m, then m and l
@@ -833,6 +834,8 @@ cudaError_t launch_few_dp(const AttnParams &p, int nb, bool hl, cudaStream_t st,
 // 128 values; cudaErrorNotSupported where the build gave it too few registers.
 size_t tc_part_bytes(int dim, int num_sms);
 cudaError_t launch_tc(const AttnParams &a, cudaStream_t st, int num_sms, int dev);
+// The kernel for few 16-bit rows, at most 32 of a sequence and cache head on the average (kv_attention_slim.cu).
+cudaError_t launch_slim(const AttnParams &a, int rows, cudaStream_t st, int num_sms, int dev);
 // The kernel for many fp32 rows (kv_attention_rows.cu).
 size_t rows_part_bytes(int dim, int num_sms);
 cudaError_t launch_rows(const AttnParams &a, cudaStream_t st, int num_sms, int dev);

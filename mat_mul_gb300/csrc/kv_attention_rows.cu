@@ -39,6 +39,7 @@ constexpr int TS = TILE / 16;  // groups of 16 tokens of a tile
 template <int DP>
 struct Rows {
     static constexpr int R = 16 * WARPS, CONSUMERS = 32 * WARPS, STAGES = 4;
+    static constexpr float SHIFT = P_SHIFT;
     static constexpr int ROW = DP == 64 ? 64 : 128, COLS = DP / ROW;
     static constexpr int SIDE = TILE * DP, STAGE = 2 * SIDE;
     static constexpr int OFF_Q = STAGES * STAGE, Q_WARP = DP / 16 * 1024;  // [WARPS][DP / 16][part][lane] fragments
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1)
                 }
             }
             if (!entire && c == 0) mine[R * DP + r] = m[h], mine[R * (DP + 1) + r] = l[h];
-            if (entire && P.lse && c == 0) P.lse[row] = l[h] != 0.0f ? (m[h] + log2f(l[h]) + BACK) * LN2 : -INFINITY;
+            if (entire && P.lse && c == 0) P.lse[row] = l[h] != 0.0f ? (m[h] + log2f(l[h]) + 20.0f - C::SHIFT) * LN2 : -INFINITY;
         }
         if (!entire) {
             __threadfence();

@@ -338,9 +338,9 @@ def test_append_refused_on_the_device(cuda_lib):
 # attention
 # ---------------------------------------------------------------------------
 def _attend(q, rng, new, lengths, page, heads, group, dim, dtype, out=None, causal=True, window=0, scale=None, spread=3,
-            single=None, qscale=1.0):
+            single=None, qscale=1.0, width=0):
     import torch
-    batch = R.Batch(rng, new, lengths, page)
+    batch = R.Batch(rng, new, lengths, page, width=width)
     cache, codes, scales = _cache(q, rng, batch, heads, dim, spread)
     x, xv = _as(qscale * rng.standard_normal((batch.T, heads * group, dim)), dtype)
     single = all(n == 1 for n in new) if single is None else single
@@ -387,6 +387,21 @@ def test_rows(cuda_lib, dtype, page, heads, group, dim, new, lengths, window):
     _attend(cuda_lib, np.random.default_rng(dim + len(new)), new, lengths, page, heads, group, dim, dtype, window=window)
 
 
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("page,heads,group,dim,new,lengths,window", [
+    (64, 2, 4, 128, [3, 4, 0, 3], [3000, 650, 40, 3], 0), (64, 2, 4, 128, [5, 8], [5000, 129], 0), (32, 3, 5, 80, [2, 3], [700, 5], 0),
+    (16, 2, 8, 64, [4, 4, 4], [90, 1000, 4], 0), (128, 1, 13, 96, [1, 1], [2000, 1], 0), (16, 2, 2, 48, [8, 8], [900, 30], 77),
+    (64, 1, 4, 16, [7, 5], [4, 2], 0), (64, 2, 1, 128, [30, 20], [300, 200], 1), (64, 2, 16, 112, [1, 1, 1], [0, 400, 16], 0)])
+def test_few_rows_of_sequences_that_may_be_long(cuda_lib, dtype, page, heads, group, dim, new, lengths, window):
+    """9 to 32 rows per cache head, tables of many pages."""
+    width = -(-8 * 160 * 128 // (len(new) * heads * page)) + 1
+    for scale, qscale in ((None, 1.0), (-0.2, 3.0)):
+        _attend(cuda_lib, np.random.default_rng(dim + len(new)), new, lengths, page, heads, group, dim, dtype, window=window,
+                width=width, scale=scale, qscale=qscale)
+    if not window:
+        _attend(cuda_lib, np.random.default_rng(3), new, lengths, page, heads, group, dim, dtype, causal=False, width=width, spread=20)
+
+
 @pytest.mark.parametrize("dtype,out", [("float32", "bfloat16"), ("bfloat16", "float32"), ("float16", "bfloat16")])
 def test_attention_result_types_scale_and_all_tokens(cuda_lib, dtype, out):
     rng = np.random.default_rng(1)
@@ -412,8 +427,9 @@ def test_nan_in_the_values_of_a_masked_token(cuda_lib):
     import torch
     q = cuda_lib
     rng = np.random.default_rng(12)
-    for dtype, new, window in (("float32", 40, 0), ("bfloat16", 3, 0), ("bfloat16", 200, 0), ("float16", 200, 50), ("bfloat16", 200, 50)):
-        batch = R.Batch(rng, [new, new], [300, 260], 64)
+    for dtype, new, window, width in (("float32", 40, 0, 0), ("bfloat16", 3, 0, 0), ("bfloat16", 200, 0, 0), ("float16", 200, 50, 0),
+                                      ("bfloat16", 200, 50, 0), ("bfloat16", 10, 0, 700), ("float16", 6, 0, 700), ("float32", 10, 0, 700)):
+        batch = R.Batch(rng, [new, new], [300, 260], 64, width=width)
         cache, codes, scales = _cache(q, rng, batch, 2, 64)
         x = _as(rng.standard_normal((batch.T, 4, 64)), dtype)[0]
         args = (x, _t(batch.table), _t(np.array(batch.lengths, np.int32)), _t(batch.offsets))
@@ -464,14 +480,14 @@ def test_one_large_query_value_leaves_the_others_theirs(cuda_lib, dtype, new):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("new", [1, 200])
-def test_nan_and_infinities_in_queries_and_keys(cuda_lib, dtype, new):
+@pytest.mark.parametrize("new,width", [(1, 0), (200, 0), (6, 700)])
+def test_nan_and_infinities_in_queries_and_keys(cuda_lib, dtype, new, width):
     """In a head's query: its results are NaN (also where every score is -inf).  In a key: those of the rows that see the
     token.  All others are as they should be."""
     q = cuda_lib
     rng = np.random.default_rng(62)
     H, D, lengths = 2, 64, [500, 300]
-    batch = R.Batch(rng, [new, new], lengths, 64)
+    batch = R.Batch(rng, [new, new], lengths, 64, width=width)
     cache, codes, scales = _cache(q, rng, batch, H, D)
     codes[0][..., 7] = 0x38                       # 1, so that one infinite query value decides all scores
     at = 300 - new // 2 - 1                       # of the second sequence: seen by half of its rows (by its only one)

@@ -110,7 +110,7 @@ def test_captured_and_replayed_with_other_lengths(cuda_lib, dtype, rows):
         assert np.array_equal(_u8(cache.k), _u8(other.k)) and torch.equal(cache.v_scale, other.v_scale)
 
 
-@pytest.mark.parametrize("new,lengths", [([1, 1], [5000, 3000]), ([200, 150], [900, 2000])])
+@pytest.mark.parametrize("new,lengths", [([1, 1], [5000, 3000]), ([200, 150], [900, 2000]), ([4, 4], [30000, 29000])])
 def test_two_graphs_of_one_stream_at_once(cuda_lib, new, lengths):
     """Graphs captured on one stream and replayed on two at the same time: each has its partial results to itself."""
     import torch
@@ -284,7 +284,7 @@ def test_many_sequences(cuda_lib):
     assert q.qmm_device_status() == 0
 
 
-@pytest.mark.parametrize("dtype,new,length", [("bfloat16", 1, 60000), ("float32", 20, 9000), ("bfloat16", 300, 60000), ("float16", 300, 60000)])
+@pytest.mark.parametrize("dtype,new,length", [("bfloat16", 1, 60000), ("bfloat16", 10, 60000), ("float32", 20, 9000), ("float32", 3, 60000), ("bfloat16", 300, 60000), ("float16", 300, 60000)])
 def test_expired_wait_is_reported_and_the_next_call_is_right(cuda_lib, dtype, new, length):
     """The copies of the first block stop after one tile: the waits for the next one run out, the kernel says so, frees
     what it holds and returns; the next call finds everything in order."""
@@ -308,7 +308,8 @@ def test_repeated_calls_agree_bit_for_bit(cuda_lib):
     import torch
     q = cuda_lib
     rng = np.random.default_rng(28)
-    for dtype, new, lengths in (("bfloat16", [1, 1], [20000, 7]), ("bfloat16", [300, 100], [3000, 100]), ("float32", [9], [5000])):
+    for dtype, new, lengths in (("bfloat16", [1, 1], [20000, 7]), ("bfloat16", [300, 100], [3000, 100]), ("float32", [9], [5000]),
+                                ("bfloat16", [5], [90000]), ("float16", [3, 4], [50000, 40000]), ("float32", [99], [3000])):
         batch, cache, _, _, x, _ = _problem(q, rng, new, lengths, dtype=dtype, page=64, H=2, G=4, D=128)
         args = (x, _t(batch.table), _i32(lengths))
         off = None if new == [1, 1] else _t(batch.offsets)

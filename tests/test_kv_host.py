@@ -111,7 +111,8 @@ for xt in range(3):
                     assert append(c=cache(page=page, dim=dim), t=xt, off=off, T=T, r=table(rot), qp=qp, kb=dim, vb=dim, qb=dim, ob=dim, oa=8 * dim) == 0
     for dim in (48, 64, 96, 128, 144, 256):
         for T in (3, 18, 45, 200):
-            assert attend(c=cache(dim=dim), t=xt, off=A, T=T, xb=dim, yb=dim, Hq=4 if T == 3 else 8, xa=2048, ya=2048) == 0
+            for width in (8, 400):
+                assert attend(c=cache(dim=dim), t=xt, off=A, T=T, xb=dim, yb=dim, Hq=4 if T == 3 else 8, xa=2048, ya=2048, width=width, ld=width) == 0
 launched = {e[2] for e in log('launch')}
 mine = {k for k in kernels() if 'kv_' in k or 'rope_' in k}
 assert len(mine) > 50 and launched <= set(kernels())
@@ -126,6 +127,10 @@ def names(n):
     fake.fake_registers(n)
     assert attend(off=A, T=600) == 0 and attend(off=A, T=600, t=0) == 0, L.qmm_last_error()
     return [e[2] for e in log('launch')]
+fake.fake_registers(64)
+assert attend(off=A, T=18, width=400, ld=400) == 0 and 'kv_attention_kernel' in log('launch')[-1][2]
+fake.fake_registers(168)
+assert attend(off=A, T=18, width=400, ld=400) == 0 and 'kv_attention_slim' in log('launch')[-1][2]
 assert all('kv_attention_kernel' in n for n in names(64))
 assert 'kv_attention_tc' in names(80)[0] and 'kv_attention_kernel' in names(80)[1]
 for n in (0, 168):
