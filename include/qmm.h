@@ -521,7 +521,8 @@ QMM_API int qmm_kv_append(const qmm_kv_append_args *args, void *stream);
  * key in all of them.
  * y must not be q, nor overlap it.  How a sequence's tokens are shared out, and with
  * it the last bits of its rows, depends on the other sequences of the call.
- * Scales are positive and finite; value scales below 2^-100 count as 2^-100.
+ * Scales are positive and finite; value scales below 2^-100 count as 2^-100, and
+ * above 2^112 the sums of probabilities lose bits for 16-bit queries.
  * scratch null: partial results go to the per-(device, stream) workspace (make
  * one call of the largest size before capture, and replay graphs that were
  * captured on one stream one after another).  Otherwise to scratch, device

@@ -30,8 +30,8 @@ bool many_rows(const KvAttention &a) {
 // over 1024, 4096, 16384 tokens 22.4, 46, 115 against 26.7, 37, 87 us, 12 rows over 4096 30.5
 // against 26.2; 4 rows, 64 sequences of 4096 tokens, 94 against 114.
 bool slim_rows(const KvAttention &a, int num_sms) {
-    const int64_t tiles = int64_t(a.batch.width) * a.c.page / kv::TILE * a.batch.B * a.c.heads;
-    return a.q.type != QMM_F32 && a.c.dim <= 128 && row_groups(a) > 1 && tiles >= 8 * int64_t(num_sms);
+    const double tiles = double(a.batch.width) * a.c.page / kv::TILE * a.batch.B * a.c.heads;
+    return a.q.type != QMM_F32 && a.c.dim <= 128 && row_groups(a) > 1 && tiles >= 8.0 * num_sms;
 }
 
 int padded_dim(const KvAttention &a) { return a.c.dim <= 64 ? 64 : a.c.dim <= 128 ? 128 : 256; }

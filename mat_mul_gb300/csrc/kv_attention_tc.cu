@@ -903,7 +903,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                                 add2(s2, s3, c, d);
                             }
                             if (i2 < 2) tmem_ld16(my_s + 16 * i2, s[i2 & 1]);
-                            l = fmaf((s0 + s1) + (s2 + s3), ex2(-20.0f - lv[h]), l);  // (L_FACTOR / the values' scale)
+                            l = fmaf(((s0 + s1) + (s2 + s3)) * L_FACTOR, ex2(-lv[h]), l);  // (over the values' scale; 2^-126 at the least)
                             if (i2 == 1 || i2 == 2) tmem_wait16(s[(i2 + 1) & 1]);
                             tmem_st8(my_s + p_column(h), p);
                         }

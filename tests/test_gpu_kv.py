@@ -421,6 +421,25 @@ def test_attention_with_scales_far_apart(cuda_lib, dtype, new):
     _attend(cuda_lib, rng, [new, new], [400, 77], 16, 2, 4, 64, dtype, qscale=50.0)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("new,width,large", [(1, 0, 112), (4, 700, 112), (70, 0, 112), (1, 0, -100), (4, 700, -100), (70, 0, -100)])
+def test_value_scales_at_the_ends_of_their_range(cuda_lib, dtype, new, width, large):
+    """Value scales of 2^112 and 2^-100, where sums of probabilities over them come near the ends of fp32."""
+    q = cuda_lib
+    rng = np.random.default_rng(63)
+    batch = R.Batch(rng, [new, new], [900, 300], 64, width=width)
+    cache, codes, scales = _cache(q, rng, batch, 2, 64)
+    scales[1][:] = 2.0 ** large
+    cache.v_scale.copy_(_t(scales[1]))
+    x, xv = _as(rng.standard_normal((batch.T, 8, 64)), dtype)
+    y, lse = q.qmm_kv_attention(cache, x, _t(batch.table), _t(np.array(batch.lengths, np.int32)), offsets=_t(batch.offsets),
+                                dtype=__import__("torch").float32, lse=True)
+    assert q.qmm_device_status() == 0
+    wy, wl, e, le = R.attention(xv, codes[0], scales[0], codes[1], scales[1], batch, 0.125)
+    _within(_np(y), wy, R.rounded(wy, e, "float32"), "y")
+    _within(_np(lse), wl, le, "lse")
+
+
 def test_nan_in_the_values_of_a_masked_token(cuda_lib):
     """A NaN among the values of a token makes the rows that see it NaN and no other, whatever tile they share; behind
     the end of a sequence, on a page that only other sequences know and outside the window it reaches nobody."""
