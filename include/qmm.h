@@ -475,8 +475,8 @@ QMM_API int qmm_rope(const qmm_rope_args *args, void *stream);
  * earlier tokens of the sequence; those tokens' codes are rounded anew when the
  * scale grows.  Codes are rounded to nearest, ties to even, from the fp32 value
  * turned (qmm_rope's accuracy); a NaN or an infinity becomes a NaN code and
- * changes no scale.  Pages that the call writes to belong to one sequence each:
- * a page shared by two of them may be read only.
+ * changes no scale.  Pages that the call writes to belong to one sequence each,
+ * and once in its table: a page in two places may be read only.
  *   k, v    : [T][heads of the cache][dim] of x_type.
  *   q       : [T][q_heads][dim] of x_type, or null; q_out may be q.  Needs rope.
  */
