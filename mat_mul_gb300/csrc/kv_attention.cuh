@@ -24,6 +24,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "kv_device.cuh"
 #include "qmm_internal.h"
 
@@ -162,6 +164,15 @@ __device__ __forceinline__ void store_typed(void *p, int64_t i, int type, float 
     if (type == QMM_F32) static_cast<float *>(p)[i] = v;
     else if (type == QMM_F16) static_cast<__half *>(p)[i] = __float2half_rn(v);
     else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// A query value as it lies in memory, and as fp32.  (A load with its conversion inside a
+// branch by type waits for its value: 16 of them one after another took 7300 cycles.)
+template <bool F32>
+using QueryRaw = typename std::conditional<F32, float, uint16_t>::type;
+__device__ __forceinline__ float query_value(float v, int) { return v; }
+__device__ __forceinline__ float query_value(uint16_t v, int type) {
+    return type == QMM_F16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(static_cast<uint32_t>(v) << 16);
 }
 
 // DP: dim rounded up to 64, 128 or 256; NB: groups of eight query rows of a
@@ -431,22 +442,22 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
 
         // queries: one warp per row, times a power of two that brings the largest to [2^13, 2^14)
         // (the last unit's barriers lie between its reading of them and this)
-        float v[NB][DP / 32];
+        QueryRaw<HL> raw[NB][DP / 32];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             const int qr = r0 + min(warp + 8 * n, rows - 1), i = token_of(P, qr);
             const int64_t at = (static_cast<int64_t>(s.row0) + i) * P.ldq_t + static_cast<int64_t>(head * P.group + (qr - i * P.group)) * P.ldq_h;
 #pragma unroll
-            for (int k = 0; k < DP / 32; ++k) v[n][k] = load_typed(P.q, at + min(lane + 32 * k, P.dim - 1), P.q_type);
+            for (int k = 0; k < DP / 32; ++k) raw[n][k] = __ldg(static_cast<const QueryRaw<HL> *>(P.q) + at + min(lane + 32 * k, P.dim - 1));
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             const int r = warp + 8 * n, i = token_of(P, r0 + min(r, rows - 1));
-            float top = 0.0f;
+            float v[DP / 32], top = 0.0f;
 #pragma unroll
             for (int k = 0; k < DP / 32; ++k) {
-                if (r >= rows || lane + 32 * k >= P.dim) v[n][k] = 0.0f;
-                const float a = fabsf(v[n][k]);
+                v[k] = r >= rows || lane + 32 * k >= P.dim ? 0.0f : query_value(raw[n][k], P.q_type);
+                const float a = fabsf(v[k]);
                 top = a <= 3.402823466e38f ? fmaxf(top, a) : top;
             }
 #pragma unroll
@@ -456,7 +467,7 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
             const float up = pow2f(e);
 #pragma unroll
             for (int k = 0; k < DP / 32; ++k) {
-                const float x = v[n][k] * up + (v[n][k] - v[n][k]);  // (an infinity as NaN: its scores may all be -inf, as if nothing was seen)
+                const float x = v[k] * up + (v[k] - v[k]);  // (an infinity as NaN: its scores may all be -inf, as if nothing was seen)
                 const __half h = __float2half_rn(x);
                 sq[r * C::QP + lane + 32 * k] = h;
                 if constexpr (HL) sq[(R + r) * C::QP + lane + 32 * k] = __float2half_rn(x - __half2float(h));

@@ -110,22 +110,22 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
 
         // queries: one warp per row, times a power of two that brings the largest to [2^13, 2^14)
         // (the last unit's barriers lie between its reading of them and this)
-        float v[2 * MT][DP / 32];
+        QueryRaw<false> raw[2 * MT][DP / 32];
 #pragma unroll
         for (int n = 0; n < 2 * MT; ++n) {
             const int qr = r0 + min(warp + 8 * n, rows - 1), i = token_of(P, qr);
             const int64_t at = (static_cast<int64_t>(s.row0) + i) * P.ldq_t + static_cast<int64_t>(head * P.group + (qr - i * P.group)) * P.ldq_h;
 #pragma unroll
-            for (int k = 0; k < DP / 32; ++k) v[n][k] = load_typed(P.q, at + min(lane + 32 * k, P.dim - 1), P.q_type);
+            for (int k = 0; k < DP / 32; ++k) raw[n][k] = __ldg(static_cast<const QueryRaw<false> *>(P.q) + at + min(lane + 32 * k, P.dim - 1));
         }
 #pragma unroll
         for (int n = 0; n < 2 * MT; ++n) {
             const int r = warp + 8 * n, i = token_of(P, r0 + min(r, rows - 1));
-            float top = 0.0f;
+            float v[DP / 32], top = 0.0f;
 #pragma unroll
             for (int k = 0; k < DP / 32; ++k) {
-                if (r >= rows || lane + 32 * k >= P.dim) v[n][k] = 0.0f;
-                const float a = fabsf(v[n][k]);
+                v[k] = r >= rows || lane + 32 * k >= P.dim ? 0.0f : query_value(raw[n][k], P.q_type);
+                const float a = fabsf(v[k]);
                 top = a <= 3.402823466e38f ? fmaxf(top, a) : top;
             }
 #pragma unroll
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
             for (int k = 0; k < DP / 32; ++k) {
                 // value d of row r: of fragment d / 16, lane 4 (r % 8) + d % 16 / 4, word 2 (d % 4 / 2) + r % 16 / 8
                 const int d = lane + 32 * k;
-                const float x = v[n][k] * up + (v[n][k] - v[n][k]);  // (an infinity as NaN)
+                const float x = v[k] * up + (v[k] - v[k]);  // (an infinity as NaN)
                 sq[(((n >> 1) * KS + (d >> 4)) * 32 + 4 * warp + (d >> 2 & 3)) * 8 + 4 * (d >> 1 & 1) + 2 * (n & 1) + (d & 1)] = __float2half_rn(x);
             }
             if (lane == 0) {
