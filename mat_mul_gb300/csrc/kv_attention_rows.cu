@@ -518,17 +518,12 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1)
             if (entire && P.lse && c == 0) P.lse[row] = l[h] != 0.0f ? (m[h] + log2f(l[h]) + 20.0f - C::SHIFT) * LN2 : -INFINITY;
         }
         if (!entire) {
-            __threadfence();
             named_barrier(1, C::CONSUMERS);
             // the CTAs of the unit's first and last tile
             const int c0 = static_cast<int>(divide((w.u0 + 1) * blocks - 1, W)), c1 = static_cast<int>(divide((w.u0 + w.tiles) * blocks - 1, W));
-            if (tid == 0) *arrived = atomicAdd(P.count + c0, 1u);
+            if (tid == 0) *arrived = arrive(P.count + c0, static_cast<unsigned>(c1 - c0));
             named_barrier(1, C::CONSUMERS);
-            if (*arrived == static_cast<unsigned>(c1 - c0)) {
-                if (tid == 0) P.count[c0] = 0u;  // zero again for the next launch
-                __threadfence();
-                join_parts<C, DP>(P, c0, c1, rows, tid, out);
-            }
+            if (*arrived == static_cast<unsigned>(c1 - c0)) join_parts<C, DP>(P, c0, c1, rows, tid, out);
         }
         advance<R>(P, w, u.nt, t1);
     }

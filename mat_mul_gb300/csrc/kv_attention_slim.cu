@@ -375,19 +375,14 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
                 }
                 if (P.lse && d == 0) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + 20.0f - C::SHIFT) * LN2 : -INFINITY;
             }
-            if (!entire && t == MT - 1) __threadfence();
             named_barrier(1, THREADS);
         }
         if (!entire) {
             const long long u0 = w.seq0 + w.unit * s.tiles, u1 = u0 + s.tiles - 1;  // first and last tile of the unit
             const int c0 = static_cast<int>(divide((u0 + 1) * blocks - 1, W)), c1 = static_cast<int>(divide((u1 + 1) * blocks - 1, W));
-            if (tid == 0) *arrived = atomicAdd(P.count + c0, 1u);
+            if (tid == 0) *arrived = arrive(P.count + c0, static_cast<unsigned>(c1 - c0));
             named_barrier(1, THREADS);
-            if (*arrived == static_cast<unsigned>(c1 - c0)) {
-                if (tid == 0) P.count[c0] = 0u;  // zero again for the next launch
-                __threadfence();
-                join_parts<C, DP>(P, c0, c1, rows, tid, out);
-            }
+            if (*arrived == static_cast<unsigned>(c1 - c0)) join_parts<C, DP>(P, c0, c1, rows, tid, out);
         }
         advance<R>(P, w, u.nt, t1);
     }
