@@ -520,7 +520,8 @@ QMM_API int qmm_kv_append(const qmm_kv_append_args *args, void *stream);
  * code those of the rows that see its token: of a value in its own element, of a
  * key in all of them.
  * y must not be q, nor overlap it.  How a sequence's tokens are shared out, and with
- * it the last bits of its rows, depends on the other sequences of the call.
+ * it the last bits of its rows, depends on the other sequences of the call and on the
+ * width of the table.
  * Scales are positive and finite; value scales below 2^-100 count as 2^-100, and
  * above 2^112 the sums of probabilities lose bits for 16-bit queries.
  * scratch null: partial results go to the per-(device, stream) workspace (make
