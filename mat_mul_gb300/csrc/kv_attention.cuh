@@ -327,6 +327,7 @@ __device__ __forceinline__ void copy_tiles(const AttnParams &P, const CUtensorMa
                 float *const d = sc + SCALES * s + lane;
                 d[0] = kg, d[8] = log2f(v), d[16] = __fdiv_rn(1.0f, v);
             }
+            __syncwarp();  // (lane 0's arrival hands over what the eight wrote; a vote orders no memory)
             const uint32_t live = __popc(__ballot_sync(0xffffffffu, id >= 0));
             if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * C::COLS * live * box);
             __syncwarp();
