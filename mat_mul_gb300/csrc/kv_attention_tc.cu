@@ -339,6 +339,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
         share0 = first;
         before0 = pre[first];
     }
+    // (the copies of codes come to where the prefix sums were: by another proxy than these accesses)
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
