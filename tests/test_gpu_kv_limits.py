@@ -39,12 +39,12 @@ def test_every_group_of_tokens_has_the_scale_of_its_page(cuda_lib, kernel):
     batch = R.Batch(rng, [new] * 6, lengths, 16, width=width)
     cache, codes, scales = _cache(q, rng, batch, 2, 64, spread=20)
     x, xv = _as(2.0 ** -18 * rng.standard_normal((batch.T, 8, 64)), dtype)
-    y, lse = _run(q, cache, x, batch)
+    y, lse = _run(q, cache, x, batch, dtype=torch.float32)   # (fp16 ends at 65504, these do not)
     wy, wl, e, le = R.attention(xv, codes[0], scales[0], codes[1], scales[1], batch, 0.125)
-    _within(_np(y), wy, R.rounded(wy, e, dtype), "y")
+    _within(_np(y), wy, R.rounded(wy, e, "float32"), "y")
     _within(_np(lse), wl, le, "lse")
     for _ in range(50):
-        again = _run(q, cache, x, batch)
+        again = _run(q, cache, x, batch, dtype=torch.float32)
         assert torch.equal(again[0], y) and torch.equal(again[1], lse)
 
 
@@ -59,10 +59,10 @@ def test_first_tiles_come_to_where_the_shares_were_found(cuda_lib, kernel):
     batch = R.Batch(rng, [new] * 40, rng.integers(new, 129, 40).tolist(), 16)
     cache, codes, scales = _cache(q, rng, batch, 2, 64, spread=20)
     x, xv = _as(2.0 ** -18 * rng.standard_normal((batch.T, 8, 64)), dtype)
-    y, lse = _run(q, cache, x, batch)
+    y, lse = _run(q, cache, x, batch, dtype=torch.float32)   # (fp16 ends at 65504, these do not)
     wy, wl, e, le = R.attention(xv, codes[0], scales[0], codes[1], scales[1], batch, 0.125)
-    _within(_np(y), wy, R.rounded(wy, e, dtype), "y")
+    _within(_np(y), wy, R.rounded(wy, e, "float32"), "y")
     _within(_np(lse), wl, le, "lse")
     for _ in range(50):
-        again = _run(q, cache, x, batch)
+        again = _run(q, cache, x, batch, dtype=torch.float32)
         assert torch.equal(again[0], y) and torch.equal(again[1], lse)
