@@ -91,6 +91,12 @@ __device__ __forceinline__ int token_of(const AttnParams &P, int r) {
     return static_cast<int>(static_cast<uint64_t>(r) * P.div_mul >> P.div_shift);
 }
 
+// The first token that the row at position pos of its sequence sees (pos - window + 1
+// may lie below -2^31: rows before the first token, windows near 2^31).
+__device__ __forceinline__ int seen_from(const AttnParams &P, int pos) {
+    return P.window ? max(pos, P.window - 1) - (P.window - 1) : 0;
+}
+
 template <int R>
 __device__ __forceinline__ bool load_seq(const AttnParams &P, int b, Seq &s) {
     s.units = 0;
@@ -103,8 +109,7 @@ __device__ __forceinline__ bool load_seq(const AttnParams &P, int b, Seq &s) {
     s.n = hi - lo;
     s.len = len;
     if (s.n == 0) return true;
-    s.lo = 0;
-    if (P.window) s.lo = max(0, len - s.n - P.window + 1) & ~(TILE - 1);
+    s.lo = seen_from(P, len - s.n) & ~(TILE - 1);
     s.tiles = max(1, (len - s.lo + TILE - 1) / TILE);
     s.blocks = (s.n * P.group + R - 1) / R;  // (the call's rows times group are below 2^31 - R)
     s.units = static_cast<int64_t>(s.blocks) * P.heads;
@@ -239,8 +244,8 @@ __device__ __forceinline__ Span span_of(const AttnParams &P, const Walk &w, long
     const int i0 = token_of(P, u.r0), i1 = token_of(P, u.r0 + u.rows - 1);
     u.hi = P.causal ? min(s.len, start + i1 + 1) : s.len;
     u.all_hi = P.causal ? min(s.len, start + i0 + 1) : s.len;
-    u.lo = P.window ? max(0, start + i0 - P.window + 1) : 0;
-    u.all_lo = P.window ? max(0, start + i1 - P.window + 1) : 0;
+    u.lo = seen_from(P, start + i0);
+    u.all_lo = seen_from(P, start + i1);
     u.from = s.lo;
     u.jb = max(w.tile, (u.lo - s.lo) / TILE);
     u.je = min(w.tile + u.nt, u.hi > s.lo ? (u.hi - s.lo + TILE - 1) / TILE : 0);
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
                 row_f[r] = P.factor * pow2f(-e);
                 if constexpr (HL) row_f[3 * R + r] = P.factor_low * pow2f(-e);
                 row_hi[r] = P.causal ? min(s.len, start + i + 1) : s.len;
-                row_lo[r] = P.window ? start + i - P.window + 1 : 0;
+                row_lo[r] = seen_from(P, start + i);
             }
         }
         named_barrier(1, THREADS);

@@ -71,7 +71,7 @@ __device__ __forceinline__ int block_tiles(const AttnParams &P, const Seq &s, in
     const int start = s.len - s.n;
     const int i0 = token_of(P, block * R), i1 = token_of(P, min(block * R + R, s.n * P.group) - 1);
     const int hi = P.causal ? min(s.len, start + i1 + 1) : s.len;
-    from = P.window ? max(0, start + i0 - P.window + 1) & ~(TILE - 1) : 0;
+    from = seen_from(P, start + i0) & ~(TILE - 1);
     return max(1, hi > from ? (hi - from + TILE - 1) / TILE : 0);
 }
 
@@ -102,8 +102,8 @@ __device__ __forceinline__ Span span_of(const AttnParams &P, const RowWalk &w, l
     const int start = s.len - s.n, i0 = token_of(P, u.r0), i1 = token_of(P, u.r0 + u.rows - 1);
     u.hi = P.causal ? min(s.len, start + i1 + 1) : s.len;
     u.all_hi = P.causal ? min(s.len, start + i0 + 1) : s.len;
-    u.lo = P.window ? max(0, start + i0 - P.window + 1) : 0;
-    u.all_lo = P.window ? max(0, start + i1 - P.window + 1) : 0;
+    u.lo = seen_from(P, start + i0);
+    u.all_lo = seen_from(P, start + i1);
     u.from = w.from;
     u.jb = w.tile;
     u.je = u.hi > u.lo ? w.tile + u.nt : w.tile;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1)
         for (int h = 0; h < 2; ++h) {
             const int qr = r0 + min(16 * warp + g + 8 * h, rows - 1), i = token_of(P, qr);
             hi[h] = P.causal ? min(s.len, start + i + 1) : s.len;
-            lo[h] = P.window ? start + i - P.window + 1 : 0;
+            lo[h] = seen_from(P, start + i);
             const float *const q = static_cast<const float *>(P.q) + (static_cast<int64_t>(s.row0) + i) * P.ldq_t +
                                    static_cast<int64_t>(head * P.group + (qr - i * P.group)) * P.ldq_h;
             float4 v[KS];

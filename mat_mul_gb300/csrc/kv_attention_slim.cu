@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
             if (lane == 0) {
                 row_f[r] = P.factor * pow2f(-e);
                 row_hi[r] = P.causal ? min(s.len, start + i + 1) : s.len;
-                row_lo[r] = P.window ? start + i - P.window + 1 : 0;
+                row_lo[r] = seen_from(P, start + i);
             }
         }
         named_barrier(1, THREADS);

@@ -118,7 +118,7 @@ __device__ __forceinline__ bool load_pair(const AttnParams &P, int p, Pair &q) {
     const int start = len - q.n;
     const int i0 = static_cast<int>(r0 / P.group), i1 = static_cast<int>((min(r0 + UNIT, rows) - 1) / P.group);
     const int end = P.causal ? min(len, start + i1 + 1) : len;
-    const int from = P.window ? max(0, start + i0 - P.window + 1) : 0;
+    const int from = seen_from(P, start + i0);
     q.tile = from / TILE;
     q.tiles = max(1, end > from ? (end + TILE - 1) / TILE - q.tile : 0);
     return true;
@@ -381,10 +381,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
     };
     // the tokens from one on that all rows of the unit see, and the end of them
     auto all_end_of = [&](const Piece &p) { return P.causal ? min(p.len, p.len - p.n + token_of(p.r0) + 1) : p.len; };
-    auto all_from_of = [&](const Piece &p) {
-        return P.window ? p.len - p.n + token_of(p.r0 + rows_of(p) - 1) - P.window + 1 : 0;
-    };
-    auto from_of = [&](const Piece &p) { return P.window ? max(0, p.len - p.n + token_of(p.r0) - P.window + 1) : 0; };
+    auto all_from_of = [&](const Piece &p) { return seen_from(P, p.len - p.n + token_of(p.r0 + rows_of(p) - 1)); };
+    auto from_of = [&](const Piece &p) { return seen_from(P, p.len - p.n + token_of(p.r0)); };
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_A));
@@ -797,7 +795,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                 have = rows > 128 * t;
                 tile0 = pc.tile, nt = pc.nt;
                 const int start = pc.len - pc.n, i = token_of(pc.r0 + min(mine, rows - 1));
-                hi = P.causal ? min(pc.len, start + i + 1) : pc.len, lo = P.window ? start + i - P.window + 1 : 0;
+                hi = P.causal ? min(pc.len, start + i + 1) : pc.len, lo = seen_from(P, start + i);
                 all_hi = all_end_of(pc), all_lo = all_from_of(pc);
             }
             float ref = -INFINITY, l = 0.0f;

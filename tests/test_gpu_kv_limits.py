@@ -66,3 +66,102 @@ def test_first_tiles_come_to_where_the_shares_were_found(cuda_lib, kernel):
     for _ in range(50):
         again = _run(q, cache, x, batch, dtype=torch.float32)
         assert torch.equal(again[0], y) and torch.equal(again[1], lse)
+
+
+# ---------------------------------------------------------------------------
+# The formula in 64 bits and the bounds that the header gives
+# ---------------------------------------------------------------------------
+U = {"float32": 2.0 ** -20, "float16": 2.0 ** -11, "bfloat16": 2.0 ** -11}
+QUERY = {"float32": 2.0 ** -38, "float16": 2.0 ** -21, "bfloat16": 2.0 ** -21}  # of the head's largest value
+
+
+def _exact(x, dtype, codes, scales, batch, scale, causal=True, window=0, small=False):
+    """(y, lse, bound of y before its rounding, bound of lse).  small: some query values are far below the head's largest,
+    so that what they may be off counts: a score then by d = |scale| max(QUERY m, 2^-114) sum |k_ji| at most, and a
+    probability by exp(2 d) - 1 of itself.  A NaN code of a value: NaN in that element of the rows that see it."""
+    T, Hq, D = x.shape
+    H = codes[0].shape[1]
+    x = x.astype(np.float64)
+    y, ey, lse, el = np.zeros((T, Hq, D)), np.zeros((T, Hq, D)), np.full((T, Hq), -np.inf), np.zeros((T, Hq))
+    for b, (m, n) in enumerate(zip(batch.new, batch.lengths)):
+        if n == 0 or m == 0:
+            continue
+        ids = batch.table[b, :-(-n // batch.page)]
+        flat = lambda a: a.transpose(1, 0, 2, 3).reshape(H, -1, D)[:, :n]
+        K, V = (flat(R.VALUES[codes[i][ids]] * scales[i][ids].astype(np.float64)[:, :, None, None]) for i in range(2))
+        s = np.repeat(scales[1][ids].astype(np.float64), batch.page, 0)[:n]
+        nan, V = np.isnan(V), np.nan_to_num(V)
+        pos, j = np.arange(n - m, n)[:, None], np.arange(n)[None, :]
+        seen = (j <= pos) & ((j > pos - window) if window else True) if causal else np.ones((m, n), bool)
+        rows, some, count = slice(batch.offsets[b], batch.offsets[b + 1]), seen.any(axis=1), seen.sum(axis=1)
+        for h in range(Hq):
+            g, Q = h // (Hq // H), x[rows, h]
+            z = np.where(seen, scale * (Q @ K[g].T), -np.inf)
+            X = np.where(seen, abs(scale) * (np.abs(Q) @ np.abs(K[g]).T), 0).max(axis=1)
+            top = np.where(some, z.max(axis=1), 0)
+            p = np.exp(z - top[:, None])
+            total = np.where(some, p.sum(axis=1), 1)
+            p /= total[:, None]
+            c = (count + (D + 64) * (1 + X)) * 2.0 ** -22
+            if small:
+                off = np.maximum(QUERY[dtype] * np.abs(Q).max(axis=1), 2.0 ** -114)
+                c = c + np.expm1(2 * abs(scale) * off * np.where(seen, np.abs(K[g]).sum(axis=1), 0).max(axis=1))
+            y[rows, h] = np.where((seen.astype(np.float64) @ nan[g]) > 0, np.nan, p @ V[g])
+            ey[rows, h] = (U[dtype] + c)[:, None] * (p @ np.abs(V[g])) + (count * 2.0 ** -22 * (p * s[:, g]).max(axis=1))[:, None]
+            lse[rows, h] = np.where(some, top + np.log(total), -np.inf)
+            el[rows, h] = c + 2.0 ** -22 * np.where(some, np.abs(lse[rows, h]), 0)
+    return y, lse, ey, el
+
+
+def _against(q, cache, codes, scales, batch, x, xv, dtype, scale=0.125, small=False, **k):
+    """The call with fp32 results against _exact."""
+    import torch
+    got = _run(q, cache, x, batch, scale=scale, dtype=torch.float32, **k)
+    wy, wl, ey, el = _exact(xv, dtype, codes, scales, batch, scale, small=small, **k)
+    _within(_np(got[0]), wy, R.rounded(wy, ey, "float32"), "y")
+    _within(_np(got[1]), wl, el, "lse")
+    return got
+
+
+def _put(cache, codes, scales):
+    import torch
+    for t, a in zip((cache.k, cache.v), codes):
+        t.view(torch.uint8).copy_(_t(a))
+    for t, a in zip((cache.k_scale, cache.v_scale), scales):
+        t.copy_(_t(a.astype(np.float32)))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_windows_near_the_end_of_32_bits(cuda_lib, kernel):
+    """A window of 2^31 - 1 is none, also where a sequence has more rows than tokens."""
+    import torch
+    q = cuda_lib
+    dtype, new, width = KERNELS[kernel]
+    new = max(new, 8)
+    rng = np.random.default_rng(72)
+    for n, lengths in (([new] * 6, [new - 3] * 6), ([new] * 6, [new - 3, new + 200, 0, 1, new, 300])):
+        batch = R.Batch(rng, n, lengths, 16, width=width)
+        cache, codes, scales = _cache(q, rng, batch, 2, 64)
+        x, xv = _as(rng.standard_normal((batch.T, 8, 64)), dtype)
+        none = _against(q, cache, codes, scales, batch, x, xv, dtype)
+        for window in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 4):
+            got = _against(q, cache, codes, scales, batch, x, xv, dtype, window=window)
+            assert torch.equal(got[0], none[0]) and torch.equal(got[1], none[1])
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_many_rows_of_few_tokens_and_a_window_as_wide_as_the_table(cuda_lib, dtype):
+    """1300 rows of 5 tokens, a table for 2^31 - 1024 tokens, a window of 2^31 - 1200."""
+    import torch
+    q = cuda_lib
+    rng = np.random.default_rng(73)
+    small = R.Batch(rng, [1300], [5], 128)
+    cache, codes, scales = _cache(q, rng, small, 1, 64)
+    x, xv = _as(rng.standard_normal((1300, 1, 64)), dtype)
+    wide = torch.zeros(1, (1 << 24) - 8, dtype=torch.int32, device="cuda")
+    wide[0, 0] = int(small.table[0, 0])
+    y, lse = q.qmm_kv_attention(cache, x, wide, _i32([5]), offsets=_i32([0, 1300]), window=2 ** 31 - 1200, dtype=torch.float32, lse=True)
+    assert q.qmm_device_status() == 0
+    wy, wl, ey, el = _exact(xv, dtype, codes, scales, small, 0.125)
+    _within(_np(y), wy, R.rounded(wy, ey, "float32"), "y")
+    _within(_np(lse), wl, el, "lse")
