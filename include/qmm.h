@@ -392,7 +392,8 @@ QMM_API int qmm_f8_moe(int x_type, const void *x, int64_t T, int64_t H, int64_t 
  * can be captured in a graph and replayed after they changed.  A sequence with
  * offsets that fall or leave the batch, or a length that its table does not
  * hold, is skipped, a page that the cache does not have is not touched; their
- * results are undefined and qmm_device_status() reports QMM_EINDEX.
+ * results are undefined and qmm_device_status() reports QMM_EINDEX.  Where
+ * offsets fall or leave the batch, other sequences may be skipped with them.
  *
  * Rows of heads (queries, new keys and values, results): element i of head h
  * of row t at t * ld_t + h * ld_h + i, type QMM_F32, QMM_F16 or QMM_BF16,

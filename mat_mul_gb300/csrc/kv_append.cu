@@ -129,8 +129,16 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && KEEP <= 4 ? 2 : 1) 
     __shared__ float reduced[2][THREADS / 32 + 1];
     pdl_wait();
     pdl_trigger();
+    // Offsets that fall can hide a sequence from every search, and another's units behind
+    // it: block u looks at those of sequence u as well (there are more units than
+    // sequences).  Loaded before the search, so that nothing waits for them.
+    const bool check = P.offsets && blockIdx.y == 0 && blockIdx.x < static_cast<unsigned>(P.B);
+    int lo = 0, hi = 0;
+    if (check) lo = __ldg(P.offsets + blockIdx.x), hi = __ldg(P.offsets + blockIdx.x + 1);
     Unit u;
-    if (!find_unit(P, blockIdx.x, u)) return;
+    const bool have = find_unit(P, blockIdx.x, u);
+    if (check && threadIdx.x == 0 && (lo < 0 || hi < lo || hi > P.T)) atomicOr(P.status, STATUS_INDEX);
+    if (!have) return;
     const int tid = threadIdx.x, kv_parts = (P.heads + P.kv_per - 1) / P.kv_per, part = blockIdx.y;
     if (part >= 2 * kv_parts) {  // queries
         const int h0 = (part - 2 * kv_parts) * P.q_per, h1 = min(P.q_heads, h0 + P.q_per);

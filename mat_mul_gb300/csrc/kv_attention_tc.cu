@@ -303,7 +303,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
         long long sum = 0;
         for (int p = tid * share; p < min(PP.pairs, (tid + 1) * share); ++p) {
             Pair q;
-            if (!load_pair(P, p, q)) atomicOr(P.status, STATUS_INDEX);
+            // (offsets that fall can hide a sequence from every search: those of sequence p
+            // are looked at by themselves; there are as many pairs as sequences, or more)
+            int lo = 0, hi = 0;
+            if (P.offsets && p < P.B) lo = __ldg(P.offsets + p), hi = __ldg(P.offsets + p + 1);
+            const bool known = load_pair(P, p, q);
+            if (!known || lo < 0 || hi < lo || hi > P.T) atomicOr(P.status, STATUS_INDEX);
             if (q.tiles > 0) sum += q.tiles + UNIT_COST;
         }
         sum *= P.heads;

@@ -165,3 +165,30 @@ def test_many_rows_of_few_tokens_and_a_window_as_wide_as_the_table(cuda_lib, dty
     wy, wl, ey, el = _exact(xv, dtype, codes, scales, small, 0.125)
     _within(_np(y), wy, R.rounded(wy, ey, "float32"), "y")
     _within(_np(lse), wl, el, "lse")
+
+
+# ---------------------------------------------------------------------------
+# offsets that fall
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("offsets", [[0, 100, 50, 200], [0, 10, 1000000, 150, 200], [0, 60, -5000, 130, 200], [0, 100, 99, 200]])
+@pytest.mark.parametrize("what", ["append", "bfloat16", "float32", "few"])
+def test_offsets_that_fall_are_always_reported(cuda_lib, what, offsets):
+    """Wherever they lie between others; rows behind the last sequence and what the batch does not hold stay."""
+    import torch
+    q = cuda_lib
+    rng = np.random.default_rng(79)
+    B, T = len(offsets) - 1, 200
+    if what == "few":
+        offsets = [min(o, 10 ** 6) // 25 for o in offsets]
+        T = 8
+    cache = q.KvCache.empty(20 * B, 2, page=16, dim=64)
+    table, lengths = _i32(np.arange(20 * B).reshape(B, 20)), _i32([250] * B)
+    dtype = torch.float32 if what == "float32" else torch.bfloat16
+    x = torch.randn(T + 4, 8, 64, device="cuda", dtype=dtype)
+    y = torch.full_like(x, 7.0)
+    if what == "append":
+        q.qmm_kv_append(cache, x[:, :2], x[:, :2], table, lengths, offsets=_i32(offsets))
+    else:
+        q.qmm_kv_attention(cache, x, table, lengths, offsets=_i32(offsets), y=y)
+    assert q.qmm_device_status() == q.QMM_EINDEX and q.qmm_device_status() == 0
+    assert bool((y[T:] == 7).all())
