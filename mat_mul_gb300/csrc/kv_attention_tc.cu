@@ -748,6 +748,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                 const int r = r0 + RPW * k;
                 const float most = NQ == 2 ? __uint_as_float(top[k] << 16) : half_bits_to_float(top[k]);
                 const int e2 = most > 0.0f ? min(max(7 - exponent_of(__float_as_uint(most)), -120), 100) : 0;
+                // (the scores' factor is positive, so that their largest is that of the exponents)
                 const float up = P.factor < 0.0f ? -pow2f(e2) : pow2f(e2);
                 if (d == 0) factors[r] = fabsf(P.factor) * pow2f(-e2);
                 const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
@@ -1106,9 +1107,6 @@ size_t tc_part_bytes(int dim, int num_sms) {
 cudaError_t launch_tc(const AttnParams &a, cudaStream_t st, int num_sms, int dev) {
     TcParams p = {};
     p.a = a;
-    // a negative factor goes to the queries; one that vanishes would lose the masks
-    const float least = 1e-30f;
-    if (a.factor > -least && a.factor < least) p.a.factor = a.factor < 0 ? -least : least;
     p.pairs = static_cast<int>(a.T * a.group / UNIT + a.B);
     auto vec = [&](const void *x, int type, int64_t ld_t, int64_t ld_h, int bytes) {
         const int es = f8_size(type);

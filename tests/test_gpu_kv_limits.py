@@ -167,6 +167,21 @@ def test_many_rows_of_few_tokens_and_a_window_as_wide_as_the_table(cuda_lib, dty
     _within(_np(lse), wl, el, "lse")
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("scale,large", [(0.0, 100), (1e-33, 100), (-1e-33, 100), (1e-36, 110)])
+def test_scales_of_the_scores_that_nearly_vanish(cuda_lib, kernel, scale, large):
+    """With 0 every row is the mean of what it sees, whatever the keys are; tiny scales of large keys."""
+    q = cuda_lib
+    dtype, new, width = KERNELS[kernel]
+    rng = np.random.default_rng(76)
+    batch = R.Batch(rng, [new] * 3, [max(n, new) for n in (300, 140, 129)], 64, width=2 * width)
+    cache, codes, scales = _cache(q, rng, batch, 2, 64)
+    scales[0] = np.full_like(scales[0], 2.0 ** large)
+    _put(cache, codes, scales)
+    x, xv = _as(rng.standard_normal((batch.T, 8, 64)), dtype)
+    _against(q, cache, codes, scales, batch, x, xv, dtype, scale=scale)
+
+
 # ---------------------------------------------------------------------------
 # offsets that fall
 # ---------------------------------------------------------------------------
