@@ -6,7 +6,9 @@
 // with one scale sk, sv per page and head.  A row's scores in powers of two,
 //   x_j = (scale log2 e) sk (q.code_j) + log2 sv,  m = max x_j,  p'_j = 2^(x_j - m),
 // carry the scale of the values: the second product then takes codes, y =
-// sum p' code / sum (p' / sv), and p' <= 1 whatever the scales are.
+// sum p' code / sum (p' / sv), and p' <= 1 whatever the scales are.  Where a page's
+// scale is far below another's, p' may vanish although p does not (a page of zeros
+// has 2^-100): the sum then has a reference of its own, see far_scale.
 //
 // What bounds it: the reading of the codes (2 dim bytes per token and head).
 // They enter the tensor cores as exact fp16 values (one conversion per two
@@ -41,7 +43,8 @@ namespace kv {
 constexpr int TILE = 128;     // tokens of a tile
 constexpr int THREADS = 256;  // 8 warps, and one for the copies
 constexpr int LEAST = 2;      // tiles per block below which fewer blocks take part
-constexpr int SCALES = 24;    // floats of a tile's scales
+constexpr int SCALES = 24;    // floats of a tile's scales: of 8 groups of tokens those of keys, log2 and inverse of those of
+                              // values (0: see far_scale)
 constexpr int SHORT = 4;      // tiles of a unit that is not cut: it goes to the block where it begins
 
 // A power of two on p', so that its low part in fp16 keeps 2^-38 of the largest.
@@ -165,6 +168,37 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+// Whether a value scale lies outside 2^-61 .. 2^29.  Within, scales are at most 2^90
+// apart, and p' of a score up to 2^35 below the row's largest stays above 2^-126,
+// which ex2 would make 0: what is lost of a row's sum is below 2^-35 of its largest
+// part for each token.  From the first tile of a unit with such a scale on (its inverse
+// scales are 0), the sum is kept apart as a FarSum.
+__device__ __forceinline__ bool far_scale(float v) { return !(v >= 0x1p-61f && v <= 0x1p29f); }
+// The sum of p without the scales, relative to 2^m of the scores alone.  In memory, as the
+// registers are those of the ordinary case.
+struct FarSum {
+    volatile float m, l;
+    // s(i): the score i of n, -inf where it is masked; unit: what p = 1 counts
+    template <class S>
+    __device__ __forceinline__ void add(int n, float unit, const S &s) {
+        const float was = m;
+        float top = was;
+#pragma unroll
+        for (int i = 0; i < n; ++i) top = fmaxf(top, s(i));
+        const float ref = top == -INFINITY ? 0.0f : top;  // (nothing was seen yet: any finite one)
+        float sum = l * ex2(was - ref);
+#pragma unroll
+        for (int i = 0; i < n; ++i) sum = fmaf(ex2(s(i) - ref), unit, sum);
+        m = top, l = sum;
+        asm volatile("" ::: "memory");  // (one after another: side by side they would take more registers)
+    }
+    // relative to 2^ref, the reference of the row's products
+    __device__ __forceinline__ float at(float ref) const { return l != 0.0f ? l * ex2(0.5f * (m - ref)) * ex2(0.5f * (m - ref)) : 0.0f; }
+};
+// v 2^d for d <= 0, also where 2^d is below fp32 (a sum over scales of 2^-100 is
+// large enough to be seen beside one over scales of 2^100).
+__device__ __forceinline__ float faded(float v, float d) { return v * ex2(fmaxf(d, -126.0f)) * ex2(fminf(d + 126.0f, 0.0f)); }
+
 __device__ __forceinline__ void store_typed(void *p, int64_t i, int type, float v) {
     if (type == QMM_F32) static_cast<float *>(p)[i] = v;
     else if (type == QMM_F16) static_cast<__half *>(p)[i] = __float2half_rn(v);
@@ -195,7 +229,7 @@ struct Few {
     static constexpr int OFF_P = OFF_Q + PARTS * R * QP * 2;
     static constexpr int OFF_RED = OFF_P + PARTS * R * PP * 2;       // [8 warps][R]
     static constexpr int OFF_ROW = OFF_RED + 8 * R * 4;              // [R] factor of the row, [R] first, [R] end, [R] the factor's low part
-    static constexpr int OFF_SC = OFF_ROW + 4 * R * 4;               // [STAGES][3][8]: key scales, log2 and inverse of value scales
+    static constexpr int OFF_SC = OFF_ROW + 4 * R * 4;               // [STAGES][SCALES]
     static constexpr int OFF_BAR = (OFF_SC + STAGES * SCALES * 4 + 7) / 8 * 8;
     static constexpr int SMEM = OFF_BAR + 16 * STAGES + 16;
     static_assert(CTAS == 1 ? SMEM <= 232448 : 2 * (SMEM + 1024) <= 233472, "shared memory");
@@ -317,6 +351,7 @@ __device__ __forceinline__ void copy_tiles(const AttnParams &P, const CUtensorMa
             return id;
         };
         int id = page_of(u.jb);
+        bool far = false;  // a value scale of the unit, up to here, is far from 1
         for (int j = u.jb; j < u.je; ++j, ++it) {
             const int64_t tile = static_cast<int64_t>(max(id, 0)) * P.heads + u.head;
             const float ks = __ldg(P.scales[0] + tile), vs = __ldg(P.scales[1] + tile);
@@ -327,10 +362,11 @@ __device__ __forceinline__ void copy_tiles(const AttnParams &P, const CUtensorMa
             if (!ok) break;
             const int src = 16 * lane / P.page;  // scales of the groups of 16 tokens
             const float kg = __shfl_sync(0xffffffffu, ks, src), vg = __shfl_sync(0xffffffffu, vs, src);
+            far = far || __any_sync(0xffffffffu, id >= 0 && far_scale(vs));
             if (lane < 8) {
                 const float v = fmaxf(vg, 0x1p-100f);
                 float *const d = sc + SCALES * s + lane;
-                d[0] = kg, d[8] = log2f(v), d[16] = __fdiv_rn(1.0f, v);
+                d[0] = kg, d[8] = log2f(v), d[16] = far ? 0.0f : __fdiv_rn(1.0f, v);
             }
             __syncwarp();  // (lane 0's arrival hands over what the eight wrote; a vote orders no memory)
             const uint32_t live = __popc(__ballot_sync(0xffffffffu, id >= 0));
@@ -355,19 +391,22 @@ __device__ __forceinline__ void copy_tiles(const AttnParams &P, const CUtensorMa
 // The number of parts of a unit that were there before this CTA's, by one thread behind a
 // barrier of those that wrote it: the fence carries their writes too.  (By all of them it
 // took 1200 cycles, and 6600 where the others read at full rate.)  The last one, with `last`
-// before it, leaves the counter zero for the next launch.
-__device__ __forceinline__ unsigned arrive(unsigned *count, unsigned last) {
+// before it, leaves the counter zero for the next launch.  In the upper half of the counter and of
+// what is returned: how many of the parts, this one included, have a value scale far from 1.
+constexpr unsigned FAR_PART = 0x10000u;
+__device__ __forceinline__ unsigned arrive(unsigned *count, unsigned last, bool far) {
     __threadfence();
-    const unsigned before = atomicAdd(count, 1u);
-    if (before == last) *count = 0u;
+    const unsigned mine = far ? FAR_PART : 0u, before = atomicAdd(count, 1u + mine);
+    if ((before & (FAR_PART - 1)) == last) *count = 0u;
     __threadfence();
-    return before;
+    return before + mine;
 }
 
 // The parts of a unit, of the CTAs c0 .. c1, joined in their order, eight at a time on
-// their way; out(r, at, row) says where row r goes.
+// their way; out(r, at, row) says where row r goes.  far: value scales may be so far apart
+// that a sum over small ones fades beside the reference of large ones.
 template <class C, int DP, class Out>
-__device__ __forceinline__ void join_parts(const AttnParams &P, int c0, int c1, int rows, int tid, const Out &out) {
+__device__ __forceinline__ void join_parts(const AttnParams &P, int c0, int c1, int rows, int tid, bool far, const Out &out) {
     for (int i = tid; i < rows * (DP / 4); i += C::CONSUMERS) {
         const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
         float top = -INFINITY, sum = 0.0f;
@@ -399,6 +438,14 @@ __device__ __forceinline__ void join_parts(const AttnParams &P, int c0, int c1, 
                 }
             }
         }
+        if (far) {
+            sum = 0.0f;
+#pragma unroll 1
+            for (int cc = c0; cc <= c1; ++cc) {
+                const float *q = P.part + (static_cast<int64_t>(cc) * 2 + (cc == c0)) * C::PART;
+                sum += faded(__ldcg(q + C::R * (DP + 1) + r), __ldcg(q + C::R * DP + r) - (top == -INFINITY ? 0.0f : top));
+            }
+        }
         const float inv = sum != 0.0f ? L_FACTOR / sum : 0.0f;
         int64_t at, row;
         out(r, at, row);
@@ -410,6 +457,30 @@ __device__ __forceinline__ void join_parts(const AttnParams &P, int c0, int c1, 
         }
         if (P.lse && d == 0) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + 20.0f - C::SHIFT) * LN2 : -INFINITY;
     }
+}
+
+// The share of tokens tok and tok + 8 of two rows' sums (far_scale); x: their products, token by
+// token; row: the rows' factors, R on the first tokens that they see, and so on.
+template <class C, bool HL>
+__device__ __forceinline__ void far_tokens(FarSum *apart, float4 x, float scale, int tok, const float *row) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int *const seen = reinterpret_cast<const int *>(row) + h;
+        const int lo = seen[C::R], hi = seen[2 * C::R];
+        const float f = row[h] * scale, low = HL ? row[3 * C::R + h] * scale : 0.0f;
+        apart[h].add(2, L_FACTOR * 0x1p14f, [&](int i) {
+            const float v = i ? (h ? x.w : x.z) : (h ? x.y : x.x);
+            const int k = tok + 8 * i;
+            return k >= lo && k < hi ? fmaf(v, f, v * low) : -INFINITY;
+        });
+    }
+}
+
+// The same as a function that is called: for four groups of rows what it takes of the registers
+// costs more (8 sequences of 1024 tokens, 6 rows: 24.6 against 25.6 us; for fewer 17.9 against 16.9).
+template <class C, bool HL>
+__device__ __noinline__ void far_tokens_called(FarSum *apart, float4 x, float scale, int tok, const float *row) {
+    far_tokens<C, HL>(apart, x, scale, tok, row);
 }
 
 template <int DP, int NB, bool HL>
@@ -518,6 +589,8 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
                 for (int i = 0; i < 4; ++i) o[k][n][i] = 0.0f;
         }
 
+        FarSum apart[NB][2];
+        bool far = false;
         for (int j = u.jb; j < u.je; ++j, ++it) {
             const int slot = it % STAGES;
             const bool ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * slot, (it / STAGES) & 1, P.status));
@@ -583,6 +656,17 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
             const int tok = tok0 + 16 * warp + g;  // this lane's tokens: tok, tok + 8
             const float *const scales = sc + SCALES * slot + warp;
             const float ks = scales[0], lv = scales[8], iv = scales[16];
+            if (iv == 0.0f) {  // the sums apart (far_scale)
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const int r = 8 * n + 2 * c;
+                    if (!far) apart[n][0].m = m[n][0], apart[n][0].l = l[n][0], apart[n][1].m = m[n][1], apart[n][1].l = l[n][1];
+                    const float4 products = make_float4(x[n][0], x[n][1], x[n][2], x[n][3]);
+                    if constexpr (NB == 4 && DP <= 128) far_tokens_called<C, HL>(apart[n], products, ks, tok, row_f + r);
+                    else far_tokens<C, HL>(apart[n], products, ks, tok, row_f + r);
+                }
+                far = true;
+            }
             uint32_t hidden = 0;  // bit 4 n + i: x[n][i] is masked
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
@@ -721,6 +805,12 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
         named_barrier(1, THREADS);
 
         // sums over the lanes and warps that share a row
+        if (far) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) l[n][h] = apart[n][h].at(m[n][h]);
+        }
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
 #pragma unroll
@@ -807,9 +897,10 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
             named_barrier(1, THREADS);
             const long long u0 = w.seq0 + w.unit * s.tiles, u1 = u0 + s.tiles - 1;  // first and last tile of the unit
             const int c0 = static_cast<int>(divide((u0 + 1) * blocks - 1, W)), c1 = static_cast<int>(divide((u1 + 1) * blocks - 1, W));
-            if (tid == 0) *arrived = arrive(P.count + c0, static_cast<unsigned>(c1 - c0));
+            if (tid == 0) *arrived = arrive(P.count + c0, static_cast<unsigned>(c1 - c0), far);
             named_barrier(1, THREADS);
-            if (*arrived == static_cast<unsigned>(c1 - c0)) join_parts<C, DP>(P, c0, c1, rows, tid, out);
+            const unsigned parts = *arrived;
+            if ((parts & (FAR_PART - 1)) == static_cast<unsigned>(c1 - c0)) join_parts<C, DP>(P, c0, c1, rows, tid, parts >= FAR_PART, out);
         }
         advance<R>(P, w, u.nt, t1);
     }

@@ -59,6 +59,36 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// 16 tokens' share of two rows' sums (far_scale), from scores of its own: a function that is
+// called, so that in the ordinary case nothing of it takes a register.  row: the rows' factors, R on
+// the first tokens that they see and 2 R on the ends of those.
+template <class C>
+__device__ __noinline__ void far_tile(FarSum *apart, uint32_t sk, const uint4 *my_q, float scale, int tok, const float *row) {
+    float y[2][4] = {};
+#pragma unroll 1
+    for (int k = 0; k < C::SIDE / TILE / 16; k += 2) {
+        uint32_t a[4];
+        ldsm4(sk ^ (k << 4), a);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 q = my_q[32 * (k + h)];
+            const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int n = 0; n < 2; ++n) mma16816(y[n], qa, halves(a[h + 2 * n]), halves_hi(a[h + 2 * n]));
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int *const seen = reinterpret_cast<const int *>(row) + 8 * h;
+        const int lo = seen[C::R], hi = seen[2 * C::R];
+        const float f = row[8 * h] * scale;
+        apart[h].add(4, L_FACTOR * 0x1p6f, [&](int i) {
+            const int k = tok + 8 * (i >> 1) + (i & 1);
+            return k >= lo && k < hi ? y[i >> 1][2 * h + (i & 1)] * f : -INFINITY;
+        });
+    }
+}
+
 template <int DP, int MT>
 __global__ void __launch_bounds__(SLIM_THREADS, 1)
     kv_attention_slim_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams P) {
@@ -169,6 +199,8 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
                 for (int i = 0; i < 4; ++i) o[t][n][i] = 0.0f;
         }
 
+        FarSum apart[MT][2];
+        bool far = false;
         for (int j = u.jb; j < u.je; ++j, ++it) {
             const int slot = it % STAGES;
             if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(full + 8 * slot, (it / STAGES) & 1, P.status));
@@ -176,6 +208,14 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
             const uint32_t sk = base + slot * C::STAGE + 16 * warp * C::ROW + C::at((lane & 7) + (lane >> 4 << 3), lane >> 3 & 1);
             const uint32_t sv = base + slot * C::STAGE + C::SIDE + 16 * warp * C::ROW + C::at(lane & 15, lane >> 4);
             const int from = u.from + j * TILE + 16 * warp;  // this warp's tokens
+            if (!dead && from < u.hi && from + 16 > u.lo && sc[SCALES * slot + 16] == 0.0f) {  // the sums apart (far_scale)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    if (!far) apart[t][0].m = m[t][0], apart[t][0].l = l[t][0], apart[t][1].m = m[t][1], apart[t][1].l = l[t][1];
+                    far_tile<C>(apart[t], sk, my_q + 32 * KS * t, sc[SCALES * slot + warp], from + 2 * c, row_f + 16 * t + g);
+                }
+                far = true;
+            }
             if (!dead && from < u.hi && from + 16 > u.lo) {
                 const bool whole = from >= u.all_lo && from + 16 <= u.all_hi;
                 uint32_t nans = 0;
@@ -311,6 +351,12 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
             if (lane == 0 && !dead) mbar_arrive(empty + 8 * slot);
         }
 
+        if (far) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) l[t][h] = apart[t][h].at(m[t][h]);
+        }
         // the warps' maxima and sums, then their O: joined, 16 rows at a time
 #pragma unroll
         for (int t = 0; t < MT; ++t)
@@ -321,7 +367,7 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
                 const int r = 16 * t + g + 8 * h;
                 if (c == 0) warp_m[warp * R + r] = m[t][h], warp_l[warp * R + r] = l[t][h];
             }
-        named_barrier(1, THREADS);
+        far = named_barrier_or(1, THREADS, far);
         auto out = [&](int r, int64_t &at, int64_t &row) {
             const int i = token_of(P, r0 + r), h = head * P.group + (r0 + r - i * P.group);
             at = (static_cast<int64_t>(s.row0) + i) * P.ldy_t + static_cast<int64_t>(h) * P.ldy_h;
@@ -341,6 +387,11 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
                 const float ref = top == -INFINITY ? 0.0f : top, scale = ex2(m[t][h] - ref);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) sum = fmaf(warp_l[k * R + r], ex2(warp_m[k * R + r] - ref), sum);
+                if (far) {  // (as where parts are joined)
+                    sum = 0.0f;
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k) sum += faded(warp_l[k * R + r], warp_m[k * R + r] - ref);
+                }
                 if (warp == 0 && c == 0) row_m[r] = top, row_l[r] = sum;
                 float *const d = sums + (warp * 16 + g + 8 * h) * C::SUM_ROW + 4 * c;
 #pragma unroll
@@ -380,9 +431,10 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
         if (!entire) {
             const long long u0 = w.seq0 + w.unit * s.tiles, u1 = u0 + s.tiles - 1;  // first and last tile of the unit
             const int c0 = static_cast<int>(divide((u0 + 1) * blocks - 1, W)), c1 = static_cast<int>(divide((u1 + 1) * blocks - 1, W));
-            if (tid == 0) *arrived = arrive(P.count + c0, static_cast<unsigned>(c1 - c0));
+            if (tid == 0) *arrived = arrive(P.count + c0, static_cast<unsigned>(c1 - c0), far);
             named_barrier(1, THREADS);
-            if (*arrived == static_cast<unsigned>(c1 - c0)) join_parts<C, DP>(P, c0, c1, rows, tid, out);
+            const unsigned parts = *arrived;
+            if ((parts & (FAR_PART - 1)) == static_cast<unsigned>(c1 - c0)) join_parts<C, DP>(P, c0, c1, rows, tid, parts >= FAR_PART, out);
         }
         advance<R>(P, w, u.nt, t1);
     }

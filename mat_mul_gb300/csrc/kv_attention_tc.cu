@@ -53,7 +53,8 @@ using f8::tc_fence_before;
 constexpr int TC_THREADS = 768, UNIT = 256;
 constexpr int TC_LEAST = 6;   // tiles (and unit costs) per CTA below which fewer CTAs take part
 constexpr int UNIT_COST = 5;  // what a unit costs beside its tiles, in tiles
-constexpr int PIECES = 3, SC_SLOTS = 4, SC_FLOATS = 16;
+constexpr int PIECES = 3, SC_SLOTS = 4;
+constexpr int SC_FLOATS = 16;  // of 8 groups of tokens: scales of keys (negative: see far_scale), log2 of those of values
 // registers per thread at launch, and after the split between roles 0..3, conversion and rows
 constexpr int REGS = 80, REGS_A = 48, REGS_B = 48, REGS_C = 96;
 static_assert(128 * (REGS_A + REGS_B + 4 * REGS_C) <= TC_THREADS * REGS, "register split");
@@ -73,7 +74,7 @@ struct Tc {
     static constexpr int RAW = TILE * DP, TILE_BYTES = TILE * DP * 2;
     static constexpr int OFF_K = 2 * NQ * KEYS, OFF_V = OFF_K + KR * KEYS, OFF_RAW = OFF_V + VR * TILE_BYTES;
     static constexpr int OFF_SHARE = OFF_RAW + VR * RAW;          // [2 halves][UNIT] what the threads of a row tell each other
-    static constexpr int OFF_SC = OFF_SHARE + 2 * UNIT * 4;       // [SC_SLOTS] key scales and log2 of value scales
+    static constexpr int OFF_SC = OFF_SHARE + 2 * UNIT * 4;       // [SC_SLOTS][SC_FLOATS]
     static constexpr int OFF_PIECES = OFF_SC + SC_SLOTS * SC_FLOATS * 4;
     static constexpr int OFF_BAR = OFF_PIECES + PIECES * 48;
     static constexpr int OFF_NANS = OFF_BAR + 320;  // [VR][4] bits of the tokens with a NaN among their values
@@ -399,6 +400,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
             int it = 0;
             bool ok = true;
             for (int np = 0; ok; ++np) {
+                bool far = false;  // a value scale of the piece, up to here, is far from 1
                 ok = __all_sync(0xffffffffu, mbar_spin(piece_bar(np), piece_parity(np), P.status));
                 if (!ok) break;
                 const Piece pc = read_piece(np);
@@ -436,9 +438,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                     // rows are done with the scales that these replace)
                     const int src = 16 * lane / P.page;
                     const float kg = __shfl_sync(0xffffffffu, ks, src), vg = __shfl_sync(0xffffffffu, vs, src);
+                    far = far || __any_sync(0xffffffffu, id >= 0 && far_scale(vs));
                     if (lane < 8) {
                         float *d = sc + (it % SC_SLOTS) * SC_FLOATS + lane;
-                        d[0] = fminf(fmaxf(kg, 0x1p-126f), 0x1p127f);
+                        const float k = fminf(fmaxf(kg, 0x1p-126f), 0x1p127f);
+                        d[0] = far ? -k : k;  // (negative: see far_scale)
                         d[8] = log2f(fminf(fmaxf(vg, 0x1p-100f), 0x1p127f));
                     }
                     __syncwarp();
@@ -805,10 +809,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                 all_hi = all_end_of(pc), all_lo = all_from_of(pc);
             }
             float ref = -INFINITY, l = 0.0f;
+            FarSum apart;
+            bool far = false;
             if (have) {
-                for (int j = 0; j < nt; ++j, ++it) {
+                int j = 0;
+                // (with value scales far from 1 in a loop of its own, as in the other kernels)
+#pragma unroll
+                for (int mode = 0; mode < 2; ++mode)
+                for (; j < nt; ++j, ++it) {
+                    if (!ok) break;
                     ok = group_wait(first, tile_bar, 256, s_full + 8 * t, it & 1);
                     if (!ok) break;
+                    if (mode == 0 && sc[((tiles + j) % SC_SLOTS) * SC_FLOATS] < 0.0f) break;
                     tc_fence_after();
                     const int tok = (tile0 + j) * TILE;
                     const bool masked = tok < all_lo || tok + TILE > all_hi;  // (as the conversion has it)
@@ -823,8 +835,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                     {
                         const float *scale = sc + ((tiles + j) % SC_SLOTS) * SC_FLOATS + half * 4;
                         const float4 a = *reinterpret_cast<const float4 *>(scale), b = *reinterpret_cast<const float4 *>(scale + 8);
-                        fk[0] = f * a.x, fk[1] = f * a.y, fk[2] = f * a.z, fk[3] = f * a.w;
+                        fk[0] = f * (mode ? -a.x : a.x), fk[1] = f * (mode ? -a.y : a.y), fk[2] = f * (mode ? -a.z : a.z), fk[3] = f * (mode ? -a.w : a.w);
                         lv[0] = b.x, lv[1] = b.y, lv[2] = b.z, lv[3] = b.w;
+                        if (mode == 1) {
+                            if (!far) apart.m = ref, apart.l = l;
+                            far = true;
+#pragma unroll 1
+                            for (int k = 0; k < HT; k += 4) {
+                                const float factor = f * fabsf(scale[k / 16]);
+                                apart.add(4, L_FACTOR * 0x1p6f, [&](int i) {
+                                    uint32_t x;
+                                    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(x) : "r"(my_s + k + i) : "memory");
+                                    return k + i >= from && k + i < to ? __uint_as_float(x) * factor : -INFINITY;
+                                });
+                            }
+                        }
                     }
                     tmem_wait16(s[0]);
                     asm volatile("" : KV_RW4(s[1], 0), KV_RW4(s[1], 4), KV_RW4(s[1], 8), KV_RW4(s[1], 12), KV_RWF4(m) : : "memory");
@@ -936,6 +961,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                 ok = group_wait(first, tile_bar, 256, pv_done + 8 * t, (it - 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
+                if (far) l = apart.at(ref);
                 *tell = l;
                 named_barrier(pair_bar, 64);
                 l += *told;
@@ -1017,9 +1043,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                     if (half == 0) part[DP * UNIT + mine] = ref, part[(DP + 1) * UNIT + mine] = l;
                     __threadfence();
                     named_barrier(tile_bar, 256);
-                    if (first && lane == 0) arrived[t] = atomicAdd(P.count + 2 * pc.c0 + t, 1u);
+                    if (first && lane == 0) arrived[t] = atomicAdd(P.count + 2 * pc.c0 + t, 1u + (far ? FAR_PART : 0u));
                     named_barrier(tile_bar, 256);
-                    if (arrived[t] == static_cast<unsigned>(pc.c1 - pc.c0)) {
+                    if ((arrived[t] & (FAR_PART - 1)) == static_cast<unsigned>(pc.c1 - pc.c0)) {
+                        far = far || arrived[t] >= FAR_PART;  // (of some part: see join_parts)
                         if (first && lane == 0) P.count[2 * pc.c0 + t] = 0u;  // zero again for the next launch
                         __threadfence();
                         auto part_of = [&](int c) { return P.part + (static_cast<int64_t>(c) * 2 + (c == pc.c0)) * C::PART; };
@@ -1028,6 +1055,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                         const float sub = top == -INFINITY ? 0.0f : top;
                         for (int c = pc.c0; c <= pc.c1; ++c)
                             sum = fmaf(__ldcg(part_of(c) + (DP + 1) * UNIT + mine), ex2(__ldcg(part_of(c) + DP * UNIT + mine) - sub), sum);
+                        if (far) {
+                            sum = 0.0f;
+#pragma unroll 1
+                            for (int c = pc.c0; c <= pc.c1; ++c)
+                                sum += faded(__ldcg(part_of(c) + (DP + 1) * UNIT + mine), __ldcg(part_of(c) + DP * UNIT + mine) - sub);
+                        }
                         const float inv = sum != 0.0f ? L_FACTOR / sum : 0.0f;
                         int64_t at, row;
                         result(at, row);

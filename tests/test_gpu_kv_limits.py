@@ -168,6 +168,31 @@ def test_many_rows_of_few_tokens_and_a_window_as_wide_as_the_table(cuda_lib, dty
 
 
 @pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("low,high", [(-100, 28), (-100, 40), (-100, 100), (-60, 100), (-100, -5)])
+def test_pages_of_value_scales_far_apart(cuda_lib, kernel, low, high):
+    """Pages of zeros, whose scale is 2^-100, or of tiny values beside pages of large ones: they have their share in the
+    sum of the probabilities, whichever come first and wherever a sequence is cut."""
+    q = cuda_lib
+    dtype, new, width = KERNELS[kernel]
+    rng = np.random.default_rng(74)
+    for page, lengths, first in ((16, [900, 300, 77], None), (64, [9000, 200, 3000], low), (64, [9000, 200, 3000], high)):
+        batch = R.Batch(rng, [new] * 3, [max(n, new) for n in lengths], page, width=2 * width)
+        cache, codes, scales = _cache(q, rng, batch, 2, 64)
+        for b in range(3):
+            ids = batch.table[b, :-(-batch.lengths[b] // page)]
+            if first is None:
+                tiny = rng.integers(0, 2, (len(ids), 2)) > 0
+            else:
+                tiny = np.repeat((np.arange(len(ids)) < len(ids) // 2)[:, None] == (first == low), 2, 1)
+            scales[1][ids] = np.where(tiny, 2.0 ** low, 2.0 ** high)
+            if low == -100:
+                codes[1][ids] = np.where(tiny[:, :, None, None], 0, codes[1][ids])
+        _put(cache, codes, scales)
+        x, xv = _as(0.1 * rng.standard_normal((batch.T, 8, 64)), dtype)
+        _against(q, cache, codes, scales, batch, x, xv, dtype)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
 @pytest.mark.parametrize("scale,large", [(0.0, 100), (1e-33, 100), (-1e-33, 100), (1e-36, 110)])
 def test_scales_of_the_scores_that_nearly_vanish(cuda_lib, kernel, scale, large):
     """With 0 every row is the mean of what it sees, whatever the keys are; tiny scales of large keys."""
