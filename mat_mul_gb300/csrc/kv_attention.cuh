@@ -145,6 +145,47 @@ __device__ __forceinline__ bool has_nan(const uint4 &v) {
     auto nan = [](uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; };  // bit 7 of a byte is set if it was 0x7f
     return ((nan(v.x) | nan(v.y) | nan(v.z) | nan(v.w)) & 0x80808080u) != 0;
 }
+// 16 codes with 0 where one is a NaN.
+__device__ __forceinline__ uint4 without_nan(const uint4 &v) {
+    auto clean = [](uint32_t w) { return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); };
+    return make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+}
+// The results that NaNs among the values reach, of rows ra .. rb - 1 of the unit (from query
+// row r0 on) and dims d0 .. d1 - 1: set(row, dim) for each.  In tiles that some rows see and
+// some do not 0 times a NaN would reach all of them, so the kernels take a NaN there for 0, note
+// that there was one, and come here once their results are written: the values of tokens from .. to - 1
+// are read again, but for those of tiles that all rows see.  By `count` threads, 16 or more.
+template <class Set>
+__device__ __forceinline__ void spread_nans(const AttnParams &P, int b, int head, int start, int r0, int ra, int rb, int d0, int d1,
+                                            int from, int to, int all_lo, int all_hi, int idx, int count, const Set &set) {
+    const int chunks = (min(d1, P.dim) - d0) / 16;
+    if (chunks <= 0 || ra >= rb) return;
+    const int step = count / chunks, chunk = idx % chunks;
+    if (idx >= step * chunks) return;
+#pragma unroll 1
+    for (int64_t k = from + idx / chunks; k < to; k += step) {
+        if (k - all_lo >= TILE && all_hi - k > TILE + step) {
+            k += (all_hi - TILE - k) / step * step - step;
+            continue;
+        }
+        const int32_t id = __ldg(P.table + static_cast<int64_t>(b) * P.ld_table + k / P.page);
+        if (id < 0 || id >= P.pages) continue;
+        const int64_t row = (static_cast<int64_t>(id) * P.heads + head) * P.page + k % P.page;
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(P.codes[1] + row * P.dim + d0) + chunk);
+        if (!has_nan(v)) continue;
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 1
+        for (int r = ra; r < rb; ++r) {
+            const int pos = start + token_of(P, r0 + r);
+            if (k < seen_from(P, pos) || (P.causal && k > pos)) continue;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if ((w[e / 4] >> (8 * (e & 3)) & 0x7f) == 0x7f) set(r, d0 + 16 * chunk + e);
+        }
+    }
+}
+constexpr uint32_t A_NAN = 0x7fffffffu;
+
 // Two codes as exact fp16 values.
 __device__ __forceinline__ uint32_t halves(uint32_t w) {
     uint32_t r;
@@ -231,7 +272,7 @@ struct Few {
     static constexpr int OFF_ROW = OFF_RED + 8 * R * 4;              // [R] factor of the row, [R] first, [R] end, [R] the factor's low part
     static constexpr int OFF_SC = OFF_ROW + 4 * R * 4;               // [STAGES][SCALES]
     static constexpr int OFF_BAR = (OFF_SC + STAGES * SCALES * 4 + 7) / 8 * 8;
-    static constexpr int SMEM = OFF_BAR + 16 * STAGES + 16;
+    static constexpr int SMEM = OFF_BAR + 16 * STAGES + 16;  // (barriers, the parts that were there, whether there was a NaN)
     static_assert(CTAS == 1 ? SMEM <= 232448 : 2 * (SMEM + 1024) <= 233472, "shared memory");
     static constexpr int PART = R * (DP + 2);  // floats of a partial result
     // byte of 16-byte chunk c of a row of a tile
@@ -501,6 +542,7 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
     float *const sc = reinterpret_cast<float *>(smem + C::OFF_SC);
     const uint32_t full = base + C::OFF_BAR, empty = full + 8 * STAGES;
     volatile unsigned *const arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 16 * STAGES);
+    volatile unsigned *const some_nan = arrived + 1;  // a NaN among values that not all rows see, in some unit up to here
 
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
@@ -508,6 +550,7 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
             mbar_init(empty + 8 * i, 8);
         }
         fence_mbar_init();
+        *some_nan = 0;
     }
     pdl_wait();
     pdl_trigger();
@@ -597,26 +640,17 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
             const uint32_t sk = base + slot * C::STAGE, sv = sk + C::SIDE;
             const int tok0 = s.lo + j * TILE;
             const bool whole = tok0 >= u.all_lo && tok0 + TILE <= u.all_hi;
-            uint32_t nans = 0;  // of this warp's tokens those with a NaN among their values
             if (ok && !whole) {
                 // What no row sees may be anything, a page that nobody sees is not even
                 // there: P of them is 0, and so are their values from here on.  A token
-                // that some rows see and some do not: 0 times a NaN would reach the
-                // others, so the NaN goes to the scores of those that see it.
+                // that some rows see and some do not: spread_nans.
 #pragma unroll 1
                 for (int i = 0; i < 16 * KS / 32; ++i) {
                     const int row = 16 * warp + (32 * i + lane) / KS;
                     uint4 *v = reinterpret_cast<uint4 *>(smem + slot * C::STAGE + C::SIDE + C::at(row, (32 * i + lane) % KS));
                     const bool seen = tok0 + row >= u.lo && tok0 + row < u.hi, bad = seen && has_nan(*v);
                     if (!seen) *v = make_uint4(0, 0, 0, 0);
-                    if (__any_sync(0xffffffffu, bad)) nans |= __reduce_or_sync(0xffffffffu, bad ? 1u << (row & 15) : 0u);
-                }
-                if (nans) {
-#pragma unroll 1
-                    for (int i = lane; i < 16 * KS; i += 32)
-                        if (nans >> (i / KS) & 1)
-                            *reinterpret_cast<uint4 *>(smem + slot * C::STAGE + C::SIDE + C::at(16 * warp + i / KS, i % KS)) =
-                                make_uint4(0, 0, 0, 0);
+                    if (bad) *v = without_nan(*v), *some_nan = 1;
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (before the next copy into the slot)
             }
@@ -674,11 +708,6 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
                 const float2 f = *reinterpret_cast<const float2 *>(row_f + r);
                 const float f0 = f.x * ks, f1 = f.y * ks;
                 float y[4];
-                if (nans) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (nans >> (g + (i >> 1) * 8) & 1) x[n][i] = __uint_as_float(0x7fffffffu);
-                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] = fmaf(x[n][i], i & 1 ? f1 : f0, lv);
                 if (!whole) {
@@ -803,6 +832,7 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
             }
         }
         named_barrier(1, THREADS);
+        const bool nans = *some_nan != 0;  // (the same for all warps: none is past the next barrier)
 
         // sums over the lanes and warps that share a row
         if (far) {
@@ -854,7 +884,10 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
             at = (static_cast<int64_t>(s.row0) + i) * P.ldy_t + static_cast<int64_t>(h) * P.ldy_h;
             row = (static_cast<int64_t>(s.row0) + i) * P.heads * P.group + h;
         };
-        if (u.nt == s.tiles) {
+        const bool entire = u.nt == s.tiles;
+        // (an entire unit's results, or a part of it: [row][dim] sums relative to m, then m and l)
+        float *const mine = P.part + (static_cast<int64_t>(blockIdx.x) * 2 + (w.tile == 0)) * C::PART;
+        if (entire) {
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -877,8 +910,6 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
                     if (P.lse && warp == 0 && g == 0) P.lse[row] = l[n][h] != 0.0f ? (m[n][h] + log2f(l[n][h]) + 20.0f - C::SHIFT) * LN2 : -INFINITY;
                 }
         } else {
-            // a part of a unit: [row][dim] sums relative to m, then m and l
-            float *const mine = P.part + (static_cast<int64_t>(blockIdx.x) * 2 + (w.tile == 0)) * C::PART;
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -894,6 +925,18 @@ __global__ void __launch_bounds__(THREADS + 32, Few<DP, NB, HL>::CTAS)
                     }
                     if (warp == 0 && g == 0) mine[R * DP + r] = m[n][h], mine[R * DP + R + r] = l[n][h];
                 }
+        }
+        if (nans) {
+            named_barrier(1, THREADS);
+            spread_nans(P, w.b, head, start, r0, 0, rows, 0, DP, max(u.from + u.jb * TILE, u.lo), min(u.from + u.je * TILE, u.hi), u.all_lo,
+                        u.all_hi, tid, THREADS, [&](int r, int d) {
+                            int64_t at, row;
+                            out(r, at, row);
+                            if (entire) store_typed(P.y, at + d, P.y_type, __uint_as_float(A_NAN));
+                            else mine[r * DP + d] = __uint_as_float(A_NAN);
+                        });
+        }
+        if (!entire) {
             named_barrier(1, THREADS);
             const long long u0 = w.seq0 + w.unit * s.tiles, u1 = u0 + s.tiles - 1;  // first and last tile of the unit
             const int c0 = static_cast<int>(divide((u0 + 1) * blocks - 1, W)), c1 = static_cast<int>(divide((u1 + 1) * blocks - 1, W));

@@ -44,8 +44,7 @@ struct Rows {
     static constexpr int SIDE = TILE * DP, STAGE = 2 * SIDE;
     static constexpr int OFF_Q = STAGES * STAGE, Q_WARP = DP / 16 * 1024;  // [WARPS][DP / 16][part][lane] fragments
     static constexpr int OFF_SC = OFF_Q + WARPS * Q_WARP;    // [STAGES] scales (as there)
-    static constexpr int OFF_NANS = OFF_SC + STAGES * SCALES * 4;    // [STAGES][8] tokens with a NaN, 16 of a warp
-    static constexpr int OFF_BAR = OFF_NANS + STAGES * 32;
+    static constexpr int OFF_BAR = OFF_SC + STAGES * SCALES * 4;
     static constexpr int SMEM = OFF_BAR + 16 * STAGES + 16;
     static_assert(SMEM <= 232448, "shared memory");
     static constexpr int PART = R * (DP + 2);
@@ -245,9 +244,9 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1)
     const uint32_t base = smem_u32(smem);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, c = lane & 3;
     float *const sc = reinterpret_cast<float *>(smem + C::OFF_SC);
-    uint32_t *const nan_words = reinterpret_cast<uint32_t *>(smem + C::OFF_NANS);
     const uint32_t full = base + C::OFF_BAR, empty = full + 8 * STAGES;
     volatile unsigned *const arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 16 * STAGES);
+    volatile unsigned *const some_nan = arrived + 1;  // a NaN among values that not all rows see, in some unit up to here
 
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
@@ -255,6 +254,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1)
             mbar_init(empty + 8 * i, WARPS);
         }
         fence_mbar_init();
+        *some_nan = 0;
     }
     pdl_wait();
     pdl_trigger();
@@ -350,10 +350,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1)
             }
             const bool whole = tok0 >= u.all_lo && tok0 + TILE <= u.all_hi;  // (the same for all warps)
             if (!whole) {
-                // What no row sees counts as 0, and a NaN among the values of a token
-                // goes to the scores of the rows that see it: as in kv_attention.cuh, each
-                // warp for 16 tokens.
-                uint32_t nans = 0;
+                // What no row sees counts as 0, and so does a NaN for now: as in
+                // kv_attention.cuh, each warp for 16 tokens.
                 if (!dead) {
                     uint8_t *const values = smem + slot * C::STAGE + C::SIDE;
 #pragma unroll 1
@@ -362,17 +360,10 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1)
                         uint4 *v = reinterpret_cast<uint4 *>(values + C::at(row, (32 * i + lane) % KS));
                         const bool seen = tok0 + row >= u.lo && tok0 + row < u.hi, bad = seen && has_nan(*v);
                         if (!seen) *v = make_uint4(0, 0, 0, 0);
-                        if (__any_sync(0xffffffffu, bad)) nans |= __reduce_or_sync(0xffffffffu, bad ? 1u << (row & 15) : 0u);
-                    }
-                    if (nans) {
-#pragma unroll 1
-                        for (int i = lane; i < 16 * KS; i += 32)
-                            if (nans >> (i / KS) & 1)
-                                *reinterpret_cast<uint4 *>(values + C::at(16 * warp + i / KS, i % KS)) = make_uint4(0, 0, 0, 0);
+                        if (bad) *v = without_nan(*v), *some_nan = 1;
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (before the next copy into the slot)
                 }
-                if (lane == 0) nan_words[slot * 8 + warp] = nans;
                 named_barrier(1, C::CONSUMERS);
             }
             if (!dead && !idle && tok0 < some_hi && tok0 + TILE > some_lo) {
@@ -412,7 +403,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1)
                         }
                     }
                 }
-                // P, the operand of the second product.  Masks and NaN values only where the
+                // P, the operand of the second product.  Masks only where the
                 // unit's rows do not all see the tile: an instance of its own.
                 uint32_t ph[TS][4], pl[TS][4];
                 float alpha[2];
@@ -420,15 +411,6 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1)
                     constexpr bool MASKED = decltype(masked)::value;
                     uint32_t hidden[TS] = {};  // bit 4 b + i of t: x[2 t + b][i] is masked
                     if constexpr (MASKED) {
-#pragma unroll
-                        for (int t = 0; t < TS; ++t) {
-                            const uint32_t bad = nan_words[slot * 8 + t];
-                            if (bad) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    if (bad >> (8 * (i >> 2) + 2 * c + (i & 1)) & 1) x[2 * t + (i >> 2)][i & 3] = __uint_as_float(0x7fffffffu);
-                            }
-                        }
 #pragma unroll
                         for (int n = 0; n < 2 * TS; ++n)
 #pragma unroll
@@ -558,6 +540,16 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1)
             }
             if (!entire && c == 0) mine[R * DP + r] = m[h], mine[R * (DP + 1) + r] = l[h];
             if (entire && P.lse && c == 0) P.lse[row] = l[h] != 0.0f ? (m[h] + log2f(l[h]) + 20.0f - C::SHIFT) * LN2 : -INFINITY;
+        }
+        // (every tile that not all rows see had a barrier behind the search)
+        if (__any_sync(0xffffffffu, *some_nan != 0)) {
+            spread_nans(P, w.b, head, start, r0, 16 * warp, min(rows, 16 * warp + 16), 0, DP, max(u.from + u.jb * TILE, u.lo),
+                        min(u.from + u.je * TILE, u.hi), u.all_lo, u.all_hi, lane, 32, [&](int r, int d) {
+                            int64_t at, row;
+                            out(r, at, row);
+                            if (entire) store_typed(P.y, at + d, P.y_type, __uint_as_float(A_NAN));
+                            else mine[r * DP + d] = __uint_as_float(A_NAN);
+                        });
         }
         if (!entire) {
             far = named_barrier_or(1, C::CONSUMERS, far);

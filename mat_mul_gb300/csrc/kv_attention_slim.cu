@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
     float *const sc = reinterpret_cast<float *>(smem + C::OFF_SC);
     const uint32_t full = base + C::OFF_BAR, empty = full + 8 * STAGES;
     volatile unsigned *const arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 16 * STAGES);
+    volatile unsigned *const some_nan = arrived + 1;  // a NaN among values that not all rows see, in some unit up to here
 
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
             mbar_init(empty + 8 * i, 8);
         }
         fence_mbar_init();
+        *some_nan = 0;
     }
     pdl_wait();
     pdl_trigger();
@@ -218,10 +220,8 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
             }
             if (!dead && from < u.hi && from + 16 > u.lo) {
                 const bool whole = from >= u.all_lo && from + 16 <= u.all_hi;
-                uint32_t nans = 0;
                 if (!whole) {
-                    // What no row sees counts as 0, and a NaN among the values of a token goes to the
-                    // scores of the rows that see it: as in kv_attention.cuh.
+                    // What no row sees counts as 0, and so does a NaN for now: as in kv_attention.cuh.
                     uint8_t *const values = smem + slot * C::STAGE + C::SIDE;
 #pragma unroll 1
                     for (int i = lane; i < 16 * KS; i += 32) {
@@ -229,12 +229,7 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
                         uint4 *p = reinterpret_cast<uint4 *>(values + C::at(16 * warp + row, i % KS));
                         const bool seen = from + row >= u.lo && from + row < u.hi, bad = seen && has_nan(*p);
                         if (!seen) *p = make_uint4(0, 0, 0, 0);
-                        if (__any_sync(0xffffffffu, bad)) nans |= __reduce_or_sync(0xffffffffu, bad ? 1u << row : 0u);
-                    }
-                    if (nans) {
-#pragma unroll 1
-                        for (int i = lane; i < 16 * KS; i += 32)
-                            if (nans >> (i / KS) & 1) *reinterpret_cast<uint4 *>(values + C::at(16 * warp + i / KS, i % KS)) = make_uint4(0, 0, 0, 0);
+                        if (bad) *p = without_nan(*p), *some_nan = 1;
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (before the next copy into the slot)
                     __syncwarp();
@@ -290,7 +285,6 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
                                 for (int i = 0; i < 2; ++i) {
                                     const int k = 8 * n + 2 * c + i;
                                     float &y = x[t][n][2 * h + i];
-                                    if (nans >> k & 1) y = __uint_as_float(0x7fffffffu);
                                     if (from + k < lo || from + k >= hi) y = -INFINITY;
                                 }
                         }
@@ -368,6 +362,7 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
                 if (c == 0) warp_m[warp * R + r] = m[t][h], warp_l[warp * R + r] = l[t][h];
             }
         far = named_barrier_or(1, THREADS, far);
+        const bool nans = *some_nan != 0;  // (the same for all warps: none is past the next barrier)
         auto out = [&](int r, int64_t &at, int64_t &row) {
             const int i = token_of(P, r0 + r), h = head * P.group + (r0 + r - i * P.group);
             at = (static_cast<int64_t>(s.row0) + i) * P.ldy_t + static_cast<int64_t>(h) * P.ldy_h;
@@ -426,6 +421,16 @@ __global__ void __launch_bounds__(SLIM_THREADS, 1)
                 }
                 if (P.lse && d == 0) P.lse[row] = sum != 0.0f ? (top + log2f(sum) + 20.0f - C::SHIFT) * LN2 : -INFINITY;
             }
+            named_barrier(1, THREADS);
+        }
+        if (nans) {
+            spread_nans(P, w.b, head, start, r0, 0, rows, 0, DP, max(u.from + u.jb * TILE, u.lo), min(u.from + u.je * TILE, u.hi), u.all_lo,
+                        u.all_hi, tid, THREADS, [&](int r, int d) {
+                            int64_t at, row;
+                            out(r, at, row);
+                            if (entire) store_typed(P.y, at + d, P.y_type, __uint_as_float(A_NAN));
+                            else mine[r * DP + d] = __uint_as_float(A_NAN);
+                        });
             named_barrier(1, THREADS);
         }
         if (!entire) {

@@ -77,8 +77,7 @@ struct Tc {
     static constexpr int OFF_SC = OFF_SHARE + 2 * UNIT * 4;       // [SC_SLOTS][SC_FLOATS]
     static constexpr int OFF_PIECES = OFF_SC + SC_SLOTS * SC_FLOATS * 4;
     static constexpr int OFF_BAR = OFF_PIECES + PIECES * 48;
-    static constexpr int OFF_NANS = OFF_BAR + 320;  // [VR][4] bits of the tokens with a NaN among their values
-    static constexpr int SMEM = OFF_NANS + VR * 16;
+    static constexpr int SMEM = OFF_BAR + 320;
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(VR * RAW >= (TC_THREADS + 1) * 8, "prefix sums lie where the codes will");
     static constexpr int PART = UNIT * (DP + 2);  // floats of a partial result
@@ -261,7 +260,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
     static_assert(16 * C::KR + 32 * C::VR + 64 + 16 + 16 * PIECES + 8 <= 296, "barriers");
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 296);
     volatile unsigned *const arrived = reinterpret_cast<volatile unsigned *>(smem + C::OFF_BAR + 304);  // per tile
-    uint32_t *const nans = reinterpret_cast<uint32_t *>(smem + C::OFF_NANS);
+    volatile unsigned *const nans = arrived + 2;  // a NaN among values that not all rows see, in some unit up to here
     int4 *const pieces = reinterpret_cast<int4 *>(smem + C::OFF_PIECES);
     float *const sc = reinterpret_cast<float *>(smem + C::OFF_SC);
     long long *const pre = reinterpret_cast<long long *>(smem + C::OFF_RAW);
@@ -290,6 +289,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
         }
         mbar_init(done, 1);
         fence_mbar_init();
+        *nans = 0;
     }
     if (warp == 3) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
@@ -624,24 +624,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                     ok = false;
                     break;
                 }
-                const uint4 *src = reinterpret_cast<const uint4 *>(smem + C::OFF_RAW + s * C::RAW);
+                uint4 *const src = reinterpret_cast<uint4 *>(smem + C::OFF_RAW + s * C::RAW);
                 uint8_t *dst = smem + C::OFF_V + s * C::TILE_BYTES;
                 if (!whole) {
-                    // A token that some rows see and some do not: 0 times a NaN would reach
-                    // the others, so its values go, and the rows that see it are told.
-                    uint32_t *const bits = nans + 4 * s;
-                    if (me < 4) bits[me] = 0;
-                    named_barrier(11, 128);
+                    // (a token that some rows see and some do not: spread_nans)
+#pragma unroll 1
                     for (int k = me; k < TILE * cpr; k += 128) {
                         const int row = k / cpr;
-                        if (row >= live0 && row < live1 && has_nan(src[k])) atomicOr(bits + row / 32, 1u << (row & 31));
+                        if (row >= live0 && row < live1 && has_nan(src[k])) src[k] = without_nan(src[k]), *nans = 1;
                     }
                     named_barrier(11, 128);
                 }
                 auto one = [&](int row, int c, uint4 v) {
                     // (what no row sees may be anything, and is not even there where a
                     // whole page is: its probabilities are 0)
-                    if (row < live0 || row >= live1 || (!whole && nans[4 * s + row / 32] >> (row & 31) & 1)) v = make_uint4(0, 0, 0, 0);
+                    if (row < live0 || row >= live1) v = make_uint4(0, 0, 0, 0);
                     uint4 a, b;
                     convert16(v, a, b);
                     // (odd halves store their second part first: no two of eight lanes on one bank)
@@ -896,12 +893,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                         }
                     }
                     const float sub = (ref == -INFINITY ? 0.0f : ref) - TC_SHIFT;  // (a row that has seen nothing yet: any finite one)
-                    uint32_t bad0 = 0, bad1 = 0;
-                    if (masked) {  // (the conversion of the tile's values has found them)
+                    if (masked) {  // (the conversion of the tile's values has looked for NaNs: with_nans reads what it found)
                         const int v = tiles + j;
                         mbar_spin(v_full + 8 * (v % C::VR), (v / C::VR) & 1, P.status);
                         __syncwarp();
-                        bad0 = nans[4 * (v % C::VR) + 2 * half], bad1 = nans[4 * (v % C::VR) + 2 * half + 1];
                     }
                     // Groups 2 and 3, whose scores are here from the maximum, then 0 and 1.
                     auto exponentials = [&](auto with_mask) {
@@ -916,12 +911,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                                 float c = __uint_as_float(s[i2 & 1][e + 2]), d = __uint_as_float(s[i2 & 1][e + 3]);
                                 fma2(a, b, fk[h], lv[h] - sub);
                                 fma2(c, d, fk[h], lv[h] - sub);
-                                    if constexpr (with_mask.value) {
-                                    if (bad0 | bad1) {  // tokens with a NaN among their values
-                                        const float nan = __uint_as_float(0x7fffffffu);
-                                        const uint32_t w = (h < 2 ? bad0 : bad1) >> (16 * (h & 1) + e);
-                                        a = w & 1 ? nan : a, b = w & 2 ? nan : b, c = w & 4 ? nan : c, d = w & 8 ? nan : d;
-                                    }
+                                if constexpr (with_mask.value) {
                                     const int k = 16 * h + e;
                                     a = k >= from && k < to ? a : -INFINITY;
                                     b = k + 1 >= from && k + 1 < to ? b : -INFINITY;
@@ -967,8 +957,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                 l += *told;
                 const Piece pc = read_piece(np);
                 const int rows = rows_of(pc);
-                auto result = [&](int64_t &at, int64_t &row) {
-                    const int qr = pc.r0 + mine, i = token_of(qr), h = pc.head * P.group + (qr - i * P.group);
+                auto result = [&](int r, int64_t &at, int64_t &row) {
+                    const int qr = pc.r0 + r, i = token_of(qr), h = pc.head * P.group + (qr - i * P.group);
                     at = static_cast<int64_t>(pc.row0 + i) * P.ldy_t + static_cast<int64_t>(h) * P.ldy_h;
                     row = (static_cast<int64_t>(pc.row0) + i) * P.heads * P.group + h;
                 };
@@ -1001,11 +991,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                         for (int e = 0; e < 16; ++e) store_typed(P.y, at + d + e, P.y_type, v[e]);
                     }
                 };
+                // the NaNs among the results that this warp has written, which are its own
+                auto with_nans = [&](const auto &set) {
+                    __syncwarp();
+                    if (__any_sync(0xffffffffu, *nans != 0))
+                        spread_nans(P, pc.b, pc.head, pc.len - pc.n, pc.r0, mine - lane, min(rows, mine - lane + 32), half * HD, half * HD + HD,
+                                    max(pc.tile * TILE, from_of(pc)), min((pc.tile + pc.nt) * TILE, end_of(pc)), all_from_of(pc), all_end_of(pc),
+                                    lane, 32, set);
+                };
                 constexpr float LN2 = 0.6931471805599453f, BACK = 20.0f - TC_SHIFT;
                 if (pc.c0 < 0) {
                     const float inv = l != 0.0f ? L_FACTOR / l : 0.0f;
                     int64_t at, row;
-                    result(at, row);
+                    result(mine, at, row);
 #pragma unroll
                     for (int k = 0; k < HD / 16; ++k) {
                         uint32_t o[16];
@@ -1022,6 +1020,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                         if (mine < rows) put(at, half * HD + 16 * k, v);
                     }
                     if (P.lse && half == 0 && mine < rows) P.lse[row] = l != 0.0f ? (ref + log2f(l) + BACK) * LN2 : -INFINITY;
+                    with_nans([&](int r, int d) {
+                        int64_t y_at, y_row;
+                        result(r, y_at, y_row);
+                        store_typed(P.y, y_at + d, P.y_type, __uint_as_float(A_NAN));
+                    });
                 } else {
                     // a part of a unit: [groups of four columns][row] sums relative to ref, then ref and l
                     float *const part = P.part + (static_cast<int64_t>(cta) * 2 + pc.begin) * C::PART;
@@ -1041,6 +1044,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                                 make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                     if (half == 0) part[DP * UNIT + mine] = ref, part[(DP + 1) * UNIT + mine] = l;
+                    with_nans([&](int r, int d) { part[(d / 4 * UNIT + r) * 4 + d % 4] = __uint_as_float(A_NAN); });
                     __threadfence();
                     named_barrier(tile_bar, 256);
                     if (first && lane == 0) arrived[t] = atomicAdd(P.count + 2 * pc.c0 + t, 1u + (far ? FAR_PART : 0u));
@@ -1063,7 +1067,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) kv_attention_tc_kernel(const __
                         }
                         const float inv = sum != 0.0f ? L_FACTOR / sum : 0.0f;
                         int64_t at, row;
-                        result(at, row);
+                        result(mine, at, row);
 #pragma unroll 1
                         for (int k = half * HD / 16; k < (half + 1) * HD / 16; ++k) {
                             float v[16];

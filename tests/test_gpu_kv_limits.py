@@ -193,6 +193,31 @@ def test_pages_of_value_scales_far_apart(cuda_lib, kernel, low, high):
 
 
 @pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("window", [0, 60])
+def test_a_nan_code_of_a_value_reaches_its_element_alone(cuda_lib, kernel, window):
+    """Of the rows that see the token, in tiles that all rows see and in tiles that a mask cuts; the other elements and
+    the log of the sum are as if the value was none.  (Codes of -0 beside it are no NaN.)"""
+    q = cuda_lib
+    dtype, new, width = KERNELS[kernel]
+    rng = np.random.default_rng(75)
+    for dim, longest in ((64, 300), (48, 300), (128, 300), (256, 300), (128, 5003)):
+        batch = R.Batch(rng, [new] * 3, [max(n, new) for n in (longest, 140, 129)], 64, width=2 * width + longest // 64)
+        cache, codes, scales = _cache(q, rng, batch, 2, dim)
+        for b in range(3):
+            n = batch.lengths[b]
+            for j in {3, 126, n // 2, n - new, n - 1 - new // 2, n - 1, max(0, n - 60), max(0, n - 61)}:
+                at = codes[1][batch.table[b, j // 64], j % 2, j % 64]
+                at[rng.integers(0, dim, 7)] = 0x80
+                at[rng.integers(0, dim, 2)] = rng.choice([0x7f, 0xff], 2)
+            codes[1][batch.table[b, (n - 1) // 64], :, (n - 1) % 64 + 1:] = 0x7f   # behind the end
+        _put(cache, codes, scales)
+        x, xv = _as(rng.standard_normal((batch.T, 8, dim)), dtype)
+        y, _ = _against(q, cache, codes, scales, batch, x, xv, dtype, window=window)
+        nan = np.isnan(_np(y))
+        assert nan.any() and not nan.all(axis=2).any()
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
 @pytest.mark.parametrize("scale,large", [(0.0, 100), (1e-33, 100), (-1e-33, 100), (1e-36, 110)])
 def test_scales_of_the_scores_that_nearly_vanish(cuda_lib, kernel, scale, large):
     """With 0 every row is the mean of what it sees, whatever the keys are; tiny scales of large keys."""
