@@ -257,3 +257,37 @@ def test_offsets_that_fall_are_always_reported(cuda_lib, what, offsets):
         q.qmm_kv_attention(cache, x, table, lengths, offsets=_i32(offsets), y=y)
     assert q.qmm_device_status() == q.QMM_EINDEX and q.qmm_device_status() == 0
     assert bool((y[T:] == 7).all())
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("lengths,window", [([32769], 0), ([20001, 77, 9000], 0), ([20001, 300, 9000], 5000),
+                                            ([3000 + 97 * b for b in range(40)], 0)])
+def test_no_tile_of_a_long_sequence_is_lost_or_counted_twice(cuda_lib, kernel, lengths, window):
+    """Queries of zero, so that every token counts the same, and values of 1 in one element for each 128 tokens: the
+    results are the numbers of tokens over their sum.  Both are whole numbers times a power of two, exact in fp32: a
+    division, a product and an exponential of 0 are left, 2^-20 at most together, and a tile is 2^-8 or more of a sum."""
+    import torch
+    q = cuda_lib
+    dtype, new, width = KERNELS[kernel]
+    rng = np.random.default_rng(76)
+    dim, heads = 128, 2
+    batch = R.Batch(rng, [new] * len(lengths), lengths, 64, width=width)
+    codes = rng.integers(0, 127, (batch.pages, heads, 64, dim), np.uint8)
+    values = np.zeros((batch.pages, heads, 64, dim), np.uint8)
+    for b, n in enumerate(lengths):
+        for page in range(-(-n // 64)):
+            values[batch.table[b, page], :, :, page // 2 % dim] = 0x38   # 1.0
+    ones = torch.ones(batch.pages, heads, device="cuda")
+    cache = q.KvCache(_t(codes).view(torch.float8_e4m3fn), _t(values).view(torch.float8_e4m3fn), ones, ones.clone())
+    x, _ = _as(np.zeros((batch.T, 4 * heads, dim)), dtype)
+    y, lse = _run(q, cache, x, batch, dtype=torch.float32, window=window)
+    end = batch.positions() + 1
+    begin = np.maximum(end - window, 0) if window else np.zeros_like(end)
+    counts = np.zeros((batch.T, dim))
+    for tile in range(-(-max(lengths) // 128)):
+        counts[:, tile % dim] += np.clip(np.minimum(end, 128 * tile + 128) - np.maximum(begin, 128 * tile), 0, None)
+    n = (end - begin).astype(np.float64)
+    want = np.broadcast_to((counts / n[:, None])[:, None], y.shape)
+    _within(_np(y), want, 2.0 ** -20 * want, "y")
+    wl = np.broadcast_to(np.log(n)[:, None], lse.shape)
+    _within(_np(lse), wl, 2.0 ** -20 * (1 + wl), "lse")
