@@ -434,7 +434,13 @@ typedef struct {
  *   QMM_ROPE_PARTS  : f_i k + f_i / scale (1 - k) with k = (r - low) / (high - low)
  *                     within 0 .. 1, r = original f_i / 2 pi the turns within the
  *                     trained length (NTK by parts; with the factor 0.1 ln(scale)
- *                     + 1, low = 1 and high = 32 this is YaRN).
+ *                     + 1, low = 1 and high = 32 this is YaRN as its paper's text has
+ *                     it, a ramp linear in r).  Many published checkpoints were tuned
+ *                     with another ramp under that name, linear in the pair i, that is
+ *                     in log r: 1 - k = (i - i(high)) / (i(low) - i(high)) within 0 .. 1,
+ *                     i(r) = rot / 2 * log_base(original / (2 pi r)), some with i(high)
+ *                     rounded down and i(low) up.  The frequencies differ by up to a
+ *                     factor of 3: such a model's go in as freqs, with QMM_ROPE_PLAIN.
  * Needs no GPU.
  */
 #define QMM_ROPE_PLAIN 0

@@ -27,7 +27,7 @@ y in float32, float16 or bfloat16:
 
 The attention layer of a step, over a paged cache of 8-bit floats (e4m3 codes, one scale per page and head):
 
-    rope = q.qmm_rope_table(128, base=500000.0, scaling="yarn", scale=8.0, original=8192)
+    rope = q.qmm_rope_table(128, base=500000.0, scaling="parts", scale=8.0, original=8192)
     cache = q.KvCache.empty(pages, heads, page=64, dim=128)
     x = q.qmm_rope(x, rope, positions)            # x [T, heads, dim]; inverse=True: its gradient
     qr = q.qmm_kv_append(cache, k, v, table, lengths, rope=rope, q=qh)   # k turned and stored, queries turned
@@ -610,7 +610,14 @@ def qmm_rope_table(rot, base=10000.0, interleaved=False, scaling=None, scale=1.0
     larger base), "parts" (frequencies with fewer than `low` turns within the
     `original` length divided by scale, those with more than `high` kept, 1 and
     4 unless given) or "yarn" (the same with 1 and 32, and the factor 0.1
-    ln(scale) + 1).  factor multiplies the rotated values."""
+    ln(scale) + 1).  factor multiplies the rotated values.
+
+    "yarn" blends as the paper's text says, linear in the turns.  Many published
+    checkpoints were tuned with a blend linear in the pair's index; theirs are
+    freqs=[f * k + f / scale * (1 - k)] with f = base^(-2i/rot), 1 - k =
+    (i - i(high)) / (i(low) - i(high)) within 0 .. 1 and i(r) = rot / 2 *
+    log(original / (2 pi r)) / log(base), and factor=0.1 ln(scale) + 1; some
+    round i(high) down and i(low) up."""
     import torch
     if scaling not in _ROPE_SCALINGS:
         raise ValueError(f"scaling must be None, 'linear', 'ntk', 'parts' or 'yarn', not {scaling!r}")

@@ -291,3 +291,22 @@ def test_no_tile_of_a_long_sequence_is_lost_or_counted_twice(cuda_lib, kernel, l
     _within(_np(y), want, 2.0 ** -20 * want, "y")
     wl = np.broadcast_to(np.log(n)[:, None], lse.shape)
     _within(_np(lse), wl, 2.0 ** -20 * (1 + wl), "lse")
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_a_ramp_over_pairs_by_frequencies_of_ones_own(cuda_lib, interleaved):
+    """What qmm_rope_table says of checkpoints tuned with a ramp over the pairs: frequencies and factor as given there."""
+    q = cuda_lib
+    rot, base, scale, original, low, high = 128, 10000.0, 16.0, 8192, 1.0, 32.0
+    i = np.arange(rot // 2)
+    f = base ** (-2.0 * i / rot)
+    ends = [rot / 2 * math.log(original / (2 * math.pi * r)) / math.log(base) for r in (high, low)]
+    keep = 1.0 - np.clip((i - ends[0]) / (ends[1] - ends[0]), 0.0, 1.0)
+    f = f * keep + f / scale * (1.0 - keep)
+    factor = 0.1 * math.log(scale) + 1.0
+    rng = np.random.default_rng(77)
+    x, xv = _as(rng.standard_normal((60, 2, rot)), "float32")
+    pos = rng.integers(0, 100000, 60).astype(np.int32)
+    y = q.qmm_rope(x, q.qmm_rope_table(rot, freqs=f, factor=factor, interleaved=interleaved), _t(pos))
+    want, e = R.rope(xv, pos, f, interleaved, False, factor)
+    _within(_np(y), want, R.rounded(want, e, "float32"))
