@@ -522,14 +522,16 @@ QMM_API int qmm_kv_append(const qmm_kv_append_args *args, void *stream);
  * 2^-20 for fp32: |dy_i| <= (u + (n + dim + 64) 2^-22 (1 + X)) * sum_j p_j |v_ji| / sum_j p_j
  * before the rounding to y's type, n the tokens seen and X the largest of the
  * row's |scale| sum_i |q_i k_ji|; 16-bit query values below 2^-13 of their head's
- * largest, m, may besides be off by 2^-21 m.
+ * largest, m, may besides be off by 2^-21 m, and those of any type by 2^-114 where m
+ * is below 2^-87.
  * A NaN or an infinity among a head's query values makes its results NaN, a NaN
- * code those of the rows that see its token: of a value in its own element, of a
- * key in all of them.
+ * code those of the rows that see its token: of a value in its own element (lse
+ * stays), of a key in all of them.
  * y must not be q, nor overlap it.  How a sequence's tokens are shared out, and with
  * it the last bits of its rows, depends on the other sequences of the call and on the
  * width of the table.
- * Scales are positive and finite; value scales below 2^-100 count as 2^-100, and
+ * Scales are positive and finite, and a row's may lie as far apart as they like; value
+ * scales below 2^-100 count as 2^-100, and
  * above 2^112 the sums of probabilities lose bits for 16-bit queries.
  * scratch null: partial results go to the per-(device, stream) workspace (make
  * one call of the largest size before capture, and replay graphs that were

@@ -15,9 +15,9 @@ int row_groups(const KvAttention &a) {
 // Whether the call's rows go to a kernel for many rows (of 256 on tcgen05 for 16-bit
 // queries, of 128 on mma.sync for fp32): heads of up to 128 values, sequences of more than 32
 // rows per cache head on the average.  Measured, a kernel for few rows against the
-// other, 8 sequences, 8 heads of 128: 16-bit, 20 rows over 1024, 4096, 16384 tokens 21, 34, 80
-// against 27, 43, 118 us; fp32, 40 rows over 4096 96 against 77, 64 rows over 1024 44
-// against 42.
+// other, 8 sequences, 8 heads of 128: fp16, 20 rows over 1024, 4096, 16384 tokens 23, 41, 95
+// against 31, 47, 125 us; fp32, 40 rows over 4096 98 against 78, 64 rows over 1024 47
+// against 43.
 bool many_rows(const KvAttention &a) {
     return a.c.dim <= 128 && a.batch.T * (a.q_heads / a.c.heads) > 32 * int64_t(a.batch.B);
 }
@@ -26,9 +26,9 @@ bool many_rows(const KvAttention &a) {
 // 16-bit queries, heads of up to 128 values, 9 to 32 rows, and sequences that may be
 // long (the lengths are on the device; the table says how long at most): eight tiles
 // of 128 tokens per multiprocessor.  Its blocks start and end 3 us later, its tiles take
-// 0.6 of the time.  Measured, the other kernel against it, 8 sequences, 8 heads of 128: 20 rows
-// over 1024, 4096, 16384 tokens 20.7, 42.8, 112 against 23.2, 33.5, 80 us, 12 rows over 1024,
-// 4096 14.5, 28.6 against 16.9, 24.3; 4 rows, 64 sequences of 4096 tokens, 94 against 109.
+// 0.6 of the time.  Measured, the other kernel against it, 8 sequences, 8 heads of 128: 20 fp16 rows
+// over 1024, 4096, 16384 tokens 22.9, 46, 120 against 26.8, 41, 95 us, 12 rows over 1024,
+// 4096 16.5, 30.8 against 20.6, 28.8; 4 rows, 64 sequences of 4096 tokens, 94 against 109.
 bool slim_rows(const KvAttention &a, int num_sms) {
     const double tiles = double(a.batch.width) * a.c.page / kv::TILE * a.batch.B * a.c.heads;
     return a.q.type != QMM_F32 && a.c.dim <= 128 && row_groups(a) > 1 && tiles >= 8.0 * num_sms;

@@ -1,6 +1,7 @@
 // kv_attention.cuh -- attention over the paged 8-bit cache for few query rows
-// per cache head (decode, drafted tokens) and for fp32 queries: one pass over
-// the cache on mma.sync, work cut along the tokens and joined.
+// per cache head (decode, drafted tokens), and for any number of them with heads of
+// more than 128 values: one pass over the cache on mma.sync, work cut along the
+// tokens and joined.
 //
 //   y = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j),  k_j = sk code, v_j = sv code,
 // with one scale sk, sv per page and head.  A row's scores in powers of two,
@@ -24,7 +25,7 @@
 // runs ahead across units.
 //
 // Measured (8 heads of 128 in the cache, 32 of the queries): 64 sequences of 4096 tokens, one
-// row each, 94 us, 5.7 TB/s of codes; one of 32768 20 us, of which the tiles take 6, the
+// row each, 94 us, 5.7 TB/s of codes; one of 32768 22 us, of which the tiles take 6, the
 // rest start (shares, page table, queries, first tile: 3) and join (5).  A tile takes 2000
 // cycles, two blocks on a multiprocessor beside each other.
 #pragma once
