@@ -543,6 +543,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1)
         }
         // (every tile that not all rows see had a barrier behind the search)
         if (__any_sync(0xffffffffu, *some_nan != 0)) {
+            __syncwarp();  // (other lanes wrote what these change; a vote orders no memory)
             spread_nans(P, w.b, head, start, r0, 16 * warp, min(rows, 16 * warp + 16), 0, DP, max(u.from + u.jb * TILE, u.lo),
                         min(u.from + u.je * TILE, u.hi), u.all_lo, u.all_hi, lane, 32, [&](int r, int d) {
                             int64_t at, row;
